@@ -65,6 +65,7 @@ extern "C" {
 /* Logit element types. */
 #define SPEC_VERIFY_BF16 0
 #define SPEC_VERIFY_FP32 1
+#define SPEC_VERIFY_FP16 2 /* queries, keys and values only */
 
 /* Host return codes. */
 #define SPEC_VERIFY_OK 0
@@ -296,6 +297,93 @@ int spec_verify_kv_compact(void *kv_pool, int64_t num_slots, size_t row_bytes, i
                            const int32_t *committed_in, int32_t *committed_out,
                            const int32_t *accept_index, const int32_t *accept_len, int B, int N,
                            int32_t *dev_status, void *stream);
+
+/*
+ * The new keys and values of a verify forward into the paged cache of one layer, rotated by their
+ * positions, and the queries rotated beside them.  With pos(n) = committed + depth of node n
+ * (`parents` NULL: a chain or prompt, depth n) and (c, s) the cosines and sines of pos(n):
+ *   k_cache[slot_table[b][committed + n]] = rotate(k), v_cache[same] = v, q_out = rotate(q)
+ *   rotate: (x_i, x_j) -> (x_i c - x_j s, x_j c + x_i s), j = i + rotary_dim/2 for i < rotary_dim/2,
+ *   or with `interleaved` the pairs (2i, 2i + 1); dimensions from rotary_dim on are kept.
+ *   q, k, v        [B * N] rows of Hq, Hkv, Hkv heads of D elements, *_stride elements apart (so the
+ *                  three may be parts of one projection's rows); dtype SPEC_VERIFY_BF16 or _FP16;
+ *                  bases 16-byte aligned, strides multiples of 8, D a multiple of 16, at most 1024
+ *   q_out          [B * N][Hq][D], contiguous; must not overlap q
+ *   k_cache, v_cache  [num_slots] slots of [Hkv][D], *_slot_stride elements apart (multiples of 8)
+ *   slot_table, committed  as for spec_verify_kv_compact: the slots and the lengths that it takes
+ *   parents        [B][N] as for spec_verify_tree (N <= 64), or NULL
+ *   num_nodes      [B] in [0, N]: nodes of each request, or NULL (all N).  The rows of nodes past it
+ *                  are not read; their q_out is 0
+ *   cos_sin        [rot_positions][rotary_dim] fp32: rotary_dim/2 cosines, then as many sines, of each
+ *                  position; a table, because the angle of a far position needs more than fp32 and
+ *                  because scaled rotations differ only in it.  rotary_dim is a multiple of 16 up
+ *                  to D; 0: no rotation, cos_sin may be NULL
+ * Arithmetic is in fp32, rounded once.  Device status codes: 3 (malformed tree), 5 (num_nodes outside
+ * [0, N], committed + num_nodes beyond max_pos, or a position past cos_sin) and 6 (a slot outside the
+ * pool).  A tree or length fault leaves the request's slots unwritten and its q_out NaN; a fault of
+ * one node's slot or rotation position does so for that node.  Requests must not share the slots
+ * written.  One launch, no workspace.
+ */
+int spec_verify_kv_append(const void *q, const void *k, const void *v, int dtype, int64_t q_stride,
+                          int64_t k_stride, int64_t v_stride, void *q_out, void *k_cache, void *v_cache,
+                          int64_t num_slots, int64_t k_slot_stride, int64_t v_slot_stride,
+                          const int32_t *slot_table, int max_pos, const int32_t *committed,
+                          const int32_t *parents, const int32_t *num_nodes, const float *cos_sin,
+                          int rot_positions, int rotary_dim, int interleaved, int B, int N, int Hq,
+                          int Hkv, int D, int32_t *dev_status, void *stream);
+
+/*
+ * Attention of a verify step's nodes over one layer's paged cache (N = 1: plain decoding).  Node n
+ * of request b sees the positions j < committed and the positions committed + a of the nodes a on
+ * its path from the root, itself included (`parents` NULL: a chain, a <= n):
+ *   out[b][n][h] = sum_j softmax_j(scale * q[b][n][h] . k_j) v_j over those j, and
+ *   lse[b][n][h] = ln sum_j e^(scale * q . k_j); query head h reads key head h / (Hq / Hkv).
+ * What a node does not see has no part in its row, whatever is stored there (NaN and infinities
+ * included).  Arguments as for spec_verify_kv_append, and
+ *   q              [B * N] rows of Hq heads of D elements, q_stride elements apart, rotated
+ *   out            [B * N][Hq][D], contiguous, of q's type;  lse  [B * N][Hq] fp32 or NULL
+ *   N <= 64, D a multiple of 16 from 64 to 128, Hq a multiple of Hkv, num_slots < 2^31,
+ *   scale > 0 and finite
+ *   workspace      spec_verify_attention_workspace_bytes(...) bytes, 256-byte aligned; zero-filled
+ *                  before its first use, shared with the verifiers' (their counters' rules hold)
+ * Sums and the softmax are in fp32; the weights are rounded to q's type for the product with v.
+ * Rows of nodes past num_nodes are 0 with lse -inf.  Device status codes 3, 5 and 6 as above (6: any
+ * of the request's slots); all rows of such a request are NaN, which the verifiers report in turn
+ * (a logit row holding NaN).  The same inputs give the same bits.
+ */
+size_t spec_verify_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int max_pos);
+int spec_verify_attention(const void *q, int dtype, int64_t q_stride, const void *k_cache,
+                          const void *v_cache, int64_t num_slots, int64_t k_slot_stride,
+                          int64_t v_slot_stride, const int32_t *slot_table, int max_pos,
+                          const int32_t *committed, const int32_t *parents, const int32_t *num_nodes,
+                          int B, int N, int Hq, int Hkv, int D, float scale, void *out, float *lse,
+                          void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * Log probabilities of given tokens, with the distribution's entropy and its most likely
+ * alternatives: what a server answers beside the tokens that verification emitted.  With
+ * x = logits / T of a row:
+ *   logprobs[b][t] = ln softmax(x)[tokens[b][t]];  entropy[b][t] = -sum p ln p (NULL: not wanted)
+ *   ranks[b][t] = 1 + the number of tokens with a larger logit (NULL: not wanted)
+ *   top_ids, top_logprobs [b][t][top_n]: the largest logits in order, ties to the lower token; -1
+ *   and -inf where no token with a finite logit is left (top_n = 0: both may be NULL; at most 32)
+ *   logits         [B][rows][V] bf16 / fp32
+ *   tokens         [B][T] int32; -1: nothing there (verification's out_tokens have it past the stop):
+ *                  the row is not read; logprobs and entropy are 0, ranks 0, alternatives -1 / -inf
+ *   row_index      [B][T] int32: the request's logit row of each token (a tree's accept_index), -1 as
+ *                  for tokens; NULL: row t (a chain)
+ *   temperatures   [B] device, or NULL: `temperature` for all.  0 (a greedy request) reports at T = 1
+ *   T <= 64, rows <= 64; workspace of spec_verify_logprobs_workspace_bytes(...) bytes, rules as above
+ * Sums are in fp32.  Device status codes 1 (token outside [-1, V)) and 2 (row_index outside [-1, rows),
+ * a temperature below 0 or NaN, a row holding NaN or +inf, or no finite value): that entry's logprob,
+ * entropy and top_logprobs are NaN, its rank and top_ids -1.  The same inputs give the same bits.
+ */
+size_t spec_verify_logprobs_workspace_bytes(int B, int T, int V, int top_n);
+int spec_verify_logprobs(const void *logits, int dtype, const int32_t *tokens, const int32_t *row_index,
+                         int B, int rows, int T, int V, const float *temperatures, float temperature,
+                         int top_n, float *logprobs, float *entropy, int32_t *ranks, int32_t *top_ids,
+                         float *top_logprobs, void *workspace, size_t ws_bytes, int32_t *dev_status,
+                         void *stream);
 
 /*
  * Workspace bytes needed by one call of the given mode (SPEC_VERIFY_MODE_*) with B requests,

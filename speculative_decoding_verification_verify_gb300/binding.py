@@ -17,7 +17,7 @@ import torch
 
 from . import _build
 
-BF16, FP32 = 0, 1
+BF16, FP32, FP16 = 0, 1, 2
 MODE_GREEDY, MODE_REJECTION, MODE_TREE, MODE_BLOCK = 0, 1, 2, 3
 OK, EINVAL, EWORKSPACE, ECUDA, ETOOBIG = 0, -1, -2, -3, -4
 NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -78,6 +78,21 @@ def _declare(lib):
     lib.spec_verify_plan_budget.restype = i32
     lib.spec_verify_plan_budget_workspace_bytes.argtypes = [i32, i32]
     lib.spec_verify_plan_budget_workspace_bytes.restype = sz
+    i64 = ctypes.c_int64
+    lib.spec_verify_kv_append.argtypes = [vp, vp, vp, i32, i64, i64, i64, vp, vp, vp, i64, i64, i64, vp,
+                                          i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32,
+                                          vp, vp]
+    lib.spec_verify_kv_append.restype = i32
+    lib.spec_verify_attention.argtypes = [vp, i32, i64, vp, vp, i64, i64, i64, vp, i32, vp, vp, vp, i32,
+                                          i32, i32, i32, i32, f32, vp, vp, vp, sz, vp, vp]
+    lib.spec_verify_attention.restype = i32
+    lib.spec_verify_attention_workspace_bytes.argtypes = [i32] * 6
+    lib.spec_verify_attention_workspace_bytes.restype = sz
+    lib.spec_verify_logprobs.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, vp, f32, i32, vp, vp, vp,
+                                         vp, vp, vp, sz, vp, vp]
+    lib.spec_verify_logprobs.restype = i32
+    lib.spec_verify_logprobs_workspace_bytes.argtypes = [i32] * 4
+    lib.spec_verify_logprobs_workspace_bytes.restype = sz
     lib.spec_verify_debug_fault.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
     lib.spec_verify_debug_fault.restype = i32
     lib.spec_verify_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
@@ -545,3 +560,241 @@ def spec_verify_plan_budget(conf: torch.Tensor, cost: torch.Tensor, num_drafts=N
     if rc != OK:
         raise SpecVerifyError("spec_verify_plan_budget", rc)
     return admitted, budget, best_rate
+
+
+# --------------------------------------------------------------------------------------------
+# Around verification: the cache's new rows, attention over it, log probabilities
+# --------------------------------------------------------------------------------------------
+class Attention(NamedTuple):
+    out: torch.Tensor
+    lse: Optional[torch.Tensor]
+
+
+class Logprobs(NamedTuple):
+    logprobs: torch.Tensor
+    entropy: torch.Tensor
+    ranks: torch.Tensor
+    top_ids: Optional[torch.Tensor]
+    top_logprobs: Optional[torch.Tensor]
+
+
+_HALF = {torch.bfloat16: BF16, torch.float16: FP16}
+
+
+def _half_dtype(name: str, t: torch.Tensor) -> int:
+    code = _HALF.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _node_rows(name: str, t: torch.Tensor, shape, like: torch.Tensor) -> int:
+    """Check [B, N, heads, D] rows whose heads are contiguous and which are evenly spaced (a view
+    into a projection's output will do); returns the elements from one row to the next."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    B, N, H, D = shape
+    sb, sn, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}'s heads must be contiguous")
+    if N == 1:
+        sn = sb if B > 1 else max(sn, H * D)
+    elif B > 1 and sb != N * sn:
+        raise ValueError(f"{name}'s rows must be evenly spaced")
+    return sn
+
+
+def _cache_slots(name: str, t: torch.Tensor, like: torch.Tensor) -> int:
+    """Check [num_slots, Hkv, D] with contiguous slot rows; returns the slot stride in elements."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [num_slots, Hkv, D]")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    S, H, D = t.shape
+    ss, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}'s slots must be contiguous")
+    return ss if S > 1 else max(ss, H * D)
+
+
+def _int32_of(name: str, t: Optional[torch.Tensor], shape, device):
+    if t is None:
+        return
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be contiguous and on {device}")
+
+
+def _result(name: str, t: Optional[torch.Tensor], shape, dtype, device, stream) -> torch.Tensor:
+    """A caller's output checked, or a new one that the stream's work may write."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        if stream is not None:
+            t.record_stream(stream)
+        return t
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+    return t
+
+
+def _status_of(dev_status, device):
+    if dev_status is not None and (dev_status.dtype != torch.int32 or dev_status.device != device):
+        raise ValueError(f"dev_status must be an int32 tensor on {device}")
+
+
+def spec_verify_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                          v_cache: torch.Tensor, slot_table: torch.Tensor, committed: torch.Tensor,
+                          cos_sin: Optional[torch.Tensor], *, parents=None, num_nodes=None,
+                          interleaved: bool = False, q_out=None, dev_status=None,
+                          stream=None) -> torch.Tensor:
+    """Write a verify forward's keys (rotated by position) and values into one layer's paged cache,
+    in place, and return the rotated queries.
+
+    q [B, N, Hq, D], k and v [B, N, Hkv, D] (bf16 / fp16; may be views into one projection's rows),
+    k_cache and v_cache [num_slots, Hkv, D], slot_table [B, max_pos] and committed [B] int32,
+    cos_sin [positions, rotary_dim] fp32 (cosines, then sines; None: no rotation), parents [B, N]
+    int32 (None: a chain or a prompt), num_nodes [B] int32 (None: all N).  Without dev_status,
+    faults in the data show in the returned rows alone (NaN)."""
+    lib = _lib or load_library()
+    code = _half_dtype("q", q)
+    if not q.is_cuda or q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be a [B, N, Hq, D] and k a [B, N, Hkv, D] CUDA tensor")
+    B, N, Hq, D = q.shape
+    Hkv, dev = k.shape[2], q.device
+    qs = _node_rows("q", q, (B, N, Hq, D), q)
+    ks = _node_rows("k", k, (B, N, Hkv, D), q)
+    vs = _node_rows("v", v, (B, N, Hkv, D), q)
+    kss = _cache_slots("k_cache", k_cache, q)
+    vss = _cache_slots("v_cache", v_cache, q)
+    slots = k_cache.shape[0]
+    if k_cache.shape[1:] != k.shape[2:] or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [num_slots, Hkv, D]")
+    _int32_of("slot_table", slot_table, (B, slot_table.shape[-1]), dev)
+    _int32_of("committed", committed, (B,), dev)
+    _int32_of("parents", parents, (B, N), dev)
+    _int32_of("num_nodes", num_nodes, (B,), dev)
+    if cos_sin is not None and (cos_sin.dim() != 2 or cos_sin.dtype != torch.float32
+                                or not cos_sin.is_contiguous() or cos_sin.device != dev):
+        raise ValueError(f"cos_sin must be a contiguous float32 [positions, rotary_dim] tensor on {dev}")
+    _status_of(dev_status, dev)
+    q_out = _result("q_out", q_out, (B, N, Hq, D), q.dtype, dev, stream)
+    positions, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+    rc = lib.spec_verify_kv_append(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), code, qs, ks, vs, q_out.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), slots, kss, vss, slot_table.data_ptr(), slot_table.shape[1],
+        committed.data_ptr(), _addr(parents), _addr(num_nodes), _addr(cos_sin), positions, rot,
+        bool(interleaved), B, N, Hq, Hkv, D, _addr(dev_status),
+        (stream or torch.cuda.current_stream(dev)).cuda_stream)
+    if rc != OK:
+        raise SpecVerifyError("spec_verify_kv_append", rc)
+    return q_out
+
+
+def spec_verify_attention_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int, max_pos: int) -> int:
+    return int(load_library().spec_verify_attention_workspace_bytes(B, N, Hq, Hkv, D, max_pos))
+
+
+def spec_verify_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          slot_table: torch.Tensor, committed: torch.Tensor, *, parents=None,
+                          num_nodes=None, scale: Optional[float] = None, out=None, lse=None,
+                          want_lse: bool = False, workspace=None, dev_status=None,
+                          stream=None) -> Attention:
+    """Attention of the verify step's nodes (N = 1: plain decoding) over one layer's paged cache:
+    each sees the committed positions and the nodes on its path from the root.
+
+    q [B, N, Hq, D] rotated, the cache and its tables as spec_verify_kv_append left them; scale
+    defaults to D ** -0.5.  Returns out [B, N, Hq, D] and, when wanted or given, lse [B, N, Hq] fp32.
+    Without dev_status, faults in the data show in the returned rows alone (NaN)."""
+    lib = _lib or load_library()
+    code = _half_dtype("q", q)
+    if not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a [B, N, Hq, D] CUDA tensor")
+    B, N, Hq, D = q.shape
+    dev = q.device
+    qs = _node_rows("q", q, (B, N, Hq, D), q)
+    kss = _cache_slots("k_cache", k_cache, q)
+    vss = _cache_slots("v_cache", v_cache, q)
+    slots, Hkv = k_cache.shape[:2]
+    if k_cache.shape[2] != D or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [num_slots, Hkv, D]")
+    max_pos = slot_table.shape[-1]
+    _int32_of("slot_table", slot_table, (B, max_pos), dev)
+    _int32_of("committed", committed, (B,), dev)
+    _int32_of("parents", parents, (B, N), dev)
+    _int32_of("num_nodes", num_nodes, (B,), dev)
+    _status_of(dev_status, dev)
+    out = _result("out", out, (B, N, Hq, D), q.dtype, dev, stream)
+    if lse is not None or want_lse:
+        lse = _result("lse", lse, (B, N, Hq), torch.float32, dev, stream)
+    stream = stream or torch.cuda.current_stream(dev)
+    if workspace is None:
+        nbytes = lib.spec_verify_attention_workspace_bytes(B, N, Hq, Hkv, D, max_pos)
+        workspace = workspace_for(nbytes, dev, stream)
+    rc = lib.spec_verify_attention(
+        q.data_ptr(), code, qs, k_cache.data_ptr(), v_cache.data_ptr(), slots, kss, vss,
+        slot_table.data_ptr(), max_pos, committed.data_ptr(), _addr(parents), _addr(num_nodes), B, N, Hq,
+        Hkv, D, D ** -0.5 if scale is None else scale, out.data_ptr(), _addr(lse), workspace.data_ptr(),
+        workspace.numel(), _addr(dev_status), stream.cuda_stream)
+    if rc != OK:
+        raise SpecVerifyError("spec_verify_attention", rc)
+    return Attention(out, lse)
+
+
+def spec_verify_logprobs_workspace_bytes(B: int, T: int, V: int, top_n: int) -> int:
+    return int(load_library().spec_verify_logprobs_workspace_bytes(B, T, V, top_n))
+
+
+def spec_verify_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, row_index=None, temperatures=None,
+                         temperature: float = 1.0, top_n: int = 0, logprobs=None, entropy=None, ranks=None,
+                         top_ids=None, top_logprobs=None, workspace=None, dev_status=None,
+                         stream=None) -> Logprobs:
+    """Log probability, rank, entropy and top_n alternatives of given tokens: logits [B, rows, V] (bf16
+    / fp32) as verified, tokens [B, T] int32 (verification's out_tokens; -1: nothing there), row_index
+    [B, T] int32 (a tree's accept_index; None: token t belongs to row t), temperatures [B] fp32.
+    Without dev_status, faults in the data show in the returned entries alone (NaN, -1)."""
+    lib = _lib or load_library()
+    _check_dev("logits", logits)
+    B, rows, V = logits.shape
+    dev = logits.device
+    T = tokens.shape[-1]
+    _int32_of("tokens", tokens, (B, T), dev)
+    _int32_of("row_index", row_index, (B, T), dev)
+    if temperatures is not None:
+        _check_dev("temperatures", temperatures, torch.float32)
+        if tuple(temperatures.shape) != (B,) or temperatures.device != dev:
+            raise ValueError(f"temperatures must be [B] on {dev}")
+    _status_of(dev_status, dev)
+    f32, i32 = torch.float32, torch.int32
+    logprobs = _result("logprobs", logprobs, (B, T), f32, dev, stream)
+    entropy = _result("entropy", entropy, (B, T), f32, dev, stream)
+    ranks = _result("ranks", ranks, (B, T), i32, dev, stream)
+    if top_n:
+        top_ids = _result("top_ids", top_ids, (B, T, top_n), i32, dev, stream)
+        top_logprobs = _result("top_logprobs", top_logprobs, (B, T, top_n), f32, dev, stream)
+    else:
+        top_ids = top_logprobs = None
+    stream = stream or torch.cuda.current_stream(dev)
+    if workspace is None:
+        nbytes = lib.spec_verify_logprobs_workspace_bytes(B, T, V, top_n)
+        workspace = workspace_for(nbytes, dev, stream)
+    rc = lib.spec_verify_logprobs(
+        logits.data_ptr(), _logits_dtype(logits), tokens.data_ptr(), _addr(row_index), B, rows, T, V,
+        _addr(temperatures), temperature, top_n, logprobs.data_ptr(), entropy.data_ptr(), ranks.data_ptr(),
+        _addr(top_ids), _addr(top_logprobs), workspace.data_ptr(), workspace.numel(), _addr(dev_status),
+        stream.cuda_stream)
+    if rc != OK:
+        raise SpecVerifyError("spec_verify_logprobs", rc)
+    return Logprobs(logprobs, entropy, ranks, top_ids, top_logprobs)

@@ -1462,8 +1462,8 @@ const char *spec_verify_strerror(int code)
     case SPEC_VERIFY_DEV_BAD_ROW: return "device: a logit row holds NaN or +inf, or no finite value";
     case SPEC_VERIFY_DEV_BAD_TREE: return "device: malformed tree (parents[0] != -1 or parents[j] outside [0, j))";
     case SPEC_VERIFY_DEV_DUP_SIBLING: return "device: two children of one node share a token";
-    case SPEC_VERIFY_DEV_BAD_KV_POSITION: return "device: KV compaction positions outside the slot table";
-    case SPEC_VERIFY_DEV_BAD_KV_SLOT: return "device: KV compaction slot outside the pool";
+    case SPEC_VERIFY_DEV_BAD_KV_POSITION: return "device: KV positions outside the slot table";
+    case SPEC_VERIFY_DEV_BAD_KV_SLOT: return "device: KV slot outside the pool";
     default: return "unknown status code";
     }
 }
@@ -1696,10 +1696,11 @@ int spec_verify_philox(uint64_t seed, uint64_t offset, int n_slot, int n_req, ui
 namespace sv {
 unsigned long long kv_debug_fault();
 unsigned long long budget_debug_fault();
+unsigned long long append_debug_fault();
 }  // namespace sv
 
 // The first out-of-range index the kernels met (debug builds), read and cleared across the
-// library's three modules; synchronous (symbol copies).
+// library's modules; synchronous (symbol copies).
 extern "C" int spec_verify_debug_fault(uint64_t *fault)
 {
     if (!fault) return SPEC_VERIFY_EINVAL;
@@ -1710,9 +1711,10 @@ extern "C" int spec_verify_debug_fault(uint64_t *fault)
         cudaMemcpyToSymbol(sv::g_sv_debug_fault, &z, sizeof z) != cudaSuccess)
         return SPEC_VERIFY_ECUDA;
 #endif
-    const unsigned long long kv = sv::kv_debug_fault(), bu = sv::budget_debug_fault();
-    if (kv == ~0ull || bu == ~0ull) return SPEC_VERIFY_ECUDA;
-    *fault = w ? w : (kv ? kv : bu);
+    const unsigned long long kv = sv::kv_debug_fault(), bu = sv::budget_debug_fault(),
+                             ap = sv::append_debug_fault();
+    if (kv == ~0ull || bu == ~0ull || ap == ~0ull) return SPEC_VERIFY_ECUDA;
+    *fault = w ? w : kv ? kv : bu ? bu : ap;
     return SPEC_VERIFY_OK;
 }
 

@@ -1,0 +1,227 @@
+// sv_append.cu -- the verify forward's new keys and values into the paged cache, with the position
+// rotation applied on the way, and the queries rotated beside them.
+//
+//   position of node n = committed + depth(n)      (chain: committed + n)
+//   slot of node n     = slot_table[committed + n]
+//   (x_i, x_j) -> (x_i cos - x_j sin, x_j cos + x_i sin), j = i + rot/2, or pairs (2i, 2i + 1)
+//
+// Bytes bound it: every row is read once and written once, and the 3 operations per element are
+// nothing beside that.  For few rows its time is the chain of dependent round trips (committed,
+// then slot and cosines, then the stores), so the rows' own loads are issued first and the index
+// chain runs under them.  A CTA takes one node: its unit of work is a pair of 16-byte vectors,
+// which under either pairing holds whole pairs (half-split: vectors rot/2 apart; adjacent: any
+// two), so a thread needs one unit's cosines and sines and no exchange with its neighbours.
+#include "sv_ops.cuh"
+
+namespace svapp {
+
+using sv::Half2;
+
+constexpr int NT = 128;  // threads per CTA
+
+struct Params {
+    const uint4 *q, *k, *v;            // rows of heads * D elements, row_*  vectors apart
+    uint4 *q_out, *k_cache, *v_cache;
+    int64_t q_row, k_row, v_row, q_out_row;  // in 16-byte vectors
+    int64_t k_slot, v_slot;                  // slot strides, in 16-byte vectors
+    int64_t num_slots;
+    const int32_t *slot_table, *committed, *parents, *num_nodes;
+    const float *cos_sin;
+    int rot_positions, rot;
+    int B, N, Hq, Hkv, D, max_pos;
+    int32_t *dev_status;
+};
+
+// Rotate the pairs of one unit: c, s hold the eight angles of the vectors' elements (half-split),
+// or four angles for each vector (adjacent pairs).
+template <bool BF, bool ADJ>
+__device__ __forceinline__ void rotate(uint4 &a, uint4 &b, const float (&c)[8], const float (&s)[8])
+{
+    uint32_t *wa = &a.x, *wb = &b.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = Half2<BF>::unpack(wa[i]), y = Half2<BF>::unpack(wb[i]);
+        if (ADJ) {
+            wa[i] = Half2<BF>::pack(x.x * c[i] - x.y * s[i], x.y * c[i] + x.x * s[i]);
+            wb[i] = Half2<BF>::pack(y.x * c[4 + i] - y.y * s[4 + i], y.y * c[4 + i] + y.x * s[4 + i]);
+        } else {
+            wa[i] = Half2<BF>::pack(x.x * c[2 * i] - y.x * s[2 * i], x.y * c[2 * i + 1] - y.y * s[2 * i + 1]);
+            wb[i] = Half2<BF>::pack(y.x * c[2 * i] + x.x * s[2 * i], y.y * c[2 * i + 1] + x.y * s[2 * i + 1]);
+        }
+    }
+}
+
+template <bool BF, bool ADJ>
+__global__ void __launch_bounds__(NT) append_kernel(const Params P)
+{
+    __shared__ int s_par[sv::MAX_TREE];
+    __shared__ int s_bad;
+    const int64_t row = blockIdx.x;
+    const int b = (int)(row / P.N), n = (int)(row - (int64_t)b * P.N), tid = threadIdx.x;
+    [[maybe_unused]] const int64_t rows = (int64_t)P.B * P.N;
+    const int hv = P.D / 8, hu = hv / 2;  // a head's vectors and units
+    const int units = (P.Hq + 2 * P.Hkv) * hu;
+    const int rv = P.rot / 8;  // rotated vectors of a head (even)
+
+    const int c = SV_INB(b, P.B, 1001) ? P.committed[b] : 0;
+    const int nn = P.num_nodes && SV_INB(b, P.B, 1002) ? P.num_nodes[b] : P.N;
+    int code = 0;
+    if (nn < 0 || nn > P.N || c < 0 || (int64_t)c + nn > P.max_pos) code = SPEC_VERIFY_DEV_BAD_KV_POSITION;
+    int depth = n;
+    if (P.parents) {
+        if (tid == 0) s_bad = 0;
+        __syncthreads();
+        if (tid < P.N && tid < nn && SV_INB((int64_t)b * P.N + tid, rows, 1003)) {
+            const int p = P.parents[(int64_t)b * P.N + tid];
+            s_par[tid] = p;
+            if (tid == 0 ? p != -1 : (p < 0 || p >= tid)) s_bad = 1;
+        }
+        __syncthreads();
+        if (s_bad) {
+            if (code < SPEC_VERIFY_DEV_BAD_TREE) code = SPEC_VERIFY_DEV_BAD_TREE;
+        } else if (!code && n < nn) {
+            depth = 0;
+            for (int j = n; j > 0; j = s_par[j]) ++depth;
+        }
+    }
+    const bool here = n < nn;
+    if (!code && here && (int64_t)c + depth >= P.rot_positions && P.rot) code = SPEC_VERIFY_DEV_BAD_KV_POSITION;
+    int64_t slot = 0;
+    if (!code && here) {
+        const int64_t i = (int64_t)b * P.max_pos + c + n;
+        slot = SV_INB(i, (int64_t)P.B * P.max_pos, 1004) ? P.slot_table[i] : -1;
+        if (slot < 0 || slot >= P.num_slots) code = SPEC_VERIFY_DEV_BAD_KV_SLOT;
+    }
+    if (code && tid == 0 && P.dev_status) atomicMax(P.dev_status, code);
+    if (code || !here) {  // nothing is appended; the row's queries are zeros (absent) or NaN (a fault)
+        const uint32_t w = code ? Half2<BF>::NAN2 : 0u;
+        for (int i = tid; i < P.Hq * hv; i += NT)
+            if (SV_INB(row * P.q_out_row + i, rows * P.q_out_row, 1005))
+                P.q_out[row * P.q_out_row + i] = make_uint4(w, w, w, w);
+        return;
+    }
+    const float *cs = P.cos_sin + ((int64_t)c + depth) * P.rot;
+    for (int u = tid; u < units; u += NT) {
+        const int head = u / hu, j = u - head * hu;
+        // The unit's two vectors: (j, j + rv/2) among the rotated ones when pairs are half a
+        // rotation apart, else neighbours.
+        int i0 = 2 * j, i1 = 2 * j + 1;
+        const bool turned = 2 * j < rv;
+        if (!ADJ && turned) {
+            i0 = j;
+            i1 = j + rv / 2;
+        }
+        const uint4 *src;
+        uint4 *dst;
+        bool spin = turned;
+        if (head < P.Hq) {
+            src = P.q + row * P.q_row + head * hv;
+            dst = P.q_out + row * P.q_out_row + head * hv;
+        } else if (head < P.Hq + P.Hkv) {
+            src = P.k + row * P.k_row + (head - P.Hq) * hv;
+            dst = P.k_cache + slot * P.k_slot + (head - P.Hq) * hv;
+        } else {
+            src = P.v + row * P.v_row + (head - P.Hq - P.Hkv) * hv;
+            dst = P.v_cache + slot * P.v_slot + (head - P.Hq - P.Hkv) * hv;
+            spin = false;
+        }
+        uint4 x = src[i0], y = src[i1];
+        if (spin) {
+            float cc[8], ss[8];
+            const float *pc = cs + 8 * j, *ps = pc + P.rot / 2;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                cc[e] = pc[e];
+                ss[e] = ps[e];
+            }
+            rotate<BF, ADJ>(x, y, cc, ss);
+        }
+        dst[i0] = x;
+        dst[i1] = y;
+    }
+}
+
+}  // namespace svapp
+
+namespace sv {
+// This module's first range violation (debug builds; 0 otherwise), cleared when read.
+unsigned long long append_debug_fault()
+{
+#ifdef SV_DEBUG
+    unsigned long long w = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&w, g_sv_debug_fault, sizeof w) != cudaSuccess ||
+        cudaMemcpyToSymbol(g_sv_debug_fault, &z, sizeof z) != cudaSuccess)
+        return ~0ull;
+    return w;
+#else
+    return 0;
+#endif
+}
+}  // namespace sv
+
+extern "C" int spec_verify_kv_append(const void *q, const void *k, const void *v, int dtype, int64_t q_stride,
+                                     int64_t k_stride, int64_t v_stride, void *q_out, void *k_cache, void *v_cache,
+                                     int64_t num_slots, int64_t k_slot_stride, int64_t v_slot_stride,
+                                     const int32_t *slot_table, int max_pos, const int32_t *committed,
+                                     const int32_t *parents, const int32_t *num_nodes, const float *cos_sin,
+                                     int rot_positions, int rotary_dim, int interleaved, int B, int N, int Hq, int Hkv,
+                                     int D, int32_t *dev_status, void *stream)
+{
+    if (!q || !k || !v || !q_out || !k_cache || !v_cache || !slot_table || !committed) return SPEC_VERIFY_EINVAL;
+    if (dtype != SPEC_VERIFY_BF16 && dtype != SPEC_VERIFY_FP16) return SPEC_VERIFY_EINVAL;
+    if (B < 1 || N < 1 || (int64_t)B * N > 0x7fffffff || (parents && N > sv::MAX_TREE) || max_pos < 1 || num_slots < 1 ||
+        num_slots > 0x7fffffff)
+        return SPEC_VERIFY_EINVAL;
+    if (Hq < 1 || Hkv < 1 || D < 16 || D % 16 || D > 1024 || (int64_t)(Hq + 2 * (int64_t)Hkv) * D > (1 << 24))
+        return SPEC_VERIFY_EINVAL;
+    if (rotary_dim < 0 || rotary_dim % 16 || rotary_dim > D || (rotary_dim && (!cos_sin || rot_positions < 1)))
+        return SPEC_VERIFY_EINVAL;
+    const int64_t qw = (int64_t)Hq * D, kw = (int64_t)Hkv * D;
+    if (q_stride % 8 || k_stride % 8 || v_stride % 8 || k_slot_stride % 8 || v_slot_stride % 8) return SPEC_VERIFY_EINVAL;
+    if (q_stride < qw || k_stride < kw || v_stride < kw || k_slot_stride < kw || v_slot_stride < kw)
+        return SPEC_VERIFY_EINVAL;
+    if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out | (uintptr_t)k_cache | (uintptr_t)v_cache |
+         (uintptr_t)cos_sin) % 16)
+        return SPEC_VERIFY_EINVAL;
+    if (((uintptr_t)slot_table | (uintptr_t)committed | (uintptr_t)parents | (uintptr_t)num_nodes |
+         (uintptr_t)dev_status) % 4)
+        return SPEC_VERIFY_EINVAL;
+    svapp::Params P;
+    P.q = static_cast<const uint4 *>(q);
+    P.k = static_cast<const uint4 *>(k);
+    P.v = static_cast<const uint4 *>(v);
+    P.q_out = static_cast<uint4 *>(q_out);
+    P.k_cache = static_cast<uint4 *>(k_cache);
+    P.v_cache = static_cast<uint4 *>(v_cache);
+    P.q_row = q_stride / 8;
+    P.k_row = k_stride / 8;
+    P.v_row = v_stride / 8;
+    P.q_out_row = qw / 8;
+    P.k_slot = k_slot_stride / 8;
+    P.v_slot = v_slot_stride / 8;
+    P.num_slots = num_slots;
+    P.slot_table = slot_table;
+    P.committed = committed;
+    P.parents = parents;
+    P.num_nodes = num_nodes;
+    P.cos_sin = cos_sin;
+    P.rot_positions = rot_positions;
+    P.rot = rotary_dim;
+    P.B = B;
+    P.N = N;
+    P.Hq = Hq;
+    P.Hkv = Hkv;
+    P.D = D;
+    P.max_pos = max_pos;
+    P.dev_status = dev_status;
+    const unsigned grid = (unsigned)((int64_t)B * N);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == SPEC_VERIFY_BF16) {
+        if (interleaved) svapp::append_kernel<true, true><<<grid, svapp::NT, 0, s>>>(P);
+        else svapp::append_kernel<true, false><<<grid, svapp::NT, 0, s>>>(P);
+    } else {
+        if (interleaved) svapp::append_kernel<false, true><<<grid, svapp::NT, 0, s>>>(P);
+        else svapp::append_kernel<false, false><<<grid, svapp::NT, 0, s>>>(P);
+    }
+    return cudaGetLastError() == cudaSuccess ? SPEC_VERIFY_OK : SPEC_VERIFY_ECUDA;
+}

@@ -1,0 +1,53 @@
+// sv_ops.cuh -- what the kernels around verification share (KV append, attention, log
+// probabilities): 16-bit element types, a node's depth and ancestors, device properties.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "spec_verify.h"
+#include "sv_check.cuh"
+
+namespace sv {
+
+constexpr int MAX_TREE = 64;  // nodes of a tree, as for tree verification
+
+// A 16-bit element type's pairs: to fp32 exactly, from fp32 rounded to nearest even.
+template <bool BF>
+struct Half2;
+
+template <>
+struct Half2<true> {
+    static __device__ __forceinline__ float2 unpack(uint32_t w)
+    {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    {
+        uint32_t d;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+        return d;
+    }
+    static constexpr uint32_t NAN2 = 0x7fff7fffu;
+    static constexpr uint32_t EXP_MASK = 0x7f80u;  // all ones in a NaN or an infinity
+};
+
+template <>
+struct Half2<false> {
+    static __device__ __forceinline__ float2 unpack(uint32_t w)
+    {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    {
+        uint32_t d;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+        return d;
+    }
+    static constexpr uint32_t NAN2 = 0x7fff7fffu;
+    static constexpr uint32_t EXP_MASK = 0x7c00u;
+};
+
+}  // namespace sv
