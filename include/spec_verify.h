@@ -83,6 +83,7 @@ extern "C" {
 #define SPEC_VERIFY_DEV_BAD_KV_POSITION 5 /* KV compaction: committed + N beyond the slot table,
                                              accept_len >= N, or a path entry outside [0, N) */
 #define SPEC_VERIFY_DEV_BAD_KV_SLOT 6     /* KV compaction: a slot outside [0, num_slots) */
+#define SPEC_VERIFY_DEV_TIMEOUT 7      /* a bounded wait inside a kernel ran out: outputs undefined */
 
 /* Modes for spec_verify_workspace_bytes. */
 #define SPEC_VERIFY_MODE_GREEDY 0

@@ -14,21 +14,23 @@ SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "sv_kv.cu", "sv_bud
                                               "sv_attention.cu", "sv_logprobs.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("sv_device.cuh", "sv_draw.cuh", "sv_stream.cuh", "sv_rescan.cuh",
                                                   "sv_decide.cuh", "sv_topkp.cuh", "sv_topkp_ring.cuh",
-                                                  "sv_check.cuh", "sv_ops.cuh")] + [
+                                                  "sv_check.cuh", "sv_ops.cuh", "sv_tc.cuh")] + [
     os.path.join(INCLUDE, "spec_verify.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
 ]
 
 
-def nvcc_command(out: str = LIB_PATH, debug: bool = False) -> list[str]:
+def _nvcc() -> str:
     nvcc = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
-    if not os.path.exists(nvcc):
-        nvcc = "nvcc"
-    return [nvcc, *NVCC_FLAGS, *(["-DSV_DEBUG"] if debug else []), "-I", INCLUDE, *SOURCES, "-o", out]
+    return nvcc if os.path.exists(nvcc) else "nvcc"
+
+
+def compile_command(source: str, out: str, debug: bool = False) -> list[str]:
+    return [_nvcc(), *NVCC_FLAGS, *(["-DSV_DEBUG"] if debug else []), "-I", INCLUDE, "-c", source, "-o", out]
 
 
 def up_to_date(path: str = LIB_PATH) -> bool:
@@ -38,25 +40,39 @@ def up_to_date(path: str = LIB_PATH) -> bool:
     return all(os.path.getmtime(d) <= t for d in DEPS)
 
 
+class _Build:
+    """A compilation under way: one nvcc per source, linked when all have ended."""
+
+    def __init__(self, path: str, debug: bool):
+        self.path = path
+        self.objects = [f"{path}.{os.path.basename(s)}.{os.getpid()}.o" for s in SOURCES]
+        self.procs = [subprocess.Popen(compile_command(s, o, debug)) for s, o in zip(SOURCES, self.objects)]
+
+    def finish(self) -> str:
+        try:
+            if any([p.wait() for p in self.procs]):
+                raise RuntimeError(f"nvcc failed building {os.path.basename(self.path)}")
+            tmp = f"{self.path}.tmp{os.getpid()}"
+            subprocess.run([_nvcc(), "-shared", *self.objects, "-o", tmp], check=True)
+            os.replace(tmp, self.path)
+        finally:
+            for o in self.objects:
+                if os.path.exists(o):
+                    os.remove(o)
+        return self.path
+
+
 def start_build(force: bool = False, debug: bool = False):
-    """Start nvcc in the background; returns the Popen (or None when already built).  debug: the
+    """Start nvcc in the background; returns the build (or None when already built).  debug: the
     range-checked library (libspecverify_debug.so) instead of the release one."""
     path = DEBUG_LIB_PATH if debug else LIB_PATH
     if not force and up_to_date(path):
         return None
-    tmp = path + f".tmp{os.getpid()}"
-    proc = subprocess.Popen(nvcc_command(tmp, debug))
-    proc._sv_tmp, proc._sv_path = tmp, path  # type: ignore[attr-defined]
-    return proc
+    return _Build(path, debug)
 
 
-def finish_build(proc) -> str:
-    if proc is None:
-        return LIB_PATH
-    if proc.wait() != 0:
-        raise RuntimeError(f"nvcc failed building {os.path.basename(proc._sv_path)}")  # type: ignore[attr-defined]
-    os.replace(proc._sv_tmp, proc._sv_path)  # type: ignore[attr-defined]
-    return proc._sv_path  # type: ignore[attr-defined]
+def finish_build(build) -> str:
+    return LIB_PATH if build is None else build.finish()
 
 
 def build(force: bool = False) -> str:

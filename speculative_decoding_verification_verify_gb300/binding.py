@@ -22,7 +22,7 @@ MODE_GREEDY, MODE_REJECTION, MODE_TREE, MODE_BLOCK = 0, 1, 2, 3
 OK, EINVAL, EWORKSPACE, ECUDA, ETOOBIG = 0, -1, -2, -3, -4
 NOALLOC_SCRATCH_BYTES = 4 << 20
 DEV_OK, DEV_BAD_TOKEN, DEV_BAD_ROW, DEV_BAD_TREE, DEV_DUP_SIBLING = 0, 1, 2, 3, 4
-DEV_BAD_KV_POSITION, DEV_BAD_KV_SLOT = 5, 6
+DEV_BAD_KV_POSITION, DEV_BAD_KV_SLOT, DEV_TIMEOUT = 5, 6, 7
 
 _lib = None
 _lock = threading.Lock()

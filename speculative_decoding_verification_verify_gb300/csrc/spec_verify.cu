@@ -1464,6 +1464,7 @@ const char *spec_verify_strerror(int code)
     case SPEC_VERIFY_DEV_DUP_SIBLING: return "device: two children of one node share a token";
     case SPEC_VERIFY_DEV_BAD_KV_POSITION: return "device: KV positions outside the slot table";
     case SPEC_VERIFY_DEV_BAD_KV_SLOT: return "device: KV slot outside the pool";
+    case SPEC_VERIFY_DEV_TIMEOUT: return "device: a bounded wait ran out, outputs undefined";
     default: return "unknown status code";
     }
 }
@@ -1697,6 +1698,7 @@ namespace sv {
 unsigned long long kv_debug_fault();
 unsigned long long budget_debug_fault();
 unsigned long long append_debug_fault();
+unsigned long long attention_debug_fault();
 }  // namespace sv
 
 // The first out-of-range index the kernels met (debug builds), read and cleared across the
@@ -1712,9 +1714,9 @@ extern "C" int spec_verify_debug_fault(uint64_t *fault)
         return SPEC_VERIFY_ECUDA;
 #endif
     const unsigned long long kv = sv::kv_debug_fault(), bu = sv::budget_debug_fault(),
-                             ap = sv::append_debug_fault();
-    if (kv == ~0ull || bu == ~0ull || ap == ~0ull) return SPEC_VERIFY_ECUDA;
-    *fault = w ? w : kv ? kv : bu ? bu : ap;
+                             ap = sv::append_debug_fault(), at = sv::attention_debug_fault();
+    if (kv == ~0ull || bu == ~0ull || ap == ~0ull || at == ~0ull) return SPEC_VERIFY_ECUDA;
+    *fault = w ? w : kv ? kv : bu ? bu : ap ? ap : at;
     return SPEC_VERIFY_OK;
 }
 
