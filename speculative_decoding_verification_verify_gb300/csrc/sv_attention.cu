@@ -15,36 +15,39 @@
 // One CTA per SM takes an equal run of the batch's tiles (a tile: 128 positions of one request and
 // key head), whatever the lengths, so one long request is split over all SMs and many short ones
 // share them; where a run cuts a request, the parts are joined by the CTA that finishes last.
-// Warp 0 gathers tiles by their slots with TMA (four rows per copy), warp 1 issues the products,
-// warps 2-3 stage the queries and the tree's mask, warps 4-7 hold a position per thread: a tile's
-// scores come to them as columns, so the exponentials are spread evenly however few the query rows.
 //
-// The softmax's reference moves only when a score passes it by more than 2^8 (a vote of the 128
-// threads per tile): the weights are then at most 2^8, exact in fp32 as in 16 bits up to their
-// rounding, and the accumulators are left alone in nearly every tile.
-#include <cuda.h>
-
-#include <mutex>
-
+// Warps 0-3 copy tiles into a ring of K and V units, a row of 16-byte chunks per slot (gathers by
+// TMA were tried first: four 128-byte rows took 61 clocks to issue, 8 bytes per clock, where an SM's
+// share of HBM is 23).  Warp 4 issues the products, warp 5 lists the run's segments (a segment: the
+// run's tiles of one request and key head) a few ahead of everybody, warps 6-7 stage the queries and
+// the tree's mask.  Warps 8-15 do the softmax, a position and half of the columns per thread: scores
+// come to them as columns, so the exponentials are spread evenly however few the query rows.
+//
+// The softmax's reference moves only when a score passes it by more than 2^8 (a vote of 128 threads
+// per tile): weights are then at most 2^8, as exact in 16 bits as below 1, and the accumulators are
+// left alone in nearly every tile.
 #include "sv_ops.cuh"
 #include "sv_tc.cuh"
+
+#include <mutex>
 
 namespace svatt {
 
 using sv::Half2;
 
-constexpr int NT = 256;
+constexpr int NT = 512;
 constexpr int TILE = 128;     // positions per tile
 constexpr int MAXD = 128;
 constexpr int MAX_CTAS = 256; // parts the workspace has room for: two per CTA
-constexpr int FLAGS = 16;     // segments whose bad-slot flags are in use at once (more than stages + 2)
+constexpr int FLAGS = 16;     // bad-slot flags: more than the segments the ring can hold
+constexpr int SEGS = 8;       // segments listed ahead
 constexpr float SLACK = 8.f;  // log2 of the largest weight
 
 struct Params {
-    const uint16_t *q, *v;
+    const uint16_t *q, *k, *v;
     uint16_t *out;
     float *lse;
-    int64_t q_row, v_slot, num_slots;
+    int64_t q_row, k_slot, v_slot, num_slots;
     const int32_t *slot_table, *committed, *parents, *num_nodes;
     int max_pos, B, N, Hq, Hkv, D, G, QT;  // G query heads per key head, QT column blocks
     float scale_log2;
@@ -53,65 +56,45 @@ struct Params {
     float *parts;
 };
 
-// Shared memory after the tiles, whose bases are multiples of 1024 bytes.
+// Shared memory: a ring of units (a K or V tile each; tile k's K is unit 2 k, its V unit 2 k + 1),
+// two query buffers, the weights, then Misc.  All bases are multiples of 1024 bytes.
 template <int NQ, int DP>
 struct Layout {
     static constexpr int HALVES = DP / 64;
-    static constexpr int UNIT = TILE * DP * 2;                  // bytes of a K or V tile
-    static constexpr int NS = (NQ <= 32 ? 3 : 2) * 128 / DP;    // stages
+    static constexpr int UNIT = TILE * DP * 2;
+    static constexpr int NU = 5 * 128 / DP;
+    // Units in flight before the oldest is waited for.  Unit u's slot is freed by products that need
+    // the units up to u - NU + 1, so these must have been handed over by then: at most NU - 2.
+    static constexpr int LAG = NU - 2 < 6 ? NU - 2 : 6;
     static constexpr int QBYTES = NQ * DP * 2;
     static constexpr int QSTEP = QBYTES < 1024 ? 1024 : QBYTES;
-    static constexpr int PBYTES = TILE * 128;                   // P: a row of 64 columns per position
-    static constexpr int K0 = 0, V0 = NS * UNIT, Q0 = 2 * NS * UNIT, P0 = Q0 + 2 * QSTEP;
-    static constexpr int M0 = P0 + PBYTES;                      // Misc
+    static constexpr int PBYTES = TILE * 128;  // a row of 64 columns per position
+    static constexpr int Q0 = NU * UNIT, P0 = Q0 + 2 * QSTEP, M0 = P0 + PBYTES;
     static constexpr int COLS = 3 * NQ <= 64 ? 64 : 3 * NQ <= 128 ? 128 : 256;  // TMEM columns
 };
 
-template <int NQ, int NS>
-struct Misc {
-    uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS];
-    uint64_t sfull[2], sempty[2], qfull[2], qempty[2], pfull, pvdone, drain;
-    unsigned long long desc[2][sv::MAX_TREE];  // nodes that see node a, of the staged queries' request
-    float nref[NQ], fac[NQ], red[4][NQ], sum[2][NQ];
-    int code[2];
-    int bad[FLAGS];
-    int8_t par[sv::MAX_TREE];
-    int begin_b, abort, issued[2];  // tiles of K and V asked for
-    int64_t begin_base, scan[NT / 32];
-    uint32_t tmem;
-    struct {
-        int on, b, h, qt, c0, c1, first0;
-    } join[2];
+// A run's tiles [j0, j1) of one request, key head and column block.
+struct __align__(16) Seg {
+    int b, h, qt, kind;        // kind 0: to attend; 1: no nodes; 2: lengths are wrong; 3: no more segments
+    int c, nn, j0, j1;
+    int part, c0, c1, first0;  // part: the workspace part it writes (-1: it is the whole); the CTAs it spans
 };
 
-// A CTA's walk over its tiles.  Every role keeps one of its own.
-struct Walk {
-    int b, item, j, ntile, c, nn;
-    int dummy;  // nothing to attend with: the request has no nodes here, or its lengths are wrong
-
-    __device__ __forceinline__ void load(const Params &P)
-    {
-        c = SV_INB(b, P.B, 1101) ? P.committed[b] : 0;
-        nn = P.num_nodes ? (SV_INB(b, P.B, 1102) ? P.num_nodes[b] : 0) : P.N;
-        const bool fault = nn < 0 || nn > P.N || c < 0 || (int64_t)c + nn > P.max_pos;
-        dummy = fault ? 2 : nn == 0 ? 1 : 0;
-        ntile = dummy ? 1 : (c + nn + TILE - 1) / TILE;
-    }
-    __device__ __forceinline__ void start(const Params &P, int b0, int64_t skip)
-    {
-        b = b0;
-        load(P);
-        item = (int)(skip / ntile);
-        j = (int)(skip - (int64_t)item * ntile);
-    }
-    __device__ __forceinline__ void next(const Params &P)
-    {
-        if (++j < ntile) return;
-        j = 0;
-        if (++item < P.Hkv * P.QT) return;
-        item = 0;
-        if (++b < P.B) load(P);
-    }
+template <int NQ, int NU>
+struct Misc {
+    uint64_t full[NU], empty[NU];
+    uint64_t sfull[2], sempty[2], qfull[2], qempty[2], segfull[SEGS], segempty[SEGS], pfull, pvdone, drain;
+    Seg seg[SEGS];
+    unsigned long long desc[2][sv::MAX_TREE];  // nodes that see node a, of the staged queries' request
+    float nref[NQ], fac[NQ], ref[NQ], red[4][NQ], red2[4][NQ];
+    int code[2], poison[2];
+    int bad[2][FLAGS];
+    int begin_b, abort;
+    int64_t begin_base, scan[NT / 32];
+    uint32_t tmem;
+    Seg join[2];
+    int joins[2];
+    int8_t par[sv::MAX_TREE];
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -144,29 +127,26 @@ __device__ __forceinline__ bool group_or(int id, int n, bool x)
     return y;
 }
 
-// Sums over the warp's lanes of NQ values per lane: halving exchanges leave column sums in the
-// lanes (31 shuffles for 32 columns instead of 5 for each).  sum[c] of columns c of v.
-template <int NQ>
-__device__ __forceinline__ void column_sums(float (&v)[NQ], float *sum, int lane)
+// Sums over the warp's lanes of W values per lane, by exchanges that halve the columns a lane still
+// holds (31 shuffles for 32 columns instead of 5 for each); lane c < W returns column c's.
+template <int W>
+__device__ __forceinline__ float column_sum(const float (&v)[W], int lane)
 {
-    constexpr int W = NQ < 32 ? NQ : 32;
+    float x[W];
 #pragma unroll
-    for (int base = 0; base < NQ; base += W) {
-        float x[W];
+    for (int i = 0; i < W; ++i) x[i] = v[i];
 #pragma unroll
-        for (int i = 0; i < W; ++i) x[i] = v[base + i];
+    for (int half = W / 2; half; half >>= 1) {
+        const bool up = lane & half;
 #pragma unroll
-        for (int half = W / 2; half; half >>= 1) {
-            const bool up = lane & half;
-#pragma unroll
-            for (int i = 0; i < half; ++i) {
-                const float keep = up ? x[i + half] : x[i], give = up ? x[i] : x[i + half];
-                x[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
-            }
+        for (int i = 0; i < half; ++i) {
+            const float keep = up ? x[i + half] : x[i], give = up ? x[i] : x[i + half];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
         }
-        if (W < 32) x[0] += __shfl_xor_sync(0xffffffffu, x[0], 16);
-        if (lane < W) sum[base + lane] = x[0];
     }
+#pragma unroll
+    for (int o = W; o < 32; o <<= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+    return x[0];
 }
 
 // Floats of one part: per column the weighted values, then references, sums, sums of the rounded
@@ -181,13 +161,30 @@ __host__ __device__ constexpr int part_floats()
 __device__ __forceinline__ int cta_of(int64_t x, int64_t total, int G) { return (int)(((x + 1) * G - 1) / total); }
 __device__ __forceinline__ int64_t run_begin(int c, int64_t total, int G) { return total * c / G; }
 
+__device__ __forceinline__ int kind_of(const Params &P, int c, int nn)
+{
+    return nn < 0 || nn > P.N || c < 0 || (int64_t)c + nn > P.max_pos ? 2 : nn == 0 ? 1 : 0;
+}
+__device__ __forceinline__ int tiles_of(int kind, int c, int nn) { return kind ? 1 : (c + nn + TILE - 1) / TILE; }
+
+__device__ __forceinline__ void lengths(const Params &P, int b, int &c, int &nn)
+{
+    c = SV_INB(b, P.B, 1101) ? P.committed[b] : 0;
+    nn = P.num_nodes ? (SV_INB(b, P.B, 1102) ? P.num_nodes[b] : 0) : P.N;
+}
+
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <bool BF, int NQ, int DP>
-__global__ void __launch_bounds__(NT, 1) attention_kernel(const __grid_constant__ CUtensorMap kmap,
-                                                          const __grid_constant__ CUtensorMap vmap, const Params P)
+__global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
 {
     using L = Layout<NQ, DP>;
-    using M = Misc<NQ, L::NS>;
-    constexpr int NS = L::NS, HALVES = L::HALVES;
+    using M = Misc<NQ, L::NU>;
+    constexpr int NU = L::NU, HALVES = L::HALVES;
     extern __shared__ __align__(1024) unsigned char smem[];
     M &ms = *reinterpret_cast<M *>(smem + L::M0);
     const uint32_t s0 = tc::smem_u32(smem);
@@ -196,29 +193,29 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const __grid_constant_
     volatile int *abort = &ms.abort;
 
     if (tid == 0) {
-        for (int s = 0; s < NS; ++s) {
-            tc::bar_init(tc::smem_u32(&ms.kfull[s]), 1);
-            tc::bar_init(tc::smem_u32(&ms.kempty[s]), 1);
-            tc::bar_init(tc::smem_u32(&ms.vfull[s]), 1);
-            tc::bar_init(tc::smem_u32(&ms.vempty[s]), 1);
+        for (int s = 0; s < NU; ++s) {
+            tc::bar_init(tc::smem_u32(&ms.full[s]), 4);
+            tc::bar_init(tc::smem_u32(&ms.empty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(tc::smem_u32(&ms.sfull[i]), 1);
-            tc::bar_init(tc::smem_u32(&ms.sempty[i]), 128);
+            tc::bar_init(tc::smem_u32(&ms.sempty[i]), 256);
             tc::bar_init(tc::smem_u32(&ms.qfull[i]), 64);
-            tc::bar_init(tc::smem_u32(&ms.qempty[i]), 2);
-            ms.join[i].on = 0;
+            tc::bar_init(tc::smem_u32(&ms.qempty[i]), 3);
+            ms.joins[i] = 0;
         }
-        tc::bar_init(tc::smem_u32(&ms.pfull), 128);
+        for (int i = 0; i < SEGS; ++i) {
+            tc::bar_init(tc::smem_u32(&ms.segfull[i]), 1);
+            tc::bar_init(tc::smem_u32(&ms.segempty[i]), 15);  // warps but the one that lists
+        }
+        tc::bar_init(tc::smem_u32(&ms.pfull), 256);
         tc::bar_init(tc::smem_u32(&ms.pvdone), 1);
         tc::bar_init(tc::smem_u32(&ms.drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        ms.abort = ms.issued[0] = ms.issued[1] = 0;
-        tc::tma_prefetch_map(&kmap);
-        tc::tma_prefetch_map(&vmap);
+        ms.abort = 0;
     }
-    if (tid < FLAGS) ms.bad[tid] = 0;
-    if (warp == 1) tc::tmem_alloc(tc::smem_u32(&ms.tmem), L::COLS);
+    if (tid < 2 * FLAGS) (&ms.bad[0][0])[tid] = 0;
+    if (warp == 4) tc::tmem_alloc(tc::smem_u32(&ms.tmem), L::COLS);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -226,12 +223,10 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const __grid_constant_
     const int HT = P.Hkv * P.QT;
     const int per = (P.B + NT - 1) / NT;
     int64_t mine = 0;
-    for (int i = 0; i < per; ++i) {
-        Walk w;
-        w.b = tid * per + i;
-        if (w.b >= P.B) break;
-        w.load(P);
-        mine += (int64_t)w.ntile * HT;
+    for (int i = 0; i < per && tid * per + i < P.B; ++i) {
+        int c, nn;
+        lengths(P, tid * per + i, c, nn);
+        mine += (int64_t)tiles_of(kind_of(P, c, nn), c, nn) * HT;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -250,567 +245,689 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const __grid_constant_
     const int G = total < (int64_t)gridDim.x ? (int)total : (int)gridDim.x;
     const int64_t t0 = cta < G ? run_begin(cta, total, G) : total, t1 = cta < G ? run_begin(cta + 1, total, G) : total;
     if (t0 >= before && t0 < before + mine) {
-        Walk w;
         int64_t at = before;
-        for (w.b = tid * per; w.b < P.B; ++w.b) {
-            w.load(P);
-            if (t0 < at + (int64_t)w.ntile * HT) break;
-            at += (int64_t)w.ntile * HT;
+        int b = tid * per;
+        for (; b < P.B; ++b) {
+            int c, nn;
+            lengths(P, b, c, nn);
+            const int64_t n = (int64_t)tiles_of(kind_of(P, c, nn), c, nn) * HT;
+            if (t0 < at + n) break;
+            at += n;
         }
-        ms.begin_b = w.b;
+        ms.begin_b = b;
         ms.begin_base = at;
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = ms.tmem;
-    const int64_t count = t1 - t0;
 
-    if (count > 0) {
-        Walk w;
-        w.start(P, ms.begin_b, t0 - ms.begin_base);
-        if (warp == 0) {
+    // The next segment, for every warp but the one that lists them; kind 3 also when a wait failed.
+    int si = 0;
+    auto take = [&](Seg &g) {
+        const bool ok = tc::bar_wait(tc::smem_u32(&ms.segfull[si % SEGS]), (si / SEGS) & 1, abort);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        g = ms.seg[si % SEGS];
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(tc::smem_u32(&ms.segempty[si % SEGS]));
+        ++si;
+        return true;
+    };
+
+    if (t1 > t0) {
+        if (warp < 4) {
             // ---- tiles into shared memory -------------------------------------------------
-            // A lane owns positions 4 lane .. 4 lane + 3 of every tile; their slots are read one
-            // tile ahead, so the table's latency lies under the wait for a free stage.
-            int slot[4], seg = -1;
+            // A row's CPR chunks go to CPR lanes, 32 / CPR rows to a warp's copy.  A lane keeps the
+            // slot of one of its warp's 32 rows; they are read one tile ahead of the copies.
+            constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI), LAG = L::LAG;
+            const int chunk = lane % CPR, sub = lane / CPR;
+            const int own = warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot it keeps
+            const int first = warp * RPI + sub;                                // its row of the first copy
+            const uint32_t to = (chunk >> 3) * TILE * 128 + first * 128 + (((chunk & 7) ^ (first & 7)) << 4);
+            const bool wide = chunk * 8 < P.D;
+            Seg g = {};
+            int seg = -1, j = 0, slot = -1, u = 0, handed = 0;
             bool ok = true;
-            auto slots_of = [&](const Walk &x) {
-                const int len = x.c + x.nn;
-                bool bad = false;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pos = x.j * TILE + 4 * lane + i;
-                    slot[i] = 0;
-                    if (!x.dummy && pos < len) {
-                        const int64_t at = (int64_t)x.b * P.max_pos + pos;
-                        const int s = SV_INB(at, (int64_t)P.B * P.max_pos, 1103) ? P.slot_table[at] : -1;
-                        bad |= s < 0 || s >= P.num_slots;
-                        slot[i] = s < 0 || s >= P.num_slots ? 0 : s;
+            auto hand_over = [&](int to_unit) {  // the units before this one have landed
+                tc::fence_async_smem();
+                __syncwarp();
+                for (; handed < to_unit; ++handed)
+                    if (lane == 0) tc::bar_arrive(tc::smem_u32(&ms.full[handed % NU]));
+            };
+            // To the next tile, and its slot: 1, or 0 when there is none.  A segment that is not listed
+            // yet may wait for units that are still here: before waiting for it (`block`) they are handed
+            // over, and without `block` the answer is 2.
+            auto seek = [&](bool block) {
+                if (seg >= 0 && !g.kind && j + 1 < g.j1) {
+                    ++j;
+                } else {
+                    do {
+                        if (!__all_sync(0xffffffffu, tc::bar_test(tc::smem_u32(&ms.segfull[si % SEGS]), (si / SEGS) & 1))) {
+                            if (!block) return 2;
+                            cp_wait<0>();
+                            hand_over(u);
+                        }
+                        if (!take(g) || g.kind == 3) return 0;
+                    } while (g.kind);
+                    ++seg;
+                    j = g.j0;
+                }
+                const int pos = j * TILE + own;
+                slot = -1;
+                if (pos < g.c + g.nn) {
+                    const int64_t at = (int64_t)g.b * P.max_pos + pos;
+                    slot = SV_INB(at, (int64_t)P.B * P.max_pos, 1103) ? P.slot_table[at] : -1;
+                    if (slot < 0 || slot >= P.num_slots) {
+                        *(volatile int *)&ms.bad[0][seg % FLAGS] = 1;
+                        *(volatile int *)&ms.bad[1][seg % FLAGS] = 1;
+                        slot = -1;
                     }
                 }
-                return bad;
+                return 1;
             };
-            bool bad = slots_of(w);
-            int k = 0, kissued = 0;
-            for (int64_t i = 0; i < count; ++i) {
-                if (!w.dummy) {
-                    if (seg < 0 || w.j == 0) ++seg;
-                    const int s = k % NS, ph = (k / NS) & 1;
-                    const int len = w.c + w.nn - w.j * TILE;
-                    const int groups = len >= TILE ? TILE / 4 : (len + 3) / 4;
-                    const uint32_t bytes = (uint32_t)groups * 4 * DP * 2;
-                    const int x = (w.item / P.QT) * P.D;
-                    const bool any = __any_sync(0xffffffffu, bad);
-                    if (any && lane == 0) *(volatile int *)&ms.bad[seg % FLAGS] = 1;
-                    if (lane == 0 && k >= NS) ok = tc::bar_wait(tc::smem_u32(&ms.kempty[s]), ph ^ 1, abort);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) break;
-                    const uint32_t kb = tc::smem_u32(&ms.kfull[s]), vb = tc::smem_u32(&ms.vfull[s]);
-                    ++kissued;
-                    if (lane == 0) tc::bar_expect(kb, bytes);
-                    __syncwarp();
-                    if (lane < groups)
+            auto copy = [&](const uint16_t *base, int64_t stride, int slots) {
+                if (u >= NU) {
+                    const bool free = tc::bar_wait(tc::smem_u32(&ms.empty[u % NU]), (u / NU + 1) & 1, abort);
+                    if (!__all_sync(0xffffffffu, free)) return false;
+                }
+                const uint32_t dst = s0 + (u % NU) * L::UNIT + to;
 #pragma unroll
-                        for (int hf = 0; hf < HALVES; ++hf)
-                            tc::tma_gather4(s0 + L::K0 + s * L::UNIT + hf * TILE * 128 + lane * 512, &kmap, kb,
-                                            x + hf * 64, slot);
-                    if (lane == 0 && k >= NS) ok = tc::bar_wait(tc::smem_u32(&ms.vempty[s]), ph ^ 1, abort);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) break;
-                    if (lane == 0) tc::bar_expect(vb, bytes);
-                    __syncwarp();
-                    if (lane < groups)
+                for (int i = 0; i < ITER; ++i) {
+                    const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
+                    const uint16_t *src = s < 0 ? base : base + s * stride;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 4 * RPI * 128), "l"(src),
+                                 "r"(s >= 0 && wide ? 16 : 0)
+                                 : "memory");
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                ++u;
+                if (u - handed > LAG) {
+                    cp_wait<LAG>();
+                    hand_over(u - LAG);
+                }
+                return true;
+            };
+            for (int found = seek(true); found == 1 && ok;) {
+                const int slots = slot;
+                const int64_t at = (int64_t)g.h * P.D + (wide ? chunk * 8 : 0);
+                found = seek(false);
+                ok = copy(P.k + at, P.k_slot, slots) && copy(P.v + at, P.v_slot, slots);
+                if (found == 2 && ok) found = seek(true);
+            }
+            // The last units, each as it lands.
+            if (ok) {
+                if (LAG >= 6) cp_wait<5>(), hand_over(u - 5);
+                if (LAG >= 5) cp_wait<4>(), hand_over(u - 4);
+                if (LAG >= 4) cp_wait<3>(), hand_over(u - 3);
+                if (LAG >= 3) cp_wait<2>(), hand_over(u - 2);
+                if (LAG >= 2) cp_wait<1>(), hand_over(u - 1);
+            }
+            cp_wait<0>();
+            if (ok) hand_over(u);
+        } else if (warp == 4) {
+            // ---- products ------------------------------------------------------------------
+            constexpr uint32_t ID_S = tc::instr_desc(BF, false, false, 128, NQ);
+            constexpr uint32_t ID_O = tc::instr_desc(BF, true, true, 128, NQ);
+            const int dsteps = P.D / 16;
+            const uint64_t kd = tc::smem_desc(s0, 0, 1024), qd = tc::smem_desc(s0 + L::Q0, 0, 1024);
+            const uint64_t vd = tc::smem_desc(s0, HALVES > 1 ? TILE * 128 : 0, 1024), pd = tc::smem_desc(s0 + L::P0, 0, 1024);
+            int k = 0, seg = -1;       // tiles whose scores are under way
+            int wk = 0, wsteps = 0, wstart = 0;  // tiles weighed; the waiting one's
+            bool ok = true;
+            Seg g = {};
+            auto ready_p = [&] {
+                const int u = 2 * wk + 1;
+                return tc::bar_test(tc::smem_u32(&ms.pfull), wk & 1) && tc::bar_test(tc::smem_u32(&ms.full[u % NU]), (u / NU) & 1);
+            };
+            auto weigh = [&] {  // O^T (+)= V^T P^T of tile wk
+                const int u = 2 * wk + 1;
+                tc::fence_after();
+                const uint64_t a = vd + (uint64_t)((u % NU) * (L::UNIT >> 4));
 #pragma unroll
-                        for (int hf = 0; hf < HALVES; ++hf)
-                            tc::tma_gather4(s0 + L::V0 + s * L::UNIT + hf * TILE * 128 + lane * 512, &vmap, vb,
-                                            x + hf * 64, slot);
+                for (int i = 0; i < 8; ++i)
+                    if (i < wsteps) tc::mma_f16(tmem + 2 * NQ, a + i * 128, pd + i * 128, ID_O, !wstart || i > 0);
+                tc::commit(tc::smem_u32(&ms.empty[u % NU]));
+                tc::commit(tc::smem_u32(&ms.pvdone));
+                ++wk;
+            };
+            // One thread does it all, and waits for nothing without weighing what is ready meanwhile.
+            int64_t begin = 0;
+            auto late = [&] {
+                if (!*abort && clock64() - begin <= tc::WAIT_CLOCKS) return false;
+                *abort = 1;
+                return true;
+            };
+            while (lane == 0) {
+                begin = clock64();
+                while (ok && !tc::bar_test(tc::smem_u32(&ms.segfull[si % SEGS]), (si / SEGS) & 1)) {
+                    if (wk < k && ready_p()) weigh();
+                    ok = !late();
+                }
+                if (!ok) break;
+                g = ms.seg[si % SEGS];
+                tc::bar_arrive(tc::smem_u32(&ms.segempty[si % SEGS]));
+                ++si;
+                if (g.kind == 3) break;
+                if (g.kind) continue;
+                ++seg;
+                for (int j = g.j0; j < g.j1 && ok; ++j) {
+                    // Scores of this tile and weighing of the one before, whichever is ready first.
+                    const int u = 2 * k, sb = k & 1;
+                    bool scored = false;
+                    begin = clock64();
+                    while (!scored || wk < k) {
+                        if (!scored && tc::bar_test(tc::smem_u32(&ms.full[u % NU]), (u / NU) & 1) &&
+                            tc::bar_test(tc::smem_u32(&ms.qfull[seg & 1]), (seg >> 1) & 1) &&
+                            (k < 2 || tc::bar_test(tc::smem_u32(&ms.sempty[sb]), ((k >> 1) & 1) ^ 1))) {
+                            tc::fence_after();
+                            const uint64_t a = kd + (uint64_t)((u % NU) * (L::UNIT >> 4));
+                            const uint64_t b = qd + (uint64_t)((seg & 1) * (L::QSTEP >> 4));
+#pragma unroll
+                            for (int d = 0; d < DP / 16; ++d)
+                                if (d < dsteps)
+                                    tc::mma_f16(tmem + sb * NQ, a + (d >> 2) * (TILE * 8) + (d & 3) * 2,
+                                                b + (d >> 2) * (NQ * 8) + (d & 3) * 2, ID_S, d > 0);
+                            tc::commit(tc::smem_u32(&ms.empty[u % NU]));
+                            tc::commit(tc::smem_u32(&ms.sfull[sb]));
+                            if (j + 1 == g.j1) tc::commit(tc::smem_u32(&ms.qempty[seg & 1]));
+                            scored = true;
+                        }
+                        if (wk < k && ready_p()) weigh();
+                        if (late()) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    const int left = g.c + g.nn - j * TILE;
+                    wsteps = left >= TILE ? TILE / 16 : (left + 15) / 16;
+                    wstart = j == g.j0;
                     ++k;
                 }
-                if (i + 1 < count) {
-                    w.next(P);
-                    bad = slots_of(w);
-                }
+                if (!ok) break;
             }
-            if (lane == 0) ms.issued[0] = kissued, ms.issued[1] = k;
-        } else if (warp == 1) {
-            // ---- products ------------------------------------------------------------------
-            if (lane == 0) {
-                constexpr uint32_t ID_S = tc::instr_desc(BF, false, false, 128, NQ);
-                constexpr uint32_t ID_O = tc::instr_desc(BF, true, true, 128, NQ);
-                const int dsteps = P.D / 16;
-                int k = 0, seg = -1, psteps = 0, pstart = 0;
-                bool ok = true;
-                auto weigh = [&](int t) {  // O^T (+)= V^T P^T of tile t
-                    const int s = t % NS;
-                    ok = tc::bar_wait(tc::smem_u32(&ms.pfull), t & 1, abort) &&
-                         tc::bar_wait(tc::smem_u32(&ms.vfull[s]), (t / NS) & 1, abort);
-                    if (!ok) return;
-                    tc::fence_after();
-                    for (int i = 0; i < psteps; ++i)
-                        tc::mma_f16(tmem + 2 * NQ,
-                                    tc::smem_desc(s0 + L::V0 + s * L::UNIT + i * 2048, HALVES > 1 ? TILE * 128 : 0, 1024),
-                                    tc::smem_desc(s0 + L::P0 + i * 2048, 0, 1024), ID_O, !pstart || i > 0);
-                    tc::commit(tc::smem_u32(&ms.vempty[s]));
-                    tc::commit(tc::smem_u32(&ms.pvdone));
-                };
-                bool begun = false;
-                for (int64_t i = 0; i < count && ok; ++i) {
-                    if (!w.dummy) {
-                        const bool start = !begun || w.j == 0;
-                        if (start) {
-                            ++seg;
-                            begun = true;
-                            if (!tc::bar_wait(tc::smem_u32(&ms.qfull[seg & 1]), (seg >> 1) & 1, abort)) break;
-                        }
-                        const int s = k % NS, sb = k & 1;
-                        ok = tc::bar_wait(tc::smem_u32(&ms.kfull[s]), (k / NS) & 1, abort);
-                        if (ok && k >= 2) ok = tc::bar_wait(tc::smem_u32(&ms.sempty[sb]), ((k >> 1) & 1) ^ 1, abort);
-                        if (!ok) break;
-                        tc::fence_after();
-                        for (int d = 0; d < dsteps; ++d)
-                            tc::mma_f16(tmem + sb * NQ,
-                                        tc::smem_desc(s0 + L::K0 + s * L::UNIT + (d >> 2) * TILE * 128 + (d & 3) * 32, 0, 1024),
-                                        tc::smem_desc(s0 + L::Q0 + (seg & 1) * L::QSTEP + (d >> 2) * NQ * 128 + (d & 3) * 32,
-                                                      0, 1024),
-                                        ID_S, d > 0);
-                        tc::commit(tc::smem_u32(&ms.kempty[s]));
-                        tc::commit(tc::smem_u32(&ms.sfull[sb]));
-                        const bool end = i + 1 == count || w.j + 1 == w.ntile;
-                        if (end) tc::commit(tc::smem_u32(&ms.qempty[seg & 1]));
-                        if (k > 0) weigh(k - 1);
-                        const int left = w.c + w.nn - w.j * TILE;
-                        psteps = left >= TILE ? TILE / 16 : (left + 15) / 16;
-                        pstart = start;
-                        ++k;
-                    }
-                    w.next(P);
-                }
-                if (ok && k > 0 && !*abort) weigh(k - 1);
+            begin = clock64();
+            while (lane == 0 && ok && wk < k) {
+                if (ready_p()) weigh();
+                ok = !late();
             }
             __syncwarp();
-        } else if (warp < 4) {
-            // ---- queries and the tree's mask -----------------------------------------------
-            const int t = tid - 64;
-            int seg = -1;
+        } else if (warp == 5) {
+            // ---- the run's segments ----------------------------------------------------------
+            // The lengths of 32 requests are read at a time.
+            int b = ms.begin_b, base = b, c = 0, nn = 0, n = 0;
+            if (b + lane < P.B) lengths(P, b + lane, c, nn);
+            int64_t at = t0, skip = t0 - ms.begin_base;  // tiles of the request before the run
+            int64_t rest = t1 - t0;
             bool ok = true;
-            for (int64_t i = 0; i < count;) {
-                if (!w.dummy) {
-                    ++seg;
-                    const int buf = seg & 1;
-                    if (seg >= 2) ok = tc::bar_wait(tc::smem_u32(&ms.qempty[buf]), ((seg >> 1) & 1) ^ 1, abort);
-                    if (group_or(2, 64, !ok)) break;
-                    // Which nodes see node a: every node's path to the root, then transposed.
-                    bool wrong = false;
-                    int p = t - 1;
-                    if (P.parents && t < w.nn) {
-                        const int64_t at = (int64_t)w.b * P.N + t;
-                        p = SV_INB(at, (int64_t)P.B * P.N, 1104) ? P.parents[at] : -1;
-                        wrong = t == 0 ? p != -1 : (p < 0 || p >= t);
-                        if (wrong) p = -1;
+            auto put = [&](const Seg &g) {
+                if (n >= SEGS) {
+                    ok = tc::bar_wait(tc::smem_u32(&ms.segempty[n % SEGS]), (n / SEGS + 1) & 1, abort);
+                    if (!__all_sync(0xffffffffu, ok)) return false;
+                }
+                if (lane == 0) {
+                    ms.seg[n % SEGS] = g;
+                    tc::bar_arrive(tc::smem_u32(&ms.segfull[n % SEGS]));
+                }
+                __syncwarp();
+                ++n;
+                return true;
+            };
+            Seg g = {};
+            while (rest > 0) {
+                if (b == base + 32) {
+                    base = b;
+                    if (b + lane < P.B) lengths(P, b + lane, c, nn);
+                }
+                g.b = b;
+                g.c = __shfl_sync(0xffffffffu, c, b - base);
+                g.nn = __shfl_sync(0xffffffffu, nn, b - base);
+                g.kind = kind_of(P, g.c, g.nn);
+                const int ntile = tiles_of(g.kind, g.c, g.nn);
+                int item = (int)(skip / ntile);
+                int j = (int)(skip - (int64_t)item * ntile);
+                skip = 0;
+                for (; item < HT && rest > 0; ++item, j = 0) {
+                    g.h = item / P.QT;
+                    g.qt = item - g.h * P.QT;
+                    g.j0 = j;
+                    g.j1 = rest < ntile - j ? j + (int)rest : ntile;
+                    g.part = -1;
+                    if (j > 0 || g.j1 < ntile) {
+                        // Its CTAs are those whose runs hold the request's tiles of this head.
+                        const int64_t ib = at - j;
+                        g.c0 = cta_of(ib, total, G);
+                        g.c1 = cta_of(ib + ntile - 1, total, G);
+                        g.first0 = run_begin(g.c0, total, G) == ib;
+                        g.part = 2 * cta + (cta == g.c0 && !g.first0);
                     }
-                    if (t == 0) ms.code[buf] = 0;
-                    ms.par[t] = (int8_t)p;
-                    const int h = w.item / P.QT, qt = w.item % P.QT;
-                    constexpr int CH = DP / 8;  // 16-byte chunks of a row
-                    for (int e = t; e < NQ * CH; e += 64) {
-                        const int r = e / CH, ch = e - r * CH, g = qt * NQ + r, n = g / P.G;
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (n < w.nn && ch * 8 < P.D) {
-                            const int64_t at = ((int64_t)w.b * P.N + n) * P.q_row + (int64_t)(h * P.G + g - n * P.G) * P.D +
+                    at += g.j1 - j;
+                    rest -= g.j1 - j;
+                    if (!put(g)) {
+                        rest = -1;
+                        break;
+                    }
+                }
+                ++b;
+            }
+            g.kind = 3;
+            if (rest == 0) put(g);
+        } else if (warp < 8) {
+            // ---- queries and the tree's mask -----------------------------------------------
+            const int t = tid - 192;
+            int seg = -1;
+            Seg g = {};
+            for (;;) {
+                const bool got = take(g);
+                if (group_or(2, 64, !got) || g.kind == 3) break;
+                if (g.kind) continue;
+                ++seg;
+                const int buf = seg & 1;
+                // Which nodes see node a: every node's path to the root, then transposed.
+                bool wrong = false;
+                int p = t - 1;
+                if (P.parents && t < g.nn) {
+                    const int64_t at = (int64_t)g.b * P.N + t;
+                    p = SV_INB(at, (int64_t)P.B * P.N, 1104) ? P.parents[at] : -1;
+                    wrong = t == 0 ? p != -1 : (p < 0 || p >= t);
+                    if (wrong) p = -1;
+                }
+                constexpr int CH = DP / 8, PER = NQ * CH / 64;  // 16-byte chunks of a row; of a thread
+                uint4 x[PER < 8 ? PER : 8];
+                bool ok = true;
+#pragma unroll
+                for (int e0 = 0; e0 < PER; e0 += 8) {
+#pragma unroll
+                    for (int i = 0; i < 8 && e0 + i < PER; ++i) {
+                        const int e = (e0 + i) * 64 + t, r = e / CH, ch = e % CH, gr = g.qt * NQ + r, n = gr / P.G;
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (n < g.nn && ch * 8 < P.D) {
+                            const int64_t at = ((int64_t)g.b * P.N + n) * P.q_row + (int64_t)(g.h * P.G + gr - n * P.G) * P.D +
                                                ch * 8;
                             if (SV_INB(at, (int64_t)P.B * P.N * P.q_row, 1105))
-                                x = *reinterpret_cast<const uint4 *>(P.q + at);
+                                x[i] = *reinterpret_cast<const uint4 *>(P.q + at);
                         }
+                    }
+                    if (e0 == 0) {
+                        if (seg >= 2) ok = tc::bar_wait(tc::smem_u32(&ms.qempty[buf]), ((seg >> 1) & 1) ^ 1, abort);
+                        ms.par[t] = (int8_t)p;
+                        if (t == 0) ms.code[buf] = ms.poison[buf] = 0;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8 && e0 + i < PER; ++i) {
+                        const int e = (e0 + i) * 64 + t, r = e / CH, ch = e % CH;
                         *reinterpret_cast<uint4 *>(smem + L::Q0 + buf * L::QSTEP + (ch >> 3) * NQ * 128 + r * 128 +
-                                                   (((ch & 7) ^ (r & 7)) << 4)) = x;
+                                                   (((ch & 7) ^ (r & 7)) << 4)) = x[i];
                     }
-                    tc::fence_async_smem();
-                    group_sync(2, 64);
-                    if (wrong) ms.code[buf] = 1;
-                    unsigned long long path = 0;
-                    if (t < w.nn) {
-                        if (P.parents)
-                            for (int n = t; n >= 0; n = ms.par[n]) path |= 1ull << n;
-                        else
-                            path = ~0ull >> (63 - t);
-                    }
-                    ms.desc[buf][t] = path;
-                    group_sync(2, 64);
-                    unsigned long long see = 0;
-                    for (int n = t; n < w.nn; ++n) see |= ((ms.desc[buf][n] >> t) & 1ull) << n;
-                    group_sync(2, 64);
-                    ms.desc[buf][t] = see;
-                    tc::bar_arrive(tc::smem_u32(&ms.qfull[buf]));
                 }
-                // On to the next segment.
-                const int64_t step = w.ntile - w.j;
-                i += step;
-                w.j = w.ntile - 1;
-                if (i < count) w.next(P);
+                tc::fence_async_smem();
+                if (group_or(2, 64, !ok)) break;
+                if (wrong) ms.code[buf] = 1;
+                unsigned long long path = 0;
+                if (t < g.nn) {
+                    if (P.parents)
+                        for (int n = t; n >= 0; n = ms.par[n]) path |= 1ull << n;
+                    else
+                        path = ~0ull >> (63 - t);
+                }
+                ms.desc[buf][t] = path;
+                group_sync(2, 64);
+                unsigned long long see = 0;
+                for (int n = t; n < g.nn; ++n) see |= ((ms.desc[buf][n] >> t) & 1ull) << n;
+                group_sync(2, 64);
+                ms.desc[buf][t] = see;
+                tc::bar_arrive(tc::smem_u32(&ms.qfull[buf]));
             }
         } else {
-            // ---- softmax: one position of a tile per thread ---------------------------------
-            const int t = tid - 128, wq = warp - 4;
-            const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
-            constexpr int NC = NQ / 16;
-            float raw[NQ], rnd[NQ];  // this position's share of the columns' sums
-            int k = 0, seg = -1, pv = 0;  // seg: segments with something to attend with
-            bool begun = false, fail = false, fresh = true;
-            int first_j = 0, poison = 0;
-            for (int64_t i = 0; i < count; ++i) {
-                const bool start = !begun || w.j == 0, end = i + 1 == count || w.j + 1 == w.ntile;
-                begun = true;
-                const int h = w.item / P.QT, qt = w.item % P.QT;
-                if (w.dummy) {
+            // ---- softmax: one position of a tile and half of its columns per thread ----------
+            constexpr int CW = NQ / 2;
+            const int t = tid & 127, wq = warp & 3, wg = (warp - 8) >> 2, bar = 4 + wg;
+            const int col0 = wg * CW;
+            const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16) + col0;
+            const uint64_t scale2 = sv::f2(P.scale_log2, P.scale_log2);
+            uint64_t raw[CW / 2], rnd[CW / 2];  // this position's share of the columns' sums
+            int k = 0, seg = -1;
+            bool fail = false;
+            Seg g = {};
+            for (;;) {
+                const bool got = take(g);
+                if (group_or(bar, 128, !got || fail) || g.kind == 3) break;
+                const int row0 = g.qt * NQ + col0, n0 = row0 / P.G, h0 = row0 - n0 * P.G;
+                if (g.kind) {
                     // Nothing to read: zeros where the request has no nodes, NaN where its lengths are wrong.
-                    const bool nan = w.dummy == 2;
-                    for (int col = 0; col < NQ; ++col) {
-                        const int g = qt * NQ + col, n = g / P.G;
-                        if (n >= P.N) break;
-                        const int64_t row = ((int64_t)w.b * P.N + n) * P.Hq + h * P.G + g - n * P.G;
+                    const bool nan = g.kind == 2;
+                    for (int c = 0, n = n0, h = h0; c < CW && n < P.N; ++c) {
+                        const int64_t row = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + h;
                         if (t < P.D && SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1106))
                             P.out[row * P.D + t] = nan ? (uint16_t)Half2<BF>::NAN2 : 0;
                         if (t == 0 && P.lse) P.lse[row] = nan ? NAN : -INFINITY;
+                        if (++h == P.G) h = 0, ++n;
                     }
                     if (nan && t == 0 && P.dev_status) atomicMax(P.dev_status, SPEC_VERIFY_DEV_BAD_KV_POSITION);
-                    w.next(P);
                     continue;
                 }
-                if (start) {
-                    ++seg;
-                    first_j = w.j;
-                    poison = 0;
-                    fresh = true;
+                ++seg;
+                const int buf = seg & 1, len = g.c + g.nn;
+                bool fresh = true;  // some column has no reference yet
+                fail |= !tc::bar_wait(tc::smem_u32(&ms.qfull[buf]), (seg >> 1) & 1, abort);  // the tree's mask
 #pragma unroll
-                    for (int c = 0; c < NQ; ++c) raw[c] = rnd[c] = 0.f;
-                    fail |= !tc::bar_wait(tc::smem_u32(&ms.qfull[seg & 1]), (seg >> 1) & 1, abort);
-                }
-                const int sb = k & 1, s = k % NS;
-                const int pos = w.j * TILE + t, len = w.c + w.nn;
-                const bool special = (w.j + 1) * TILE > w.c;  // holds nodes, or ends inside
-                unsigned long long vis = ~0ull;               // the columns that see this position
-                if (special) {
-                    if (pos >= len) {
+                for (int c = 0; c < CW / 2; ++c) raw[c] = rnd[c] = 0;
+                for (int j = g.j0; j < g.j1; ++j, ++k) {
+                    const int sb = k & 1, pos = j * TILE + t;
+                    const bool special = (j + 1) * TILE > g.c;  // holds nodes, or ends inside
+                    fail |= !tc::bar_wait(tc::smem_u32(&ms.sfull[sb]), (k >> 1) & 1, abort);
+                    tc::fence_after();
+                    float x[CW];
+                    tc::tmem_ld(lanes + sb * NQ, x);
+                    tc::wait_ld(x);
+                    // Exponents against the references; what this position's columns do not see is -inf.
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < CW; c += 2) {
+                        const float2 d = sv::f2_split(sv::f2_fma(sv::f2(x[c], x[c + 1]), scale2,
+                                                                 *reinterpret_cast<const uint64_t *>(&ms.nref[col0 + c])));
+                        x[c] = d.x;
+                        x[c + 1] = d.y;
+                    }
+                    unsigned vis = 0xffffffffu;  // the columns that see this position
+                    if (special) {
                         vis = 0;
-                    } else if (pos >= w.c) {
-                        const unsigned long long see = ms.desc[seg & 1][pos - w.c];
-                        vis = 0;
-                        int n = qt * NQ / P.G, g = qt * NQ - n * P.G;
-                        for (int c = 0; c < NQ; ++c) {
-                            if (n < w.nn) vis |= ((see >> n) & 1ull) << c;
-                            if (++g == P.G) g = 0, ++n;
+                        if (pos < g.c) {
+                            vis = 0xffffffffu;
+                        } else if (pos < len) {
+                            const unsigned long long see = ms.desc[buf][pos - g.c];
+                            for (int c = 0, n = n0, h = h0; c < CW && n < g.nn; ++c) {
+                                vis |= (unsigned)((see >> n) & 1ull) << c;
+                                if (++h == P.G) h = 0, ++n;
+                            }
                         }
+#pragma unroll
+                        for (int c = 0; c < CW; ++c) x[c] = (vis >> c) & 1 ? x[c] : -INFINITY;
                     }
-                }
-                fail |= !tc::bar_wait(tc::smem_u32(&ms.sfull[sb]), (k >> 1) & 1, abort);
-                tc::fence_after();
-                float x[NC][16];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) tc::tmem_ld16(lanes + sb * NQ + c * 16, x[c]);
-                tc::wait_ld(x);
-                tc::fence_before();
-                tc::bar_arrive(tc::smem_u32(&ms.sempty[sb]));
-                bool over = fresh | fail;
+                    for (int c = 0; c < CW; ++c) top = fmaxf(top, x[c]);
+                    if (group_or(bar, 128, fresh || fail || top > SLACK)) {
+                        if (group_or(bar, 128, fail)) break;
+                        // Move the references to the columns' maxima.
+                        tc::tmem_ld(lanes + sb * NQ, x);
+                        tc::wait_ld(x);
+                        float m = 0.f;
 #pragma unroll
-                for (int c = 0; c < NQ; ++c) {
-                    const float d = fmaf(x[c / 16][c % 16], P.scale_log2, ms.nref[c]);
-                    over |= d > SLACK && ((vis >> c) & 1);
-                }
-                if (group_or(1, 128, over)) {
-                    if (group_or(1, 128, fail)) break;
-                    // Move the references to the columns' maxima.
-#pragma unroll
-                    for (int c = 0; c < NQ; ++c) {
-                        const float y = (vis >> c) & 1 ? x[c / 16][c % 16] * P.scale_log2 : -INFINITY;
-                        const float m = warp_max(y);
-                        if (lane == 0) ms.red[wq][c] = m;
-                    }
-                    group_sync(1, 128);
-                    bool none = false;
-                    if (t < NQ) {
-                        const float m = fmaxf(fmaxf(ms.red[0][t], ms.red[1][t]), fmaxf(ms.red[2][t], ms.red[3][t]));
-                        const float old = start ? -INFINITY : ms.sum[0][t];  // the reference, -inf: none yet
-                        const float to = fmaxf(m, old);
-                        ms.sum[0][t] = to;
-                        ms.nref[t] = to == -INFINITY ? 0.f : -to;
-                        ms.fac[t] = old == -INFINITY ? 0.f : ex2(old - to);
-                        none = to == -INFINITY;
-                    }
-                    fresh = group_or(1, 128, none);
-                    if (!start) {
-#pragma unroll
-                        for (int c = 0; c < NQ; ++c) {
-                            raw[c] *= ms.fac[c];
-                            rnd[c] *= ms.fac[c];
+                        for (int c = 0; c < CW; ++c) {
+                            x[c] = (vis >> c) & 1 ? x[c] * P.scale_log2 : -INFINITY;
+                            const float y = warp_max(x[c]);
+                            if (lane == c) m = y;
                         }
-                        // The accumulators follow, once the products before have come to an end.
-                        if (pv < k) {
+                        if (lane < CW) ms.red[wq][col0 + lane] = m;
+                        group_sync(bar, 128);
+                        bool none = false;
+                        if (t < CW) {
+                            const int c = col0 + t;
+                            m = fmaxf(fmaxf(ms.red[0][c], ms.red[1][c]), fmaxf(ms.red[2][c], ms.red[3][c]));
+                            const float old = j == g.j0 ? -INFINITY : ms.ref[c];
+                            const float now = fmaxf(m, old);
+                            ms.ref[c] = now;
+                            ms.nref[c] = now == -INFINITY ? 0.f : -now;
+                            ms.fac[c] = old == -INFINITY ? 0.f : ex2(old - now);
+                            none = now == -INFINITY;
+                        }
+                        fresh = group_or(bar, 128, none);
+                        if (j > g.j0) {
+#pragma unroll
+                            for (int c = 0; c < CW; c += 2) {
+                                const uint64_t f = *reinterpret_cast<const uint64_t *>(&ms.fac[col0 + c]);
+                                raw[c / 2] = sv::f2_mul(raw[c / 2], f);
+                                rnd[c / 2] = sv::f2_mul(rnd[c / 2], f);
+                            }
+                            // The accumulators follow, once the products before have come to an end.
                             fail |= !tc::bar_wait(tc::smem_u32(&ms.pvdone), (k - 1) & 1, abort);
-                            pv = k;
-                        }
-                        tc::fence_after();
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) {
-                            float o[1][16];
-                            tc::tmem_ld16(lanes + 2 * NQ + c * 16, o[0]);
+                            tc::fence_after();
+                            float o[CW];
+                            tc::tmem_ld(lanes + 2 * NQ, o);
                             tc::wait_ld(o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[0][e] *= ms.fac[c * 16 + e];
-                            tc::tmem_st16(lanes + 2 * NQ + c * 16, o[0]);
+                            for (int c = 0; c < CW; ++c) o[c] *= ms.fac[col0 + c];
+                            tc::tmem_st(lanes + 2 * NQ, o);
+                            tc::wait_st();
                         }
-                        tc::wait_st();
-                    }
-                }
-                // The weights, rounded to the values' type; both sums go on.
-                uint32_t pk[NQ / 2];
 #pragma unroll
-                for (int c = 0; c < NQ; c += 2) {
-                    float a = ex2(fmaf(x[c / 16][c % 16], P.scale_log2, ms.nref[c]));
-                    float b = ex2(fmaf(x[c / 16][c % 16 + 1], P.scale_log2, ms.nref[c + 1]));
-                    if (special) {
-                        if (!((vis >> c) & 1)) a = 0.f;
-                        if (!((vis >> (c + 1)) & 1)) b = 0.f;
+                        for (int c = 0; c < CW; ++c) x[c] += ms.nref[col0 + c];
                     }
-                    pk[c / 2] = Half2<BF>::pack(a, b);
-                    const float2 r = Half2<BF>::unpack(pk[c / 2]);
-                    raw[c] += a;
-                    raw[c + 1] += b;
-                    rnd[c] += r.x;
-                    rnd[c + 1] += r.y;
-                }
-                if (special && pos >= w.c) {
-                    // Values nobody may see with weight 0: rows past the end become zeros, and what is
-                    // not finite in a node's row is set aside (its readers get it at the end).
-                    fail |= !tc::bar_wait(tc::smem_u32(&ms.vfull[s]), (k / NS) & 1, abort);
+                    tc::fence_before();
+                    tc::bar_arrive(tc::smem_u32(&ms.sempty[sb]));
+                    // The weights, rounded to the values' type; both sums go on.
+                    uint32_t pk[CW / 2];
 #pragma unroll
-                    for (int hf = 0; hf < HALVES; ++hf)
-                        for (int ch = 0; ch < 8; ++ch) {
-                            uint4 *at = reinterpret_cast<uint4 *>(smem + L::V0 + s * L::UNIT + hf * TILE * 128 + t * 128 +
-                                                                  ch * 16);
-                            if (pos >= len) {
-                                *at = make_uint4(0, 0, 0, 0);
-                                continue;
-                            }
+                    for (int c = 0; c < CW; c += 2) {
+                        const float a = ex2(x[c]), b = ex2(x[c + 1]);
+                        pk[c / 2] = Half2<BF>::pack(a, b);
+                        const float2 r = Half2<BF>::unpack(pk[c / 2]);
+                        raw[c / 2] = sv::f2_add(raw[c / 2], sv::f2(a, b));
+                        rnd[c / 2] = sv::f2_add(rnd[c / 2], sv::f2(r.x, r.y));
+                    }
+                    if (special && pos >= g.c && pos < len) {
+                        // A weight of 0 does not undo an infinity or a NaN: what is not finite in a node's
+                        // values is set aside, and its readers get it at the segment's end.
+                        const int u = 2 * k + 1;
+                        fail |= !tc::bar_wait(tc::smem_u32(&ms.full[u % NU]), (u / NU) & 1, abort);
+                        bool odd = false;
+                        for (int ch = wg * (DP / 16); ch < (wg + 1) * (DP / 16); ++ch) {
+                            uint4 *at = reinterpret_cast<uint4 *>(smem + (u % NU) * L::UNIT + (ch >> 3) * TILE * 128 + t * 128 +
+                                                                  (ch & 7) * 16);
                             uint4 y = *at;
                             uint32_t *wd = &y.x;
-                            bool odd = false;
+                            bool mend = false;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                if ((wd[e] & Half2<BF>::EXP_MASK) == Half2<BF>::EXP_MASK) wd[e] &= 0xffff0000u, odd = true;
-                                if (((wd[e] >> 16) & Half2<BF>::EXP_MASK) == Half2<BF>::EXP_MASK) wd[e] &= 0xffffu, odd = true;
+                                if ((wd[e] & Half2<BF>::EXP_MASK) == Half2<BF>::EXP_MASK) wd[e] &= 0xffff0000u, mend = true;
+                                if (((wd[e] >> 16) & Half2<BF>::EXP_MASK) == Half2<BF>::EXP_MASK) wd[e] &= 0xffffu, mend = true;
                             }
-                            if (odd) {
-                                *at = y;
-                                poison = 1;
-                            }
+                            if (mend) *at = y;
+                            odd |= mend;
                         }
-                }
-                if (pv < k) {
-                    fail |= !tc::bar_wait(tc::smem_u32(&ms.pvdone), (k - 1) & 1, abort);
-                    pv = k;
-                }
+                        if (odd) *(volatile int *)&ms.poison[buf] = 1;
+                    }
+                    if (k > 0) fail |= !tc::bar_wait(tc::smem_u32(&ms.pvdone), (k - 1) & 1, abort);
 #pragma unroll
-                for (int ch = 0; ch < NQ / 8; ++ch)
-                    *reinterpret_cast<uint4 *>(smem + L::P0 + t * 128 + ((ch ^ (t & 7)) << 4)) =
-                        make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
-                tc::fence_async_smem();
-                tc::fence_before();
-                tc::bar_arrive(tc::smem_u32(&ms.pfull));
-                ++k;
-                if (!end) {
-                    w.next(P);
-                    continue;
+                    for (int ch = 0; ch < CW / 8; ++ch)
+                        *reinterpret_cast<uint4 *>(smem + L::P0 + t * 128 + (((col0 / 8 + ch) ^ (t & 7)) << 4)) =
+                            make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+                    tc::fence_async_smem();
+                    tc::fence_before();
+                    tc::bar_arrive(tc::smem_u32(&ms.pfull));
                 }
 
                 // ---- the segment's end: join the columns' sums, write rows or a part -----------
-                fail |= !tc::bar_wait(tc::smem_u32(&ms.pvdone), (k - 1) & 1, abort);
-                pv = k;
-                if (group_or(1, 128, fail)) break;
-                tc::fence_after();
-                float o[NC][16];
+                {
+                    float y[CW];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) tc::tmem_ld16(lanes + 2 * NQ + c * 16, o[c]);
-                column_sums<NQ>(raw, ms.red[wq], lane);
+                    for (int c = 0; c < CW; c += 2) {
+                        const float2 f = sv::f2_split(raw[c / 2]);
+                        y[c] = f.x;
+                        y[c + 1] = f.y;
+                    }
+                    const float a = column_sum<CW>(y, lane);
+#pragma unroll
+                    for (int c = 0; c < CW; c += 2) {
+                        const float2 f = sv::f2_split(rnd[c / 2]);
+                        y[c] = f.x;
+                        y[c + 1] = f.y;
+                    }
+                    const float b = column_sum<CW>(y, lane);
+                    if (lane < CW) {
+                        ms.red[wq][col0 + lane] = a;
+                        ms.red2[wq][col0 + lane] = b;
+                    }
+                }
+                if (k > 0) fail |= !tc::bar_wait(tc::smem_u32(&ms.pvdone), (k - 1) & 1, abort);
+                if (group_or(bar, 128, fail)) break;
+                tc::fence_after();
+                float o[CW];
+                tc::tmem_ld(lanes + 2 * NQ, o);
                 tc::wait_ld(o);
-                group_sync(1, 128);
-                if (t < NQ) ms.fac[t] = ms.red[0][t] + ms.red[1][t] + ms.red[2][t] + ms.red[3][t];
-                group_sync(1, 128);
-                column_sums<NQ>(rnd, ms.red[wq], lane);
-                const bool any_poison = group_or(1, 128, poison);
-                if (t < NQ) ms.sum[1][t] = ms.red[0][t] + ms.red[1][t] + ms.red[2][t] + ms.red[3][t];
-                if (any_poison && t < P.D) {
-                    const int from = first_j * TILE, to = len < (w.j + 1) * TILE ? len : (w.j + 1) * TILE;
-                    for (int y = from > w.c ? from : w.c; y < to; ++y) {
-                        const int64_t st = (int64_t)w.b * P.max_pos + y;
+                if (*(volatile int *)&ms.poison[buf] && t < P.D) {
+                    const int from = g.j0 * TILE, to = len < g.j1 * TILE ? len : g.j1 * TILE;
+                    for (int y = from > g.c ? from : g.c; y < to; ++y) {
+                        const int64_t st = (int64_t)g.b * P.max_pos + y;
                         const int slot = SV_INB(st, (int64_t)P.B * P.max_pos, 1107) ? P.slot_table[st] : -1;
                         if (slot < 0 || slot >= P.num_slots) continue;
-                        const uint32_t bits = P.v[(int64_t)slot * P.v_slot + h * P.D + t];
+                        const uint32_t bits = P.v[(int64_t)slot * P.v_slot + g.h * P.D + t];
                         if ((bits & Half2<BF>::EXP_MASK) != Half2<BF>::EXP_MASK) continue;
                         const float val = Half2<BF>::unpack(bits).x;
-                        const unsigned long long see = ms.desc[seg & 1][y - w.c];
+                        const unsigned long long see = ms.desc[buf][y - g.c];
 #pragma unroll
-                        for (int c = 0; c < NQ; ++c) {
-                            const int n = (qt * NQ + c) / P.G;
-                            if (n < w.nn && ((see >> n) & 1)) o[c / 16][c % 16] += val;
+                        for (int c = 0; c < CW; ++c) {
+                            const int n = (row0 + c) / P.G;
+                            if (n < g.nn && ((see >> n) & 1)) o[c] += val;
                         }
                     }
                 }
-                const int raise = *(volatile int *)&ms.bad[seg % FLAGS] ? SPEC_VERIFY_DEV_BAD_KV_SLOT
-                                  : ms.code[seg & 1]                    ? SPEC_VERIFY_DEV_BAD_TREE
-                                                                        : 0;
-                group_sync(1, 128);
+                const int raise = *(volatile int *)&ms.bad[wg][seg % FLAGS] ? SPEC_VERIFY_DEV_BAD_KV_SLOT
+                                  : ms.code[buf]                            ? SPEC_VERIFY_DEV_BAD_TREE
+                                                                            : 0;
+                // What a thread t < CW says of column t.
+                float sum = 0.f, rsum = 0.f;
+                if (t < CW) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        sum += ms.red[w][col0 + t];
+                        rsum += ms.red2[w][col0 + t];
+                    }
+                    ms.fac[col0 + t] = raise ? NAN : 1.f / rsum;
+                }
+                group_sync(bar, 128);
                 if (t == 0) {
                     if (raise && P.dev_status) atomicMax(P.dev_status, raise);
-                    *(volatile int *)&ms.bad[seg % FLAGS] = 0;
-                    tc::bar_arrive(tc::smem_u32(&ms.qempty[seg & 1]));
+                    *(volatile int *)&ms.bad[wg][seg % FLAGS] = 0;
+                    tc::bar_arrive(tc::smem_u32(&ms.qempty[buf]));
                 }
-                if (first_j == 0 && w.j + 1 == w.ntile) {
-                    int n = qt * NQ / P.G, g = qt * NQ - n * P.G;
+                if (g.part < 0) {
+                    uint16_t *out = P.out + (((int64_t)g.b * P.N + n0) * P.Hq + g.h * P.G + h0) * P.D + t;
+                    const int64_t wrap = (int64_t)(P.Hq - P.G + 1) * P.D;  // to the next node's first head
+                    int n = n0, h = h0;
+                    if (t < P.D) {
 #pragma unroll
-                    for (int c = 0; c < NQ; ++c) {
-                        if (n < P.N) {
-                            const int64_t row = ((int64_t)w.b * P.N + n) * P.Hq + h * P.G + g;
-                            float y = n < w.nn ? o[c / 16][c % 16] / ms.sum[1][c] : 0.f;
-                            if (raise) y = NAN;
-                            if (t < P.D && SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1108))
-                                P.out[row * P.D + t] = (uint16_t)Half2<BF>::pack(y, y);
-                            if (t == c && P.lse && SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1109))
-                                P.lse[row] = raise ? NAN
-                                             : n < w.nn ? (log2f(ms.fac[c]) - ms.nref[c]) * 0.69314718f
-                                                        : -INFINITY;
+                        for (int c = 0; c < CW; ++c) {
+                            if (n >= P.N) break;
+                            const float y = n < g.nn ? o[c] * ms.fac[col0 + c] : raise ? NAN : 0.f;
+                            if (SV_INB(out - P.out, (int64_t)P.B * P.N * P.Hq * P.D, 1108))
+                                *out = (uint16_t)Half2<BF>::pack(y, y);
+                            if (++h == P.G) h = 0, ++n, out += wrap;
+                            else out += P.D;
                         }
-                        if (++g == P.G) g = 0, ++n;
                     }
-                    group_sync(1, 128);
+                    const int nt = (row0 + t) / P.G;
+                    if (t < CW && nt < P.N && P.lse) {
+                        const int64_t row = ((int64_t)g.b * P.N + nt) * P.Hq + g.h * P.G + row0 + t - nt * P.G;
+                        if (SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1109))
+                            P.lse[row] = raise ? NAN : nt < g.nn ? (log2f(sum) - ms.nref[col0 + t]) * 0.69314718f : -INFINITY;
+                    }
                 } else {
-                    // A part of a request: its CTAs are those whose runs hold the segment's tiles.
-                    const int64_t ib = t0 + i - w.j, total_ = total;
-                    const int c0 = cta_of(ib, total_, G), c1 = cta_of(ib + w.ntile - 1, total_, G);
-                    const int first0 = run_begin(c0, total_, G) == ib;
-                    const int slot = 2 * cta + (cta == c0 && !first0);
-                    float *part = P.parts + (int64_t)slot * part_floats<NQ>();
+                    float *part = P.parts + (int64_t)g.part * part_floats<NQ>();
 #pragma unroll
-                    for (int c = 0; c < NQ; ++c) part[c * MAXD + t] = raise ? NAN : o[c / 16][c % 16];
-                    if (t < NQ) {
-                        float *r = part + NQ * MAXD;
-                        r[t] = ms.sum[0][t];
-                        r[NQ + t] = raise ? NAN : ms.fac[t];
-                        r[2 * NQ + t] = raise ? NAN : ms.sum[1][t];
+                    for (int c = 0; c < CW; ++c) part[(col0 + c) * MAXD + t] = o[c];
+                    if (t < CW) {
+                        float *r = part + NQ * MAXD + col0 + t;
+                        r[0] = ms.ref[col0 + t];
+                        r[NQ] = raise ? NAN : sum;
+                        r[2 * NQ] = raise ? NAN : rsum;
                     }
                     __threadfence();
-                    group_sync(1, 128);
-                    if (t == 0) {
-                        const unsigned n = (unsigned)(c1 - c0);
-                        const unsigned was = atomicAdd(&P.counters[c0], 1u);
-                        if (was == n) {
-                            P.counters[c0] = 0;
-                            auto &jn = ms.join[cta == c0 ? 1 : 0];
-                            jn.on = 1;
-                            jn.b = w.b;
-                            jn.h = h;
-                            jn.qt = qt;
-                            jn.c0 = c0;
-                            jn.c1 = c1;
-                            jn.first0 = first0;
-                        }
+                    group_sync(bar, 128);
+                    // Both halves of the columns count, of every CTA.
+                    if (t == 0 && atomicAdd(&P.counters[g.c0], 1u) == 2u * (unsigned)(g.c1 - g.c0) + 1u) {
+                        P.counters[g.c0] = 0;
+                        ms.joins[cta == g.c0] = 1;
+                        ms.join[cta == g.c0] = g;
                     }
                 }
-                w.next(P);
+                // The references and factors are read until here; the next segment writes them anew.
             }
+
+            // ---- joins left to this CTA ----------------------------------------------------------
+            group_sync(3, 256);
+            if (!*abort)
+                for (int i = 0; i < 2; ++i) {
+                    if (!ms.joins[i]) continue;
+                    __threadfence();
+                    g = ms.join[i];
+                    // A thread takes four dimensions of a column; the parts are read in their order, so
+                    // the result does not depend on who joins.
+                    for (int e = tid - 256; e < NQ * (MAXD / 4); e += 256) {
+                        const int c = e / (MAXD / 4), d = (e - c * (MAXD / 4)) * 4;
+                        const int gr = g.qt * NQ + c, n = gr / P.G;
+                        if (n >= P.N) break;
+                        auto part_of = [&](int x) {
+                            return P.parts + (int64_t)(2 * x + (x == g.c0 && !g.first0)) * part_floats<NQ>();
+                        };
+                        float top = -INFINITY;
+#pragma unroll 4
+                        for (int x = g.c0; x <= g.c1; ++x) top = fmaxf(top, __ldcg(part_of(x) + NQ * MAXD + c));
+                        float sum = 0.f, rsum = 0.f;
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                        for (int x = g.c0; x <= g.c1; ++x) {
+                            const float *part = part_of(x);
+                            const float m = __ldcg(part + NQ * MAXD + c), l = __ldcg(part + NQ * MAXD + NQ + c);
+                            const float r = __ldcg(part + NQ * MAXD + 2 * NQ + c);
+                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + c * MAXD + d));
+                            if (l != 0.f) {  // 0: the part's positions have no weight in this row
+                                const float f = ex2(m == -INFINITY ? 0.f : m - top);
+                                sum += f * l;
+                                rsum += f * r;
+                                acc.x += f * y.x;
+                                acc.y += f * y.y;
+                                acc.z += f * y.z;
+                                acc.w += f * y.w;
+                            }
+                        }
+                        const int64_t row = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + gr - n * P.G;
+                        const bool bad = sum != sum;
+                        if (d < P.D && SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1110)) {
+                            uint2 y = make_uint2(0, 0);
+                            if (n < g.nn || bad) {
+                                const float inv = 1.f / rsum;
+                                y = make_uint2(Half2<BF>::pack(acc.x * inv, acc.y * inv),
+                                               Half2<BF>::pack(acc.z * inv, acc.w * inv));
+                            }
+                            *reinterpret_cast<uint2 *>(P.out + row * P.D + d) = y;
+                        }
+                        if (d == 0 && P.lse)
+                            P.lse[row] = n < g.nn || bad ? ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.69314718f : -INFINITY;
+                    }
+                }
         }
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     if (ms.abort) {
-        // A bounded wait ran out: what is written is not an answer.  The copies and products in
-        // flight end (again with a limit) before their memory is given back.
-        const uint64_t begin = tc::now_ns();
-        if (tid == 0)
-            for (int kv = 0; kv < 2; ++kv)
-                for (int n = ms.issued[kv], i = n > NS ? n - NS : 0; i < n; ++i)
-                    while (!tc::bar_try(tc::smem_u32(kv ? &ms.vfull[i % NS] : &ms.kfull[i % NS]), (i / NS) & 1) &&
-                           tc::now_ns() - begin < tc::WAIT_NS) {}
-        if (tid == 32) {
+        // A bounded wait ran out: what is written is not an answer.  The products in flight end
+        // (again with a limit) before their memory is given back; the copies were waited for.
+        if (tid == 128) {
+            const int64_t begin = clock64();
             tc::commit(tc::smem_u32(&ms.drain));
-            while (!tc::bar_try(tc::smem_u32(&ms.drain), 0) && tc::now_ns() - begin < tc::WAIT_NS) {}
+            while (!tc::bar_try(tc::smem_u32(&ms.drain), 0) && clock64() - begin < tc::WAIT_CLOCKS) {}
+            if (P.dev_status) atomicMax(P.dev_status, SPEC_VERIFY_DEV_TIMEOUT);
         }
-        if (tid == 0 && P.dev_status) atomicMax(P.dev_status, SPEC_VERIFY_DEV_TIMEOUT);
         __syncthreads();
     }
-    if (warp == 1) tc::tmem_free(tmem, L::COLS);
-    if (ms.abort) return;
-
-    // ---- joins left to this CTA, by all its threads -----------------------------------------
-    for (int i = 0; i < 2; ++i) {
-        if (!ms.join[i].on) continue;
-        __threadfence();
-        const auto jn = ms.join[i];
-        const int b = jn.b, nn = P.num_nodes ? P.num_nodes[b] : P.N;
-        auto part_of = [&](int c) {
-            return P.parts + (int64_t)(2 * c + (c == jn.c0 && !jn.first0)) * part_floats<NQ>();
-        };
-        // A thread takes four dimensions of a column; the parts are read in their order, so the
-        // result does not depend on who joins.
-        for (int e = tid; e < NQ * (MAXD / 4); e += NT) {
-            const int c = e / (MAXD / 4), d = (e - c * (MAXD / 4)) * 4;
-            const int g = jn.qt * NQ + c, n = g / P.G;
-            if (n >= P.N) break;
-            float top = -INFINITY;
-            for (int x = jn.c0; x <= jn.c1; ++x) top = fmaxf(top, __ldcg(part_of(x) + NQ * MAXD + c));
-            float sum = 0.f, rsum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int x = jn.c0; x <= jn.c1; ++x) {
-                const float *part = part_of(x);
-                const float m = __ldcg(part + NQ * MAXD + c), l = __ldcg(part + NQ * MAXD + NQ + c);
-                const float r = __ldcg(part + NQ * MAXD + 2 * NQ + c);
-                const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + c * MAXD + d));
-                const float f = l == 0.f ? 0.f : ex2(m == -INFINITY ? 0.f : m - top);
-                if (l != 0.f) {
-                    sum += f * l;
-                    rsum += f * r;
-                    acc.x += f * y.x;
-                    acc.y += f * y.y;
-                    acc.z += f * y.z;
-                    acc.w += f * y.w;
-                }
-            }
-            const int64_t row = ((int64_t)b * P.N + n) * P.Hq + jn.h * P.G + g - n * P.G;
-            if (d < P.D && SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1110)) {
-                uint2 y = make_uint2(0, 0);
-                if (n < nn) {
-                    const float inv = 1.f / rsum;
-                    y = make_uint2(Half2<BF>::pack(acc.x * inv, acc.y * inv), Half2<BF>::pack(acc.z * inv, acc.w * inv));
-                }
-                *reinterpret_cast<uint2 *>(P.out + row * P.D + d) = y;
-            }
-            if (d == 0 && P.lse)
-                P.lse[row] = n < nn ? ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.69314718f : -INFINITY;
-        }
-    }
+    if (warp == 4) tc::tmem_free(tmem, L::COLS);
 }
 
 // -------------------------------------------------------------------------------------------------
 // Host side.
 // -------------------------------------------------------------------------------------------------
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 struct DevInfo {
     int sms = 0;
 };
 static std::mutex g_mu;
 static DevInfo g_dev[64];
-static EncodeFn g_encode;
 
 template <bool BF, int NQ, int DP>
 constexpr size_t smem_bytes()
 {
     using L = Layout<NQ, DP>;
-    return L::M0 + sizeof(Misc<NQ, L::NS>);
+    return L::M0 + sizeof(Misc<NQ, L::NU>);
 }
 
 template <bool BF, int NQ, int DP>
@@ -821,7 +938,7 @@ static bool allow()
                                 (int)smem_bytes<BF, NQ, DP>()) == cudaSuccess;
 }
 
-// Once per device: the kernels' shared memory, the SM count, the driver's tensor-map encoder.
+// Once per device: the kernels' shared memory, the SM count.
 static const DevInfo *device_info()
 {
     int dev = 0;
@@ -830,33 +947,16 @@ static const DevInfo *device_info()
     DevInfo &d = g_dev[dev];
     if (d.sms == 0) {
         int sms = 0;
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult how;
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &how) != cudaSuccess ||
-            how != cudaDriverEntryPointSuccess || !fn ||
             !(allow<true, 16, 64>() && allow<true, 32, 64>() && allow<true, 64, 64>() && allow<true, 16, 128>() &&
               allow<true, 32, 128>() && allow<true, 64, 128>() && allow<false, 16, 64>() && allow<false, 32, 64>() &&
               allow<false, 64, 64>() && allow<false, 16, 128>() && allow<false, 32, 128>() && allow<false, 64, 128>())) {
             cudaGetLastError();
             return nullptr;
         }
-        g_encode = reinterpret_cast<EncodeFn>(fn);
         d.sms = sms;
     }
     return &d;
-}
-
-// The cache as a matrix: a row per slot, a gather's box 64 elements of a row.
-static bool encode(CUtensorMap *map, bool bf16, const void *base, int64_t slots, int64_t stride, int64_t width)
-{
-    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)slots};
-    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, 1}, elem[2] = {1, 1};
-    return g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                    const_cast<void *>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Columns per CTA: the fewest of 16, 32, 64 that hold a key head's query rows, 64 at most (a
@@ -866,7 +966,7 @@ static int columns(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 constexpr size_t COUNTER_BYTES = 65536 * 4;  // the workspace's fixed region of counters
 
 template <bool BF, int NQ, int DP>
-static cudaError_t launch(const CUtensorMap &km, const CUtensorMap &vm, const Params &P, int grid, cudaStream_t s)
+static cudaError_t launch(const Params &P, int grid, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -878,20 +978,20 @@ static cudaError_t launch(const CUtensorMap &km, const CUtensorMap &vm, const Pa
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_kernel<BF, NQ, DP>, km, vm, P);
+    return cudaLaunchKernelEx(&cfg, attention_kernel<BF, NQ, DP>, P);
 }
 
 template <bool BF>
-static cudaError_t dispatch(int nq, int dp, const CUtensorMap &km, const CUtensorMap &vm, const Params &P, int grid,
+static cudaError_t dispatch(int nq, int dp, const Params &P, int grid,
                             cudaStream_t s)
 {
     if (dp == 64)
-        return nq == 16 ? launch<BF, 16, 64>(km, vm, P, grid, s)
-               : nq == 32 ? launch<BF, 32, 64>(km, vm, P, grid, s)
-                          : launch<BF, 64, 64>(km, vm, P, grid, s);
-    return nq == 16 ? launch<BF, 16, 128>(km, vm, P, grid, s)
-           : nq == 32 ? launch<BF, 32, 128>(km, vm, P, grid, s)
-                      : launch<BF, 64, 128>(km, vm, P, grid, s);
+        return nq == 16 ? launch<BF, 16, 64>(P, grid, s)
+               : nq == 32 ? launch<BF, 32, 64>(P, grid, s)
+                          : launch<BF, 64, 64>(P, grid, s);
+    return nq == 16 ? launch<BF, 16, 128>(P, grid, s)
+           : nq == 32 ? launch<BF, 32, 128>(P, grid, s)
+                      : launch<BF, 64, 128>(P, grid, s);
 }
 
 }  // namespace svatt
@@ -943,16 +1043,15 @@ extern "C" int spec_verify_attention(const void *q, int dtype, int64_t q_stride,
     if (ws_bytes < need || (uintptr_t)workspace % 256) return SPEC_VERIFY_EWORKSPACE;
     const DevInfo *dev = device_info();
     if (!dev) return SPEC_VERIFY_ECUDA;
-    CUtensorMap km, vm;
     const bool bf = dtype == SPEC_VERIFY_BF16;
-    if (!encode(&km, bf, k_cache, num_slots, k_slot_stride, kw) || !encode(&vm, bf, v_cache, num_slots, v_slot_stride, kw))
-        return SPEC_VERIFY_EINVAL;
     Params P;
     P.q = static_cast<const uint16_t *>(q);
+    P.k = static_cast<const uint16_t *>(k_cache);
     P.v = static_cast<const uint16_t *>(v_cache);
     P.out = static_cast<uint16_t *>(out);
     P.lse = lse;
     P.q_row = q_stride;
+    P.k_slot = k_slot_stride;
     P.v_slot = v_slot_stride;
     P.num_slots = num_slots;
     P.slot_table = slot_table;
@@ -977,7 +1076,7 @@ extern "C" int spec_verify_attention(const void *q, int dtype, int64_t q_stride,
     if (most < grid) grid = (int)most;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int dp = D <= 64 ? 64 : 128;
-    const cudaError_t e = bf ? dispatch<true>(nq, dp, km, vm, P, grid, s) : dispatch<false>(nq, dp, km, vm, P, grid, s);
+    const cudaError_t e = bf ? dispatch<true>(nq, dp, P, grid, s) : dispatch<false>(nq, dp, P, grid, s);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return SPEC_VERIFY_ECUDA;

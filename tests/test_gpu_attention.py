@@ -294,3 +294,20 @@ def test_refusals():
         call(make([5], 2, 4, 3, 64, BF))  # heads do not divide
     with pytest.raises(sv.SpecVerifyError):
         call(make([5], 2, 4, 2, 72, BF))
+
+
+def test_long_rows_of_empty_requests_between_others():
+    """Runs of requests without nodes (and with wrong lengths) before, between and after live ones: more
+    segments without work than any part of the kernel lists ahead."""
+    committed = [0] * 7 + [300] + [5] * 60 + [130, 1000] + [0] * 40 + [64]
+    s = make(committed, 2, 8, 8, 64, BF, seed=15)
+    nn = [2 if c in (300, 130, 1000, 64) else 0 for c in committed]
+    check(s, num_nodes=nn)
+    want = call(s, num_nodes=torch.tensor(nn, dtype=torch.int32, device=DEV))
+    nn[20] = -1
+    nn[-3] = 3
+    got = call(s, num_nodes=torch.tensor(nn, dtype=torch.int32, device=DEV))
+    bad = [20, len(nn) - 3]
+    assert torch.isnan(got.out[bad].float()).all()
+    keep = [b for b in range(len(nn)) if b not in bad]
+    assert torch.equal(got.out[keep], want.out[keep])
