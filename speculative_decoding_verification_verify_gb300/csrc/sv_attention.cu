@@ -63,9 +63,6 @@ struct Layout {
     static constexpr int HALVES = DP / 64;
     static constexpr int UNIT = TILE * DP * 2;
     static constexpr int NU = 5 * 128 / DP;
-    // Units in flight before the oldest is waited for.  Unit u's slot is freed by products that need
-    // the units up to u - NU + 1, so these must have been handed over by then: at most NU - 2.
-    static constexpr int LAG = NU - 2 < 6 ? NU - 2 : 6;
     static constexpr int QBYTES = NQ * DP * 2;
     static constexpr int QSTEP = QBYTES < 1024 ? 1024 : QBYTES;
     static constexpr int PBYTES = TILE * 128;  // a row of 64 columns per position
@@ -173,12 +170,6 @@ __device__ __forceinline__ void lengths(const Params &P, int b, int &c, int &nn)
     nn = P.num_nodes ? (SV_INB(b, P.B, 1102) ? P.num_nodes[b] : 0) : P.N;
 }
 
-template <int N>
-__device__ __forceinline__ void cp_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <bool BF, int NQ, int DP>
 __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
 {
@@ -194,7 +185,7 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
 
     if (tid == 0) {
         for (int s = 0; s < NU; ++s) {
-            tc::bar_init(tc::smem_u32(&ms.full[s]), 4);
+            tc::bar_init(tc::smem_u32(&ms.full[s]), 128);
             tc::bar_init(tc::smem_u32(&ms.empty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -279,34 +270,25 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
             // ---- tiles into shared memory -------------------------------------------------
             // A row's CPR chunks go to CPR lanes, 32 / CPR rows to a warp's copy.  A lane keeps the
             // slot of one of its warp's 32 rows; they are read one tile ahead of the copies.
-            constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI), LAG = L::LAG;
+            constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
             const int chunk = lane % CPR, sub = lane / CPR;
             const int own = warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot it keeps
             const int first = warp * RPI + sub;                                // its row of the first copy
             const uint32_t to = (chunk >> 3) * TILE * 128 + first * 128 + (((chunk & 7) ^ (first & 7)) << 4);
             const bool wide = chunk * 8 < P.D;
             Seg g = {};
-            int seg = -1, j = 0, slot = -1, u = 0, handed = 0;
+            int seg = -1, j = 0, slot = -1, u = 0;
             bool ok = true;
-            auto hand_over = [&](int to_unit) {  // the units before this one have landed
-                tc::fence_async_smem();
-                __syncwarp();
-                for (; handed < to_unit; ++handed)
-                    if (lane == 0) tc::bar_arrive(tc::smem_u32(&ms.full[handed % NU]));
-            };
-            // To the next tile, and its slot: 1, or 0 when there is none.  A segment that is not listed
-            // yet may wait for units that are still here: before waiting for it (`block`) they are handed
-            // over, and without `block` the answer is 2.
+            // To the next tile, and its slot: 1, or 0 when there is none.  A segment that is not listed yet
+            // may wait for the tile at hand: without `block` the answer is then 2.
             auto seek = [&](bool block) {
                 if (seg >= 0 && !g.kind && j + 1 < g.j1) {
                     ++j;
                 } else {
                     do {
-                        if (!__all_sync(0xffffffffu, tc::bar_test(tc::smem_u32(&ms.segfull[si % SEGS]), (si / SEGS) & 1))) {
-                            if (!block) return 2;
-                            cp_wait<0>();
-                            hand_over(u);
-                        }
+                        if (!block &&
+                            !__all_sync(0xffffffffu, tc::bar_test(tc::smem_u32(&ms.segfull[si % SEGS]), (si / SEGS) & 1)))
+                            return 2;
                         if (!take(g) || g.kind == 3) return 0;
                     } while (g.kind);
                     ++seg;
@@ -317,53 +299,56 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                 if (pos < g.c + g.nn) {
                     const int64_t at = (int64_t)g.b * P.max_pos + pos;
                     slot = SV_INB(at, (int64_t)P.B * P.max_pos, 1103) ? P.slot_table[at] : -1;
-                    if (slot < 0 || slot >= P.num_slots) {
-                        *(volatile int *)&ms.bad[0][seg % FLAGS] = 1;
-                        *(volatile int *)&ms.bad[1][seg % FLAGS] = 1;
-                        slot = -1;
-                    }
                 }
                 return 1;
             };
-            auto copy = [&](const uint16_t *base, int64_t stride, int slots) {
+            // The slot read ahead, in the pool or -1 (past the end, or wrong: its segment is marked).
+            auto check = [&](bool past) {
+                if (!past && (slot < 0 || slot >= P.num_slots)) {
+                    *(volatile int *)&ms.bad[0][seg % FLAGS] = 1;
+                    *(volatile int *)&ms.bad[1][seg % FLAGS] = 1;
+                    slot = -1;
+                }
+                return slot;
+            };
+            auto copy = [&](const unsigned char *base, uint32_t stride, int slots) {
                 if (u >= NU) {
                     const bool free = tc::bar_wait(tc::smem_u32(&ms.empty[u % NU]), (u / NU + 1) & 1, abort);
                     if (!__all_sync(0xffffffffu, free)) return false;
                 }
                 const uint32_t dst = s0 + (u % NU) * L::UNIT + to;
+                if (__all_sync(0xffffffffu, slots >= 0 && wide)) {
 #pragma unroll
-                for (int i = 0; i < ITER; ++i) {
-                    const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
-                    const uint16_t *src = s < 0 ? base : base + s * stride;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 4 * RPI * 128), "l"(src),
-                                 "r"(s >= 0 && wide ? 16 : 0)
-                                 : "memory");
+                    for (int i = 0; i < ITER; ++i) {
+                        const uint32_t s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 4 * RPI * 128),
+                                     "l"(base + (uint64_t)s * stride)
+                                     : "memory");
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < ITER; ++i) {  // zeros where there is nothing to copy
+                        const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 4 * RPI * 128),
+                                     "l"(s < 0 ? base : base + (uint64_t)(uint32_t)s * stride), "r"(s >= 0 && wide ? 16 : 0)
+                                     : "memory");
+                    }
                 }
-                asm volatile("cp.async.commit_group;" ::: "memory");
+                // The unit's barrier hears of each thread's copies as they land; nobody waits for them here.
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&ms.full[u % NU]))
+                             : "memory");
                 ++u;
-                if (u - handed > LAG) {
-                    cp_wait<LAG>();
-                    hand_over(u - LAG);
-                }
                 return true;
             };
             for (int found = seek(true); found == 1 && ok;) {
-                const int slots = slot;
+                const int slots = check(j * TILE + own >= g.c + g.nn);
                 const int64_t at = (int64_t)g.h * P.D + (wide ? chunk * 8 : 0);
                 found = seek(false);
-                ok = copy(P.k + at, P.k_slot, slots) && copy(P.v + at, P.v_slot, slots);
+                ok = copy(reinterpret_cast<const unsigned char *>(P.k + at), (uint32_t)P.k_slot * 2, slots) &&
+                     copy(reinterpret_cast<const unsigned char *>(P.v + at), (uint32_t)P.v_slot * 2, slots);
                 if (found == 2 && ok) found = seek(true);
             }
-            // The last units, each as it lands.
-            if (ok) {
-                if (LAG >= 6) cp_wait<5>(), hand_over(u - 5);
-                if (LAG >= 5) cp_wait<4>(), hand_over(u - 4);
-                if (LAG >= 4) cp_wait<3>(), hand_over(u - 3);
-                if (LAG >= 3) cp_wait<2>(), hand_over(u - 2);
-                if (LAG >= 2) cp_wait<1>(), hand_over(u - 1);
-            }
-            cp_wait<0>();
-            if (ok) hand_over(u);
+            asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp == 4) {
             // ---- products ------------------------------------------------------------------
             constexpr uint32_t ID_S = tc::instr_desc(BF, false, false, 128, NQ);
@@ -382,10 +367,16 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
             auto weigh = [&] {  // O^T (+)= V^T P^T of tile wk
                 const int u = 2 * wk + 1;
                 tc::fence_after();
+                tc::fence_async_smem();  // the copies are ordinary writes; this thread has seen them land
                 const uint64_t a = vd + (uint64_t)((u % NU) * (L::UNIT >> 4));
+                if (wsteps == 8) {  // straight-line code for whole tiles
+                    tc::mma_f16(tmem + 2 * NQ, a, pd, ID_O, !wstart);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < wsteps) tc::mma_f16(tmem + 2 * NQ, a + i * 128, pd + i * 128, ID_O, !wstart || i > 0);
+                    for (int i = 1; i < 8; ++i) tc::mma_f16(tmem + 2 * NQ, a + i * 128, pd + i * 128, ID_O, true);
+                } else {
+                    for (int i = 0; i < wsteps; ++i)
+                        tc::mma_f16(tmem + 2 * NQ, a + i * 128, pd + i * 128, ID_O, !wstart || i > 0);
+                }
                 tc::commit(tc::smem_u32(&ms.empty[u % NU]));
                 tc::commit(tc::smem_u32(&ms.pvdone));
                 ++wk;
@@ -397,7 +388,8 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                 *abort = 1;
                 return true;
             };
-            while (lane == 0) {
+            const bool me = tc::elect();
+            while (me) {
                 begin = clock64();
                 while (ok && !tc::bar_test(tc::smem_u32(&ms.segfull[si % SEGS]), (si / SEGS) & 1)) {
                     if (wk < k && ready_p()) weigh();
@@ -420,13 +412,19 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                             tc::bar_test(tc::smem_u32(&ms.qfull[seg & 1]), (seg >> 1) & 1) &&
                             (k < 2 || tc::bar_test(tc::smem_u32(&ms.sempty[sb]), ((k >> 1) & 1) ^ 1))) {
                             tc::fence_after();
+                            tc::fence_async_smem();
                             const uint64_t a = kd + (uint64_t)((u % NU) * (L::UNIT >> 4));
                             const uint64_t b = qd + (uint64_t)((seg & 1) * (L::QSTEP >> 4));
+                            if (dsteps == DP / 16) {
 #pragma unroll
-                            for (int d = 0; d < DP / 16; ++d)
-                                if (d < dsteps)
+                                for (int d = 0; d < DP / 16; ++d)
                                     tc::mma_f16(tmem + sb * NQ, a + (d >> 2) * (TILE * 8) + (d & 3) * 2,
                                                 b + (d >> 2) * (NQ * 8) + (d & 3) * 2, ID_S, d > 0);
+                            } else {
+                                for (int d = 0; d < dsteps; ++d)
+                                    tc::mma_f16(tmem + sb * NQ, a + (d >> 2) * (TILE * 8) + (d & 3) * 2,
+                                                b + (d >> 2) * (NQ * 8) + (d & 3) * 2, ID_S, d > 0);
+                            }
                             tc::commit(tc::smem_u32(&ms.empty[u % NU]));
                             tc::commit(tc::smem_u32(&ms.sfull[sb]));
                             if (j + 1 == g.j1) tc::commit(tc::smem_u32(&ms.qempty[seg & 1]));
@@ -446,7 +444,7 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                 if (!ok) break;
             }
             begin = clock64();
-            while (lane == 0 && ok && wk < k) {
+            while (me && ok && wk < k) {
                 if (ready_p()) weigh();
                 ok = !late();
             }
@@ -1034,7 +1032,8 @@ extern "C" int spec_verify_attention(const void *q, int dtype, int64_t q_stride,
     const size_t need = spec_verify_attention_workspace_bytes(B, N, Hq, Hkv, D, max_pos);
     if (!need || num_slots < 1 || num_slots > 0x7fffffff || !(scale > 0.f) || scale > 3e38f) return SPEC_VERIFY_EINVAL;
     const int64_t qw = (int64_t)Hq * D, kw = (int64_t)Hkv * D;
-    if (q_stride % 8 || k_slot_stride % 8 || v_slot_stride % 8 || q_stride < qw || k_slot_stride < kw || v_slot_stride < kw)
+    if (q_stride % 8 || k_slot_stride % 8 || v_slot_stride % 8 || q_stride < qw || k_slot_stride < kw || v_slot_stride < kw ||
+        k_slot_stride >= (1ll << 31) || v_slot_stride >= (1ll << 31))
         return SPEC_VERIFY_EINVAL;
     if (((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out) % 16) return SPEC_VERIFY_EINVAL;
     if (((uintptr_t)slot_table | (uintptr_t)committed | (uintptr_t)parents | (uintptr_t)num_nodes | (uintptr_t)lse |
