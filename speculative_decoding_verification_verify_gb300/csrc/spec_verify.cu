@@ -1699,6 +1699,7 @@ unsigned long long kv_debug_fault();
 unsigned long long budget_debug_fault();
 unsigned long long append_debug_fault();
 unsigned long long attention_debug_fault();
+unsigned long long logprobs_debug_fault();
 }  // namespace sv
 
 // The first out-of-range index the kernels met (debug builds), read and cleared across the
@@ -1713,10 +1714,12 @@ extern "C" int spec_verify_debug_fault(uint64_t *fault)
         cudaMemcpyToSymbol(sv::g_sv_debug_fault, &z, sizeof z) != cudaSuccess)
         return SPEC_VERIFY_ECUDA;
 #endif
-    const unsigned long long kv = sv::kv_debug_fault(), bu = sv::budget_debug_fault(),
-                             ap = sv::append_debug_fault(), at = sv::attention_debug_fault();
-    if (kv == ~0ull || bu == ~0ull || ap == ~0ull || at == ~0ull) return SPEC_VERIFY_ECUDA;
-    *fault = w ? w : kv ? kv : bu ? bu : ap ? ap : at;
+    for (unsigned long long x : {sv::kv_debug_fault(), sv::budget_debug_fault(), sv::append_debug_fault(),
+                                 sv::attention_debug_fault(), sv::logprobs_debug_fault()}) {
+        if (x == ~0ull) return SPEC_VERIFY_ECUDA;
+        if (!w) w = x;
+    }
+    *fault = w;
     return SPEC_VERIFY_OK;
 }
 
