@@ -7,26 +7,36 @@
 // Reading the rows once bounds it.  The rows that have a token are cut into tiles of NT * VPT 16-byte
 // vectors and every CTA takes an equal run of tiles, so few rows are spread over the GPU and absent
 // ones cost nothing; where a run cuts a row, the CTA that finishes last joins its parts in order.
+// One thread of a CTA streams its tiles through shared memory with bulk copies, STAGES of them in
+// flight across rows' ends; loads into registers, a tile ahead, gave half the bandwidth.
 //
-// Threads keep (m, Z, S) of their own; m moves only when a vector passes it by more than 8.  It is kept
+// Threads keep (m, Z, S) of their own; m moves only when a tile passes it by more than 8.  It is kept
 // as the rounded product x c, so that t is one fused operation and parts join without another rounding.
-// Alternatives: every warp keeps its best `top` logits sorted across its lanes and a vector is
-// looked at only when its maximum reaches a bound below which no alternative can lie: the least, over
-// the warps, of each warp's ceil(top / NW)-th best (together these are `top` logits that reach it).
-// A row's first tile gives the bound from the lanes' maxima, so that its logits do not all enter.
+//
+// Alternatives cost the fold one store per thread and tile: its maximum there, the maximum of a cell of VPT
+// vectors.  When a row is folded, the `top`-th best of the warps' best lane maxima bounds its `top`-th best from
+// below; only the cells that reach it, a few more than `top`, are read again (from L2) by one more warp, while
+// the others are at the next row.  (Looking for candidates while folding, behind a bound shared by the
+// warps, took twice the fold's own time, in every form tried.)
 #include "sv_ops.cuh"
+#include "sv_tc.cuh"
 
 #include <mutex>
 
 namespace svlp {
 
-constexpr int NT = 256, NW = NT / 32;
-constexpr int VPT = 4;               // 16-byte vectors per thread and tile
-constexpr int CTAS_PER_SM = 3;
-constexpr int MAX_CTAS = 1024;
+constexpr int NT = 256, NW = NT / 32;  // folding threads; one more warp copies, and one finishes rows
+constexpr int NT_ALL = NT + 64;
 constexpr int MAX_TOP = 32;
-constexpr int ROWS = 256;            // rows of its run that a CTA lists at a time
-constexpr int CAP = 512;             // candidates ranked at once
+constexpr int VPT = 4;               // 16-byte vectors per thread and tile
+constexpr int TILE_VEC = NT * VPT;
+constexpr int STAGES = 4;
+constexpr int CAP = 512;             // candidates the list holds
+constexpr int SLOTS = 16;            // cells per thread and row; longer rows have cells of several tiles
+constexpr int SAMPLE = 2 * MAX_TOP / NW;  // lane maxima of each warp that the bound comes from: 64 in all
+constexpr int CTAS_PER_SM = 2;
+constexpr int MAX_CTAS = 1024;
+constexpr int ROWS = 128;            // rows of its run that a CTA lists at a time
 constexpr float SLACK = 8.f;         // log2 of the largest term
 constexpr float LEAST = -0x1.92p99f;  // about -1e30, a bf16 value; logits below it count as it: 2^t is 0 and t stays finite
 constexpr float NEG_INF = -__builtin_huge_valf();
@@ -53,7 +63,7 @@ struct Cand {
 };
 __device__ __forceinline__ bool better(float v, int i, float ov, int oi) { return v > ov || (v == ov && i < oi); }
 
-// A part of a row: reference, sums, larger logits than the token's, whether a NaN or +inf was seen.
+// A part of a row: reference, sums, larger logits than the token's; its best, sorted.
 struct Part {
     float m, z, s;
     int count;
@@ -79,24 +89,6 @@ __device__ __forceinline__ float warp_max(float x)
     float y;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
-}
-
-__device__ __forceinline__ float4 lds_volatile(const float *p)
-{
-    float4 r;
-    asm volatile("ld.volatile.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
-                 : "r"((uint32_t)__cvta_generic_to_shared(p)));
-    return r;
-}
-
-__device__ __forceinline__ uint4 ldg_stream(const void *p)
-{
-    uint4 r;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-        : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-        : "l"(p));
-    return r;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -125,10 +117,9 @@ struct Elt<__nv_bfloat16> {
         const uint32_t m = max2(max2(w.x, w.y), max2(w.z, w.w));
         return fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
     }
-    static __device__ __forceinline__ float get(const uint4 &w, int e)
+    static __device__ __forceinline__ float get(const uint4 *v, int e)
     {
-        const uint32_t x = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
-        return __uint_as_float(e & 1 ? x & 0xffff0000u : x << 16);
+        return __uint_as_float((uint32_t) reinterpret_cast<const unsigned short *>(v)[e] << 16);
     }
     static __device__ __forceinline__ void set(uint4 &w, int e, const void *row, int64_t c)
     {
@@ -182,10 +173,7 @@ struct Elt<float> {
         return fmax_nan(fmax_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
                         fmax_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
     }
-    static __device__ __forceinline__ float get(const uint4 &w, int e)
-    {
-        return __uint_as_float(e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w);
-    }
+    static __device__ __forceinline__ float get(const uint4 *v, int e) { return reinterpret_cast<const float *>(v)[e]; }
     static __device__ __forceinline__ void set(uint4 &w, int e, const void *row, int64_t c)
     {
         (e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w) = __ldg((const unsigned *)row + c);
@@ -212,78 +200,115 @@ struct Elt<float> {
     };
 };
 
-struct Smem {
-    __align__(16) float bound[NW];  // each warp's ceil(top / NW)-th best so far
-    float m[NW], z[NW], s[NW];
-    int count[NW], scan[NW];
-    Cand list[NW * MAX_TOP];  // the warps' lists, then the ranked candidates
-    Cand cand[CAP];
-    Cand best[MAX_TOP];
-    int n, rows[ROWS], flag, join[2];
+// An entry with a row to read.
+struct Row {
+    int64_t first;  // the row's first logit
+    int r, tok;
+    float temp, x;  // x: the token's logit
 };
 
-// The best `top` of total candidates get(0 .. total - 1), sorted, into sm.best; `bound`: at least `top` of
-// them reach it (or it is -inf).  All threads of the CTA; sm.best is valid after the last barrier.
-template <typename Get>
-__device__ __forceinline__ void choose(Smem &sm, int total, int top, float bound, Get get)
+// What a row's warps share; two of them, so that the next row may begin before the last one is done.
+struct Shared {
+    __align__(16) float cell[SLOTS][NT];
+    __align__(16) float best[NW * SAMPLE];  // each warp's best lane maxima
+    float m[NW], z[NW], s[NW];
+    int count[NW];
+};
+
+// The finishing warp's.
+struct Finish {
+    Cand list[CAP + 32], top[MAX_TOP];
+    int hit[CAP], hits;
+};
+
+struct Smem {
+    uint4 ring[STAGES][TILE_VEC];
+    uint64_t full[STAGES], empty[STAGES], folded[2], freed[2];
+    Shared row[2];
+    Row rows[ROWS];
+    Finish fin;
+    int scan[NW];
+    int abort;
+};
+
+// The best `top` of fin.list[0 .. n), sorted, into fin.top, by a warp.  A candidate's place is the number
+// of better ones; their order in the list does not matter.
+__device__ __forceinline__ void rank(Finish &fin, int n, int top)
 {
-    const int tid = threadIdx.x;
-    if (tid == 0) sm.n = 0;
-    if (tid < MAX_TOP) sm.best[tid] = {NEG_INF, -1};
-    __syncthreads();
-    for (int e = tid; e < total; e += NT) {
-        const Cand x = get(e);
-        if (x.v >= bound && x.i >= 0) {
-            const int at = atomicAdd(&sm.n, 1);
-            if (at < CAP) sm.cand[at] = x;
-        }
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    fin.top[lane] = {NEG_INF, -1};
+    __syncwarp();
+    for (int e = lane; e < n; e += 32) {
+        const Cand x = fin.list[e];
+        int place = 0;
+        for (int o = 0; o < n; ++o) place += better(fin.list[o].v, fin.list[o].i, x.v, x.i);
+        if (place < top) fin.top[place] = x;
     }
-    __syncthreads();
-    const int n = sm.n;
-    if (n <= CAP) {
-        // A candidate's place is the number of better ones; their order in the list does not matter.
-        for (int e = tid; e < n; e += NT) {
-            const Cand x = sm.cand[e];
-            int place = 0;
-            for (int o = 0; o < n; ++o) place += better(sm.cand[o].v, sm.cand[o].i, x.v, x.i);
-            if (place < top) sm.best[place] = x;
-        }
-        __syncthreads();
-        return;
-    }
-    // Many equal logits: the next best, one after the other.
-    Cand last = {__builtin_huge_valf(), -1};
-    for (int k = 0; k < top; ++k) {
-        Cand b = {NEG_INF, 0x7fffffff};
-        for (int e = tid; e < total; e += NT) {
-            const Cand x = get(e);
-            if (x.i >= 0 && better(last.v, last.i, x.v, x.i) && better(x.v, x.i, b.v, b.i)) b = x;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const float v = __shfl_xor_sync(0xffffffffu, b.v, o);
-            const int i = __shfl_xor_sync(0xffffffffu, b.i, o);
-            if (better(v, i, b.v, b.i)) b = {v, i};
-        }
-        __syncthreads();
-        if (tid % 32 == 0) sm.cand[tid / 32] = b;
-        __syncthreads();
-        for (int w = 0; w < NW; ++w)
-            if (better(sm.cand[w].v, sm.cand[w].i, b.v, b.i)) b = sm.cand[w];
-        last = b;
-        if (tid == 0) sm.best[k] = b;
-    }
-    __syncthreads();
+    __syncwarp();
 }
 
-__device__ __forceinline__ int64_t run_begin(int c, int64_t total, int G) { return total * c / G; }
-__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int G) { return (int)(((x + 1) * G - 1) / total); }
+// The `top`-th best of the warps' best lane maxima: at least `top` of the row's logits reach it.
+__device__ __forceinline__ float bound_of(const Shared &sh, int top)
+{
+    const int lane = threadIdx.x & 31;
+    const float y0 = sh.best[lane], y1 = sh.best[32 + lane];
+    int p0 = 0, p1 = 0;  // places; among equals, by their order
+#pragma unroll 4
+    for (int a = 0; a < NW * SAMPLE; a += 4) {
+        const float4 o4 = *reinterpret_cast<const float4 *>(&sh.best[a]);
+        const float o[4] = {o4.x, o4.y, o4.z, o4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p0 += o[i] > y0 || (o[i] == y0 && a + i < lane);
+            p1 += o[i] > y1 || (o[i] == y1 && a + i < 32 + lane);
+        }
+    }
+    const unsigned w0 = __ballot_sync(0xffffffffu, p0 == top - 1), w1 = __ballot_sync(0xffffffffu, p1 == top - 1);
+    return __shfl_sync(0xffffffffu, w0 ? y0 : y1, __ffs(w0 | w1) - 1);
+}
+
+// The candidates of columns [from, to) of a row whose list overflowed, read again by a warp, with the
+// exact bound whenever the list is full.  They go from lower to higher tokens: one that equals the
+// `top`-th best is no candidate, and once that is the row's maximum the search is over.
+template <typename T>
+__device__ __noinline__ void list_again(const Params &P, Finish &fin, const Row &w, int64_t from, int64_t to, int top, float most)
+{
+    const int lane = threadIdx.x & 31;
+    const T *row = static_cast<const T *>(P.logits) + w.first;
+    if (from < 0) from = 0;
+    if (to > P.V) to = P.V;
+    int n = 0;
+    float bound = NEG_INF;  // NEG_INF is never a candidate
+    for (int64_t c0 = from; c0 < to && bound < most; c0 += 32) {
+        const float y = c0 + lane < to ? Elt<T>::load(row, c0 + lane) : NEG_INF;
+        const unsigned in = __ballot_sync(0xffffffffu, y > bound);
+        if ((in >> lane) & 1) fin.list[n + __popc(in & ((1u << lane) - 1))] = {y, (int)(c0 + lane)};
+        n += __popc(in);
+        if (n < CAP && !(n >= top && bound == NEG_INF)) continue;
+        rank(fin, n, top);
+        fin.list[lane] = fin.top[lane];
+        bound = fin.top[top - 1].v;
+        n = top;
+        __syncwarp();
+    }
+    rank(fin, n, top);
+}
+
+// Quotients of tile counts: in 32 bits wherever they fit, for 64-bit division is a hundred instructions.
+__device__ __noinline__ int64_t quotient64(int64_t a, int64_t b) { return a / b; }
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    return (uint64_t)(a | b) >> 32 ? quotient64(a, b) : (int64_t)((unsigned)a / (unsigned)b);
+}
+__device__ __forceinline__ int64_t run_begin(int c, int64_t total, int G) { return quotient(total * c, G); }
+__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int G) { return (int)quotient((x + 1) * G - 1, total); }
 
 // An entry's fault (a device status code), or whether it has a row to read.
 __device__ __forceinline__ int fault_of(const Params &P, int64_t r, bool &present, int &tok, int &idx, float &temp)
 {
     [[maybe_unused]] const int64_t n = (int64_t)P.B * P.T;
-    const int b = (int)(r / P.T);
+    const int b = (int)((unsigned)r / (unsigned)P.T);
     tok = SV_INB(r, n, 1201) ? P.tokens[r] : -1;
     idx = P.row_index ? (SV_INB(r, n, 1202) ? P.row_index[r] : -1) : (int)(r - (int64_t)b * P.T);
     temp = P.temperatures ? (SV_INB(b, P.B, 1203) ? P.temperatures[b] : 1.f) : P.temperature;
@@ -296,88 +321,248 @@ __device__ __forceinline__ int fault_of(const Params &P, int64_t r, bool &presen
     return code;
 }
 
-// The answers for entry r, by all threads; best: its alternatives.
+// The answers for a row's entry, by a warp; fin.top: its alternatives.
 template <typename T>
-__device__ __noinline__ void answer(const Params &P, Smem &sm, int64_t r, const void *row, int tok, float temp, float m, float z, float s,
-                       int count)
+__device__ __forceinline__ void answer(const Params &P, const Finish &fin, const Row &w, float m, float z, float s, int count)
 {
-    const int tid = threadIdx.x;
-    const float top1 = sm.best[0].v;
+    const int lane = threadIdx.x & 31;
+    const int64_t r = w.r;
+    const float temp = w.temp;
+    const T *row = static_cast<const T *>(P.logits) + w.first;
+    const float top1 = fin.top[0].v;
     const float c = 1.44269504f / temp;
     // A reference of such size is too coarse for the fused product (a row of nothing but finite masks):
     // differences are taken before the scale.
-    const bool low = sm.best[0].i >= 0 && !(fabsf(top1) * c < 1e7f);
+    const bool low = fin.top[0].i >= 0 && !(fabsf(top1) * c < 1e7f);
     if (low) {
-        float zz = 0.f, ss = 0.f;
-        for (int i = tid; i < P.V; i += NT) {
+        z = s = 0.f;
+        for (int i = lane; i < P.V; i += 32) {
             const float t = (Elt<T>::load(row, i) - top1) * c, e = ex2(t);
-            zz += e;
-            if (e > 0.f) ss += e * t;
+            z += e;
+            if (e > 0.f) s += e * t;
         }
         for (int o = 16; o; o >>= 1) {
-            zz += __shfl_xor_sync(0xffffffffu, zz, o);
-            ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+            s += __shfl_xor_sync(0xffffffffu, s, o);
         }
-        __syncthreads();
-        if (tid % 32 == 0) sm.z[tid / 32] = zz, sm.s[tid / 32] = ss;
-        __syncthreads();
-        z = s = 0.f;
-        for (int w = 0; w < NW; ++w) z += sm.z[w], s += sm.s[w];
     }
-    const bool bad = sm.best[0].i < 0 || !(z < __builtin_huge_valf());
+    const bool bad = fin.top[0].i < 0 || !(z < __builtin_huge_valf());
     const float log_z = log2f(z);
     auto said = [&](float x) {
         if (low || x < LEAST) return (x - (low ? top1 : 0.f)) / temp - log_z * 0.69314718f;
         return (fmaf(x, c, -m) - log_z) * 0.69314718f;
     };
-    if (tid == 0) {
-        P.logprobs[r] = bad ? NAN : said(Elt<T>::load(row, tok));
+    if (lane == 0) {
+        P.logprobs[r] = bad ? NAN : said(w.x);
         if (P.entropy) P.entropy[r] = bad ? NAN : fmaxf((log_z - s / z) * 0.69314718f, 0.f);
         if (P.ranks) P.ranks[r] = bad ? -1 : count + 1;
         if (bad && P.dev_status) atomicMax(P.dev_status, SPEC_VERIFY_DEV_BAD_ROW);
     }
-    if (tid < P.top) {
-        const Cand y = sm.best[tid];
-        if (SV_INB(r * P.top + tid, (int64_t)P.B * P.T * P.top, 1204)) {
-            P.top_ids[r * P.top + tid] = bad ? -1 : y.i;
-            P.top_logprobs[r * P.top + tid] = bad ? NAN : y.i < 0 ? NEG_INF : said(y.v);
+    if (lane < P.top) {
+        const Cand y = fin.top[lane];
+        if (SV_INB(r * P.top + lane, (int64_t)P.B * P.T * P.top, 1204)) {
+            P.top_ids[r * P.top + lane] = bad ? -1 : y.i;
+            P.top_logprobs[r * P.top + lane] = bad ? NAN : y.i < 0 ? NEG_INF : said(y.v);
         }
     }
 }
 
+// A row, or its part in this CTA's run (tiles [j0, j1)), is folded: by the finishing warp.  A part goes
+// to the workspace, and the warp that brings a row's last part joins them, in order.
 template <typename T>
-__global__ void __launch_bounds__(NT, CTAS_PER_SM) logprobs_kernel(const Params P)
+__device__ __forceinline__ void finish(const Params &P, Finish &fin, const Shared &sh, const Row &w, int64_t q, int64_t j0, int64_t j1,
+                                    int64_t total, int G, int top)
+{
+    const int lane = threadIdx.x & 31, cta = blockIdx.x;
+    float M = lane < NW ? sh.m[lane] : NEG_INF;
+    M = warp_max(M);
+    float z = lane < NW ? sh.z[lane] : 0.f, s = 0.f;
+    int n = lane < NW ? sh.count[lane] : 0;
+    auto sum = [&] {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            n += __shfl_xor_sync(0xffffffffu, n, o);
+        }
+    };
+    if (lane < NW && z != 0.f) {
+        const float d = M - sh.m[lane], f = ex2(-d);
+        s = f * fmaf(-d, z, sh.s[lane]);
+        z *= f;
+    }
+    sum();
+    // The logits that reach the bound, in the cells whose maxima do; then the best of them.
+    using E = Elt<T>;
+    constexpr int LOGITS = VPT * E::VEC;  // of a cell and tile: at most one per lane
+    const int head = (int)((unsigned)(w.first + P.mis) & (E::VEC - 1));
+    const T *row = static_cast<const T *>(P.logits) + w.first;
+    const float bound = bound_of(sh, top);
+    const int step = (int)(j1 - j0 + SLOTS - 1) / SLOTS, slots = (int)(j1 - j0 + step - 1) / step;
+    if (lane == 0) fin.hits = 0;
+    __syncwarp();
+#pragma unroll 4
+    for (int c = lane * 4; c < slots * NT; c += 128) {
+        const float4 y = *reinterpret_cast<const float4 *>(&sh.cell[0][0] + c);
+        if (fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)) >= bound) {
+            const float e[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (e[i] >= bound && e[i] > NEG_INF) {
+                    const int at = atomicAdd(&fin.hits, 1);
+                    if (at < CAP) fin.hit[at] = c + i;
+                }
+        }
+    }
+    __syncwarp();
+    const int hits = fin.hits;
+    int listed = hits > CAP ? CAP + 1 : 0;
+    // A lane works out a cell's place, then all lanes read the cells' logits, FLY cells in flight.
+    constexpr int FLY = 8;
+    const unsigned off = (unsigned)((lane / E::VEC) * NT * E::VEC + lane % E::VEC);
+    for (int e0 = 0; e0 < hits * step && listed <= CAP; e0 += 32) {
+        unsigned place = 1u << 31;  // past every row
+        if (e0 + lane < hits * step) {
+            const int cell = fin.hit[step == 1 ? e0 + lane : (e0 + lane) / step];
+            const int64_t j = j0 + (int64_t)(cell / NT) * step + (step == 1 ? 0 : (e0 + lane) % step);
+            if (j < j1) place = (unsigned)((j * TILE_VEC + cell % NT) * E::VEC - head);
+        }
+        const int cells = hits * step - e0 < 32 ? hits * step - e0 : 32;
+        for (int a0 = 0; a0 < cells; a0 += FLY) {
+            float y[FLY];
+            unsigned col[FLY];
+#pragma unroll
+            for (int a = 0; a < FLY; ++a) {
+                col[a] = __shfl_sync(0xffffffffu, place, a0 + a) + off;
+                const bool in = col[a] < (unsigned)P.V && lane < LOGITS;
+                y[a] = E::load(row, in ? col[a] : 0);
+                if (!in) y[a] = NEG_INF;
+            }
+#pragma unroll
+            for (int a = 0; a < FLY; ++a) {
+                const unsigned in = __ballot_sync(0xffffffffu, y[a] >= bound && y[a] > NEG_INF);
+                if (in && listed <= CAP) {
+                    if ((in >> lane) & 1) fin.list[listed + __popc(in & ((1u << lane) - 1))] = {y[a], (int)col[a]};
+                    listed += __popc(in);
+                }
+            }
+        }
+    }
+    if (listed > CAP) list_again<T>(P, fin, w, j0 * TILE_VEC * E::VEC - head, j1 * TILE_VEC * E::VEC - head, top, bound_of(sh, 1));
+    else rank(fin, listed, top);
+    if (j0 == 0 && j1 == P.tpr) {
+        answer<T>(P, fin, w, M, z, s, n);
+        return;
+    }
+    const int c0 = cta_of(q * P.tpr, total, G), c1 = cta_of((q + 1) * P.tpr - 1, total, G);
+    const bool first0 = run_begin(c0, total, G) == q * P.tpr;
+    auto part_of = [&](int x) { return reinterpret_cast<Part *>(P.parts) + 2 * x + (x == c0 && !first0); };
+    Part *part = part_of(cta);
+    if (lane == 0) part->m = M, part->z = z, part->s = s, part->count = n;
+    if (lane < top) part->top[lane] = fin.top[lane];
+    __threadfence();
+    __syncwarp();
+    bool last = false;
+    if (lane == 0) {
+        last = atomicAdd(&P.counters[c0], 1u) == (unsigned)(c1 - c0);
+        if (last) P.counters[c0] = 0;
+    }
+    if (!__any_sync(0xffffffffu, last)) return;
+    __threadfence();
+    M = NEG_INF;
+    float floor_ = NEG_INF;  // `top` logits reach the largest of the parts' `top`-th best
+    for (int x = c0 + lane; x <= c1; x += 32) {
+        M = fmaxf(M, __ldcg(&part_of(x)->m));
+        floor_ = fmaxf(floor_, __ldcg(&part_of(x)->top[top - 1].v));
+    }
+    M = warp_max(M);
+    floor_ = warp_max(floor_);
+    z = s = 0.f;
+    n = 0;
+    for (int x = c0 + lane; x <= c1; x += 32) {
+        const Part *p = part_of(x);
+        const float pz = __ldcg(&p->z);
+        n += __ldcg(&p->count);
+        if (pz != 0.f) {
+            const float d = M - __ldcg(&p->m), f = ex2(-d);
+            s += f * fmaf(-d, pz, __ldcg(&p->s));
+            z += f * pz;
+        }
+    }
+    sum();
+    int have = 0;
+    for (int x0 = c0; x0 <= c1; x0 += 8) {
+        int2 y[8];
+#pragma unroll
+        for (int a = 0; a < 8; ++a)
+            y[a] = x0 + a <= c1 && lane < top ? __ldcg(reinterpret_cast<const int2 *>(&part_of(x0 + a)->top[lane]))
+                                              : make_int2(0, -1);
+#pragma unroll
+        for (int a = 0; a < 8; ++a) {
+            const unsigned in = __ballot_sync(0xffffffffu, y[a].y >= 0 && __int_as_float(y[a].x) >= floor_);
+            if ((in >> lane) & 1) fin.list[have + __popc(in & ((1u << lane) - 1))] = {__int_as_float(y[a].x), y[a].y};
+            have += __popc(in);
+            if (have > CAP) {  // many equal logits
+                rank(fin, have, top);
+                if (lane < top) fin.list[lane] = fin.top[lane];
+                have = top;
+                __syncwarp();
+            }
+        }
+    }
+    rank(fin, have, top);
+    answer<T>(P, fin, w, M, z, s, n);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Params P)
 {
     using E = Elt<T>;
     constexpr int VEC = E::VEC;
-    __shared__ Smem sm;
+    extern __shared__ __align__(16) unsigned char smem[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
     const int top = P.top > 0 ? P.top : 1;  // the best one is the row's maximum
-    const int quota = (top + NW - 1) / NW;
-    if (tid < 2) sm.join[tid] = -1;
+    volatile int *abort = &sm.abort;
+    if (tid == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            tc::bar_init(tc::smem_u32(&sm.full[i]), 1);
+            tc::bar_init(tc::smem_u32(&sm.empty[i]), NW);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(tc::smem_u32(&sm.folded[i]), NW);
+            tc::bar_init(tc::smem_u32(&sm.freed[i]), 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sm.abort = 0;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // The entries that have a row; what the others answer is written here, each by one CTA.
     const int64_t R = (int64_t)P.B * P.T;
     const int64_t per = (R + NT - 1) / NT;
-    const int64_t w0 = run_begin(cta, R, gridDim.x), w1 = run_begin(cta + 1, R, gridDim.x);
     int mine = 0;
-    for (int64_t r = tid * per; r < (tid + 1) * per && r < R; ++r) {
-        bool present;
-        int tok, idx;
-        float temp;
-        const int code = fault_of(P, r, present, tok, idx, temp);
-        mine += present;
-        if (!present && r >= w0 && r < w1) {
-            P.logprobs[r] = code ? NAN : 0.f;
-            if (P.entropy) P.entropy[r] = code ? NAN : 0.f;
-            if (P.ranks) P.ranks[r] = code ? -1 : 0;
-            for (int k = 0; k < P.top; ++k) {
-                P.top_ids[r * P.top + k] = -1;
-                P.top_logprobs[r * P.top + k] = code ? NAN : NEG_INF;
+    unsigned long long which = 0;  // of the thread's first 64 entries
+    if (tid < NT) {
+        for (int64_t i = 0; i < per && tid * per + i < R; ++i) {
+            const int64_t r = tid * per + i;
+            bool present;
+            int tok, idx;
+            float temp;
+            const int code = fault_of(P, r, present, tok, idx, temp);
+            mine += present;
+            if (i < 64) which |= (unsigned long long)present << i;
+            if (!present && (unsigned)r % gridDim.x == (unsigned)cta) {
+                P.logprobs[r] = code ? NAN : 0.f;
+                if (P.entropy) P.entropy[r] = code ? NAN : 0.f;
+                if (P.ranks) P.ranks[r] = code ? -1 : 0;
+                for (int k = 0; k < P.top; ++k) {
+                    P.top_ids[r * P.top + k] = -1;
+                    P.top_logprobs[r * P.top + k] = code ? NAN : NEG_INF;
+                }
+                if (code && P.dev_status) atomicMax(P.dev_status, code);
             }
-            if (code && P.dev_status) atomicMax(P.dev_status, code);
         }
     }
     int incl = mine;
@@ -386,7 +571,7 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) logprobs_kernel(const Params 
         const int x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
-    if (lane == 31) sm.scan[warp] = incl;
+    if (lane == 31 && warp < NW) sm.scan[warp] = incl;
     __syncthreads();
     int64_t before = incl - mine, nrows = 0;
     for (int w = 0; w < NW; ++w) {
@@ -397,103 +582,160 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) logprobs_kernel(const Params 
     const int G = total < (int64_t)gridDim.x ? (int)total : (int)gridDim.x;
     if (cta >= G) return;
     const int64_t t0 = run_begin(cta, total, G), t1 = run_begin(cta + 1, total, G);
-    const int64_t row_first = t0 / P.tpr, row_last = (t1 - 1) / P.tpr;
+    const int64_t row_first = quotient(t0, P.tpr), row_last = quotient(t1 - 1, P.tpr);
+    const uintptr_t base_addr = reinterpret_cast<uintptr_t>(P.logits);
+    const uintptr_t end_addr = base_addr + (uintptr_t)P.B * P.rows * P.V * sizeof(T);
+    const uintptr_t copy_from = (base_addr + 15) & ~(uintptr_t)15, copy_to = end_addr & ~(uintptr_t)15;
 
+    int k = 0, rr = 0;  // tiles copied or folded; rows folded
     for (int64_t base = row_first; base <= row_last; base += ROWS) {
         // Entries of the run's next rows.
-        __syncthreads();
-        if (before + mine > base && before < base + ROWS) {
+        if (base > row_first) __syncthreads();
+        if (mine && before + mine > base && before < base + ROWS) {
             int64_t at = before;
-            for (int64_t r = tid * per; r < (tid + 1) * per && r < R && at < base + ROWS; ++r) {
-                bool present;
-                int tok, idx;
-                float temp;
-                fault_of(P, r, present, tok, idx, temp);
+            for (int64_t i = 0; i < per && tid * per + i < R && at < base + ROWS; ++i) {
+                const int64_t r = tid * per + i;
+                bool present = (which >> (i & 63)) & 1;
+                if (i >= 64) {
+                    int tok, idx;
+                    float temp;
+                    fault_of(P, r, present, tok, idx, temp);
+                }
                 if (!present) continue;
-                if (at >= base) sm.rows[at - base] = (int)r;
+                if (at >= base) {
+                    int tok, idx;
+                    float temp;
+                    fault_of(P, r, present, tok, idx, temp);
+                    Row &w = sm.rows[at - base];
+                    w.first = ((int64_t)((unsigned)r / (unsigned)P.T) * P.rows + idx) * P.V;
+                    w.r = (int)r;
+                    w.tok = tok;
+                    w.temp = temp;
+                }
                 ++at;
             }
         }
         __syncthreads();
-        for (int64_t q = base; q < base + ROWS && q <= row_last; ++q) {
-            const int64_t r = sm.rows[q - base];
-            bool present;
-            int tok, idx;
-            float temp;
-            fault_of(P, r, present, tok, idx, temp);
-            const int64_t rowf = ((r / P.T) * P.rows + idx) * P.V;
+        if (warp == NW) {
+            // ---- copies ------------------------------------------------------------------------
+            if (lane == 0)
+                for (int64_t q = base; q < base + ROWS && q <= row_last; ++q) {
+                    bool ok = true;
+                    const int64_t rowf = sm.rows[q - base].first;
+                    const int head = (int)((unsigned)(rowf + P.mis) & (VEC - 1));
+                    const int nvec = (int)(((unsigned)P.V + head + VEC - 1) / VEC);
+                    const int64_t j0 = q == row_first ? t0 - q * P.tpr : 0, j1 = q == row_last ? t1 - q * P.tpr : P.tpr;
+                    const uintptr_t first = base_addr + (uintptr_t)(rowf - head) * sizeof(T);  // may lie before the logits
+                    for (int64_t j = j0; j < j1; ++j, ++k) {
+                        const int s = k % STAGES;
+                        if (k >= STAGES)
+                            ok = tc::bar_wait(tc::smem_u32(&sm.empty[s]), (k / STAGES + 1) & 1, abort);
+                        if (!ok) break;
+                        const uintptr_t t = first + (uintptr_t)j * TILE_VEC * 16;
+                        uintptr_t a = t, z = t + TILE_VEC * 16;
+                        if (z > first + (uintptr_t)nvec * 16) z = first + (uintptr_t)nvec * 16;
+                        if (a < copy_from) a = copy_from;  // vectors that the logits do not fill are not copied
+                        if (z > copy_to) z = copy_to;
+                        const uint32_t bytes = z > a ? (uint32_t)(z - a) : 0, bar = tc::smem_u32(&sm.full[s]);
+                        tc::bar_expect(bar, bytes);
+                        if (bytes)
+                            asm volatile(
+                                "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                    tc::smem_u32(sm.ring[s]) + (uint32_t)(a - t)),
+                                "l"(a), "r"(bytes), "r"(bar)
+                                : "memory");
+                    }
+                    if (!ok) break;
+                }
+            __syncwarp();
+            continue;
+        }
+        if (warp > NW) {
+            // ---- rows that are folded ----------------------------------------------------------
+            for (int64_t q = base; q < base + ROWS && q <= row_last; ++q, ++rr) {
+                Row w = sm.rows[q - base];
+                if (SV_INB(w.first + w.tok, (int64_t)P.B * P.rows * P.V, 1206))
+                    w.x = E::load(static_cast<const T *>(P.logits) + w.first, w.tok);
+                const bool ok = tc::bar_wait(tc::smem_u32(&sm.folded[rr & 1]), (rr / 2) & 1, abort);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                finish<T>(P, sm.fin, sm.row[rr & 1], w, q, q == row_first ? t0 - q * P.tpr : 0,
+                          q == row_last ? t1 - q * P.tpr : P.tpr, total, G, top);
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(tc::smem_u32(&sm.freed[rr & 1]));
+            }
+            continue;
+        }
+        // ---- folds -----------------------------------------------------------------------------
+        for (int64_t q = base; q < base + ROWS && q <= row_last; ++q, ++rr) {
+            const int64_t rowf = sm.rows[q - base].first;
+            const float temp = sm.rows[q - base].temp;
             const T *row = static_cast<const T *>(P.logits) + rowf;
-            const int head = (int)((rowf + P.mis) % VEC);  // the row's first element in its first vector
-            const int nvec = (int)(((int64_t)head + P.V + VEC - 1) / VEC);
+            const int head = (int)((unsigned)(rowf + P.mis) & (VEC - 1));  // the row's first element in its first vector
+            const int nvec = (int)(((unsigned)P.V + head + VEC - 1) / VEC);
             const int64_t j0 = q == row_first ? t0 - q * P.tpr : 0, j1 = q == row_last ? t1 - q * P.tpr : P.tpr;
+            const int step = (int)(j1 - j0 + SLOTS - 1) / SLOTS;
             const float c = 1.44269504f / temp;
             const uint64_t c2 = sv::f2(c, c);
+            Shared &sh = sm.row[rr & 1];
+            const float tok_x = SV_INB(rowf + sm.rows[q - base].tok, (int64_t)P.B * P.rows * P.V, 1205)
+                                    ? E::load(row, sm.rows[q - base].tok) : 0.f;
+            if (rr >= 2) tc::bar_wait(tc::smem_u32(&sm.freed[rr & 1]), (rr / 2 + 1) & 1, abort);
 
-            auto load = [&](int64_t j, uint4 (&w)[VPT]) {
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const int64_t v = (j * VPT + i) * NT + tid;
-                    const int64_t col = v * VEC - head;
-                    if (v < nvec && col >= 0 && col + VEC <= P.V) {
-                        if (SV_INB(rowf + col + VEC - 1, (int64_t)P.B * P.rows * P.V, 1205)) w[i] = ldg_stream(row + col);
-                    } else {  // the row's ends, element by element; past them -inf
-                        w[i] = make_uint4(E::NEG, E::NEG, E::NEG, E::NEG);
-                        if (v < nvec)
-                            for (int e = 0; e < VEC; ++e)
-                                if (col + e >= 0 && col + e < P.V) E::set(w[i], e, row, col + e);
-                    }
-                }
-            };
             float m = NEG_INF, limit = 0.1f * LEAST;  // reference; the value that moves it
             uint64_t nmc2 = sv::f2(LEAST, LEAST), z2[2] = {0, 0}, s2[2] = {0, 0};
-            float lv = NEG_INF;  // lane k: the warp's k-th best
-            int li = 0x7fffffff;
+            float best = NEG_INF, cell = NEG_INF;  // the lane's maximum: of the row, of the cell
+            int slot = 0, left = step;
             typename E::Count count;
-            uint4 w[VPT], next[VPT];
-            load(j0, w);
-            count.start(E::load(row, tok));
-            float bound = NEG_INF;
-            {
-                // The bound from the first tile's maxima.
-                float x = NEG_INF;
+            count.start(tok_x);
+            for (int64_t j = j0; j < j1; ++j, ++k) {
+                const int st = k % STAGES;
+                tc::bar_wait(tc::smem_u32(&sm.full[st]), (k / STAGES) & 1, abort);
+                uint4 x4[VPT];
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) x = fmaxf(x, E::vmax(w[i]));
-                float y = NEG_INF;
-                for (int k = 0; k < quota; ++k) {
-                    y = warp_max(x);
-                    const unsigned who = __ballot_sync(0xffffffffu, x == y);
-                    if (lane == __ffs(who) - 1) x = NEG_INF;
+                for (int i = 0; i < VPT; ++i) x4[i] = sm.ring[st][i * NT + tid];
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(tc::smem_u32(&sm.empty[st]));
+                if (j == 0 || (j + 1) * TILE_VEC >= nvec) {
+                    // The row's ends: what lies outside counts as -inf; a vector that the logits do not fill
+                    // was not copied.
+#pragma unroll
+                    for (int i = 0; i < VPT; ++i) {
+                        const int v = (int)(j * TILE_VEC) + i * NT + tid;
+                        const int64_t col = (int64_t)v * VEC - head;
+                        if (col >= 0 && col + VEC <= P.V) continue;
+                        x4[i] = make_uint4(E::NEG, E::NEG, E::NEG, E::NEG);
+                        if (v < nvec)
+                            for (int e = 0; e < VEC; ++e)
+                                if (col + e >= 0 && col + e < P.V) E::set(x4[i], e, row, col + e);
+                    }
                 }
-                __syncthreads();  // the row before has been read to its end
-                if (lane == 0) sm.bound[warp] = y;
-                __syncthreads();
-            }
-            for (int64_t j = j0; j < j1; ++j) {
-                if (j + 1 < j1) load(j + 1, next);
+                float tm = NEG_INF;
 #pragma unroll
-                for (int k = 0; k < NW; k += 4) {
-                    const float4 y = lds_volatile(&sm.bound[k]);
-                    const float l = fminf(fminf(y.x, y.y), fminf(y.z, y.w));
-                    bound = k == 0 ? l : fminf(bound, l);
+                for (int i = 0; i < VPT; ++i) tm = fmaxf(tm, E::vmax(x4[i]));
+                best = fmaxf(best, tm);
+                cell = fmaxf(cell, tm);
+                if (--left == 0 || j + 1 == j1) {
+                    sh.cell[slot++][tid] = cell;
+                    cell = NEG_INF;
+                    left = step;
+                }
+                if (tm > limit) {
+                    // A new reference: 2^-d of the sums, t of every term less by d.
+                    const float now = tm * c, d = m == NEG_INF ? 0.f : now - m, f = ex2(-d);
+                    float2 za = sv::f2_split(z2[0]), zb = sv::f2_split(z2[1]);
+                    float2 sa = sv::f2_split(s2[0]), sb = sv::f2_split(s2[1]);
+                    s2[0] = sv::f2(f * fmaf(-d, za.x, sa.x), f * fmaf(-d, za.y, sa.y));
+                    s2[1] = sv::f2(f * fmaf(-d, zb.x, sb.x), f * fmaf(-d, zb.y, sb.y));
+                    z2[0] = sv::f2(f * za.x, f * za.y);
+                    z2[1] = sv::f2(f * zb.x, f * zb.y);
+                    m = now;
+                    limit = fmaf(SLACK * 0.69314718f, temp, tm);
+                    nmc2 = sv::f2(-now, -now);
                 }
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
-                    const float vm = E::vmax(w[i]);
-                    if (vm > limit) {
-                        // A new reference: 2^-d of the sums, t of every term less by d.
-                        const float now = vm * c, d = m == NEG_INF ? 0.f : now - m, f = ex2(-d);
-                        float2 z0 = sv::f2_split(z2[0]), z1 = sv::f2_split(z2[1]);
-                        float2 s0 = sv::f2_split(s2[0]), s1 = sv::f2_split(s2[1]);
-                        s2[0] = sv::f2(f * fmaf(-d, z0.x, s0.x), f * fmaf(-d, z0.y, s0.y));
-                        s2[1] = sv::f2(f * fmaf(-d, z1.x, s1.x), f * fmaf(-d, z1.y, s1.y));
-                        z2[0] = sv::f2(f * z0.x, f * z0.y);
-                        z2[1] = sv::f2(f * z1.x, f * z1.y);
-                        m = now;
-                        limit = fmaf(SLACK * 0.69314718f, temp, vm);
-                        nmc2 = sv::f2(-now, -now);
-                    }
                     uint64_t x[VEC / 2];
-                    E::pairs(w[i], x);
+                    E::pairs(x4[i], x);
 #pragma unroll
                     for (int e = 0; e < VEC / 2; ++e) {
                         const uint64_t t = sv::f2_fma(x[e], c2, nmc2);
@@ -502,45 +744,13 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) logprobs_kernel(const Params 
                         z2[e & 1] = sv::f2_add(z2[e & 1], p);
                         s2[e & 1] = sv::f2_fma(p, t, s2[e & 1]);
                     }
-                    count.add(w[i]);
-                    // Candidates of this warp's 32 vectors.
-                    unsigned who = __ballot_sync(0xffffffffu, vm >= bound && vm > NEG_INF);
-                    if (who) {
-                        do {
-                            const int src = __ffs(who) - 1;
-                            who &= who - 1;
-                            uint4 u;
-                            u.x = __shfl_sync(0xffffffffu, w[i].x, src);
-                            u.y = __shfl_sync(0xffffffffu, w[i].y, src);
-                            u.z = __shfl_sync(0xffffffffu, w[i].z, src);
-                            u.w = __shfl_sync(0xffffffffu, w[i].w, src);
-                            const int col = (int)(((j * VPT + i) * NT + warp * 32 + src) * VEC) - head;
-                            const float mv = E::get(u, lane & (VEC - 1));
-                            const float last = __shfl_sync(0xffffffffu, lv, top - 1);
-                            unsigned in = __ballot_sync(0xffffffffu, lane < VEC && mv >= bound && mv >= last && mv > NEG_INF);
-                            while (in) {
-                                const int e = __ffs(in) - 1;
-                                in &= in - 1;
-                                const float v = __shfl_sync(0xffffffffu, mv, e);
-                                const int place = __popc(__ballot_sync(0xffffffffu, better(lv, li, v, col + e)));
-                                const float uv = __shfl_up_sync(0xffffffffu, lv, 1);
-                                const int ui = __shfl_up_sync(0xffffffffu, li, 1);
-                                if (lane > place) lv = uv, li = ui;
-                                if (lane == place) lv = v, li = col + e;
-                            }
-                        } while (who);
-                        const float own = __shfl_sync(0xffffffffu, lv, quota - 1);
-                        if (lane == 0 && own > sm.bound[warp]) *(volatile float *)&sm.bound[warp] = own;
-                        bound = fmaxf(bound, __shfl_sync(0xffffffffu, lv, top - 1));
-                    }
+                    count.add(x4[i]);
                 }
                 count.tile_done();
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) w[i] = next[i];
             }
 
-            // ---- the row's end, or the run's: join the threads ---------------------------------
-            float2 za = sv::f2_split(sv::f2_add(z2[0], z2[1])), sa = sv::f2_split(sv::f2_add(s2[0], s2[1]));
+            // ---- the row's end, or the run's: this warp's share ----------------------------------
+            const float2 za = sv::f2_split(sv::f2_add(z2[0], z2[1])), sa = sv::f2_split(sv::f2_add(s2[0], s2[1]));
             float z = za.x + za.y, s = sa.x + sa.y;
             int n = count.n;
             const float wm = warp_max(m);
@@ -557,78 +767,32 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) logprobs_kernel(const Params 
                 s += __shfl_xor_sync(0xffffffffu, s, o);
                 n += __shfl_xor_sync(0xffffffffu, n, o);
             }
-            if (lane == 0) sm.m[warp] = wm, sm.z[warp] = z, sm.s[warp] = s, sm.count[warp] = n;
-            if (lane < top) sm.list[warp * MAX_TOP + lane] = {lv, lv == NEG_INF ? -1 : li};
-            __syncthreads();
-            float M = NEG_INF;
-            for (int k = 0; k < NW; ++k) M = fmaxf(M, sm.m[k]);
-            z = s = 0.f;
-            n = 0;
-            float least = sm.bound[0];
-            for (int k = 0; k < NW; ++k) {
-                least = fminf(least, sm.bound[k]);
-                n += sm.count[k];
-                if (sm.z[k] != 0.f) {
-                    const float d = M - sm.m[k], f = ex2(-d);
-                    s += f * fmaf(-d, sm.z[k], sm.s[k]);
-                    z += f * sm.z[k];
-                }
-            }
-            choose(sm, NW * top, top, least, [&](int e) { return sm.list[(e / top) * MAX_TOP + e % top]; });
-            if (j0 == 0 && j1 == P.tpr) {
-                answer<T>(P, sm, r, row, tok, temp, M, z, s, n);
-                continue;
-            }
-            // A part: this CTA's slot of the workspace.
-            const int c0 = cta_of(q * P.tpr, total, G), c1 = cta_of((q + 1) * P.tpr - 1, total, G);
-            const bool first0 = run_begin(c0, total, G) == q * P.tpr;
-            auto part_of = [&](int x) {
-                return reinterpret_cast<Part *>(P.parts) + 2 * x + (x == c0 && !first0);
-            };
-            Part *part = part_of(cta);
-            if (tid == 0) part->m = M, part->z = z, part->s = s, part->count = n;
-            if (tid < top) part->top[tid] = sm.best[tid];
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                sm.flag = atomicAdd(&P.counters[c0], 1u) == (unsigned)(c1 - c0);
-                if (sm.flag) P.counters[c0] = 0;
-            }
-            __syncthreads();
-            if (!sm.flag) continue;
-            // The last part to be written: join them, in order.
-            __threadfence();
-            M = NEG_INF;
-            float floor_ = NEG_INF;
-            for (int x = c0 + lane; x <= c1; x += 32) {
-                M = fmaxf(M, __ldcg(&part_of(x)->m));
-                floor_ = fmaxf(floor_, __ldcg(&part_of(x)->top[top - 1].v));  // `top` logits reach the best of these
-            }
-            M = warp_max(M);
-            floor_ = warp_max(floor_);
-            z = s = 0.f;
-            n = 0;
-            for (int x = c0 + lane; x <= c1; x += 32) {
-                const Part *p = part_of(x);
-                const float pz = __ldcg(&p->z);
-                n += __ldcg(&p->count);
-                if (pz != 0.f) {
-                    const float d = M - __ldcg(&p->m), f = ex2(-d);
-                    s += f * fmaf(-d, pz, __ldcg(&p->s));
-                    z += f * pz;
-                }
-            }
 #pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                z += __shfl_xor_sync(0xffffffffu, z, o);
-                s += __shfl_xor_sync(0xffffffffu, s, o);
-                n += __shfl_xor_sync(0xffffffffu, n, o);
+            for (int a = 0; a < SAMPLE; ++a) {
+                const float y = warp_max(best);
+                const unsigned who = __ballot_sync(0xffffffffu, best == y);
+                if (lane == __ffs(who) - 1) best = NEG_INF;
+                if (lane == 0) sh.best[warp * SAMPLE + a] = y;
             }
-            choose(sm, (c1 - c0 + 1) * top, top, floor_, [&](int e) {
-                const int2 y = __ldcg(reinterpret_cast<const int2 *>(&part_of(c0 + e / top)->top[e % top]));
-                return Cand{__int_as_float(y.x), y.y};
-            });
-            answer<T>(P, sm, r, row, tok, temp, M, z, s, n);
+            if (lane == 0) {
+                sh.m[warp] = wm;
+                sh.z[warp] = z;
+                sh.s[warp] = s;
+                sh.count[warp] = n;
+            }
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(tc::smem_u32(&sm.folded[rr & 1]));
+        }
+    }
+    if (*abort && lane == 0) {
+        // A bounded wait ran out.  Copies land before the CTA ends, folded or not.
+        if (warp == NW) {
+            const int64_t begin = clock64();
+            for (int i = k > STAGES ? k - STAGES : 0; i < k; ++i)
+                while (!tc::bar_try(tc::smem_u32(&sm.full[i % STAGES]), (i / STAGES) & 1) &&
+                       clock64() - begin < tc::WAIT_CLOCKS) {}
+        } else if (P.dev_status) {
+            atomicMax(P.dev_status, SPEC_VERIFY_DEV_TIMEOUT);
         }
     }
 }
@@ -639,14 +803,22 @@ __global__ void __launch_bounds__(NT, CTAS_PER_SM) logprobs_kernel(const Params 
 static std::mutex g_mu;
 static int g_sms[64];
 
+// Once per device: the SM count, the kernels' shared memory.
 static int device_sms()
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     std::lock_guard<std::mutex> lk(g_mu);
-    if (!g_sms[dev] && cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
+    if (!g_sms[dev]) {
+        int sms = 0;
+        const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaFuncSetAttribute((const void *)logprobs_kernel<__nv_bfloat16>, attr, (int)sizeof(Smem)) != cudaSuccess ||
+            cudaFuncSetAttribute((const void *)logprobs_kernel<float>, attr, (int)sizeof(Smem)) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        g_sms[dev] = sms;
     }
     return g_sms[dev];
 }
@@ -658,7 +830,8 @@ static cudaError_t launch(const Params &P, int grid, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(NT);
+    cfg.blockDim = dim3(NT_ALL);
+    cfg.dynamicSmemBytes = sizeof(Smem);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -731,7 +904,7 @@ extern "C" int spec_verify_logprobs(const void *logits, int dtype, const int32_t
     P.top_logprobs = top_logprobs;
     P.dev_status = dev_status;
     P.mis = (int)((uintptr_t)logits % 16) / size;
-    P.tpr = (((int64_t)V + 2 * vec - 2) / vec + NT * VPT - 1) / (NT * VPT);  // wherever the row begins
+    P.tpr = (((int64_t)V + 2 * vec - 2) / vec + TILE_VEC - 1) / TILE_VEC;  // wherever the row begins
     P.counters = static_cast<unsigned *>(workspace);
     P.parts = static_cast<unsigned char *>(workspace) + COUNTER_BYTES;
     int grid = sms * CTAS_PER_SM < MAX_CTAS ? sms * CTAS_PER_SM : MAX_CTAS;
