@@ -33,6 +33,7 @@ constexpr int TILE_VEC = NT * VPT;
 constexpr int STAGES = 4;
 constexpr int CAP = 512;             // candidates the list holds
 constexpr int SLOTS = 16;            // cells per thread and row; longer rows have cells of several tiles
+static_assert(SLOTS * NT / 128 <= 32, "a bit for each of a lane's cells");
 constexpr int SAMPLE = 2 * MAX_TOP / NW;  // lane maxima of each warp that the bound comes from: 64 in all
 constexpr int CTAS_PER_SM = 2;
 constexpr int MAX_CTAS = 1024;
@@ -64,7 +65,7 @@ struct Cand {
 __device__ __forceinline__ bool better(float v, int i, float ov, int oi) { return v > ov || (v == ov && i < oi); }
 
 // A part of a row: reference, sums, larger logits than the token's; its best, sorted.
-struct Part {
+struct __align__(16) Part {
     float m, z, s;
     int count;
     Cand top[MAX_TOP];
@@ -117,9 +118,15 @@ struct Elt<__nv_bfloat16> {
         const uint32_t m = max2(max2(w.x, w.y), max2(w.z, w.w));
         return fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
     }
-    static __device__ __forceinline__ float get(const uint4 *v, int e)
+    // The vector's first logit, which is then shifted out.
+    static __device__ __forceinline__ float shift(uint4 &w)
     {
-        return __uint_as_float((uint32_t) reinterpret_cast<const unsigned short *>(v)[e] << 16);
+        const float y = __uint_as_float(w.x << 16);
+        w.x = __funnelshift_r(w.x, w.y, 16);
+        w.y = __funnelshift_r(w.y, w.z, 16);
+        w.z = __funnelshift_r(w.z, w.w, 16);
+        w.w >>= 16;
+        return y;
     }
     static __device__ __forceinline__ void set(uint4 &w, int e, const void *row, int64_t c)
     {
@@ -173,7 +180,14 @@ struct Elt<float> {
         return fmax_nan(fmax_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
                         fmax_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
     }
-    static __device__ __forceinline__ float get(const uint4 *v, int e) { return reinterpret_cast<const float *>(v)[e]; }
+    static __device__ __forceinline__ float shift(uint4 &w)
+    {
+        const float y = __uint_as_float(w.x);
+        w.x = w.y;
+        w.y = w.z;
+        w.z = w.w;
+        return y;
+    }
     static __device__ __forceinline__ void set(uint4 &w, int e, const void *row, int64_t c)
     {
         (e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w) = __ldg((const unsigned *)row + c);
@@ -218,7 +232,7 @@ struct Shared {
 // The finishing warp's.
 struct Finish {
     Cand list[CAP + 32], top[MAX_TOP];
-    int hit[CAP], hits;
+    int hit[CAP], n;
 };
 
 struct Smem {
@@ -254,7 +268,7 @@ __device__ __forceinline__ float bound_of(const Shared &sh, int top)
     const int lane = threadIdx.x & 31;
     const float y0 = sh.best[lane], y1 = sh.best[32 + lane];
     int p0 = 0, p1 = 0;  // places; among equals, by their order
-#pragma unroll 4
+#pragma unroll 1
     for (int a = 0; a < NW * SAMPLE; a += 4) {
         const float4 o4 = *reinterpret_cast<const float4 *>(&sh.best[a]);
         const float o[4] = {o4.x, o4.y, o4.z, o4.w};
@@ -304,21 +318,21 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 __device__ __forceinline__ int64_t run_begin(int c, int64_t total, int G) { return quotient(total * c, G); }
 __device__ __forceinline__ int cta_of(int64_t x, int64_t total, int G) { return (int)quotient((x + 1) * G - 1, total); }
 
-// An entry's fault (a device status code), or whether it has a row to read.
-__device__ __forceinline__ int fault_of(const Params &P, int64_t r, bool &present, int &tok, int &idx, float &temp)
+// Whether entry r has a row to read (0), nothing (-1), or a fault (a device status code).
+__device__ __forceinline__ int fault_of(const Params &P, int64_t r)
 {
     [[maybe_unused]] const int64_t n = (int64_t)P.B * P.T;
-    const int b = (int)((unsigned)r / (unsigned)P.T);
-    tok = SV_INB(r, n, 1201) ? P.tokens[r] : -1;
-    idx = P.row_index ? (SV_INB(r, n, 1202) ? P.row_index[r] : -1) : (int)(r - (int64_t)b * P.T);
-    temp = P.temperatures ? (SV_INB(b, P.B, 1203) ? P.temperatures[b] : 1.f) : P.temperature;
-    const int code = tok < -1 || tok >= P.V                                     ? SPEC_VERIFY_DEV_BAD_TOKEN
-                     : idx < -1 || idx >= P.rows                                ? SPEC_VERIFY_DEV_BAD_ROW
-                     : tok >= 0 && idx >= 0 && !(temp >= 0.f && temp < 3.4e38f) ? SPEC_VERIFY_DEV_BAD_ROW
-                                                                                : 0;
-    present = !code && tok >= 0 && idx >= 0;
-    if (temp == 0.f) temp = 1.f;
-    return code;
+    const int tok = SV_INB(r, n, 1201) ? P.tokens[r] : -1;
+    const int idx = P.row_index ? (SV_INB(r, n, 1202) ? P.row_index[r] : -1) : 0;
+    if (tok < -1 || tok >= P.V) return SPEC_VERIFY_DEV_BAD_TOKEN;
+    if (idx < -1 || idx >= P.rows) return SPEC_VERIFY_DEV_BAD_ROW;
+    if (tok < 0 || idx < 0) return -1;
+    if (P.temperatures) {
+        const int b = (int)((unsigned)r / (unsigned)P.T);
+        const float temp = SV_INB(b, P.B, 1203) ? P.temperatures[b] : 1.f;
+        if (!(temp >= 0.f && temp < 3.4e38f)) return SPEC_VERIFY_DEV_BAD_ROW;
+    }
+    return 0;
 }
 
 // The answers for a row's entry, by a warp; fin.top: its alternatives.
@@ -394,60 +408,78 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
     sum();
     // The logits that reach the bound, in the cells whose maxima do; then the best of them.
     using E = Elt<T>;
-    constexpr int LOGITS = VPT * E::VEC;  // of a cell and tile: at most one per lane
     const int head = (int)((unsigned)(w.first + P.mis) & (E::VEC - 1));
     const T *row = static_cast<const T *>(P.logits) + w.first;
     const float bound = bound_of(sh, top);
     const int step = (int)(j1 - j0 + SLOTS - 1) / SLOTS, slots = (int)(j1 - j0 + step - 1) / step;
-    if (lane == 0) fin.hits = 0;
-    __syncwarp();
-#pragma unroll 4
-    for (int c = lane * 4; c < slots * NT; c += 128) {
-        const float4 y = *reinterpret_cast<const float4 *>(&sh.cell[0][0] + c);
-        if (fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)) >= bound) {
-            const float e[4] = {y.x, y.y, y.z, y.w};
+    // A lane marks its cells, 4 of every 128, then all write theirs behind one another.
+    unsigned mark[4] = {0, 0, 0, 0};
+#pragma unroll 2
+    for (int c = 0; c < slots * (NT / 128); ++c) {
+        const float4 y = *reinterpret_cast<const float4 *>(&sh.cell[0][0] + c * 128 + lane * 4);
+        mark[0] |= (unsigned)(y.x >= bound && y.x > NEG_INF) << c;
+        mark[1] |= (unsigned)(y.y >= bound && y.y > NEG_INF) << c;
+        mark[2] |= (unsigned)(y.z >= bound && y.z > NEG_INF) << c;
+        mark[3] |= (unsigned)(y.w >= bound && y.w > NEG_INF) << c;
+    }
+    const int mine = __popc(mark[0]) + __popc(mark[1]) + __popc(mark[2]) + __popc(mark[3]);
+    int at = mine;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (e[i] >= bound && e[i] > NEG_INF) {
-                    const int at = atomicAdd(&fin.hits, 1);
-                    if (at < CAP) fin.hit[at] = c + i;
-                }
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += x;
+    }
+    const int hits = __shfl_sync(0xffffffffu, at, 31);
+    at -= mine;
+    if (hits <= CAP)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            while (mark[i]) {
+                fin.hit[at++] = (__ffs(mark[i]) - 1) * 128 + lane * 4 + i;
+                mark[i] &= mark[i] - 1;
+            }
+    __syncwarp();
+    // Their vectors, one per lane, FLY of them in flight: under the folding warps' streams a read takes
+    // a microsecond.  (What runs once per row is written to be short: its first run is bound by the
+    // fetching of its instructions, at some ten clocks each.)
+    constexpr int FLY = 3;
+    if (lane == 0) fin.n = hits > CAP ? CAP + 1 : 0;
+    __syncwarp();
+    const int vecs = hits > CAP ? 0 : hits * step * VPT;
+#pragma unroll 1
+    for (int e0 = 0; e0 < vecs; e0 += 32 * FLY) {
+        uint4 x[FLY];
+        int col[FLY];
+#pragma unroll
+        for (int f = 0; f < FLY; ++f) {
+            const int e = e0 + f * 32 + lane, h = e / VPT;
+            x[f] = make_uint4(E::NEG, E::NEG, E::NEG, E::NEG);
+            col[f] = 0;
+            if (e < vecs) {
+                const int cell = fin.hit[step == 1 ? h : h / step];
+                const int64_t j = j0 + (int64_t)(cell / NT) * step + (step == 1 ? 0 : h % step);
+                const int64_t at = ((j * VPT + e % VPT) * NT + cell % NT) * E::VEC - head;
+                col[f] = (int)at;
+                if (j < j1 && at >= 0 && at + E::VEC <= P.V)
+                    x[f] = __ldg(reinterpret_cast<const uint4 *>(row + at));
+                else if (j < j1)
+                    for (int i = 0; i < E::VEC; ++i)
+                        if (at + i >= 0 && at + i < P.V) E::set(x[f], i, row, at + i);
+            }
         }
+#pragma unroll
+        for (int f = 0; f < FLY; ++f)
+#pragma unroll 1
+            for (int i = 0; i < E::VEC; ++i) {
+                const float y = E::shift(x[f]);
+                if (y >= bound && y > NEG_INF) {
+                    const int at = atomicAdd(&fin.n, 1);
+                    if (at < CAP) fin.list[at] = {y, col[f] + i};
+                }
+            }
     }
     __syncwarp();
-    const int hits = fin.hits;
-    int listed = hits > CAP ? CAP + 1 : 0;
-    // A lane works out a cell's place, then all lanes read the cells' logits, FLY cells in flight.
-    constexpr int FLY = 8;
-    const unsigned off = (unsigned)((lane / E::VEC) * NT * E::VEC + lane % E::VEC);
-    for (int e0 = 0; e0 < hits * step && listed <= CAP; e0 += 32) {
-        unsigned place = 1u << 31;  // past every row
-        if (e0 + lane < hits * step) {
-            const int cell = fin.hit[step == 1 ? e0 + lane : (e0 + lane) / step];
-            const int64_t j = j0 + (int64_t)(cell / NT) * step + (step == 1 ? 0 : (e0 + lane) % step);
-            if (j < j1) place = (unsigned)((j * TILE_VEC + cell % NT) * E::VEC - head);
-        }
-        const int cells = hits * step - e0 < 32 ? hits * step - e0 : 32;
-        for (int a0 = 0; a0 < cells; a0 += FLY) {
-            float y[FLY];
-            unsigned col[FLY];
-#pragma unroll
-            for (int a = 0; a < FLY; ++a) {
-                col[a] = __shfl_sync(0xffffffffu, place, a0 + a) + off;
-                const bool in = col[a] < (unsigned)P.V && lane < LOGITS;
-                y[a] = E::load(row, in ? col[a] : 0);
-                if (!in) y[a] = NEG_INF;
-            }
-#pragma unroll
-            for (int a = 0; a < FLY; ++a) {
-                const unsigned in = __ballot_sync(0xffffffffu, y[a] >= bound && y[a] > NEG_INF);
-                if (in && listed <= CAP) {
-                    if ((in >> lane) & 1) fin.list[listed + __popc(in & ((1u << lane) - 1))] = {y[a], (int)col[a]};
-                    listed += __popc(in);
-                }
-            }
-        }
-    }
+    const int listed = fin.n;
     if (listed > CAP) list_again<T>(P, fin, w, j0 * TILE_VEC * E::VEC - head, j1 * TILE_VEC * E::VEC - head, top, bound_of(sh, 1));
     else rank(fin, listed, top);
     if (j0 == 0 && j1 == P.tpr) {
@@ -469,37 +501,49 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
     }
     if (!__any_sync(0xffffffffu, last)) return;
     __threadfence();
+    // All of a round's reads are in flight together.
+    constexpr int FLYP = 8;
+    auto best_of = [&](int x) {
+        return x <= c1 && lane < top ? __ldcg(reinterpret_cast<const int2 *>(&part_of(x)->top[lane])) : make_int2(0, -1);
+    };
+    int2 y[FLYP];
+#pragma unroll
+    for (int a = 0; a < FLYP; ++a) y[a] = best_of(c0 + a);
     M = NEG_INF;
-    float floor_ = NEG_INF;  // `top` logits reach the largest of the parts' `top`-th best
-    for (int x = c0 + lane; x <= c1; x += 32) {
-        M = fmaxf(M, __ldcg(&part_of(x)->m));
-        floor_ = fmaxf(floor_, __ldcg(&part_of(x)->top[top - 1].v));
-    }
-    M = warp_max(M);
-    floor_ = warp_max(floor_);
     z = s = 0.f;
     n = 0;
-    for (int x = c0 + lane; x <= c1; x += 32) {
-        const Part *p = part_of(x);
-        const float pz = __ldcg(&p->z);
-        n += __ldcg(&p->count);
-        if (pz != 0.f) {
-            const float d = M - __ldcg(&p->m), f = ex2(-d);
-            s += f * fmaf(-d, pz, __ldcg(&p->s));
-            z += f * pz;
+    float floor_ = NEG_INF;  // `top` logits reach the largest of the parts' `top`-th best
+    for (int x = c0 + lane; x <= c1; x += 32) {  // (a lane's parts in turn, if there are more than 32)
+        const float4 p = __ldcg(reinterpret_cast<const float4 *>(part_of(x)));
+        floor_ = fmaxf(floor_, __ldcg(&part_of(x)->top[top - 1].v));
+        n += __float_as_int(p.w);
+        if (p.y != 0.f) {
+            const float now = fmaxf(M, p.x), f0 = ex2(M - now), f1 = ex2(p.x - now);
+            s = (z == 0.f ? 0.f : f0 * fmaf(M - now, z, s)) + f1 * fmaf(p.x - now, p.y, p.z);
+            z = (z == 0.f ? 0.f : f0 * z) + f1 * p.y;
+            M = now;
+        }
+    }
+    floor_ = warp_max(floor_);
+    {
+        const float own = M;
+        M = warp_max(M);
+        if (z != 0.f) {
+            const float d = M - own, f = ex2(-d);
+            s = f * fmaf(-d, z, s);
+            z *= f;
         }
     }
     sum();
     int have = 0;
-    for (int x0 = c0; x0 <= c1; x0 += 8) {
-        int2 y[8];
+    for (int x0 = c0; x0 <= c1; x0 += FLYP) {
+        if (x0 > c0)
 #pragma unroll
-        for (int a = 0; a < 8; ++a)
-            y[a] = x0 + a <= c1 && lane < top ? __ldcg(reinterpret_cast<const int2 *>(&part_of(x0 + a)->top[lane]))
-                                              : make_int2(0, -1);
+            for (int a = 0; a < FLYP; ++a) y[a] = best_of(x0 + a);
 #pragma unroll
-        for (int a = 0; a < 8; ++a) {
+        for (int a = 0; a < FLYP; ++a) {
             const unsigned in = __ballot_sync(0xffffffffu, y[a].y >= 0 && __int_as_float(y[a].x) >= floor_);
+            if (!in) continue;
             if ((in >> lane) & 1) fin.list[have + __popc(in & ((1u << lane) - 1))] = {__int_as_float(y[a].x), y[a].y};
             have += __popc(in);
             if (have > CAP) {  // many equal logits
@@ -545,23 +589,23 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
     int mine = 0;
     unsigned long long which = 0;  // of the thread's first 64 entries
     if (tid < NT) {
+#pragma unroll 2
         for (int64_t i = 0; i < per && tid * per + i < R; ++i) {
             const int64_t r = tid * per + i;
-            bool present;
-            int tok, idx;
-            float temp;
-            const int code = fault_of(P, r, present, tok, idx, temp);
-            mine += present;
-            if (i < 64) which |= (unsigned long long)present << i;
-            if (!present && (unsigned)r % gridDim.x == (unsigned)cta) {
-                P.logprobs[r] = code ? NAN : 0.f;
-                if (P.entropy) P.entropy[r] = code ? NAN : 0.f;
-                if (P.ranks) P.ranks[r] = code ? -1 : 0;
+            const int code = fault_of(P, r);
+            if (code == 0) {
+                ++mine;
+                if (i < 64) which |= 1ull << i;
+            } else if ((unsigned)r % gridDim.x == (unsigned)cta) {
+                P.logprobs[r] = code > 0 ? NAN : 0.f;
+                if (P.entropy) P.entropy[r] = code > 0 ? NAN : 0.f;
+                if (P.ranks) P.ranks[r] = code > 0 ? -1 : 0;
+#pragma unroll 1
                 for (int k = 0; k < P.top; ++k) {
                     P.top_ids[r * P.top + k] = -1;
-                    P.top_logprobs[r * P.top + k] = code ? NAN : NEG_INF;
+                    P.top_logprobs[r * P.top + k] = code > 0 ? NAN : NEG_INF;
                 }
-                if (code && P.dev_status) atomicMax(P.dev_status, code);
+                if (code > 0 && P.dev_status) atomicMax(P.dev_status, code);
             }
         }
     }
@@ -581,8 +625,10 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
     const int64_t total = nrows * P.tpr;
     const int G = total < (int64_t)gridDim.x ? (int)total : (int)gridDim.x;
     if (cta >= G) return;
-    const int64_t t0 = run_begin(cta, total, G), t1 = run_begin(cta + 1, total, G);
-    const int64_t row_first = quotient(t0, P.tpr), row_last = quotient(t1 - 1, P.tpr);
+    // Odd lanes work on the run's end, even ones on its beginning.
+    const int64_t edge = run_begin(cta + (lane & 1), total, G) - (lane & 1), edge_row = quotient(edge, P.tpr);
+    const int64_t t0 = __shfl_sync(0xffffffffu, edge, 0), t1 = __shfl_sync(0xffffffffu, edge, 1) + 1;
+    const int64_t row_first = __shfl_sync(0xffffffffu, edge_row, 0), row_last = __shfl_sync(0xffffffffu, edge_row, 1);
     const uintptr_t base_addr = reinterpret_cast<uintptr_t>(P.logits);
     const uintptr_t end_addr = base_addr + (uintptr_t)P.B * P.rows * P.V * sizeof(T);
     const uintptr_t copy_from = (base_addr + 15) & ~(uintptr_t)15, copy_to = end_addr & ~(uintptr_t)15;
@@ -593,24 +639,19 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
         if (base > row_first) __syncthreads();
         if (mine && before + mine > base && before < base + ROWS) {
             int64_t at = before;
+#pragma unroll 1
             for (int64_t i = 0; i < per && tid * per + i < R && at < base + ROWS; ++i) {
                 const int64_t r = tid * per + i;
-                bool present = (which >> (i & 63)) & 1;
-                if (i >= 64) {
-                    int tok, idx;
-                    float temp;
-                    fault_of(P, r, present, tok, idx, temp);
-                }
-                if (!present) continue;
+                if (i < 64 ? !((which >> i) & 1) : fault_of(P, r) != 0) continue;
                 if (at >= base) {
-                    int tok, idx;
-                    float temp;
-                    fault_of(P, r, present, tok, idx, temp);
+                    const int b = (int)((unsigned)r / (unsigned)P.T);
+                    const int idx = P.row_index ? P.row_index[r] : (int)(r - (int64_t)b * P.T);
+                    const float temp = P.temperatures ? P.temperatures[b] : P.temperature;
                     Row &w = sm.rows[at - base];
-                    w.first = ((int64_t)((unsigned)r / (unsigned)P.T) * P.rows + idx) * P.V;
+                    w.first = ((int64_t)b * P.rows + idx) * P.V;
                     w.r = (int)r;
-                    w.tok = tok;
-                    w.temp = temp;
+                    w.tok = P.tokens[r];
+                    w.temp = temp == 0.f ? 1.f : temp;
                 }
                 ++at;
             }
