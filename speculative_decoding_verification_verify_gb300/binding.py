@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -579,80 +580,96 @@ class Logprobs(NamedTuple):
 
 
 _HALF = {torch.bfloat16: BF16, torch.float16: FP16}
+_INT32, _FP32 = torch.int32, torch.float32
 
 
-def _half_dtype(name: str, t: torch.Tensor) -> int:
-    code = _HALF.get(t.dtype)
+def _half_dtype(q: torch.Tensor) -> int:
+    code = _HALF.get(q.dtype)
     if code is None:
-        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
     return code
 
 
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _same(what, device: int, **tensors):
+    """What the first tensor's type and device are, the others' have to be."""
+    for name, t in tensors.items():
+        if t.dtype is not what:
+            raise TypeError(f"{name} must be {what}, got {t.dtype}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on cuda:{device}")
 
 
-def _node_rows(name: str, t: torch.Tensor, shape, like: torch.Tensor) -> int:
-    """Check [B, N, heads, D] rows whose heads are contiguous and which are evenly spaced (a view
-    into a projection's output will do); returns the elements from one row to the next."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
-    B, N, H, D = shape
+def _device_of(name: str, t: torch.Tensor) -> int:
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return device
+
+
+def _row_stride(name: str, t: torch.Tensor, B: int, N: int, H: int, D: int) -> int:
+    """Elements from one [heads, D] row of [B, N, heads, D] to the next: heads contiguous, rows evenly
+    spaced (a view into a projection's output will do)."""
     sb, sn, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}'s heads must be contiguous")
     if N == 1:
-        sn = sb if B > 1 else max(sn, H * D)
-    elif B > 1 and sb != N * sn:
+        return sb if B > 1 else max(sn, H * D)
+    if B > 1 and sb != N * sn:
         raise ValueError(f"{name}'s rows must be evenly spaced")
     return sn
 
 
-def _cache_slots(name: str, t: torch.Tensor, like: torch.Tensor) -> int:
-    """Check [num_slots, Hkv, D] with contiguous slot rows; returns the slot stride in elements."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [num_slots, Hkv, D]")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
-    S, H, D = t.shape
+def _slot_stride(name: str, t: torch.Tensor, H: int, D: int) -> int:
+    """Elements from one slot of [num_slots, Hkv, D] to the next: slots contiguous, any distance apart."""
     ss, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}'s slots must be contiguous")
-    return ss if S > 1 else max(ss, H * D)
+    return max(ss, H * D)
 
 
-def _int32_of(name: str, t: Optional[torch.Tensor], shape, device):
-    if t is None:
-        return
-    if t.dtype != torch.int32:
+def _index(name: str, t: torch.Tensor, shape, device: int) -> int:
+    """An int32 index tensor's address."""
+    if t.dtype is not _INT32:
         raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be contiguous and on {device}")
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on cuda:{device}")
+    return t.data_ptr()
 
 
-def _result(name: str, t: Optional[torch.Tensor], shape, dtype, device, stream) -> torch.Tensor:
+def _result(name: str, t: Optional[torch.Tensor], shape, dtype, device: int, stream) -> torch.Tensor:
     """A caller's output checked, or a new one that the stream's work may write."""
     if t is None:
         t = torch.empty(shape, dtype=dtype, device=device)
         if stream is not None:
             t.record_stream(stream)
-        return t
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+    elif t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{device}")
     return t
 
 
-def _status_of(dev_status, device):
-    if dev_status is not None and (dev_status.dtype != torch.int32 or dev_status.device != device):
-        raise ValueError(f"dev_status must be an int32 tensor on {device}")
+def _status(dev_status: Optional[torch.Tensor], device: int):
+    if dev_status is None:
+        return None
+    if dev_status.dtype is not _INT32 or dev_status.get_device() != device:
+        raise ValueError(f"dev_status must be an int32 tensor on cuda:{device}")
+    return dev_status.data_ptr()
+
+
+def _raw_stream(stream, device: int) -> int:
+    # (torch.cuda.current_stream builds an object for each call, a tenth of a small call's host time.)
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _workspace(nbytes: int, device: int, stream, raw: int) -> torch.Tensor:
+    """workspace_for, zero-filled on the stream that will use it."""
+    ws = _ws_cache.get((device, raw))
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.stream(stream):
+            ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        _ws_cache[device, raw] = ws
+    return ws
 
 
 def spec_verify_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -669,40 +686,38 @@ def spec_verify_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_c
     int32 (None: a chain or a prompt), num_nodes [B] int32 (None: all N).  Without dev_status,
     faults in the data show in the returned rows alone (NaN)."""
     lib = _lib or load_library()
-    code = _half_dtype("q", q)
-    if not q.is_cuda or q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q must be a [B, N, Hq, D] and k a [B, N, Hkv, D] CUDA tensor")
+    code, dt, dev = _half_dtype(q), q.dtype, _device_of("q", q)
     B, N, Hq, D = q.shape
-    Hkv, dev = k.shape[2], q.device
-    qs = _node_rows("q", q, (B, N, Hq, D), q)
-    ks = _node_rows("k", k, (B, N, Hkv, D), q)
-    vs = _node_rows("v", v, (B, N, Hkv, D), q)
-    kss = _cache_slots("k_cache", k_cache, q)
-    vss = _cache_slots("v_cache", v_cache, q)
-    slots = k_cache.shape[0]
-    if k_cache.shape[1:] != k.shape[2:] or v_cache.shape != k_cache.shape:
+    S, Hkv, _ = csh = k_cache.shape
+    if csh[2] != D or v_cache.shape != csh:
         raise ValueError("k_cache and v_cache must be [num_slots, Hkv, D]")
-    _int32_of("slot_table", slot_table, (B, slot_table.shape[-1]), dev)
-    _int32_of("committed", committed, (B,), dev)
-    _int32_of("parents", parents, (B, N), dev)
-    _int32_of("num_nodes", num_nodes, (B,), dev)
-    if cos_sin is not None and (cos_sin.dim() != 2 or cos_sin.dtype != torch.float32
-                                or not cos_sin.is_contiguous() or cos_sin.device != dev):
-        raise ValueError(f"cos_sin must be a contiguous float32 [positions, rotary_dim] tensor on {dev}")
-    _status_of(dev_status, dev)
-    q_out = _result("q_out", q_out, (B, N, Hq, D), q.dtype, dev, stream)
-    positions, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+    if k.shape != (B, N, Hkv, D) or v.shape != (B, N, Hkv, D):
+        raise ValueError(f"k and v must be {[B, N, Hkv, D]}")
+    _same(dt, dev, k=k, v=v, k_cache=k_cache, v_cache=v_cache)
+    rot_positions = rot = cs = 0
+    if cos_sin is not None:
+        if cos_sin.dtype is not _FP32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() \
+                or cos_sin.get_device() != dev:
+            raise ValueError(f"cos_sin must be a contiguous float32 [positions, rotary_dim] tensor on cuda:{dev}")
+        rot_positions, rot = cos_sin.shape
+        cs = cos_sin.data_ptr()
+    max_pos = slot_table.shape[-1]
+    q_out = _result("q_out", q_out, (B, N, Hq, D), dt, dev, stream)
     rc = lib.spec_verify_kv_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), code, qs, ks, vs, q_out.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), slots, kss, vss, slot_table.data_ptr(), slot_table.shape[1],
-        committed.data_ptr(), _addr(parents), _addr(num_nodes), _addr(cos_sin), positions, rot,
-        bool(interleaved), B, N, Hq, Hkv, D, _addr(dev_status),
-        (stream or torch.cuda.current_stream(dev)).cuda_stream)
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), code, _row_stride("q", q, B, N, Hq, D),
+        _row_stride("k", k, B, N, Hkv, D), _row_stride("v", v, B, N, Hkv, D), q_out.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), S, _slot_stride("k_cache", k_cache, Hkv, D),
+        _slot_stride("v_cache", v_cache, Hkv, D), _index("slot_table", slot_table, (B, max_pos), dev), max_pos,
+        _index("committed", committed, (B,), dev),
+        None if parents is None else _index("parents", parents, (B, N), dev),
+        None if num_nodes is None else _index("num_nodes", num_nodes, (B,), dev), cs, rot_positions, rot,
+        bool(interleaved), B, N, Hq, Hkv, D, _status(dev_status, dev), _raw_stream(stream, dev))
     if rc != OK:
         raise SpecVerifyError("spec_verify_kv_append", rc)
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def spec_verify_attention_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int, max_pos: int) -> int:
     return int(load_library().spec_verify_attention_workspace_bytes(B, N, Hq, Hkv, D, max_pos))
 
@@ -719,40 +734,33 @@ def spec_verify_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     defaults to D ** -0.5.  Returns out [B, N, Hq, D] and, when wanted or given, lse [B, N, Hq] fp32.
     Without dev_status, faults in the data show in the returned rows alone (NaN)."""
     lib = _lib or load_library()
-    code = _half_dtype("q", q)
-    if not q.is_cuda or q.dim() != 4:
-        raise ValueError("q must be a [B, N, Hq, D] CUDA tensor")
+    code, dt, dev = _half_dtype(q), q.dtype, _device_of("q", q)
     B, N, Hq, D = q.shape
-    dev = q.device
-    qs = _node_rows("q", q, (B, N, Hq, D), q)
-    kss = _cache_slots("k_cache", k_cache, q)
-    vss = _cache_slots("v_cache", v_cache, q)
-    slots, Hkv = k_cache.shape[:2]
-    if k_cache.shape[2] != D or v_cache.shape != k_cache.shape:
+    S, Hkv, _ = csh = k_cache.shape
+    if csh[2] != D or v_cache.shape != csh:
         raise ValueError("k_cache and v_cache must be [num_slots, Hkv, D]")
+    _same(dt, dev, k_cache=k_cache, v_cache=v_cache)
     max_pos = slot_table.shape[-1]
-    _int32_of("slot_table", slot_table, (B, max_pos), dev)
-    _int32_of("committed", committed, (B,), dev)
-    _int32_of("parents", parents, (B, N), dev)
-    _int32_of("num_nodes", num_nodes, (B,), dev)
-    _status_of(dev_status, dev)
-    out = _result("out", out, (B, N, Hq, D), q.dtype, dev, stream)
+    out = _result("out", out, (B, N, Hq, D), dt, dev, stream)
     if lse is not None or want_lse:
-        lse = _result("lse", lse, (B, N, Hq), torch.float32, dev, stream)
-    stream = stream or torch.cuda.current_stream(dev)
+        lse = _result("lse", lse, (B, N, Hq), _FP32, dev, stream)
+    raw = _raw_stream(stream, dev)
     if workspace is None:
-        nbytes = lib.spec_verify_attention_workspace_bytes(B, N, Hq, Hkv, D, max_pos)
-        workspace = workspace_for(nbytes, dev, stream)
+        workspace = _workspace(spec_verify_attention_workspace_bytes(B, N, Hq, Hkv, D, max_pos), dev, stream, raw)
     rc = lib.spec_verify_attention(
-        q.data_ptr(), code, qs, k_cache.data_ptr(), v_cache.data_ptr(), slots, kss, vss,
-        slot_table.data_ptr(), max_pos, committed.data_ptr(), _addr(parents), _addr(num_nodes), B, N, Hq,
-        Hkv, D, D ** -0.5 if scale is None else scale, out.data_ptr(), _addr(lse), workspace.data_ptr(),
-        workspace.numel(), _addr(dev_status), stream.cuda_stream)
+        q.data_ptr(), code, _row_stride("q", q, B, N, Hq, D), k_cache.data_ptr(), v_cache.data_ptr(), S,
+        _slot_stride("k_cache", k_cache, Hkv, D), _slot_stride("v_cache", v_cache, Hkv, D),
+        _index("slot_table", slot_table, (B, max_pos), dev), max_pos, _index("committed", committed, (B,), dev),
+        None if parents is None else _index("parents", parents, (B, N), dev),
+        None if num_nodes is None else _index("num_nodes", num_nodes, (B,), dev), B, N, Hq, Hkv, D,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _status(dev_status, dev), raw)
     if rc != OK:
         raise SpecVerifyError("spec_verify_attention", rc)
     return Attention(out, lse)
 
 
+@functools.lru_cache(maxsize=256)
 def spec_verify_logprobs_workspace_bytes(B: int, T: int, V: int, top_n: int) -> int:
     return int(load_library().spec_verify_logprobs_workspace_bytes(B, T, V, top_n))
 
@@ -766,35 +774,32 @@ def spec_verify_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, row_inde
     [B, T] int32 (a tree's accept_index; None: token t belongs to row t), temperatures [B] fp32.
     Without dev_status, faults in the data show in the returned entries alone (NaN, -1)."""
     lib = _lib or load_library()
-    _check_dev("logits", logits)
+    dev = _device_of("logits", logits)
+    if not logits.is_contiguous():
+        raise ValueError("logits must be contiguous")
     B, rows, V = logits.shape
-    dev = logits.device
     T = tokens.shape[-1]
-    _int32_of("tokens", tokens, (B, T), dev)
-    _int32_of("row_index", row_index, (B, T), dev)
-    if temperatures is not None:
-        _check_dev("temperatures", temperatures, torch.float32)
-        if tuple(temperatures.shape) != (B,) or temperatures.device != dev:
-            raise ValueError(f"temperatures must be [B] on {dev}")
-    _status_of(dev_status, dev)
-    f32, i32 = torch.float32, torch.int32
-    logprobs = _result("logprobs", logprobs, (B, T), f32, dev, stream)
-    entropy = _result("entropy", entropy, (B, T), f32, dev, stream)
-    ranks = _result("ranks", ranks, (B, T), i32, dev, stream)
+    if temperatures is not None and (temperatures.dtype is not _FP32 or temperatures.shape != (B,)
+                                     or temperatures.get_device() != dev or not temperatures.is_contiguous()):
+        raise ValueError(f"temperatures must be a contiguous float32 tensor [{B}] on cuda:{dev}")
+    logprobs = _result("logprobs", logprobs, (B, T), _FP32, dev, stream)
+    entropy = _result("entropy", entropy, (B, T), _FP32, dev, stream)
+    ranks = _result("ranks", ranks, (B, T), _INT32, dev, stream)
     if top_n:
-        top_ids = _result("top_ids", top_ids, (B, T, top_n), i32, dev, stream)
-        top_logprobs = _result("top_logprobs", top_logprobs, (B, T, top_n), f32, dev, stream)
+        top_ids = _result("top_ids", top_ids, (B, T, top_n), _INT32, dev, stream)
+        top_logprobs = _result("top_logprobs", top_logprobs, (B, T, top_n), _FP32, dev, stream)
     else:
         top_ids = top_logprobs = None
-    stream = stream or torch.cuda.current_stream(dev)
+    raw = _raw_stream(stream, dev)
     if workspace is None:
-        nbytes = lib.spec_verify_logprobs_workspace_bytes(B, T, V, top_n)
-        workspace = workspace_for(nbytes, dev, stream)
+        workspace = _workspace(spec_verify_logprobs_workspace_bytes(B, T, V, top_n), dev, stream, raw)
     rc = lib.spec_verify_logprobs(
-        logits.data_ptr(), _logits_dtype(logits), tokens.data_ptr(), _addr(row_index), B, rows, T, V,
-        _addr(temperatures), temperature, top_n, logprobs.data_ptr(), entropy.data_ptr(), ranks.data_ptr(),
-        _addr(top_ids), _addr(top_logprobs), workspace.data_ptr(), workspace.numel(), _addr(dev_status),
-        stream.cuda_stream)
+        logits.data_ptr(), _logits_dtype(logits), _index("tokens", tokens, (B, T), dev),
+        None if row_index is None else _index("row_index", row_index, (B, T), dev), B, rows, T, V,
+        None if temperatures is None else temperatures.data_ptr(), temperature, top_n, logprobs.data_ptr(),
+        entropy.data_ptr(), ranks.data_ptr(), None if top_ids is None else top_ids.data_ptr(),
+        None if top_logprobs is None else top_logprobs.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _status(dev_status, dev), raw)
     if rc != OK:
         raise SpecVerifyError("spec_verify_logprobs", rc)
     return Logprobs(logprobs, entropy, ranks, top_ids, top_logprobs)
