@@ -624,7 +624,7 @@ def _slot_stride(name: str, t: torch.Tensor, H: int, D: int) -> int:
     ss, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}'s slots must be contiguous")
-    return max(ss, H * D)
+    return ss if t.shape[0] > 1 else max(ss, H * D)
 
 
 def _index(name: str, t: torch.Tensor, shape, device: int) -> int:

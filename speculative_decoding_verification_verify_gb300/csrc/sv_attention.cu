@@ -12,9 +12,10 @@
 //   S^T [128 positions][rows] = K [128][D] . Q^T          both operands from shared memory
 //   O^T [128 dims][rows]     += V^T [dims][128] . P^T     V as it lies in the cache, read transposed
 //
-// One CTA per SM takes an equal run of the batch's tiles (a tile: 128 positions of one request and
-// key head), whatever the lengths, so one long request is split over all SMs and many short ones
-// share them; where a run cuts a request, the parts are joined by the CTA that finishes last.
+// One CTA per SM takes an equal run of the batch's work, whatever the lengths: tiles (128 positions of one
+// request and key head) at COST_TILE each and segments (a request and key head) at COST_SEGMENT for
+// their beginning and end.  So one long request is split over all SMs and many short ones share them;
+// where a run cuts a request, the parts are joined by the CTA that finishes last.
 //
 // Warps 0-3 copy tiles into a ring of K and V units, a row of 16-byte chunks per slot (gathers by
 // TMA were tried first: four 128-byte rows took 61 clocks to issue, 8 bytes per clock, where an SM's
@@ -42,6 +43,7 @@ constexpr int MAX_CTAS = 256; // parts the workspace has room for: two per CTA
 constexpr int FLAGS = 16;     // bad-slot flags: more than the segments the ring can hold
 constexpr int SEGS = 8;       // segments listed ahead
 constexpr float SLACK = 8.f;  // log2 of the largest weight
+constexpr int COST_TILE = 2, COST_SEGMENT = 4;
 
 struct Params {
     const uint16_t *q, *k, *v;
@@ -74,7 +76,7 @@ struct Layout {
 struct __align__(16) Seg {
     int b, h, qt, kind;        // kind 0: to attend; 1: no nodes; 2: lengths are wrong; 3: no more segments
     int c, nn, j0, j1;
-    int part, c0, c1, first0;  // part: the workspace part it writes (-1: it is the whole); the CTAs it spans
+    int part, c0, c1, pad;     // part: the workspace part it writes (-1: it is the whole); the CTAs it spans
 };
 
 template <int NQ, int NU>
@@ -154,15 +156,24 @@ __host__ __device__ constexpr int part_floats()
     return NQ * MAXD + 3 * NQ;
 }
 
-// The CTA whose run holds tile x, and a run's first tile.
-__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int G) { return (int)(((x + 1) * G - 1) / total); }
+// Runs are cut at multiples of total / G on the axis of costs.  A cut x into a segment of n tiles leaves the
+// tiles before `cut_tile` to the run before; cuts are at least COST_TILE apart, so no run between two
+// cuts of a segment is empty.
 __device__ __forceinline__ int64_t run_begin(int c, int64_t total, int G) { return total * c / G; }
+__device__ __forceinline__ int cut_tile(int64_t x, int n)
+{
+    const int64_t t = x - COST_SEGMENT + COST_TILE / 2;
+    return t <= 0 ? 0 : t / COST_TILE < n ? (int)(t / COST_TILE) : n;
+}
+// The last run that begins before x.
+__device__ __forceinline__ int run_before(int64_t x, int64_t total, int G) { return (int)((x * G + total - 1) / total) - 1; }
 
 __device__ __forceinline__ int kind_of(const Params &P, int c, int nn)
 {
     return nn < 0 || nn > P.N || c < 0 || (int64_t)c + nn > P.max_pos ? 2 : nn == 0 ? 1 : 0;
 }
 __device__ __forceinline__ int tiles_of(int kind, int c, int nn) { return kind ? 1 : (c + nn + TILE - 1) / TILE; }
+__device__ __forceinline__ int64_t cost_of(int tiles) { return COST_SEGMENT + (int64_t)tiles * COST_TILE; }
 
 __device__ __forceinline__ void lengths(const Params &P, int b, int &c, int &nn)
 {
@@ -210,14 +221,14 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // The batch's tiles, and the request that this CTA's run begins in.
+    // The batch's cost, and the request that this CTA's run begins in.
     const int HT = P.Hkv * P.QT;
     const int per = (P.B + NT - 1) / NT;
     int64_t mine = 0;
     for (int i = 0; i < per && tid * per + i < P.B; ++i) {
         int c, nn;
         lengths(P, tid * per + i, c, nn);
-        mine += (int64_t)tiles_of(kind_of(P, c, nn), c, nn) * HT;
+        mine += cost_of(tiles_of(kind_of(P, c, nn), c, nn)) * HT;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -232,8 +243,8 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
         if (w < warp) before += ms.scan[w];
         total += ms.scan[w];
     }
-    // Every run holds a tile: a batch of fewer tiles than CTAs leaves the last CTAs out.
-    const int G = total < (int64_t)gridDim.x ? (int)total : (int)gridDim.x;
+    // Small batches leave the last CTAs out: a run costs COST_TILE at least.
+    const int G = total / COST_TILE < (int64_t)gridDim.x ? (int)(total / COST_TILE) : (int)gridDim.x;
     const int64_t t0 = cta < G ? run_begin(cta, total, G) : total, t1 = cta < G ? run_begin(cta + 1, total, G) : total;
     if (t0 >= before && t0 < before + mine) {
         int64_t at = before;
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
         for (; b < P.B; ++b) {
             int c, nn;
             lengths(P, b, c, nn);
-            const int64_t n = (int64_t)tiles_of(kind_of(P, c, nn), c, nn) * HT;
+            const int64_t n = cost_of(tiles_of(kind_of(P, c, nn), c, nn)) * HT;
             if (t0 < at + n) break;
             at += n;
         }
@@ -454,8 +465,7 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
             // The lengths of 32 requests are read at a time.
             int b = ms.begin_b, base = b, c = 0, nn = 0, n = 0;
             if (b + lane < P.B) lengths(P, b + lane, c, nn);
-            int64_t at = t0, skip = t0 - ms.begin_base;  // tiles of the request before the run
-            int64_t rest = t1 - t0;
+            int64_t at = ms.begin_base;  // the cost before the item
             bool ok = true;
             auto put = [&](const Seg &g) {
                 if (n >= SEGS) {
@@ -471,7 +481,8 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                 return true;
             };
             Seg g = {};
-            while (rest > 0) {
+            bool first = true;
+            while (at < t1 && ok) {
                 if (b == base + 32) {
                     base = b;
                     if (b + lane < P.B) lengths(P, b + lane, c, nn);
@@ -481,34 +492,32 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                 g.nn = __shfl_sync(0xffffffffu, nn, b - base);
                 g.kind = kind_of(P, g.c, g.nn);
                 const int ntile = tiles_of(g.kind, g.c, g.nn);
-                int item = (int)(skip / ntile);
-                int j = (int)(skip - (int64_t)item * ntile);
-                skip = 0;
-                for (; item < HT && rest > 0; ++item, j = 0) {
+                const int64_t cost = cost_of(ntile);
+                int item = 0;
+                if (first) {  // items before the one that the run begins in
+                    item = (int)((t0 - at) / cost);
+                    at += item * cost;
+                    first = false;
+                }
+                for (; item < HT && at < t1 && ok; ++item, at += cost) {
                     g.h = item / P.QT;
                     g.qt = item - g.h * P.QT;
-                    g.j0 = j;
-                    g.j1 = rest < ntile - j ? j + (int)rest : ntile;
+                    g.j0 = cut_tile(t0 - at, ntile);
+                    g.j1 = cut_tile(t1 - at, ntile);
+                    if (g.j0 >= g.j1) continue;
                     g.part = -1;
-                    if (j > 0 || g.j1 < ntile) {
-                        // Its CTAs are those whose runs hold the request's tiles of this head.
-                        const int64_t ib = at - j;
-                        g.c0 = cta_of(ib, total, G);
-                        g.c1 = cta_of(ib + ntile - 1, total, G);
-                        g.first0 = run_begin(g.c0, total, G) == ib;
-                        g.part = 2 * cta + (cta == g.c0 && !g.first0);
+                    if (g.j0 > 0 || g.j1 < ntile) {
+                        // The runs that hold its first and its last tile, and all between.
+                        g.c0 = run_before(at + COST_SEGMENT + COST_TILE / 2, total, G);
+                        g.c1 = run_before(at + cost - COST_TILE / 2, total, G);
+                        g.part = 2 * cta + (cta == g.c0);
                     }
-                    at += g.j1 - j;
-                    rest -= g.j1 - j;
-                    if (!put(g)) {
-                        rest = -1;
-                        break;
-                    }
+                    put(g);
                 }
                 ++b;
             }
             g.kind = 3;
-            if (rest == 0) put(g);
+            if (ok) put(g);
         } else if (warp < 8) {
             // ---- queries and the tree's mask -----------------------------------------------
             const int t = tid - 192;
@@ -643,8 +652,9 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                     }
 #pragma unroll
                     for (int c = 0; c < CW; ++c) top = fmaxf(top, x[c]);
-                    if (group_or(bar, 128, fresh || fail || top > SLACK)) {
-                        if (group_or(bar, 128, fail)) break;
+                    // (A segment's first tile needs no vote.)
+                    if (j == g.j0 || group_or(bar, 128, fresh || fail || top > SLACK)) {
+                        if (j > g.j0 && group_or(bar, 128, fail)) break;
                         // Move the references to the columns' maxima.
                         tc::tmem_ld(lanes + sb * NQ, x);
                         tc::wait_ld(x);
@@ -707,21 +717,27 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                         // values is set aside, and its readers get it at the segment's end.
                         const int u = 2 * k + 1;
                         fail |= !tc::bar_wait(tc::smem_u32(&ms.full[u % NU]), (u / NU) & 1, abort);
-                        bool odd = false;
-                        for (int ch = wg * (DP / 16); ch < (wg + 1) * (DP / 16); ++ch) {
-                            uint4 *at = reinterpret_cast<uint4 *>(smem + (u % NU) * L::UNIT + (ch >> 3) * TILE * 128 + t * 128 +
-                                                                  (ch & 7) * 16);
-                            uint4 y = *at;
-                            uint32_t *wd = &y.x;
-                            bool mend = false;
+                        // An exponent of all ones carries into the sign's place.
+                        constexpr uint32_t EXP2 = Half2<BF>::EXP_MASK * 0x10001u;
+                        constexpr uint32_t ONE2 = (0x8000u - Half2<BF>::EXP_MASK) * 0x10001u;
+                        unsigned char *const at = smem + (u % NU) * L::UNIT + t * 128 +
+                                                  (HALVES > 1 ? wg * TILE * 128 : wg * 64);
+                        constexpr int CHS = DP / 16;
+                        uint32_t carry = 0;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if ((wd[e] & Half2<BF>::EXP_MASK) == Half2<BF>::EXP_MASK) wd[e] &= 0xffff0000u, mend = true;
-                                if (((wd[e] >> 16) & Half2<BF>::EXP_MASK) == Half2<BF>::EXP_MASK) wd[e] &= 0xffffu, mend = true;
-                            }
-                            if (mend) *at = y;
-                            odd |= mend;
+                        for (int ch = 0; ch < CHS; ++ch) {
+                            const uint4 y = *reinterpret_cast<const uint4 *>(at + ch * 16);
+                            carry |= ((y.x & EXP2) + ONE2) | ((y.y & EXP2) + ONE2) | ((y.z & EXP2) + ONE2) | ((y.w & EXP2) + ONE2);
                         }
+                        const bool odd = carry & 0x80008000u;
+                        if (odd)
+#pragma unroll 1
+                            for (int e = 0; e < CHS * 4; ++e) {
+                                uint32_t *w = reinterpret_cast<uint32_t *>(at) + e, y = *w;
+                                if ((y & Half2<BF>::EXP_MASK) == Half2<BF>::EXP_MASK) y &= 0xffff0000u;
+                                if (((y >> 16) & Half2<BF>::EXP_MASK) == Half2<BF>::EXP_MASK) y &= 0xffffu;
+                                *w = y;
+                            }
                         if (odd) *(volatile int *)&ms.poison[buf] = 1;
                     }
                     if (k > 0) fail |= !tc::bar_wait(tc::smem_u32(&ms.pvdone), (k - 1) & 1, abort);
@@ -829,19 +845,23 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                         r[NQ] = raise ? NAN : sum;
                         r[2 * NQ] = raise ? NAN : rsum;
                     }
-                    __threadfence();
+                    if (t == 0 && wg == 0) ms.join[cta == g.c0] = g, ms.joins[cta == g.c0] = 1;
                     group_sync(bar, 128);
-                    // Both halves of the columns count, of every CTA.
-                    if (t == 0 && atomicAdd(&P.counters[g.c0], 1u) == 2u * (unsigned)(g.c1 - g.c0) + 1u) {
-                        P.counters[g.c0] = 0;
-                        ms.joins[cta == g.c0] = 1;
-                        ms.join[cta == g.c0] = g;
-                    }
                 }
                 // The references and factors are read until here; the next segment writes them anew.
             }
 
-            // ---- joins left to this CTA ----------------------------------------------------------
+            // ---- the parts: who writes a segment's last one joins them -------------------------------
+            __threadfence();
+            group_sync(3, 256);
+            if (tid == 256 && !*abort)
+                for (int i = 0; i < 2; ++i)
+                    if (ms.joins[i]) {
+                        unsigned *n = &P.counters[ms.join[i].c0];
+                        const bool last = atomicAdd(n, 1u) == (unsigned)(ms.join[i].c1 - ms.join[i].c0);
+                        if (last) *n = 0;
+                        ms.joins[i] = last;
+                    }
             group_sync(3, 256);
             if (!*abort)
                 for (int i = 0; i < 2; ++i) {
@@ -855,7 +875,7 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                         const int gr = g.qt * NQ + c, n = gr / P.G;
                         if (n >= P.N) break;
                         auto part_of = [&](int x) {
-                            return P.parts + (int64_t)(2 * x + (x == g.c0 && !g.first0)) * part_floats<NQ>();
+                            return P.parts + (int64_t)(2 * x + (x == g.c0)) * part_floats<NQ>();
                         };
                         float top = -INFINITY;
 #pragma unroll 4
