@@ -39,7 +39,7 @@ using sv::Half2;
 constexpr int NT = 512;
 constexpr int TILE = 128;     // positions per tile
 constexpr int MAXD = 128;
-constexpr int MAX_CTAS = 256; // parts the workspace has room for: two per CTA
+constexpr int MAX_CTAS = 192; // parts the workspace has room for: two per CTA
 constexpr int FLAGS = 16;     // bad-slot flags: more than the segments the ring can hold
 constexpr int SEGS = 8;       // segments listed ahead
 constexpr float SLACK = 8.f;  // log2 of the largest weight
@@ -538,18 +538,20 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                     wrong = t == 0 ? p != -1 : (p < 0 || p >= t);
                     if (wrong) p = -1;
                 }
-                constexpr int CH = DP / 8, PER = NQ * CH / 64;  // 16-byte chunks of a row; of a thread
-                uint4 x[PER < 8 ? PER : 8];
+                constexpr int CH = DP / 8, RPI = 64 / CH, PER = NQ / RPI;  // 16-byte chunks of a row; rows at a time
+                const int ch = t % CH, r0 = t / CH;
                 bool ok = true;
-#pragma unroll
+#pragma unroll 1
                 for (int e0 = 0; e0 < PER; e0 += 8) {
+                    uint4 x[8];
 #pragma unroll
-                    for (int i = 0; i < 8 && e0 + i < PER; ++i) {
-                        const int e = (e0 + i) * 64 + t, r = e / CH, ch = e % CH, gr = g.qt * NQ + r, n = gr / P.G;
+                    for (int i = 0; i < 8; ++i) {
+                        if (e0 + i >= PER) break;
+                        const unsigned gr = g.qt * NQ + r0 + (e0 + i) * RPI, n = gr / (unsigned)P.G;
                         x[i] = make_uint4(0, 0, 0, 0);
-                        if (n < g.nn && ch * 8 < P.D) {
-                            const int64_t at = ((int64_t)g.b * P.N + n) * P.q_row + (int64_t)(g.h * P.G + gr - n * P.G) * P.D +
-                                               ch * 8;
+                        if ((int)n < g.nn && ch * 8 < P.D) {
+                            const int64_t at = ((int64_t)g.b * P.N + n) * P.q_row +
+                                               (int64_t)(int)(g.h * P.G + gr - n * P.G) * P.D + ch * 8;
                             if (SV_INB(at, (int64_t)P.B * P.N * P.q_row, 1105))
                                 x[i] = *reinterpret_cast<const uint4 *>(P.q + at);
                         }
@@ -560,8 +562,9 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                         if (t == 0) ms.code[buf] = ms.poison[buf] = 0;
                     }
 #pragma unroll
-                    for (int i = 0; i < 8 && e0 + i < PER; ++i) {
-                        const int e = (e0 + i) * 64 + t, r = e / CH, ch = e % CH;
+                    for (int i = 0; i < 8; ++i) {
+                        if (e0 + i >= PER) break;
+                        const int r = r0 + (e0 + i) * RPI;
                         *reinterpret_cast<uint4 *>(smem + L::Q0 + buf * L::QSTEP + (ch >> 3) * NQ * 128 + r * 128 +
                                                    (((ch & 7) ^ (r & 7)) << 4)) = x[i];
                     }
@@ -625,16 +628,6 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                     tc::fence_after();
                     float x[CW];
                     tc::tmem_ld(lanes + sb * NQ, x);
-                    tc::wait_ld(x);
-                    // Exponents against the references; what this position's columns do not see is -inf.
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < CW; c += 2) {
-                        const float2 d = sv::f2_split(sv::f2_fma(sv::f2(x[c], x[c + 1]), scale2,
-                                                                 *reinterpret_cast<const uint64_t *>(&ms.nref[col0 + c])));
-                        x[c] = d.x;
-                        x[c + 1] = d.y;
-                    }
                     unsigned vis = 0xffffffffu;  // the columns that see this position
                     if (special) {
                         vis = 0;
@@ -647,23 +640,48 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                                 if (++h == P.G) h = 0, ++n;
                             }
                         }
-#pragma unroll
-                        for (int c = 0; c < CW; ++c) x[c] = (vis >> c) & 1 ? x[c] : -INFINITY;
                     }
+                    tc::wait_ld(x);
+                    // What this position's columns do not see is -inf.
+                    auto mask = [&] {
+                        if (special) {
 #pragma unroll
-                    for (int c = 0; c < CW; ++c) top = fmaxf(top, x[c]);
-                    // (A segment's first tile needs no vote.)
-                    if (j == g.j0 || group_or(bar, 128, fresh || fail || top > SLACK)) {
-                        if (j > g.j0 && group_or(bar, 128, fail)) break;
+                            for (int c = 0; c < CW; ++c) x[c] = (vis >> c) & 1 ? x[c] : -INFINITY;
+                        }
+                    };
+                    mask();
+                    // Exponents against the references.
+                    auto exponents = [&] {
+#pragma unroll
+                        for (int c = 0; c < CW; c += 2) {
+                            const float2 d = sv::f2_split(sv::f2_fma(sv::f2(x[c], x[c + 1]), scale2,
+                                                                     *reinterpret_cast<const uint64_t *>(&ms.nref[col0 + c])));
+                            x[c] = d.x;
+                            x[c + 1] = d.y;
+                        }
+                    };
+                    bool move = j == g.j0;  // a segment's first tile needs no vote
+                    if (!move) {
+                        exponents();
+                        float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                        for (int c = 4; c < CW; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
+                        move = group_or(bar, 128, fresh || fail ||
+                                                      fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > SLACK);
+                    }
+                    if (move) {
+                        if (j > g.j0) {
+                            if (group_or(bar, 128, fail)) break;
+                            tc::tmem_ld(lanes + sb * NQ, x);
+                            tc::wait_ld(x);
+                            mask();
+                        }
                         // Move the references to the columns' maxima.
-                        tc::tmem_ld(lanes + sb * NQ, x);
-                        tc::wait_ld(x);
                         float m = 0.f;
 #pragma unroll
                         for (int c = 0; c < CW; ++c) {
-                            x[c] = (vis >> c) & 1 ? x[c] * P.scale_log2 : -INFINITY;
                             const float y = warp_max(x[c]);
-                            if (lane == c) m = y;
+                            if (lane == c) m = y * P.scale_log2;
                         }
                         if (lane < CW) ms.red[wq][col0 + lane] = m;
                         group_sync(bar, 128);
@@ -697,8 +715,7 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                             tc::tmem_st(lanes + 2 * NQ, o);
                             tc::wait_st();
                         }
-#pragma unroll
-                        for (int c = 0; c < CW; ++c) x[c] += ms.nref[col0 + c];
+                        exponents();
                     }
                     tc::fence_before();
                     tc::bar_arrive(tc::smem_u32(&ms.sempty[sb]));
@@ -868,50 +885,77 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                     if (!ms.joins[i]) continue;
                     __threadfence();
                     g = ms.join[i];
-                    // A thread takes four dimensions of a column; the parts are read in their order, so
-                    // the result does not depend on who joins.
-                    for (int e = tid - 256; e < NQ * (MAXD / 4); e += 256) {
-                        const int c = e / (MAXD / 4), d = (e - c * (MAXD / 4)) * 4;
-                        const int gr = g.qt * NQ + c, n = gr / P.G;
-                        if (n >= P.N) break;
-                        auto part_of = [&](int x) {
-                            return P.parts + (int64_t)(2 * x + (x == g.c0)) * part_floats<NQ>();
-                        };
-                        float top = -INFINITY;
-#pragma unroll 4
-                        for (int x = g.c0; x <= g.c1; ++x) top = fmaxf(top, __ldcg(part_of(x) + NQ * MAXD + c));
-                        float sum = 0.f, rsum = 0.f;
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                        for (int x = g.c0; x <= g.c1; ++x) {
-                            const float *part = part_of(x);
-                            const float m = __ldcg(part + NQ * MAXD + c), l = __ldcg(part + NQ * MAXD + NQ + c);
-                            const float r = __ldcg(part + NQ * MAXD + 2 * NQ + c);
-                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + c * MAXD + d));
-                            if (l != 0.f) {  // 0: the part's positions have no weight in this row
-                                const float f = ex2(m == -INFINITY ? 0.f : m - top);
-                                sum += f * l;
-                                rsum += f * r;
-                                acc.x += f * y.x;
-                                acc.y += f * y.y;
-                                acc.z += f * y.z;
-                                acc.w += f * y.w;
-                            }
-                        }
-                        const int64_t row = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + gr - n * P.G;
-                        const bool bad = sum != sum;
-                        if (d < P.D && SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1110)) {
-                            uint2 y = make_uint2(0, 0);
-                            if (n < g.nn || bad) {
-                                const float inv = 1.f / rsum;
-                                y = make_uint2(Half2<BF>::pack(acc.x * inv, acc.y * inv),
-                                               Half2<BF>::pack(acc.z * inv, acc.w * inv));
-                            }
-                            *reinterpret_cast<uint2 *>(P.out + row * P.D + d) = y;
-                        }
-                        if (d == 0 && P.lse)
-                            P.lse[row] = n < g.nn || bad ? ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.69314718f : -INFINITY;
+                    // The parts' references and sums first, all read at once, into the ring (which is done with);
+                    // then a thread takes four dimensions of NQ / 8 columns.  The parts are added in their
+                    // order, so the result does not depend on who joins.
+                    const int parts = g.c1 - g.c0 + 1, t = tid - 256;
+                    float *const jm = reinterpret_cast<float *>(smem), *const jl = jm + parts * NQ, *const jr = jl + parts * NQ;
+                    auto part_of = [&](int x) { return P.parts + (int64_t)(2 * (g.c0 + x) + (x == 0)) * part_floats<NQ>(); };
+                    for (int e = t; e < parts * NQ; e += 256) {
+                        const float *r = part_of(e / NQ) + NQ * MAXD + e % NQ;
+                        jm[e] = __ldcg(r);
+                        jl[e] = __ldcg(r + NQ);
+                        jr[e] = __ldcg(r + 2 * NQ);
                     }
+                    group_sync(3, 256);
+                    if (t < NQ) {
+                        float top = -INFINITY, sum = 0.f, rsum = 0.f;
+                        for (int x = 0; x < parts; ++x) top = fmaxf(top, jm[x * NQ + t]);
+                        for (int x = 0; x < parts; ++x) {
+                            const float m = jm[x * NQ + t], l = jl[x * NQ + t];
+                            // 0: the part's positions have no weight in this row
+                            const float f = l == 0.f ? 0.f : ex2(m == -INFINITY ? 0.f : m - top);
+                            if (l != 0.f) sum += f * l, rsum += f * jr[x * NQ + t];
+                            jm[x * NQ + t] = f;
+                        }
+                        const int gr = g.qt * NQ + t, n = gr / P.G;
+                        const bool bad = sum != sum;
+                        ms.fac[t] = n < g.nn || bad ? 1.f / rsum : 0.f;
+                        if (n < P.N && P.lse) {
+                            const int64_t row = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + gr - n * P.G;
+                            if (SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1111))
+                                P.lse[row] = n < g.nn || bad ? ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.69314718f
+                                                             : -INFINITY;
+                        }
+                    }
+                    group_sync(3, 256);
+                    constexpr int IT = NQ / 8;
+                    const int d = (t & 31) * 4, c0 = t >> 5;  // columns c0, c0 + 8, ...
+                    float4 acc[IT];
+#pragma unroll
+                    for (int i = 0; i < IT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                    for (int x = 0; x < parts; ++x) {
+                        const float *part = part_of(x);
+                        float4 y[IT];
+#pragma unroll
+                        for (int i = 0; i < IT; ++i)
+                            y[i] = __ldcg(reinterpret_cast<const float4 *>(part + (c0 + 8 * i) * MAXD + d));
+#pragma unroll
+                        for (int i = 0; i < IT; ++i) {
+                            const float f = jm[x * NQ + c0 + 8 * i];
+                            if (f == 0.f) continue;
+                            acc[i].x += f * y[i].x;
+                            acc[i].y += f * y[i].y;
+                            acc[i].z += f * y[i].z;
+                            acc[i].w += f * y[i].w;
+                        }
+                    }
+                    if (d < P.D)
+#pragma unroll
+                        for (int i = 0; i < IT; ++i) {
+                            const int gr = g.qt * NQ + c0 + 8 * i, n = gr / P.G;
+                            if (n >= P.N) break;
+                            const int64_t row = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + gr - n * P.G;
+                            const float inv = ms.fac[c0 + 8 * i];
+                            uint2 y = make_uint2(0, 0);
+                            if (inv != 0.f)
+                                y = make_uint2(Half2<BF>::pack(acc[i].x * inv, acc[i].y * inv),
+                                               Half2<BF>::pack(acc[i].z * inv, acc[i].w * inv));
+                            if (SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1110))
+                                *reinterpret_cast<uint2 *>(P.out + row * P.D + d) = y;
+                        }
+                    group_sync(3, 256);
                 }
         }
     }
