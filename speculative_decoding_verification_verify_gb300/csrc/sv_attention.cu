@@ -94,6 +94,7 @@ struct Misc {
     Seg join[2];
     int joins[2];
     int8_t par[sv::MAX_TREE];
+    __align__(16) uint8_t node[2][NQ];  // the columns' nodes, of the staged queries
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -560,6 +561,10 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                         if (seg >= 2) ok = tc::bar_wait(tc::smem_u32(&ms.qempty[buf]), ((seg >> 1) & 1) ^ 1, abort);
                         ms.par[t] = (int8_t)p;
                         if (t == 0) ms.code[buf] = ms.poison[buf] = 0;
+                        if (t < NQ) {
+                            const unsigned n = (unsigned)(g.qt * NQ + t) / (unsigned)P.G;
+                            ms.node[buf][t] = (uint8_t)(n < 63 ? n : 63);
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -634,10 +639,14 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                         if (pos < g.c) {
                             vis = 0xffffffffu;
                         } else if (pos < len) {
+                            // (A node past the request's is nobody's descendant; columns past the last node are node
+                            // 63's, whatever they get is not written.)
                             const unsigned long long see = ms.desc[buf][pos - g.c];
-                            for (int c = 0, n = n0, h = h0; c < CW && n < g.nn; ++c) {
-                                vis |= (unsigned)((see >> n) & 1ull) << c;
-                                if (++h == P.G) h = 0, ++n;
+#pragma unroll
+                            for (int c = 0; c < CW; c += 4) {
+                                const uchar4 n = *reinterpret_cast<const uchar4 *>(&ms.node[buf][col0 + c]);
+                                vis |= (unsigned)((see >> n.x) & 1ull) << c | (unsigned)((see >> n.y) & 1ull) << (c + 1) |
+                                       (unsigned)((see >> n.z) & 1ull) << (c + 2) | (unsigned)((see >> n.w) & 1ull) << (c + 3);
                             }
                         }
                     }
@@ -719,15 +728,23 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                     }
                     tc::fence_before();
                     tc::bar_arrive(tc::smem_u32(&ms.sempty[sb]));
-                    // The weights, rounded to the values' type; both sums go on.
-                    uint32_t pk[CW / 2];
+                    // The weights, rounded to the values' type, go where the tile before's were read from; both
+                    // sums go on.
+                    if (k > 0) fail |= !tc::bar_wait(tc::smem_u32(&ms.pvdone), (k - 1) & 1, abort);
 #pragma unroll
-                    for (int c = 0; c < CW; c += 2) {
-                        const float a = ex2(x[c]), b = ex2(x[c + 1]);
-                        pk[c / 2] = Half2<BF>::pack(a, b);
-                        const float2 r = Half2<BF>::unpack(pk[c / 2]);
-                        raw[c / 2] = sv::f2_add(raw[c / 2], sv::f2(a, b));
-                        rnd[c / 2] = sv::f2_add(rnd[c / 2], sv::f2(r.x, r.y));
+                    for (int ch = 0; ch < CW / 8; ++ch) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = ch * 8 + 2 * i;
+                            const float a = ex2(x[c]), b = ex2(x[c + 1]);
+                            pk[i] = Half2<BF>::pack(a, b);
+                            const float2 r = Half2<BF>::unpack(pk[i]);
+                            raw[c / 2] = sv::f2_add(raw[c / 2], sv::f2(a, b));
+                            rnd[c / 2] = sv::f2_add(rnd[c / 2], sv::f2(r.x, r.y));
+                        }
+                        *reinterpret_cast<uint4 *>(smem + L::P0 + t * 128 + (((col0 / 8 + ch) ^ (t & 7)) << 4)) =
+                            make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
                     if (special && pos >= g.c && pos < len) {
                         // A weight of 0 does not undo an infinity or a NaN: what is not finite in a node's
@@ -757,11 +774,6 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                             }
                         if (odd) *(volatile int *)&ms.poison[buf] = 1;
                     }
-                    if (k > 0) fail |= !tc::bar_wait(tc::smem_u32(&ms.pvdone), (k - 1) & 1, abort);
-#pragma unroll
-                    for (int ch = 0; ch < CW / 8; ++ch)
-                        *reinterpret_cast<uint4 *>(smem + L::P0 + t * 128 + (((col0 / 8 + ch) ^ (t & 7)) << 4)) =
-                            make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
                     tc::fence_async_smem();
                     tc::fence_before();
                     tc::bar_arrive(tc::smem_u32(&ms.pfull));
@@ -919,35 +931,37 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                         }
                     }
                     group_sync(3, 256);
-                    constexpr int IT = NQ / 8;
+                    constexpr int IT = NQ < 32 ? NQ / 8 : 4;
                     const int d = (t & 31) * 4, c0 = t >> 5;  // columns c0, c0 + 8, ...
-                    float4 acc[IT];
+#pragma unroll 1
+                    for (int b0 = c0; b0 < NQ; b0 += 8 * IT) {
+                        float4 acc[IT];
 #pragma unroll
-                    for (int i = 0; i < IT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int i = 0; i < IT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-                    for (int x = 0; x < parts; ++x) {
-                        const float *part = part_of(x);
-                        float4 y[IT];
+                        for (int x = 0; x < parts; ++x) {
+                            const float *part = part_of(x);
+                            float4 y[IT];
 #pragma unroll
-                        for (int i = 0; i < IT; ++i)
-                            y[i] = __ldcg(reinterpret_cast<const float4 *>(part + (c0 + 8 * i) * MAXD + d));
+                            for (int i = 0; i < IT; ++i)
+                                y[i] = __ldcg(reinterpret_cast<const float4 *>(part + (b0 + 8 * i) * MAXD + d));
 #pragma unroll
-                        for (int i = 0; i < IT; ++i) {
-                            const float f = jm[x * NQ + c0 + 8 * i];
-                            if (f == 0.f) continue;
-                            acc[i].x += f * y[i].x;
-                            acc[i].y += f * y[i].y;
-                            acc[i].z += f * y[i].z;
-                            acc[i].w += f * y[i].w;
+                            for (int i = 0; i < IT; ++i) {
+                                const float f = jm[x * NQ + b0 + 8 * i];
+                                if (f == 0.f) continue;
+                                acc[i].x += f * y[i].x;
+                                acc[i].y += f * y[i].y;
+                                acc[i].z += f * y[i].z;
+                                acc[i].w += f * y[i].w;
+                            }
                         }
-                    }
-                    if (d < P.D)
+                        if (d >= P.D) continue;
 #pragma unroll
                         for (int i = 0; i < IT; ++i) {
-                            const int gr = g.qt * NQ + c0 + 8 * i, n = gr / P.G;
+                            const int c = b0 + 8 * i, gr = g.qt * NQ + c, n = gr / P.G;
                             if (n >= P.N) break;
                             const int64_t row = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + gr - n * P.G;
-                            const float inv = ms.fac[c0 + 8 * i];
+                            const float inv = ms.fac[c];
                             uint2 y = make_uint2(0, 0);
                             if (inv != 0.f)
                                 y = make_uint2(Half2<BF>::pack(acc[i].x * inv, acc[i].y * inv),
@@ -955,6 +969,7 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                             if (SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1110))
                                 *reinterpret_cast<uint2 *>(P.out + row * P.D + d) = y;
                         }
+                    }
                     group_sync(3, 256);
                 }
         }
