@@ -17,7 +17,8 @@ namespace svapp {
 
 using sv::Half2;
 
-constexpr int NT = 128;  // threads per CTA
+constexpr int NT = 128;    // threads per CTA
+constexpr int UNROLL = 3;  // units of a thread in flight: a row of 48 heads of 128
 
 struct Params {
     const uint4 *q, *k, *v;            // rows of heads * D elements, row_*  vectors apart
@@ -57,17 +58,55 @@ __global__ void __launch_bounds__(NT) append_kernel(const Params P)
     __shared__ int s_par[sv::MAX_TREE];
     __shared__ int s_bad;
     const int64_t row = blockIdx.x;
-    const int b = (int)(row / P.N), n = (int)(row - (int64_t)b * P.N), tid = threadIdx.x;
+    const int b = (int)((unsigned)row / (unsigned)P.N), n = (int)(row - (int64_t)b * P.N), tid = threadIdx.x;
     [[maybe_unused]] const int64_t rows = (int64_t)P.B * P.N;
     const int hv = P.D / 8, hu = hv / 2;  // a head's vectors and units
     const int units = (P.Hq + 2 * P.Hkv) * hu;
     const int rv = P.rot / 8;  // rotated vectors of a head (even)
 
+    // A unit's two vectors: (j, j + rv/2) among the rotated ones when pairs are half a rotation
+    // apart, else neighbours.
+    struct Unit {
+        int head, j, i0, i1;
+        bool turned;
+    };
+    auto unit = [&](int u) {
+        Unit x;
+        x.head = (unsigned)u / (unsigned)hu;
+        x.j = u - x.head * hu;
+        x.turned = 2 * x.j < rv;
+        x.i0 = !ADJ && x.turned ? x.j : 2 * x.j;
+        x.i1 = !ADJ && x.turned ? x.j + rv / 2 : 2 * x.j + 1;
+        return x;
+    };
+    auto load = [&](const Unit &x, uint4 &a, uint4 &c) {
+        const bool is_q = x.head < P.Hq, is_k = x.head < P.Hq + P.Hkv;
+        const uint4 *base = is_q ? P.q : is_k ? P.k : P.v;
+        const int64_t stride = is_q ? P.q_row : is_k ? P.k_row : P.v_row;
+        const int64_t at = row * stride + (x.head - (is_q ? 0 : is_k ? P.Hq : P.Hq + P.Hkv)) * hv;
+        if (!SV_INB(at + x.i1, (rows - 1) * stride + (is_q ? P.Hq : P.Hkv) * hv, 1006)) return;
+        a = base[at + x.i0];
+        c = base[at + x.i1];
+    };
+
+    // The row's first vectors, before anything is known of where they go.
+    uint4 va[UNROLL], vb[UNROLL];
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i)
+        if (tid + i * NT < units) load(unit(tid + i * NT), va[i], vb[i]);
+
     const int c = SV_INB(b, P.B, 1001) ? P.committed[b] : 0;
     const int nn = P.num_nodes && SV_INB(b, P.B, 1002) ? P.num_nodes[b] : P.N;
     int code = 0;
     if (nn < 0 || nn > P.N || c < 0 || (int64_t)c + nn > P.max_pos) code = SPEC_VERIFY_DEV_BAD_KV_POSITION;
+    const bool here = n < nn;
+    int slot = 0;
+    if (!code && here) {
+        const int64_t i = (int64_t)b * P.max_pos + c + n;
+        slot = SV_INB(i, (int64_t)P.B * P.max_pos, 1004) ? P.slot_table[i] : -1;
+    }
     int depth = n;
+    bool bad_tree = false;
     if (P.parents) {
         if (tid == 0) s_bad = 0;
         __syncthreads();
@@ -77,21 +116,18 @@ __global__ void __launch_bounds__(NT) append_kernel(const Params P)
             if (tid == 0 ? p != -1 : (p < 0 || p >= tid)) s_bad = 1;
         }
         __syncthreads();
-        if (s_bad) {
-            if (code < SPEC_VERIFY_DEV_BAD_TREE) code = SPEC_VERIFY_DEV_BAD_TREE;
-        } else if (!code && n < nn) {
+        bad_tree = s_bad;
+        if (!bad_tree && !code && here) {
             depth = 0;
             for (int j = n; j > 0; j = s_par[j]) ++depth;
         }
     }
-    const bool here = n < nn;
-    if (!code && here && (int64_t)c + depth >= P.rot_positions && P.rot) code = SPEC_VERIFY_DEV_BAD_KV_POSITION;
-    int64_t slot = 0;
-    if (!code && here) {
-        const int64_t i = (int64_t)b * P.max_pos + c + n;
-        slot = SV_INB(i, (int64_t)P.B * P.max_pos, 1004) ? P.slot_table[i] : -1;
-        if (slot < 0 || slot >= P.num_slots) code = SPEC_VERIFY_DEV_BAD_KV_SLOT;
+    // The faults, the later ones of the list only where the earlier ones leave them a meaning.
+    if (!code && here && !bad_tree) {
+        if (P.rot && (int64_t)c + depth >= P.rot_positions) code = SPEC_VERIFY_DEV_BAD_KV_POSITION;
+        else if (slot < 0 || slot >= P.num_slots) code = SPEC_VERIFY_DEV_BAD_KV_SLOT;
     }
+    if (!code && bad_tree) code = SPEC_VERIFY_DEV_BAD_TREE;
     if (code && tid == 0 && P.dev_status) atomicMax(P.dev_status, code);
     if (code || !here) {  // nothing is appended; the row's queries are zeros (absent) or NaN (a fault)
         const uint32_t w = code ? Half2<BF>::NAN2 : 0u;
@@ -101,43 +137,31 @@ __global__ void __launch_bounds__(NT) append_kernel(const Params P)
         return;
     }
     const float *cs = P.cos_sin + ((int64_t)c + depth) * P.rot;
-    for (int u = tid; u < units; u += NT) {
-        const int head = u / hu, j = u - head * hu;
-        // The unit's two vectors: (j, j + rv/2) among the rotated ones when pairs are half a
-        // rotation apart, else neighbours.
-        int i0 = 2 * j, i1 = 2 * j + 1;
-        const bool turned = 2 * j < rv;
-        if (!ADJ && turned) {
-            i0 = j;
-            i1 = j + rv / 2;
-        }
-        const uint4 *src;
-        uint4 *dst;
-        bool spin = turned;
-        if (head < P.Hq) {
-            src = P.q + row * P.q_row + head * hv;
-            dst = P.q_out + row * P.q_out_row + head * hv;
-        } else if (head < P.Hq + P.Hkv) {
-            src = P.k + row * P.k_row + (head - P.Hq) * hv;
-            dst = P.k_cache + slot * P.k_slot + (head - P.Hq) * hv;
-        } else {
-            src = P.v + row * P.v_row + (head - P.Hq - P.Hkv) * hv;
-            dst = P.v_cache + slot * P.v_slot + (head - P.Hq - P.Hkv) * hv;
-            spin = false;
-        }
-        uint4 x = src[i0], y = src[i1];
-        if (spin) {
-            float cc[8], ss[8];
-            const float *pc = cs + 8 * j, *ps = pc + P.rot / 2;
+    for (int u0 = 0; u0 < units; u0 += UNROLL * NT) {
+        if (u0 > 0)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                cc[e] = pc[e];
-                ss[e] = ps[e];
+            for (int i = 0; i < UNROLL; ++i)
+                if (u0 + tid + i * NT < units) load(unit(u0 + tid + i * NT), va[i], vb[i]);
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+            if (u0 + tid + i * NT >= units) break;
+            const Unit x = unit(u0 + tid + i * NT);
+            const bool is_q = x.head < P.Hq, is_k = x.head < P.Hq + P.Hkv;
+            if (x.turned && is_k) {
+                const float4 *pc = reinterpret_cast<const float4 *>(cs + 8 * x.j);
+                const float4 *ps = reinterpret_cast<const float4 *>(cs + 8 * x.j + P.rot / 2);
+                const float4 c0 = __ldg(pc), c1 = __ldg(pc + 1), s0 = __ldg(ps), s1 = __ldg(ps + 1);
+                const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+                rotate<BF, ADJ>(va[i], vb[i], cc, ss);
             }
-            rotate<BF, ADJ>(x, y, cc, ss);
+            uint4 *const dst = (is_q    ? P.q_out + row * P.q_out_row
+                                : is_k ? P.k_cache + (int64_t)slot * P.k_slot - P.Hq * hv
+                                       : P.v_cache + (int64_t)slot * P.v_slot - (P.Hq + P.Hkv) * hv) +
+                               x.head * hv;
+            dst[x.i0] = va[i];
+            dst[x.i1] = vb[i];
         }
-        dst[i0] = x;
-        dst[i1] = y;
     }
 }
 
