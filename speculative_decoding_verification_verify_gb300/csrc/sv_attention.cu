@@ -84,7 +84,7 @@ struct Misc {
     uint64_t full[NU], empty[NU];
     uint64_t sfull[2], sempty[2], qfull[2], qempty[2], segfull[SEGS], segempty[SEGS], pfull, pvdone, drain;
     Seg seg[SEGS];
-    unsigned long long desc[2][sv::MAX_TREE];  // nodes that see node a, of the staged queries' request
+    unsigned long long desc[2][sv::MAX_TREE];  // columns that see node a, of the staged queries
     float nref[NQ], fac[NQ], ref[NQ], red[4][NQ], red2[4][NQ];
     int code[2], poison[2];
     int bad[2][FLAGS];
@@ -94,7 +94,6 @@ struct Misc {
     Seg join[2];
     int joins[2];
     int8_t par[sv::MAX_TREE];
-    __align__(16) uint8_t node[2][NQ];  // the columns' nodes, of the staged queries
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -160,14 +159,20 @@ __host__ __device__ constexpr int part_floats()
 // Runs are cut at multiples of total / G on the axis of costs.  A cut x into a segment of n tiles leaves the
 // tiles before `cut_tile` to the run before; cuts are at least COST_TILE apart, so no run between two
 // cuts of a segment is empty.
-__device__ __forceinline__ int64_t run_begin(int c, int64_t total, int G) { return total * c / G; }
+// (Quotients in 32 bits wherever they fit: 64-bit division is a hundred instructions.)
+__device__ __noinline__ int64_t quotient64(int64_t a, int64_t b) { return a / b; }
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    return (uint64_t)(a | b) >> 32 ? quotient64(a, b) : (int64_t)((unsigned)a / (unsigned)b);
+}
+__device__ __forceinline__ int64_t run_begin(int c, int64_t total, int G) { return quotient(total * c, G); }
 __device__ __forceinline__ int cut_tile(int64_t x, int n)
 {
-    const int64_t t = x - COST_SEGMENT + COST_TILE / 2;
-    return t <= 0 ? 0 : t / COST_TILE < n ? (int)(t / COST_TILE) : n;
+    const int64_t t = (x - COST_SEGMENT + COST_TILE / 2) / COST_TILE;
+    return t <= 0 ? 0 : t < n ? (int)t : n;
 }
 // The last run that begins before x.
-__device__ __forceinline__ int run_before(int64_t x, int64_t total, int G) { return (int)((x * G + total - 1) / total) - 1; }
+__device__ __forceinline__ int run_before(int64_t x, int64_t total, int G) { return (int)quotient(x * G + total - 1, total) - 1; }
 
 __device__ __forceinline__ int kind_of(const Params &P, int c, int nn)
 {
@@ -226,6 +231,7 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
     const int HT = P.Hkv * P.QT;
     const int per = (P.B + NT - 1) / NT;
     int64_t mine = 0;
+#pragma unroll 1
     for (int i = 0; i < per && tid * per + i < P.B; ++i) {
         int c, nn;
         lengths(P, tid * per + i, c, nn);
@@ -246,11 +252,14 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
     }
     // Small batches leave the last CTAs out: a run costs COST_TILE at least.
     const int G = total / COST_TILE < (int64_t)gridDim.x ? (int)(total / COST_TILE) : (int)gridDim.x;
-    const int64_t t0 = cta < G ? run_begin(cta, total, G) : total, t1 = cta < G ? run_begin(cta + 1, total, G) : total;
+    // Odd lanes work out the run's end, even ones its beginning.
+    const int64_t edge = cta + (lane & 1) <= G ? run_begin(cta + (lane & 1), total, G) : total;
+    const int64_t t0 = __shfl_sync(0xffffffffu, edge, 0), t1 = __shfl_sync(0xffffffffu, edge, 1);
     if (t0 >= before && t0 < before + mine) {
         int64_t at = before;
         int b = tid * per;
-        for (; b < P.B; ++b) {
+#pragma unroll 1
+        for (; per > 1 && b < P.B; ++b) {
             int c, nn;
             lengths(P, b, c, nn);
             const int64_t n = cost_of(tiles_of(kind_of(P, c, nn), c, nn)) * HT;
@@ -496,7 +505,7 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                 const int64_t cost = cost_of(ntile);
                 int item = 0;
                 if (first) {  // items before the one that the run begins in
-                    item = (int)((t0 - at) / cost);
+                    item = (int)quotient(t0 - at, cost);
                     at += item * cost;
                     first = false;
                 }
@@ -509,8 +518,9 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                     g.part = -1;
                     if (g.j0 > 0 || g.j1 < ntile) {
                         // The runs that hold its first and its last tile, and all between.
-                        g.c0 = run_before(at + COST_SEGMENT + COST_TILE / 2, total, G);
-                        g.c1 = run_before(at + cost - COST_TILE / 2, total, G);
+                        const int run = run_before(at + (lane & 1 ? cost - COST_TILE / 2 : COST_SEGMENT + COST_TILE / 2), total, G);
+                        g.c0 = __shfl_sync(0xffffffffu, run, 0);
+                        g.c1 = __shfl_sync(0xffffffffu, run, 1);
                         g.part = 2 * cta + (cta == g.c0);
                     }
                     put(g);
@@ -561,10 +571,6 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                         if (seg >= 2) ok = tc::bar_wait(tc::smem_u32(&ms.qempty[buf]), ((seg >> 1) & 1) ^ 1, abort);
                         ms.par[t] = (int8_t)p;
                         if (t == 0) ms.code[buf] = ms.poison[buf] = 0;
-                        if (t < NQ) {
-                            const unsigned n = (unsigned)(g.qt * NQ + t) / (unsigned)P.G;
-                            ms.node[buf][t] = (uint8_t)(n < 63 ? n : 63);
-                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -586,8 +592,12 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                 }
                 ms.desc[buf][t] = path;
                 group_sync(2, 64);
+                // Of a node that sees this thread's, all columns: P.G of them from its first one on.
                 unsigned long long see = 0;
-                for (int n = t; n < g.nn; ++n) see |= ((ms.desc[buf][n] >> t) & 1ull) << n;
+                for (int n = t, c = t * P.G - g.qt * NQ; n < g.nn && c < NQ; ++n, c += P.G) {
+                    const int from = c > 0 ? c : 0, to = c + P.G < 64 ? c + P.G : 64;
+                    if (to > from && ((ms.desc[buf][n] >> t) & 1)) see |= ~0ull >> (64 - (to - from)) << from;
+                }
                 group_sync(2, 64);
                 ms.desc[buf][t] = see;
                 tc::bar_arrive(tc::smem_u32(&ms.qfull[buf]));
@@ -639,15 +649,7 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                         if (pos < g.c) {
                             vis = 0xffffffffu;
                         } else if (pos < len) {
-                            // (A node past the request's is nobody's descendant; columns past the last node are node
-                            // 63's, whatever they get is not written.)
-                            const unsigned long long see = ms.desc[buf][pos - g.c];
-#pragma unroll
-                            for (int c = 0; c < CW; c += 4) {
-                                const uchar4 n = *reinterpret_cast<const uchar4 *>(&ms.node[buf][col0 + c]);
-                                vis |= (unsigned)((see >> n.x) & 1ull) << c | (unsigned)((see >> n.y) & 1ull) << (c + 1) |
-                                       (unsigned)((see >> n.z) & 1ull) << (c + 2) | (unsigned)((see >> n.w) & 1ull) << (c + 3);
-                            }
+                            vis = (unsigned)(ms.desc[buf][pos - g.c] >> col0);
                         }
                     }
                     tc::wait_ld(x);
@@ -716,12 +718,15 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                             // The accumulators follow, once the products before have come to an end.
                             fail |= !tc::bar_wait(tc::smem_u32(&ms.pvdone), (k - 1) & 1, abort);
                             tc::fence_after();
-                            float o[CW];
-                            tc::tmem_ld(lanes + 2 * NQ, o);
-                            tc::wait_ld(o);
+#pragma unroll 1
+                            for (int c0 = 0; c0 < CW; c0 += 8) {
+                                float o[8];
+                                tc::tmem_ld(lanes + 2 * NQ + c0, o);
+                                tc::wait_ld(o);
 #pragma unroll
-                            for (int c = 0; c < CW; ++c) o[c] *= ms.fac[col0 + c];
-                            tc::tmem_st(lanes + 2 * NQ, o);
+                                for (int c = 0; c < 8; ++c) o[c] *= ms.fac[col0 + c0 + c];
+                                tc::tmem_st(lanes + 2 * NQ + c0, o);
+                            }
                             tc::wait_st();
                         }
                         exponents();
@@ -780,25 +785,27 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                 }
 
                 // ---- the segment's end: join the columns' sums, write rows or a part -----------
-                {
-                    float y[CW];
+                constexpr int W = CW < 16 ? CW : 16;
 #pragma unroll
-                    for (int c = 0; c < CW; c += 2) {
-                        const float2 f = sv::f2_split(raw[c / 2]);
+                for (int c0 = 0; c0 < CW; c0 += W) {
+                    float y[W];
+#pragma unroll
+                    for (int c = 0; c < W; c += 2) {
+                        const float2 f = sv::f2_split(raw[(c0 + c) / 2]);
                         y[c] = f.x;
                         y[c + 1] = f.y;
                     }
-                    const float a = column_sum<CW>(y, lane);
+                    const float a = column_sum<W>(y, lane);
 #pragma unroll
-                    for (int c = 0; c < CW; c += 2) {
-                        const float2 f = sv::f2_split(rnd[c / 2]);
+                    for (int c = 0; c < W; c += 2) {
+                        const float2 f = sv::f2_split(rnd[(c0 + c) / 2]);
                         y[c] = f.x;
                         y[c + 1] = f.y;
                     }
-                    const float b = column_sum<CW>(y, lane);
-                    if (lane < CW) {
-                        ms.red[wq][col0 + lane] = a;
-                        ms.red2[wq][col0 + lane] = b;
+                    const float b = column_sum<W>(y, lane);
+                    if (lane < W) {
+                        ms.red[wq][col0 + c0 + lane] = a;
+                        ms.red2[wq][col0 + c0 + lane] = b;
                     }
                 }
                 if (k > 0) fail |= !tc::bar_wait(tc::smem_u32(&ms.pvdone), (k - 1) & 1, abort);
@@ -816,12 +823,10 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                         const uint32_t bits = P.v[(int64_t)slot * P.v_slot + g.h * P.D + t];
                         if ((bits & Half2<BF>::EXP_MASK) != Half2<BF>::EXP_MASK) continue;
                         const float val = Half2<BF>::unpack(bits).x;
-                        const unsigned long long see = ms.desc[buf][y - g.c];
+                        const unsigned see = (unsigned)(ms.desc[buf][y - g.c] >> col0);
 #pragma unroll
-                        for (int c = 0; c < CW; ++c) {
-                            const int n = (row0 + c) / P.G;
-                            if (n < g.nn && ((see >> n) & 1)) o[c] += val;
-                        }
+                        for (int c = 0; c < CW; ++c)
+                            if ((see >> c) & 1) o[c] += val;
                     }
                 }
                 const int raise = *(volatile int *)&ms.bad[wg][seg % FLAGS] ? SPEC_VERIFY_DEV_BAD_KV_SLOT
