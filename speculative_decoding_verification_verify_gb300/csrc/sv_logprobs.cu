@@ -25,13 +25,14 @@
 
 namespace svlp {
 
-constexpr int NT = 256, NW = NT / 32;  // folding threads; one more warp copies, and one finishes rows
-constexpr int NT_ALL = NT + 64;
+constexpr int NT = 256, NW = NT / 32;  // folding threads; one more warp copies, and two finish rows in turn
+constexpr int NT_ALL = NT + 96;
 constexpr int MAX_TOP = 32;
 constexpr int VPT = 4;               // 16-byte vectors per thread and tile
 constexpr int TILE_VEC = NT * VPT;
 constexpr int STAGES = 4;
-constexpr int CAP = 512;             // candidates the list holds
+constexpr int CAP = 256;             // candidates the list holds
+constexpr int FLY = 4;               // vectors that a finishing lane asks for at once
 constexpr int SLOTS = 16;            // cells per thread and row; longer rows have cells of several tiles
 static_assert(SLOTS * NT / 128 <= 32, "a bit for each of a lane's cells");
 constexpr int SAMPLE = 2 * MAX_TOP / NW;  // lane maxima of each warp that the bound comes from: 64 in all
@@ -40,7 +41,7 @@ constexpr int MAX_CTAS = 1024;
 constexpr int ROWS = 128;            // rows of its run that a CTA lists at a time
 constexpr float SLACK = 8.f;         // log2 of the largest term
 constexpr float LEAST = -0x1.92p99f;  // about -1e30, a bf16 value; logits below it count as it: 2^t is 0 and t stays finite
-constexpr float NEG_INF = -__builtin_huge_valf();
+constexpr float NEG_INF = -__builtin_huge_valf(), LOWEST = -0x1.fffffep127f;
 
 struct Params {
     const void *logits;
@@ -118,15 +119,21 @@ struct Elt<__nv_bfloat16> {
         const uint32_t m = max2(max2(w.x, w.y), max2(w.z, w.w));
         return fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
     }
-    // The vector's first logit, which is then shifted out.
-    static __device__ __forceinline__ float shift(uint4 &w)
+    // A bit for each logit that reaches the bound.
+    static __device__ __forceinline__ unsigned reach(const uint4 &w, float bound)
     {
-        const float y = __uint_as_float(w.x << 16);
-        w.x = __funnelshift_r(w.x, w.y, 16);
-        w.y = __funnelshift_r(w.y, w.z, 16);
-        w.z = __funnelshift_r(w.z, w.w, 16);
-        w.w >>= 16;
-        return y;
+        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+        unsigned mask = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (__uint_as_float(a[i] << 16) >= bound) mask |= 1u << 2 * i;
+            if (__uint_as_float(a[i] & 0xffff0000u) >= bound) mask |= 2u << 2 * i;
+        }
+        return mask;
+    }
+    static __device__ __forceinline__ float at(const uint4 *w, int e)
+    {
+        return __uint_as_float((uint32_t)reinterpret_cast<const unsigned short *>(w)[e] << 16);
     }
     static __device__ __forceinline__ void set(uint4 &w, int e, const void *row, int64_t c)
     {
@@ -180,14 +187,12 @@ struct Elt<float> {
         return fmax_nan(fmax_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
                         fmax_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
     }
-    static __device__ __forceinline__ float shift(uint4 &w)
+    static __device__ __forceinline__ unsigned reach(const uint4 &w, float bound)
     {
-        const float y = __uint_as_float(w.x);
-        w.x = w.y;
-        w.y = w.z;
-        w.z = w.w;
-        return y;
+        return (__uint_as_float(w.x) >= bound ? 1u : 0u) | (__uint_as_float(w.y) >= bound ? 2u : 0u) |
+               (__uint_as_float(w.z) >= bound ? 4u : 0u) | (__uint_as_float(w.w) >= bound ? 8u : 0u);
     }
+    static __device__ __forceinline__ float at(const uint4 *w, int e) { return reinterpret_cast<const float *>(w)[e]; }
     static __device__ __forceinline__ void set(uint4 &w, int e, const void *row, int64_t c)
     {
         (e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w) = __ldg((const unsigned *)row + c);
@@ -229,8 +234,10 @@ struct Shared {
     int count[NW];
 };
 
-// The finishing warp's.
+// A finishing warp's.
 struct Finish {
+    uint4 vec[FLY][32];  // each lane's vectors
+    int col[FLY][32];    // and their first columns
     Cand list[CAP + 32], top[MAX_TOP];
     int hit[CAP], n;
 };
@@ -240,7 +247,7 @@ struct Smem {
     uint64_t full[STAGES], empty[STAGES], folded[2], freed[2];
     Shared row[2];
     Row rows[ROWS];
-    Finish fin;
+    Finish fin[2];
     int scan[NW];
     int abort;
 };
@@ -262,24 +269,20 @@ __device__ __forceinline__ void rank(Finish &fin, int n, int top)
     __syncwarp();
 }
 
-// The `top`-th best of the warps' best lane maxima: at least `top` of the row's logits reach it.
+// The `top`-th best of the warps' best lane maxima, the greatest that `top` of them reach: at least `top` of
+// the row's logits reach it.
 __device__ __forceinline__ float bound_of(const Shared &sh, int top)
 {
     const int lane = threadIdx.x & 31;
     const float y0 = sh.best[lane], y1 = sh.best[32 + lane];
-    int p0 = 0, p1 = 0;  // places; among equals, by their order
-#pragma unroll 1
+    int p0 = 0, p1 = 0;
+#pragma unroll 2
     for (int a = 0; a < NW * SAMPLE; a += 4) {
-        const float4 o4 = *reinterpret_cast<const float4 *>(&sh.best[a]);
-        const float o[4] = {o4.x, o4.y, o4.z, o4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            p0 += o[i] > y0 || (o[i] == y0 && a + i < lane);
-            p1 += o[i] > y1 || (o[i] == y1 && a + i < 32 + lane);
-        }
+        const float4 o = *reinterpret_cast<const float4 *>(&sh.best[a]);
+        p0 += (o.x >= y0) + (o.y >= y0) + (o.z >= y0) + (o.w >= y0);
+        p1 += (o.x >= y1) + (o.y >= y1) + (o.z >= y1) + (o.w >= y1);
     }
-    const unsigned w0 = __ballot_sync(0xffffffffu, p0 == top - 1), w1 = __ballot_sync(0xffffffffu, p1 == top - 1);
-    return __shfl_sync(0xffffffffu, w0 ? y0 : y1, __ffs(w0 | w1) - 1);
+    return warp_max(fmaxf(p0 >= top ? y0 : NEG_INF, p1 >= top ? y1 : NEG_INF));
 }
 
 // The candidates of columns [from, to) of a row whose list overflowed, read again by a warp, with the
@@ -324,15 +327,12 @@ __device__ __forceinline__ int fault_of(const Params &P, int64_t r)
     [[maybe_unused]] const int64_t n = (int64_t)P.B * P.T;
     const int tok = SV_INB(r, n, 1201) ? P.tokens[r] : -1;
     const int idx = P.row_index ? (SV_INB(r, n, 1202) ? P.row_index[r] : -1) : 0;
+    const int b = (int)((unsigned)r / (unsigned)P.T);
+    const float temp = P.temperatures && SV_INB(b, P.B, 1203) ? P.temperatures[b] : 1.f;
     if (tok < -1 || tok >= P.V) return SPEC_VERIFY_DEV_BAD_TOKEN;
     if (idx < -1 || idx >= P.rows) return SPEC_VERIFY_DEV_BAD_ROW;
     if (tok < 0 || idx < 0) return -1;
-    if (P.temperatures) {
-        const int b = (int)((unsigned)r / (unsigned)P.T);
-        const float temp = SV_INB(b, P.B, 1203) ? P.temperatures[b] : 1.f;
-        if (!(temp >= 0.f && temp < 3.4e38f)) return SPEC_VERIFY_DEV_BAD_ROW;
-    }
-    return 0;
+    return temp >= 0.f && temp < 3.4e38f ? 0 : SPEC_VERIFY_DEV_BAD_ROW;
 }
 
 // The answers for a row's entry, by a warp; fin.top: its alternatives.
@@ -410,17 +410,18 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
     using E = Elt<T>;
     const int head = (int)((unsigned)(w.first + P.mis) & (E::VEC - 1));
     const T *row = static_cast<const T *>(P.logits) + w.first;
-    const float bound = bound_of(sh, top);
+    const float bound = fmaxf(bound_of(sh, top), LOWEST);  // -inf is no candidate
     const int step = (int)(j1 - j0 + SLOTS - 1) / SLOTS, slots = (int)(j1 - j0 + step - 1) / step;
     // A lane marks its cells, 4 of every 128, then all write theirs behind one another.
     unsigned mark[4] = {0, 0, 0, 0};
 #pragma unroll 2
     for (int c = 0; c < slots * (NT / 128); ++c) {
         const float4 y = *reinterpret_cast<const float4 *>(&sh.cell[0][0] + c * 128 + lane * 4);
-        mark[0] |= (unsigned)(y.x >= bound && y.x > NEG_INF) << c;
-        mark[1] |= (unsigned)(y.y >= bound && y.y > NEG_INF) << c;
-        mark[2] |= (unsigned)(y.z >= bound && y.z > NEG_INF) << c;
-        mark[3] |= (unsigned)(y.w >= bound && y.w > NEG_INF) << c;
+        const unsigned bit = 1u << c;
+        if (y.x >= bound) mark[0] |= bit;
+        if (y.y >= bound) mark[1] |= bit;
+        if (y.z >= bound) mark[2] |= bit;
+        if (y.w >= bound) mark[3] |= bit;
     }
     const int mine = __popc(mark[0]) + __popc(mark[1]) + __popc(mark[2]) + __popc(mark[3]);
     int at = mine;
@@ -439,49 +440,45 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
                 mark[i] &= mark[i] - 1;
             }
     __syncwarp();
-    // Their vectors, one per lane, FLY of them in flight: under the folding warps' streams a read takes
-    // a microsecond.  (What runs once per row is written to be short: its first run is bound by the
-    // fetching of its instructions, at some ten clocks each.)
-    constexpr int FLY = 3;
+    // Their vectors, FLY per lane in flight: under the folding warps' streams a read takes a microsecond.
+    // (What runs once per row is written to be short: its first run is bound by the fetching of its
+    // instructions, at some ten clocks each.)
     if (lane == 0) fin.n = hits > CAP ? CAP + 1 : 0;
     __syncwarp();
     const int vecs = hits > CAP ? 0 : hits * step * VPT;
 #pragma unroll 1
     for (int e0 = 0; e0 < vecs; e0 += 32 * FLY) {
-        uint4 x[FLY];
-        int col[FLY];
-#pragma unroll
-        for (int f = 0; f < FLY; ++f) {
-            const int e = e0 + f * 32 + lane, h = e / VPT;
-            x[f] = make_uint4(E::NEG, E::NEG, E::NEG, E::NEG);
-            col[f] = 0;
-            if (e < vecs) {
-                const int cell = fin.hit[step == 1 ? h : h / step];
-                const int64_t j = j0 + (int64_t)(cell / NT) * step + (step == 1 ? 0 : h % step);
-                const int64_t at = ((j * VPT + e % VPT) * NT + cell % NT) * E::VEC - head;
-                col[f] = (int)at;
-                if (j < j1 && at >= 0 && at + E::VEC <= P.V)
-                    x[f] = __ldg(reinterpret_cast<const uint4 *>(row + at));
-                else if (j < j1)
-                    for (int i = 0; i < E::VEC; ++i)
-                        if (at + i >= 0 && at + i < P.V) E::set(x[f], i, row, at + i);
+#pragma unroll 1
+        for (int f = 0; f < FLY && e0 + f * 32 + lane < vecs; ++f) {
+            const int e = e0 + f * 32 + lane, h = e / VPT, cell = fin.hit[step == 1 ? h : h / step];
+            const int64_t j = j0 + (int64_t)(cell / NT) * step + (step == 1 ? 0 : h % step);
+            const int64_t at = ((j * VPT + e % VPT) * NT + cell % NT) * E::VEC - head;
+            fin.col[f][lane] = (int)at;
+            if (j < j1 && at >= 0 && at + E::VEC <= P.V) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(&fin.vec[f][lane])), "l"(row + at)
+                             : "memory");
+            } else {
+                uint4 x = make_uint4(E::NEG, E::NEG, E::NEG, E::NEG);
+                for (int i = 0; i < E::VEC; ++i)
+                    if (j < j1 && at + i >= 0 && at + i < P.V) E::set(x, i, row, at + i);
+                fin.vec[f][lane] = x;
             }
         }
-#pragma unroll
-        for (int f = 0; f < FLY; ++f)
+        asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
-            for (int i = 0; i < E::VEC; ++i) {
-                const float y = E::shift(x[f]);
-                if (y >= bound && y > NEG_INF) {
-                    const int at = atomicAdd(&fin.n, 1);
-                    if (at < CAP) fin.list[at] = {y, col[f] + i};
-                }
+        for (int f = 0; f < FLY && e0 + f * 32 + lane < vecs; ++f)
+            for (unsigned mask = E::reach(fin.vec[f][lane], bound); mask; mask &= mask - 1) {
+                const int i = __ffs(mask) - 1, at = atomicAdd(&fin.n, 1);
+                if (at < CAP) fin.list[at] = {E::at(&fin.vec[f][lane], i), fin.col[f][lane] + i};
             }
     }
     __syncwarp();
     const int listed = fin.n;
-    if (listed > CAP) list_again<T>(P, fin, w, j0 * TILE_VEC * E::VEC - head, j1 * TILE_VEC * E::VEC - head, top, bound_of(sh, 1));
-    else rank(fin, listed, top);
+    if (listed > CAP)
+        list_again<T>(P, fin, w, j0 * TILE_VEC * E::VEC - head, j1 * TILE_VEC * E::VEC - head, top,
+                      warp_max(fmaxf(sh.best[lane], sh.best[32 + lane])));
+    else
+        rank(fin, listed, top);
     if (j0 == 0 && j1 == P.tpr) {
         answer<T>(P, fin, w, M, z, s, n);
         return;
@@ -492,15 +489,14 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
     Part *part = part_of(cta);
     if (lane == 0) part->m = M, part->z = z, part->s = s, part->count = n;
     if (lane < top) part->top[lane] = fin.top[lane];
-    __threadfence();
     __syncwarp();
-    bool last = false;
-    if (lane == 0) {
-        last = atomicAdd(&P.counters[c0], 1u) == (unsigned)(c1 - c0);
-        if (last) P.counters[c0] = 0;
-    }
-    if (!__any_sync(0xffffffffu, last)) return;
-    __threadfence();
+    unsigned came = 0;
+    if (lane == 0)
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(came) : "l"(&P.counters[c0]) : "memory");
+    came = __shfl_sync(0xffffffffu, came, 0);
+    __syncwarp();
+    if (came != (unsigned)(c1 - c0)) return;
+    if (lane == 0) P.counters[c0] = 0;
     // All of a round's reads are in flight together.
     constexpr int FLYP = 8;
     auto best_of = [&](int x) {
@@ -694,12 +690,13 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
         if (warp > NW) {
             // ---- rows that are folded ----------------------------------------------------------
             for (int64_t q = base; q < base + ROWS && q <= row_last; ++q, ++rr) {
+                if ((rr & 1) != warp - NW - 1) continue;
                 Row w = sm.rows[q - base];
                 if (SV_INB(w.first + w.tok, (int64_t)P.B * P.rows * P.V, 1206))
                     w.x = E::load(static_cast<const T *>(P.logits) + w.first, w.tok);
                 const bool ok = tc::bar_wait(tc::smem_u32(&sm.folded[rr & 1]), (rr / 2) & 1, abort);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                finish<T>(P, sm.fin, sm.row[rr & 1], w, q, q == row_first ? t0 - q * P.tpr : 0,
+                finish<T>(P, sm.fin[rr & 1], sm.row[rr & 1], w, q, q == row_first ? t0 - q * P.tpr : 0,
                           q == row_last ? t1 - q * P.tpr : P.tpr, total, G, top);
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem_u32(&sm.freed[rr & 1]));
