@@ -35,7 +35,10 @@ constexpr int CAP = 256;             // candidates the list holds
 constexpr int FLY = 4;               // vectors that a finishing lane asks for at once
 constexpr int SLOTS = 16;            // cells per thread and row; longer rows have cells of several tiles
 static_assert(SLOTS * NT / 128 <= 32, "a bit for each of a lane's cells");
-constexpr int SAMPLE = 2 * MAX_TOP / NW;  // lane maxima of each warp that the bound comes from: 64 in all
+// Lane maxima of each warp that the bound comes from: 2 * top in all, so that a warp with more than its share of the
+// best costs a few candidates only.
+__device__ __forceinline__ int sample_of(int top) { return (2 * top + NW - 1) / NW; }
+constexpr int SAMPLES = 2 * MAX_TOP;
 constexpr int CTAS_PER_SM = 2;
 constexpr int MAX_CTAS = 1024;
 constexpr int ROWS = 128;            // rows of its run that a CTA lists at a time
@@ -229,7 +232,7 @@ struct Row {
 // What a row's warps share; two of them, so that the next row may begin before the last one is done.
 struct Shared {
     __align__(16) float cell[SLOTS][NT];
-    __align__(16) float best[NW * SAMPLE];  // each warp's best lane maxima
+    __align__(16) float best[SAMPLES];  // each warp's best lane maxima
     float m[NW], z[NW], s[NW];
     int count[NW];
 };
@@ -274,10 +277,11 @@ __device__ __forceinline__ void rank(Finish &fin, int n, int top)
 __device__ __forceinline__ float bound_of(const Shared &sh, int top)
 {
     const int lane = threadIdx.x & 31;
-    const float y0 = sh.best[lane], y1 = sh.best[32 + lane];
+    const int n = NW * sample_of(top);
+    const float y0 = lane < n ? sh.best[lane] : NEG_INF, y1 = 32 + lane < n ? sh.best[32 + lane] : NEG_INF;
     int p0 = 0, p1 = 0;
 #pragma unroll 2
-    for (int a = 0; a < NW * SAMPLE; a += 4) {
+    for (int a = 0; a < n; a += 4) {
         const float4 o = *reinterpret_cast<const float4 *>(&sh.best[a]);
         p0 += (o.x >= y0) + (o.y >= y0) + (o.z >= y0) + (o.w >= y0);
         p1 += (o.x >= y1) + (o.y >= y1) + (o.z >= y1) + (o.w >= y1);
@@ -381,11 +385,12 @@ __device__ __forceinline__ void answer(const Params &P, const Finish &fin, const
     }
 }
 
-// A row, or its part in this CTA's run (tiles [j0, j1)), is folded: by the finishing warp.  A part goes
-// to the workspace, and the warp that brings a row's last part joins them, in order.
+// A row, or its part in this CTA's run (tiles [j0, j1)), is folded: by a finishing warp.  A part goes
+// to the workspace, and the warp that brings a row's last part joins them, in order.  CTAs c0 to c1 have
+// the row's parts; first0: c0's run begins with it.
 template <typename T>
-__device__ __forceinline__ void finish(const Params &P, Finish &fin, const Shared &sh, const Row &w, int64_t q, int64_t j0, int64_t j1,
-                                    int64_t total, int G, int top)
+__device__ __forceinline__ void finish(const Params &P, Finish &fin, const Shared &sh, const Row &w, int64_t j0, int64_t j1, int c0,
+                                    int c1, bool first0, int top)
 {
     const int lane = threadIdx.x & 31, cta = blockIdx.x;
     float M = lane < NW ? sh.m[lane] : NEG_INF;
@@ -414,7 +419,7 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
     const int step = (int)(j1 - j0 + SLOTS - 1) / SLOTS, slots = (int)(j1 - j0 + step - 1) / step;
     // A lane marks its cells, 4 of every 128, then all write theirs behind one another.
     unsigned mark[4] = {0, 0, 0, 0};
-#pragma unroll 2
+#pragma unroll 4
     for (int c = 0; c < slots * (NT / 128); ++c) {
         const float4 y = *reinterpret_cast<const float4 *>(&sh.cell[0][0] + c * 128 + lane * 4);
         const unsigned bit = 1u << c;
@@ -450,9 +455,9 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
     for (int e0 = 0; e0 < vecs; e0 += 32 * FLY) {
 #pragma unroll 1
         for (int f = 0; f < FLY && e0 + f * 32 + lane < vecs; ++f) {
-            const int e = e0 + f * 32 + lane, h = e / VPT, cell = fin.hit[step == 1 ? h : h / step];
-            const int64_t j = j0 + (int64_t)(cell / NT) * step + (step == 1 ? 0 : h % step);
-            const int64_t at = ((j * VPT + e % VPT) * NT + cell % NT) * E::VEC - head;
+            const unsigned e = e0 + f * 32 + lane, h = e / VPT, cell = fin.hit[step == 1 ? h : h / step];
+            const int j = (int)j0 + (int)(cell / NT) * step + (step == 1 ? 0 : (int)(h % step));
+            const int64_t at = (int64_t)((((unsigned)j * VPT + e % VPT) * NT + cell % NT) * E::VEC) - head;
             fin.col[f][lane] = (int)at;
             if (j < j1 && at >= 0 && at + E::VEC <= P.V) {
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(&fin.vec[f][lane])), "l"(row + at)
@@ -476,15 +481,13 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
     const int listed = fin.n;
     if (listed > CAP)
         list_again<T>(P, fin, w, j0 * TILE_VEC * E::VEC - head, j1 * TILE_VEC * E::VEC - head, top,
-                      warp_max(fmaxf(sh.best[lane], sh.best[32 + lane])));
+                      warp_max(lane < NW ? sh.best[lane * sample_of(top)] : NEG_INF));
     else
         rank(fin, listed, top);
-    if (j0 == 0 && j1 == P.tpr) {
+    if (c0 == c1) {
         answer<T>(P, fin, w, M, z, s, n);
         return;
     }
-    const int c0 = cta_of(q * P.tpr, total, G), c1 = cta_of((q + 1) * P.tpr - 1, total, G);
-    const bool first0 = run_begin(c0, total, G) == q * P.tpr;
     auto part_of = [&](int x) { return reinterpret_cast<Part *>(P.parts) + 2 * x + (x == c0 && !first0); };
     Part *part = part_of(cta);
     if (lane == 0) part->m = M, part->z = z, part->s = s, part->count = n;
@@ -694,10 +697,17 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
                 Row w = sm.rows[q - base];
                 if (SV_INB(w.first + w.tok, (int64_t)P.B * P.rows * P.V, 1206))
                     w.x = E::load(static_cast<const T *>(P.logits) + w.first, w.tok);
+                const int64_t j0 = q == row_first ? t0 - q * P.tpr : 0, j1 = q == row_last ? t1 - q * P.tpr : P.tpr;
+                int c0 = cta, c1 = cta;
+                bool first0 = true;
+                if (j0 > 0 || j1 < P.tpr) {
+                    c0 = cta_of(q * P.tpr, total, G);
+                    c1 = cta_of((q + 1) * P.tpr - 1, total, G);
+                    first0 = run_begin(c0, total, G) == q * P.tpr;
+                }
                 const bool ok = tc::bar_wait(tc::smem_u32(&sm.folded[rr & 1]), (rr / 2) & 1, abort);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                finish<T>(P, sm.fin[rr & 1], sm.row[rr & 1], w, q, q == row_first ? t0 - q * P.tpr : 0,
-                          q == row_last ? t1 - q * P.tpr : P.tpr, total, G, top);
+                finish<T>(P, sm.fin[rr & 1], sm.row[rr & 1], w, j0, j1, c0, c1, first0, top);
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem_u32(&sm.freed[rr & 1]));
             }
@@ -805,12 +815,13 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
                 s += __shfl_xor_sync(0xffffffffu, s, o);
                 n += __shfl_xor_sync(0xffffffffu, n, o);
             }
-#pragma unroll
-            for (int a = 0; a < SAMPLE; ++a) {
+            const int sample = sample_of(top);
+#pragma unroll 1
+            for (int a = 0; a < sample; ++a) {
                 const float y = warp_max(best);
                 const unsigned who = __ballot_sync(0xffffffffu, best == y);
                 if (lane == __ffs(who) - 1) best = NEG_INF;
-                if (lane == 0) sh.best[warp * SAMPLE + a] = y;
+                if (lane == 0) sh.best[warp * sample + a] = y;
             }
             if (lane == 0) {
                 sh.m[warp] = wm;
