@@ -326,9 +326,9 @@ __device__ __forceinline__ int64_t run_begin(int c, int64_t total, int G) { retu
 __device__ __forceinline__ int cta_of(int64_t x, int64_t total, int G) { return (int)quotient((x + 1) * G - 1, total); }
 
 // Whether entry r has a row to read (0), nothing (-1), or a fault (a device status code).
-__device__ __forceinline__ int fault_of(const Params &P, int64_t r)
+__device__ __forceinline__ int fault_of(const Params &P, int r)
 {
-    [[maybe_unused]] const int64_t n = (int64_t)P.B * P.T;
+    [[maybe_unused]] const int n = P.B * P.T;
     const int tok = SV_INB(r, n, 1201) ? P.tokens[r] : -1;
     const int idx = P.row_index ? (SV_INB(r, n, 1202) ? P.row_index[r] : -1) : 0;
     const int b = (int)((unsigned)r / (unsigned)P.T);
@@ -583,26 +583,25 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // The entries that have a row; what the others answer is written here, each by one CTA.
-    const int64_t R = (int64_t)P.B * P.T;
-    const int64_t per = (R + NT - 1) / NT;
+    const int R = P.B * P.T, per = (int)((unsigned)(R + NT - 1) / NT);
+    const int r0 = tid * per, r1 = tid < NT ? min(r0 + per, R) : 0;  // the thread's
     int mine = 0;
-    unsigned long long which = 0;  // of the thread's first 64 entries
-    if (tid < NT) {
+    unsigned which = 0;  // of its first 32
+    {
 #pragma unroll 2
-        for (int64_t i = 0; i < per && tid * per + i < R; ++i) {
-            const int64_t r = tid * per + i;
+        for (int r = r0; r < r1; ++r) {
             const int code = fault_of(P, r);
             if (code == 0) {
                 ++mine;
-                if (i < 64) which |= 1ull << i;
+                if (r - r0 < 32) which |= 1u << (r - r0);
             } else if ((unsigned)r % gridDim.x == (unsigned)cta) {
                 P.logprobs[r] = code > 0 ? NAN : 0.f;
                 if (P.entropy) P.entropy[r] = code > 0 ? NAN : 0.f;
                 if (P.ranks) P.ranks[r] = code > 0 ? -1 : 0;
 #pragma unroll 1
                 for (int k = 0; k < P.top; ++k) {
-                    P.top_ids[r * P.top + k] = -1;
-                    P.top_logprobs[r * P.top + k] = code > 0 ? NAN : NEG_INF;
+                    P.top_ids[(int64_t)r * P.top + k] = -1;
+                    P.top_logprobs[(int64_t)r * P.top + k] = code > 0 ? NAN : NEG_INF;
                 }
                 if (code > 0 && P.dev_status) atomicMax(P.dev_status, code);
             }
@@ -616,39 +615,35 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
     }
     if (lane == 31 && warp < NW) sm.scan[warp] = incl;
     __syncthreads();
-    int64_t before = incl - mine, nrows = 0;
-    for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += sm.scan[w];
-        nrows += sm.scan[w];
-    }
-    const int64_t total = nrows * P.tpr;
+    const int in = lane < NW ? sm.scan[lane] : 0;
+    const int before = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? in : 0), nrows = __reduce_add_sync(0xffffffffu, in);
+    const int64_t total = (int64_t)nrows * P.tpr;
     const int G = total < (int64_t)gridDim.x ? (int)total : (int)gridDim.x;
     if (cta >= G) return;
     // Odd lanes work on the run's end, even ones on its beginning.
     const int64_t edge = run_begin(cta + (lane & 1), total, G) - (lane & 1), edge_row = quotient(edge, P.tpr);
     const int64_t t0 = __shfl_sync(0xffffffffu, edge, 0), t1 = __shfl_sync(0xffffffffu, edge, 1) + 1;
-    const int64_t row_first = __shfl_sync(0xffffffffu, edge_row, 0), row_last = __shfl_sync(0xffffffffu, edge_row, 1);
+    const int row_first = __shfl_sync(0xffffffffu, (int)edge_row, 0), row_last = __shfl_sync(0xffffffffu, (int)edge_row, 1);
     const uintptr_t base_addr = reinterpret_cast<uintptr_t>(P.logits);
     const uintptr_t end_addr = base_addr + (uintptr_t)P.B * P.rows * P.V * sizeof(T);
     const uintptr_t copy_from = (base_addr + 15) & ~(uintptr_t)15, copy_to = end_addr & ~(uintptr_t)15;
 
     int k = 0, rr = 0;  // tiles copied or folded; rows folded
-    for (int64_t base = row_first; base <= row_last; base += ROWS) {
+    for (int base = row_first; base <= row_last; base += ROWS) {
         // Entries of the run's next rows.
         if (base > row_first) __syncthreads();
         if (mine && before + mine > base && before < base + ROWS) {
-            int64_t at = before;
+            int at = before;
 #pragma unroll 1
-            for (int64_t i = 0; i < per && tid * per + i < R && at < base + ROWS; ++i) {
-                const int64_t r = tid * per + i;
-                if (i < 64 ? !((which >> i) & 1) : fault_of(P, r) != 0) continue;
+            for (int r = r0; r < r1 && at < base + ROWS; ++r) {
+                if (r - r0 < 32 ? !((which >> (r - r0)) & 1) : fault_of(P, r) != 0) continue;
                 if (at >= base) {
                     const int b = (int)((unsigned)r / (unsigned)P.T);
-                    const int idx = P.row_index ? P.row_index[r] : (int)(r - (int64_t)b * P.T);
+                    const int idx = P.row_index ? P.row_index[r] : r - b * P.T;
                     const float temp = P.temperatures ? P.temperatures[b] : P.temperature;
                     Row &w = sm.rows[at - base];
                     w.first = ((int64_t)b * P.rows + idx) * P.V;
-                    w.r = (int)r;
+                    w.r = r;
                     w.tok = P.tokens[r];
                     w.temp = temp == 0.f ? 1.f : temp;
                 }
@@ -659,7 +654,7 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
         if (warp == NW) {
             // ---- copies ------------------------------------------------------------------------
             if (lane == 0)
-                for (int64_t q = base; q < base + ROWS && q <= row_last; ++q) {
+                for (int q = base; q < base + ROWS && q <= row_last; ++q) {
                     bool ok = true;
                     const int64_t rowf = sm.rows[q - base].first;
                     const int head = (int)((unsigned)(rowf + P.mis) & (VEC - 1));
@@ -692,7 +687,7 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
         }
         if (warp > NW) {
             // ---- rows that are folded ----------------------------------------------------------
-            for (int64_t q = base; q < base + ROWS && q <= row_last; ++q, ++rr) {
+            for (int q = base; q < base + ROWS && q <= row_last; ++q, ++rr) {
                 if ((rr & 1) != warp - NW - 1) continue;
                 Row w = sm.rows[q - base];
                 if (SV_INB(w.first + w.tok, (int64_t)P.B * P.rows * P.V, 1206))
@@ -714,7 +709,7 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
             continue;
         }
         // ---- folds -----------------------------------------------------------------------------
-        for (int64_t q = base; q < base + ROWS && q <= row_last; ++q, ++rr) {
+        for (int q = base; q < base + ROWS && q <= row_last; ++q, ++rr) {
             const int64_t rowf = sm.rows[q - base].first;
             const float temp = sm.rows[q - base].temp;
             const T *row = static_cast<const T *>(P.logits) + rowf;
