@@ -57,7 +57,7 @@ struct Params {
     float *top_logprobs;
     int32_t *dev_status;
     int mis;       // logits base address mod 16, in elements
-    int64_t tpr;   // tiles per row
+    int tpr;       // tiles per row
     unsigned *counters;
     unsigned char *parts;
 };
@@ -389,7 +389,7 @@ __device__ __forceinline__ void answer(const Params &P, const Finish &fin, const
 // to the workspace, and the warp that brings a row's last part joins them, in order.  CTAs c0 to c1 have
 // the row's parts; first0: c0's run begins with it.
 template <typename T>
-__device__ __forceinline__ void finish(const Params &P, Finish &fin, const Shared &sh, const Row &w, int64_t j0, int64_t j1, int c0,
+__device__ __forceinline__ void finish(const Params &P, Finish &fin, const Shared &sh, const Row &w, int j0, int j1, int c0,
                                     int c1, bool first0, int top)
 {
     const int lane = threadIdx.x & 31, cta = blockIdx.x;
@@ -416,7 +416,7 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
     const int head = (int)((unsigned)(w.first + P.mis) & (E::VEC - 1));
     const T *row = static_cast<const T *>(P.logits) + w.first;
     const float bound = fmaxf(bound_of(sh, top), LOWEST);  // -inf is no candidate
-    const int step = (int)(j1 - j0 + SLOTS - 1) / SLOTS, slots = (int)(j1 - j0 + step - 1) / step;
+    const int step = (int)((unsigned)(j1 - j0 + SLOTS - 1) / SLOTS), slots = (int)((unsigned)(j1 - j0 + step - 1) / (unsigned)step);
     // A lane marks its cells, 4 of every 128, then all write theirs behind one another.
     unsigned mark[4] = {0, 0, 0, 0};
 #pragma unroll 4
@@ -456,7 +456,7 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
 #pragma unroll 1
         for (int f = 0; f < FLY && e0 + f * 32 + lane < vecs; ++f) {
             const unsigned e = e0 + f * 32 + lane, h = e / VPT, cell = fin.hit[step == 1 ? h : h / step];
-            const int j = (int)j0 + (int)(cell / NT) * step + (step == 1 ? 0 : (int)(h % step));
+            const int j = j0 + (int)(cell / NT) * step + (step == 1 ? 0 : (int)(h % step));
             const int64_t at = (int64_t)((((unsigned)j * VPT + e % VPT) * NT + cell % NT) * E::VEC) - head;
             fin.col[f][lane] = (int)at;
             if (j < j1 && at >= 0 && at + E::VEC <= P.V) {
@@ -480,7 +480,7 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
     __syncwarp();
     const int listed = fin.n;
     if (listed > CAP)
-        list_again<T>(P, fin, w, j0 * TILE_VEC * E::VEC - head, j1 * TILE_VEC * E::VEC - head, top,
+        list_again<T>(P, fin, w, (int64_t)j0 * TILE_VEC * E::VEC - head, (int64_t)j1 * TILE_VEC * E::VEC - head, top,
                       warp_max(lane < NW ? sh.best[lane * sample_of(top)] : NEG_INF));
     else
         rank(fin, listed, top);
@@ -624,6 +624,7 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
     const int64_t edge = run_begin(cta + (lane & 1), total, G) - (lane & 1), edge_row = quotient(edge, P.tpr);
     const int64_t t0 = __shfl_sync(0xffffffffu, edge, 0), t1 = __shfl_sync(0xffffffffu, edge, 1) + 1;
     const int row_first = __shfl_sync(0xffffffffu, (int)edge_row, 0), row_last = __shfl_sync(0xffffffffu, (int)edge_row, 1);
+    const int begin = (int)(t0 - (int64_t)row_first * P.tpr), end = (int)(t1 - (int64_t)row_last * P.tpr);  // the run's tiles of these
     const uintptr_t base_addr = reinterpret_cast<uintptr_t>(P.logits);
     const uintptr_t end_addr = base_addr + (uintptr_t)P.B * P.rows * P.V * sizeof(T);
     const uintptr_t copy_from = (base_addr + 15) & ~(uintptr_t)15, copy_to = end_addr & ~(uintptr_t)15;
@@ -659,9 +660,9 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
                     const int64_t rowf = sm.rows[q - base].first;
                     const int head = (int)((unsigned)(rowf + P.mis) & (VEC - 1));
                     const int nvec = (int)(((unsigned)P.V + head + VEC - 1) / VEC);
-                    const int64_t j0 = q == row_first ? t0 - q * P.tpr : 0, j1 = q == row_last ? t1 - q * P.tpr : P.tpr;
+                    const int j0 = q == row_first ? begin : 0, j1 = q == row_last ? end : P.tpr;
                     const uintptr_t first = base_addr + (uintptr_t)(rowf - head) * sizeof(T);  // may lie before the logits
-                    for (int64_t j = j0; j < j1; ++j, ++k) {
+                    for (int j = j0; j < j1; ++j, ++k) {
                         const int s = k % STAGES;
                         if (k >= STAGES)
                             ok = tc::bar_wait(tc::smem_u32(&sm.empty[s]), (k / STAGES + 1) & 1, abort);
@@ -692,13 +693,14 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
                 Row w = sm.rows[q - base];
                 if (SV_INB(w.first + w.tok, (int64_t)P.B * P.rows * P.V, 1206))
                     w.x = E::load(static_cast<const T *>(P.logits) + w.first, w.tok);
-                const int64_t j0 = q == row_first ? t0 - q * P.tpr : 0, j1 = q == row_last ? t1 - q * P.tpr : P.tpr;
+                const int j0 = q == row_first ? begin : 0, j1 = q == row_last ? end : P.tpr;
                 int c0 = cta, c1 = cta;
                 bool first0 = true;
                 if (j0 > 0 || j1 < P.tpr) {
-                    c0 = cta_of(q * P.tpr, total, G);
-                    c1 = cta_of((q + 1) * P.tpr - 1, total, G);
-                    first0 = run_begin(c0, total, G) == q * P.tpr;
+                    const int64_t t = (int64_t)q * P.tpr;
+                    c0 = cta_of(t, total, G);
+                    c1 = cta_of(t + P.tpr - 1, total, G);
+                    first0 = run_begin(c0, total, G) == t;
                 }
                 const bool ok = tc::bar_wait(tc::smem_u32(&sm.folded[rr & 1]), (rr / 2) & 1, abort);
                 if (!__all_sync(0xffffffffu, ok)) break;
@@ -715,8 +717,8 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
             const T *row = static_cast<const T *>(P.logits) + rowf;
             const int head = (int)((unsigned)(rowf + P.mis) & (VEC - 1));  // the row's first element in its first vector
             const int nvec = (int)(((unsigned)P.V + head + VEC - 1) / VEC);
-            const int64_t j0 = q == row_first ? t0 - q * P.tpr : 0, j1 = q == row_last ? t1 - q * P.tpr : P.tpr;
-            const int step = (int)(j1 - j0 + SLOTS - 1) / SLOTS;
+            const int j0 = q == row_first ? begin : 0, j1 = q == row_last ? end : P.tpr;
+            const int step = (int)((unsigned)(j1 - j0 + SLOTS - 1) / SLOTS);
             const float c = 1.44269504f / temp;
             const uint64_t c2 = sv::f2(c, c);
             Shared &sh = sm.row[rr & 1];
@@ -730,7 +732,7 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
             int slot = 0, left = step;
             typename E::Count count;
             count.start(tok_x);
-            for (int64_t j = j0; j < j1; ++j, ++k) {
+            for (int j = j0; j < j1; ++j, ++k) {
                 const int st = k % STAGES;
                 tc::bar_wait(tc::smem_u32(&sm.full[st]), (k / STAGES) & 1, abort);
                 uint4 x4[VPT];
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
                     // was not copied.
 #pragma unroll
                     for (int i = 0; i < VPT; ++i) {
-                        const int v = (int)(j * TILE_VEC) + i * NT + tid;
+                        const int v = j * TILE_VEC + i * NT + tid;
                         const int64_t col = (int64_t)v * VEC - head;
                         if (col >= 0 && col + VEC <= P.V) continue;
                         x4[i] = make_uint4(E::NEG, E::NEG, E::NEG, E::NEG);
@@ -948,7 +950,7 @@ extern "C" int spec_verify_logprobs(const void *logits, int dtype, const int32_t
     P.top_logprobs = top_logprobs;
     P.dev_status = dev_status;
     P.mis = (int)((uintptr_t)logits % 16) / size;
-    P.tpr = (((int64_t)V + 2 * vec - 2) / vec + TILE_VEC - 1) / TILE_VEC;  // wherever the row begins
+    P.tpr = (int)((((int64_t)V + 2 * vec - 2) / vec + TILE_VEC - 1) / TILE_VEC);  // wherever the row begins
     P.counters = static_cast<unsigned *>(workspace);
     P.parts = static_cast<unsigned char *>(workspace) + COUNTER_BYTES;
     int grid = sms * CTAS_PER_SM < MAX_CTAS ? sms * CTAS_PER_SM : MAX_CTAS;
