@@ -32,7 +32,7 @@ constexpr int VPT = 4;               // 16-byte vectors per thread and tile
 constexpr int TILE_VEC = NT * VPT;
 constexpr int STAGES = 4;
 constexpr int CAP = 256;             // candidates the list holds
-constexpr int FLY = 4;               // vectors that a finishing lane asks for at once
+constexpr int FLY = 4;               // vectors that a finishing lane asks for at once; a bit for each of their logits
 constexpr int SLOTS = 16;            // cells per thread and row; longer rows have cells of several tiles
 static_assert(SLOTS * NT / 128 <= 32, "a bit for each of a lane's cells");
 // Lane maxima of each warp that the bound comes from: 2 * top in all, so that a warp with more than its share of the
@@ -242,7 +242,7 @@ struct Finish {
     uint4 vec[FLY][32];  // each lane's vectors
     int col[FLY][32];    // and their first columns
     Cand list[CAP + 32], top[MAX_TOP];
-    int hit[CAP], n;
+    int hit[CAP];
 };
 
 struct Smem {
@@ -448,8 +448,7 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
     // Their vectors, FLY per lane in flight: under the folding warps' streams a read takes a microsecond.
     // (What runs once per row is written to be short: its first run is bound by the fetching of its
     // instructions, at some ten clocks each.)
-    if (lane == 0) fin.n = hits > CAP ? CAP + 1 : 0;
-    __syncwarp();
+    int listed = hits > CAP ? CAP + 1 : 0;
     const int vecs = hits > CAP ? 0 : hits * step * VPT;
 #pragma unroll 1
     for (int e0 = 0; e0 < vecs; e0 += 32 * FLY) {
@@ -470,15 +469,18 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        unsigned mask = 0;
 #pragma unroll 1
-        for (int f = 0; f < FLY && e0 + f * 32 + lane < vecs; ++f)
-            for (unsigned mask = E::reach(fin.vec[f][lane], bound); mask; mask &= mask - 1) {
-                const int i = __ffs(mask) - 1, at = atomicAdd(&fin.n, 1);
-                if (at < CAP) fin.list[at] = {E::at(&fin.vec[f][lane], i), fin.col[f][lane] + i};
-            }
+        for (int f = 0; f < FLY && e0 + f * 32 + lane < vecs; ++f) mask |= E::reach(fin.vec[f][lane], bound) << f * E::VEC;
+        __syncwarp();
+        // Each lane's next one, until no lane has any.
+        for (unsigned in; (in = __ballot_sync(0xffffffffu, mask != 0)) != 0; mask &= mask - 1) {
+            const int i = __ffs(mask) - 1, f = i / E::VEC, at = listed + __popc(in & ((1u << lane) - 1));
+            if (mask && at < CAP) fin.list[at] = {E::at(&fin.vec[f][lane], i % E::VEC), fin.col[f][lane] + i % E::VEC};
+            listed += __popc(in);
+        }
     }
     __syncwarp();
-    const int listed = fin.n;
     if (listed > CAP)
         list_again<T>(P, fin, w, (int64_t)j0 * TILE_VEC * E::VEC - head, (int64_t)j1 * TILE_VEC * E::VEC - head, top,
                       warp_max(lane < NW ? sh.best[lane * sample_of(top)] : NEG_INF));

@@ -138,7 +138,9 @@ def test_peaked_and_flat():
 def test_absent_tokens_and_row_indices():
     x, tok = rows(5, 6, 3001, BF, seed=7)
     x[1, 2] = math.nan  # a row that nothing asks for
-    index = torch.stack([torch.randperm(6) for _ in range(5)]).int().to(DEV)
+    g = torch.Generator().manual_seed(7)
+    index = torch.stack([torch.randperm(6, generator=g) for _ in range(5)]).int().to(DEV)
+    index[1] = torch.tensor([0, 2, 1, 4, 3, 5])  # the row of NaN stays with an entry whose token is absent
     tok[0, 3:], tok[1], tok[4, 0] = -1, -1, -1
     check(x, tok, 3)
     index[2, 4:] = -1
