@@ -417,33 +417,27 @@ __device__ __forceinline__ void finish(const Params &P, Finish &fin, const Share
     const T *row = static_cast<const T *>(P.logits) + w.first;
     const float bound = fmaxf(bound_of(sh, top), LOWEST);  // -inf is no candidate
     const int step = (int)((unsigned)(j1 - j0 + SLOTS - 1) / SLOTS), slots = (int)((unsigned)(j1 - j0 + step - 1) / (unsigned)step);
-    // A lane marks its cells, 4 of every 128, then all write theirs behind one another.
-    unsigned mark[4] = {0, 0, 0, 0};
+    // A lane marks which of its fours of cells have one, then all list theirs in turn.
+    unsigned mark = 0;
 #pragma unroll 4
     for (int c = 0; c < slots * (NT / 128); ++c) {
         const float4 y = *reinterpret_cast<const float4 *>(&sh.cell[0][0] + c * 128 + lane * 4);
-        const unsigned bit = 1u << c;
-        if (y.x >= bound) mark[0] |= bit;
-        if (y.y >= bound) mark[1] |= bit;
-        if (y.z >= bound) mark[2] |= bit;
-        if (y.w >= bound) mark[3] |= bit;
+        if (fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)) >= bound) mark |= 1u << c;
     }
-    const int mine = __popc(mark[0]) + __popc(mark[1]) + __popc(mark[2]) + __popc(mark[3]);
-    int at = mine;
+    int hits = 0;
+    for (; __any_sync(0xffffffffu, mark != 0); mark &= mark - 1) {
+        const int four = (__ffs(mark) - 1) * 128 + lane * 4;
+        float4 y = make_float4(NEG_INF, NEG_INF, NEG_INF, NEG_INF);
+        if (mark) y = *reinterpret_cast<const float4 *>(&sh.cell[0][0] + four);
+        const float a[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, at, o);
-        if (lane >= o) at += x;
+        for (int i = 0; i < 4; ++i) {
+            const unsigned in = __ballot_sync(0xffffffffu, a[i] >= bound);
+            const int at = hits + __popc(in & ((1u << lane) - 1));
+            if (a[i] >= bound && at < CAP) fin.hit[at] = four + i;
+            hits += __popc(in);
+        }
     }
-    const int hits = __shfl_sync(0xffffffffu, at, 31);
-    at -= mine;
-    if (hits <= CAP)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            while (mark[i]) {
-                fin.hit[at++] = (__ffs(mark[i]) - 1) * 128 + lane * 4 + i;
-                mark[i] &= mark[i] - 1;
-            }
     __syncwarp();
     // Their vectors, FLY per lane in flight: under the folding warps' streams a read takes a microsecond.
     // (What runs once per row is written to be short: its first run is bound by the fetching of its
