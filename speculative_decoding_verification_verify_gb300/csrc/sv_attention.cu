@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
             tc::bar_init(tc::smem_u32(&ms.sfull[i]), 1);
             tc::bar_init(tc::smem_u32(&ms.sempty[i]), 256);
             tc::bar_init(tc::smem_u32(&ms.qfull[i]), 64);
-            tc::bar_init(tc::smem_u32(&ms.qempty[i]), 3);
+            tc::bar_init(tc::smem_u32(&ms.qempty[i]), 9);  // the last scores' products, the softmax's warps
             ms.joins[i] = 0;
         }
         for (int i = 0; i < SEGS; ++i) {
@@ -245,11 +245,12 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
     }
     if (lane == 31) ms.scan[warp] = incl;
     __syncthreads();
-    int64_t before = incl - mine, total = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) before += ms.scan[w];
-        total += ms.scan[w];
-    }
+    // (Sums over the warps in two halves of 32 bits: costs are below 2^56.)
+    const int64_t in = lane < NT / 32 ? ms.scan[lane] : 0;
+    auto sum = [](int64_t x) {
+        return ((int64_t)__reduce_add_sync(0xffffffffu, (unsigned)(x >> 24)) << 24) + __reduce_add_sync(0xffffffffu, (unsigned)x & 0xffffffu);
+    };
+    const int64_t before = incl - mine + sum(lane < warp ? in : 0), total = sum(in);
     // Small batches leave the last CTAs out: a run costs COST_TILE at least.
     const int G = total / COST_TILE < (int64_t)gridDim.x ? (int)(total / COST_TILE) : (int)gridDim.x;
     // Odd lanes work out the run's end, even ones its beginning.
@@ -532,6 +533,9 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
         } else if (warp < 8) {
             // ---- queries and the tree's mask -----------------------------------------------
             const int t = tid - 192;
+            constexpr int CH = DP / 8, RPI = 64 / CH, PER = NQ / RPI;  // 16-byte chunks of a row; rows at a time
+            const int step_n = (int)((unsigned)RPI / (unsigned)P.G), step_h = RPI - step_n * P.G;  // RPI rows in nodes and heads
+            const int64_t src_step = step_n * P.q_row + step_h * P.D, src_wrap = P.q_row - (int64_t)P.G * P.D;
             int seg = -1;
             Seg g = {};
             for (;;) {
@@ -549,23 +553,26 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                     wrong = t == 0 ? p != -1 : (p < 0 || p >= t);
                     if (wrong) p = -1;
                 }
-                constexpr int CH = DP / 8, RPI = 64 / CH, PER = NQ / RPI;  // 16-byte chunks of a row; rows at a time
                 const int ch = t % CH, r0 = t / CH;
                 bool ok = true;
+                const unsigned gr = g.qt * NQ + r0;
+                int n = (int)(gr / (unsigned)P.G), h = (int)gr - n * P.G;
+                const uint16_t *src = P.q + ((int64_t)g.b * P.N + n) * P.q_row + (int64_t)(g.h * P.G + h) * P.D + ch * 8;
+                const bool wide = ch * 8 < P.D;
 #pragma unroll 1
                 for (int e0 = 0; e0 < PER; e0 += 8) {
                     uint4 x[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         if (e0 + i >= PER) break;
-                        const unsigned gr = g.qt * NQ + r0 + (e0 + i) * RPI, n = gr / (unsigned)P.G;
                         x[i] = make_uint4(0, 0, 0, 0);
-                        if ((int)n < g.nn && ch * 8 < P.D) {
-                            const int64_t at = ((int64_t)g.b * P.N + n) * P.q_row +
-                                               (int64_t)(int)(g.h * P.G + gr - n * P.G) * P.D + ch * 8;
-                            if (SV_INB(at, (int64_t)P.B * P.N * P.q_row, 1105))
-                                x[i] = *reinterpret_cast<const uint4 *>(P.q + at);
-                        }
+                        if (n < g.nn && wide && SV_INB(src - P.q, (int64_t)P.B * P.N * P.q_row, 1105))
+                            x[i] = *reinterpret_cast<const uint4 *>(src);
+                        // RPI rows on
+                        n += step_n;
+                        h += step_h;
+                        src += src_step;
+                        if (h >= P.G) h -= P.G, ++n, src += src_wrap;
                     }
                     if (e0 == 0) {
                         if (seg >= 2) ok = tc::bar_wait(tc::smem_u32(&ms.qempty[buf]), ((seg >> 1) & 1) ^ 1, abort);
@@ -808,6 +815,34 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                         ms.red2[wq][col0 + c0 + lane] = b;
                     }
                 }
+                group_sync(bar, 128);
+                // While the last products run, a thread t < CW says what there is to say of column t.
+                const int raise = *(volatile int *)&ms.bad[wg][seg % FLAGS] ? SPEC_VERIFY_DEV_BAD_KV_SLOT
+                                  : ms.code[buf]                            ? SPEC_VERIFY_DEV_BAD_TREE
+                                                                            : 0;
+                float *const part = P.parts + (int64_t)g.part * part_floats<NQ>();
+                if (t < CW) {
+                    float sum = 0.f, rsum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        sum += ms.red[w][col0 + t];
+                        rsum += ms.red2[w][col0 + t];
+                    }
+                    if (g.part < 0) {
+                        ms.fac[col0 + t] = raise ? NAN : 1.f / rsum;
+                        const int nt = (row0 + t) / P.G;
+                        if (nt < P.N && P.lse) {
+                            const int64_t row = ((int64_t)g.b * P.N + nt) * P.Hq + g.h * P.G + row0 + t - nt * P.G;
+                            if (SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1109))
+                                P.lse[row] = raise ? NAN : nt < g.nn ? (log2f(sum) - ms.nref[col0 + t]) * 0.69314718f : -INFINITY;
+                        }
+                    } else {
+                        float *r = part + NQ * MAXD + col0 + t;
+                        r[0] = ms.ref[col0 + t];
+                        r[NQ] = raise ? NAN : sum;
+                        r[2 * NQ] = raise ? NAN : rsum;
+                    }
+                }
                 if (k > 0) fail |= !tc::bar_wait(tc::smem_u32(&ms.pvdone), (k - 1) & 1, abort);
                 if (group_or(bar, 128, fail)) break;
                 tc::fence_after();
@@ -829,56 +864,32 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                             if ((see >> c) & 1) o[c] += val;
                     }
                 }
-                const int raise = *(volatile int *)&ms.bad[wg][seg % FLAGS] ? SPEC_VERIFY_DEV_BAD_KV_SLOT
-                                  : ms.code[buf]                            ? SPEC_VERIFY_DEV_BAD_TREE
-                                                                            : 0;
-                // What a thread t < CW says of column t.
-                float sum = 0.f, rsum = 0.f;
-                if (t < CW) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        sum += ms.red[w][col0 + t];
-                        rsum += ms.red2[w][col0 + t];
-                    }
-                    ms.fac[col0 + t] = raise ? NAN : 1.f / rsum;
-                }
-                group_sync(bar, 128);
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(tc::smem_u32(&ms.qempty[buf]));
                 if (t == 0) {
                     if (raise && P.dev_status) atomicMax(P.dev_status, raise);
                     *(volatile int *)&ms.bad[wg][seg % FLAGS] = 0;
-                    tc::bar_arrive(tc::smem_u32(&ms.qempty[buf]));
                 }
                 if (g.part < 0) {
                     uint16_t *out = P.out + (((int64_t)g.b * P.N + n0) * P.Hq + g.h * P.G + h0) * P.D + t;
                     const int64_t wrap = (int64_t)(P.Hq - P.G + 1) * P.D;  // to the next node's first head
-                    int n = n0, h = h0;
+                    const int cols = P.N * P.G - row0, live = g.nn * P.G - row0;  // columns that are rows; that are nodes'
+                    const float rest = raise ? NAN : 0.f;
+                    int h = h0;
                     if (t < P.D) {
 #pragma unroll
                         for (int c = 0; c < CW; ++c) {
-                            if (n >= P.N) break;
-                            const float y = n < g.nn ? o[c] * ms.fac[col0 + c] : raise ? NAN : 0.f;
-                            if (SV_INB(out - P.out, (int64_t)P.B * P.N * P.Hq * P.D, 1108))
+                            const float y = c < live ? o[c] * ms.fac[col0 + c] : rest;
+                            if (c < cols && SV_INB(out - P.out, (int64_t)P.B * P.N * P.Hq * P.D, 1108))
                                 *out = (uint16_t)Half2<BF>::pack(y, y);
-                            if (++h == P.G) h = 0, ++n, out += wrap;
-                            else out += P.D;
+                            const bool next = ++h == P.G;
+                            h = next ? 0 : h;
+                            out += next ? wrap : (int64_t)P.D;
                         }
                     }
-                    const int nt = (row0 + t) / P.G;
-                    if (t < CW && nt < P.N && P.lse) {
-                        const int64_t row = ((int64_t)g.b * P.N + nt) * P.Hq + g.h * P.G + row0 + t - nt * P.G;
-                        if (SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1109))
-                            P.lse[row] = raise ? NAN : nt < g.nn ? (log2f(sum) - ms.nref[col0 + t]) * 0.69314718f : -INFINITY;
-                    }
                 } else {
-                    float *part = P.parts + (int64_t)g.part * part_floats<NQ>();
 #pragma unroll
                     for (int c = 0; c < CW; ++c) part[(col0 + c) * MAXD + t] = o[c];
-                    if (t < CW) {
-                        float *r = part + NQ * MAXD + col0 + t;
-                        r[0] = ms.ref[col0 + t];
-                        r[NQ] = raise ? NAN : sum;
-                        r[2 * NQ] = raise ? NAN : rsum;
-                    }
                     if (t == 0 && wg == 0) ms.join[cta == g.c0] = g, ms.joins[cta == g.c0] = 1;
                     group_sync(bar, 128);
                 }
