@@ -890,23 +890,23 @@ __global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
                 } else {
 #pragma unroll
                     for (int c = 0; c < CW; ++c) part[(col0 + c) * MAXD + t] = o[c];
-                    if (t == 0 && wg == 0) ms.join[cta == g.c0] = g, ms.joins[cta == g.c0] = 1;
+                    // Both warpgroups of every CTA come to the segment's counter; the last one's CTA joins the parts.
+                    // The part that a run begins with is there early, so that it seldom joins two at its end.
                     group_sync(bar, 128);
+                    if (t == 0 && !fail) {
+                        __threadfence();
+                        unsigned *n = &P.counters[g.c0];
+                        if (atomicAdd(n, 1u) == (unsigned)(2 * (g.c1 - g.c0) + 1)) {
+                            *n = 0;
+                            ms.join[cta == g.c0] = g;
+                            ms.joins[cta == g.c0] = 1;
+                        }
+                    }
                 }
                 // The references and factors are read until here; the next segment writes them anew.
             }
 
-            // ---- the parts: who writes a segment's last one joins them -------------------------------
-            __threadfence();
-            group_sync(3, 256);
-            if (tid == 256 && !*abort)
-                for (int i = 0; i < 2; ++i)
-                    if (ms.joins[i]) {
-                        unsigned *n = &P.counters[ms.join[i].c0];
-                        const bool last = atomicAdd(n, 1u) == (unsigned)(ms.join[i].c1 - ms.join[i].c0);
-                        if (last) *n = 0;
-                        ms.joins[i] = last;
-                    }
+            // ---- the parts of which this CTA brought the last --------------------------------------
             group_sync(3, 256);
             if (!*abort)
                 for (int i = 0; i < 2; ++i) {
