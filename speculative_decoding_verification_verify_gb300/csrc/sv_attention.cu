@@ -39,11 +39,14 @@ using sv::Half2;
 constexpr int NT = 512;
 constexpr int TILE = 128;     // positions per tile
 constexpr int MAXD = 128;
-constexpr int MAX_CTAS = 192; // parts the workspace has room for: two per CTA
+constexpr int MAX_SMS = 192;  // the workspace has room for two parts per CTA
 constexpr int FLAGS = 16;     // bad-slot flags: more than the segments the ring can hold
 constexpr int SEGS = 8;       // segments listed ahead
 constexpr float SLACK = 8.f;  // log2 of the largest weight
 constexpr int COST_TILE = 2, COST_SEGMENT = 4;
+
+// CTAs that an SM holds: see below.
+__host__ __device__ constexpr int ctas_per_sm(int nq) { return nq == 16 ? 2 : 1; }
 
 struct Params {
     const uint16_t *q, *k, *v;
@@ -64,7 +67,7 @@ template <int NQ, int DP>
 struct Layout {
     static constexpr int HALVES = DP / 64;
     static constexpr int UNIT = TILE * DP * 2;
-    static constexpr int NU = 5 * 128 / DP;
+    static constexpr int NU = ctas_per_sm(NQ) == 2 ? (DP == 64 ? 5 : 2) : 5 * 128 / DP;
     static constexpr int QBYTES = NQ * DP * 2;
     static constexpr int QSTEP = QBYTES < 1024 ? 1024 : QBYTES;
     static constexpr int PBYTES = TILE * 128;  // a row of 64 columns per position
@@ -188,7 +191,7 @@ __device__ __forceinline__ void lengths(const Params &P, int b, int &c, int &nn)
 }
 
 template <bool BF, int NQ, int DP>
-__global__ void __launch_bounds__(NT, 1) attention_kernel(const Params P)
+__global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Params P)
 {
     using L = Layout<NQ, DP>;
     using M = Misc<NQ, L::NU>;
@@ -1111,7 +1114,7 @@ extern "C" size_t spec_verify_attention_workspace_bytes(int B, int N, int Hq, in
         D > svatt::MAXD || D % 16 || max_pos < 1)
         return 0;
     const size_t nq = (size_t)svatt::columns(N * (Hq / Hkv));
-    return svatt::COUNTER_BYTES + 2 * svatt::MAX_CTAS * (nq * svatt::MAXD + 3 * nq) * sizeof(float);
+    return svatt::COUNTER_BYTES + 2 * svatt::MAX_SMS * svatt::ctas_per_sm((int)nq) * (nq * svatt::MAXD + 3 * nq) * sizeof(float);
 }
 
 extern "C" int spec_verify_attention(const void *q, int dtype, int64_t q_stride, const void *k_cache,
@@ -1165,7 +1168,7 @@ extern "C" int spec_verify_attention(const void *q, int dtype, int64_t q_stride,
     P.dev_status = dev_status;
     P.counters = static_cast<unsigned *>(workspace);
     P.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + COUNTER_BYTES);
-    int grid = dev->sms < MAX_CTAS ? dev->sms : MAX_CTAS;
+    int grid = (dev->sms < MAX_SMS ? dev->sms : MAX_SMS) * ctas_per_sm(nq);
     const int64_t most = (int64_t)B * Hkv * P.QT * ((max_pos + TILE - 1) / TILE);
     if (most < grid) grid = (int)most;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
