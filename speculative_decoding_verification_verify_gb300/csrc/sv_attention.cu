@@ -36,7 +36,6 @@ namespace svatt {
 
 using sv::Half2;
 
-constexpr int NT = 512;
 constexpr int TILE = 128;     // positions per tile
 constexpr int MAXD = 128;
 constexpr int MAX_SMS = 192;  // the workspace has room for two parts per CTA
@@ -45,6 +44,9 @@ constexpr int SEGS = 8;       // segments listed ahead
 constexpr float SLACK = 8.f;  // log2 of the largest weight
 constexpr int COST_TILE = 2, COST_SEGMENT = 4;
 
+// Warpgroups of the softmax: a position and a share of the columns per thread.
+__host__ __device__ constexpr int groups(int nq) { return nq == 64 ? 4 : 2; }
+__host__ __device__ constexpr int threads(int nq) { return 256 + 128 * groups(nq); }
 // CTAs that an SM holds: see below.
 __host__ __device__ constexpr int ctas_per_sm(int nq) { return nq == 16 ? 2 : 1; }
 
@@ -85,12 +87,13 @@ struct __align__(16) Seg {
 template <int NQ, int NU>
 struct Misc {
     uint64_t full[NU], empty[NU];
+    static constexpr int NT = threads(NQ), WG = groups(NQ);
     uint64_t sfull[2], sempty[2], qfull[2], qempty[2], segfull[SEGS], segempty[SEGS], pfull, pvdone, drain;
     Seg seg[SEGS];
     unsigned long long desc[2][sv::MAX_TREE];  // columns that see node a, of the staged queries
     float nref[NQ], fac[NQ], ref[NQ], red[4][NQ], red2[4][NQ];
     int code[2], poison[2];
-    int bad[2][FLAGS];
+    int bad[WG][FLAGS];
     int begin_b, abort;
     int64_t begin_base, scan[NT / 32];
     uint32_t tmem;
@@ -191,11 +194,11 @@ __device__ __forceinline__ void lengths(const Params &P, int b, int &c, int &nn)
 }
 
 template <bool BF, int NQ, int DP>
-__global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Params P)
+__global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel(const Params P)
 {
     using L = Layout<NQ, DP>;
     using M = Misc<NQ, L::NU>;
-    constexpr int NU = L::NU, HALVES = L::HALVES;
+    constexpr int NU = L::NU, HALVES = L::HALVES, NT = threads(NQ), WG = groups(NQ);
     extern __shared__ __align__(1024) unsigned char smem[];
     M &ms = *reinterpret_cast<M *>(smem + L::M0);
     const uint32_t s0 = tc::smem_u32(smem);
@@ -210,22 +213,22 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Pa
         }
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(tc::smem_u32(&ms.sfull[i]), 1);
-            tc::bar_init(tc::smem_u32(&ms.sempty[i]), 256);
+            tc::bar_init(tc::smem_u32(&ms.sempty[i]), 128 * WG);
             tc::bar_init(tc::smem_u32(&ms.qfull[i]), 64);
-            tc::bar_init(tc::smem_u32(&ms.qempty[i]), 9);  // the last scores' products, the softmax's warps
+            tc::bar_init(tc::smem_u32(&ms.qempty[i]), 1 + 4 * WG);  // the last scores' products, the softmax's warps
             ms.joins[i] = 0;
         }
         for (int i = 0; i < SEGS; ++i) {
             tc::bar_init(tc::smem_u32(&ms.segfull[i]), 1);
-            tc::bar_init(tc::smem_u32(&ms.segempty[i]), 15);  // warps but the one that lists
+            tc::bar_init(tc::smem_u32(&ms.segempty[i]), NT / 32 - 1);  // warps but the one that lists
         }
-        tc::bar_init(tc::smem_u32(&ms.pfull), 256);
+        tc::bar_init(tc::smem_u32(&ms.pfull), 128 * WG);
         tc::bar_init(tc::smem_u32(&ms.pvdone), 1);
         tc::bar_init(tc::smem_u32(&ms.drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         ms.abort = 0;
     }
-    if (tid < 2 * FLAGS) (&ms.bad[0][0])[tid] = 0;
+    if (tid < WG * FLAGS) (&ms.bad[0][0])[tid] = 0;
     if (warp == 4) tc::tmem_alloc(tc::smem_u32(&ms.tmem), L::COLS);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -330,8 +333,8 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Pa
             // The slot read ahead, in the pool or -1 (past the end, or wrong: its segment is marked).
             auto check = [&](bool past) {
                 if (!past && (slot < 0 || slot >= P.num_slots)) {
-                    *(volatile int *)&ms.bad[0][seg % FLAGS] = 1;
-                    *(volatile int *)&ms.bad[1][seg % FLAGS] = 1;
+#pragma unroll
+                    for (int i = 0; i < WG; ++i) *(volatile int *)&ms.bad[i][seg % FLAGS] = 1;
                     slot = -1;
                 }
                 return slot;
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Pa
             }
         } else {
             // ---- softmax: one position of a tile and half of its columns per thread ----------
-            constexpr int CW = NQ / 2;
+            constexpr int CW = NQ / WG;
             const int t = tid & 127, wq = warp & 3, wg = (warp - 8) >> 2, bar = 4 + wg;
             const int col0 = wg * CW;
             const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16) + col0;
@@ -761,7 +764,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Pa
                         *reinterpret_cast<uint4 *>(smem + L::P0 + t * 128 + (((col0 / 8 + ch) ^ (t & 7)) << 4)) =
                             make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
-                    if (special && pos >= g.c && pos < len) {
+                    if (wg < 2 && special && pos >= g.c && pos < len) {
                         // A weight of 0 does not undo an infinity or a NaN: what is not finite in a node's
                         // values is set aside, and its readers get it at the segment's end.
                         const int u = 2 * k + 1;
@@ -899,7 +902,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Pa
                     if (t == 0 && !fail) {
                         __threadfence();
                         unsigned *n = &P.counters[g.c0];
-                        if (atomicAdd(n, 1u) == (unsigned)(2 * (g.c1 - g.c0) + 1)) {
+                        if (atomicAdd(n, 1u) == (unsigned)(WG * (g.c1 - g.c0 + 1) - 1)) {
                             *n = 0;
                             ms.join[cta == g.c0] = g;
                             ms.joins[cta == g.c0] = 1;
@@ -910,25 +913,25 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Pa
             }
 
             // ---- the parts of which this CTA brought the last --------------------------------------
-            group_sync(3, 256);
+            group_sync(3, 128 * WG);
             if (!*abort)
                 for (int i = 0; i < 2; ++i) {
                     if (!ms.joins[i]) continue;
                     __threadfence();
                     g = ms.join[i];
                     // The parts' references and sums first, all read at once, into the ring (which is done with);
-                    // then a thread takes four dimensions of NQ / 8 columns.  The parts are added in their
+                    // then a thread takes four dimensions of some columns.  The parts are added in their
                     // order, so the result does not depend on who joins.
                     const int parts = g.c1 - g.c0 + 1, t = tid - 256;
                     float *const jm = reinterpret_cast<float *>(smem), *const jl = jm + parts * NQ, *const jr = jl + parts * NQ;
                     auto part_of = [&](int x) { return P.parts + (int64_t)(2 * (g.c0 + x) + (x == 0)) * part_floats<NQ>(); };
-                    for (int e = t; e < parts * NQ; e += 256) {
+                    for (int e = t; e < parts * NQ; e += 128 * WG) {
                         const float *r = part_of(e / NQ) + NQ * MAXD + e % NQ;
                         jm[e] = __ldcg(r);
                         jl[e] = __ldcg(r + NQ);
                         jr[e] = __ldcg(r + 2 * NQ);
                     }
-                    group_sync(3, 256);
+                    group_sync(3, 128 * WG);
                     if (t < NQ) {
                         float top = -INFINITY, sum = 0.f, rsum = 0.f;
                         for (int x = 0; x < parts; ++x) top = fmaxf(top, jm[x * NQ + t]);
@@ -949,11 +952,11 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Pa
                                                              : -INFINITY;
                         }
                     }
-                    group_sync(3, 256);
-                    constexpr int IT = NQ < 32 ? NQ / 8 : 4;
-                    const int d = (t & 31) * 4, c0 = t >> 5;  // columns c0, c0 + 8, ...
+                    group_sync(3, 128 * WG);
+                    constexpr int WARPS = 4 * WG, IT = NQ / WARPS < 4 ? NQ / WARPS : 4;
+                    const int d = (t & 31) * 4, c0 = t >> 5;  // columns c0, c0 + WARPS, ...
 #pragma unroll 1
-                    for (int b0 = c0; b0 < NQ; b0 += 8 * IT) {
+                    for (int b0 = c0; b0 < NQ; b0 += WARPS * IT) {
                         float4 acc[IT];
 #pragma unroll
                         for (int i = 0; i < IT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -963,10 +966,10 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Pa
                             float4 y[IT];
 #pragma unroll
                             for (int i = 0; i < IT; ++i)
-                                y[i] = __ldcg(reinterpret_cast<const float4 *>(part + (b0 + 8 * i) * MAXD + d));
+                                y[i] = __ldcg(reinterpret_cast<const float4 *>(part + (b0 + WARPS * i) * MAXD + d));
 #pragma unroll
                             for (int i = 0; i < IT; ++i) {
-                                const float f = jm[x * NQ + b0 + 8 * i];
+                                const float f = jm[x * NQ + b0 + WARPS * i];
                                 if (f == 0.f) continue;
                                 acc[i].x += f * y[i].x;
                                 acc[i].y += f * y[i].y;
@@ -977,7 +980,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Pa
                         if (d >= P.D) continue;
 #pragma unroll
                         for (int i = 0; i < IT; ++i) {
-                            const int c = b0 + 8 * i, gr = g.qt * NQ + c, n = gr / P.G;
+                            const int c = b0 + WARPS * i, gr = g.qt * NQ + c, n = gr / P.G;
                             if (n >= P.N) break;
                             const int64_t row = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + gr - n * P.G;
                             const float inv = ms.fac[c];
@@ -989,7 +992,7 @@ __global__ void __launch_bounds__(NT, ctas_per_sm(NQ)) attention_kernel(const Pa
                                 *reinterpret_cast<uint2 *>(P.out + row * P.D + d) = y;
                         }
                     }
-                    group_sync(3, 256);
+                    group_sync(3, 128 * WG);
                 }
         }
     }
@@ -1066,7 +1069,7 @@ static cudaError_t launch(const Params &P, int grid, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(NT);
+    cfg.blockDim = dim3(threads(NQ));
     cfg.dynamicSmemBytes = smem_bytes<BF, NQ, DP>();
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
