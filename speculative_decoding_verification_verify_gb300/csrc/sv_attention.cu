@@ -39,6 +39,7 @@ using sv::Half2;
 constexpr int TILE = 128;     // positions per tile
 constexpr int MAXD = 128;
 constexpr int MAX_SMS = 192;  // the workspace has room for two parts per CTA
+constexpr int COUNTERS = 2 * MAX_SMS;
 constexpr int FLAGS = 16;     // bad-slot flags: more than the segments the ring can hold
 constexpr int SEGS = 8;       // segments listed ahead
 constexpr float SLACK = 8.f;  // log2 of the largest weight
@@ -59,7 +60,8 @@ struct Params {
     int max_pos, B, N, Hq, Hkv, D, G, QT;  // G query heads per key head, QT column blocks
     float scale_log2;
     int32_t *dev_status;
-    unsigned *counters;  // [CTAs] arrivals at the join of the segment that CTA began
+    unsigned *counters;  // arrivals at joins, COUNTERS each: of a segment's first group (by the CTA that began the segment),
+                         // of its others (by the group's first CTA), of the groups (by the segment's CTA)
     float *parts;
 };
 
@@ -84,6 +86,21 @@ struct __align__(16) Seg {
     int part, c0, c1, pad;     // part: the workspace part it writes (-1: it is the whole); the CTAs it spans
 };
 
+// Parts to be joined: of segment g, `n` from the `first` on, `step` apart.
+struct Join {
+    Seg g;
+    int first, n, step;
+};
+
+// A segment's parts in groups: more than 8 are joined in two levels, for one CTA reads them at 50 bytes a clock.
+__device__ __forceinline__ int group_size(int parts)
+{
+    if (parts <= 8) return parts;
+    int s = 3;
+    while (s * s < parts) ++s;
+    return s;
+}
+
 template <int NQ, int NU>
 struct Misc {
     uint64_t full[NU], empty[NU];
@@ -97,7 +114,7 @@ struct Misc {
     int begin_b, abort;
     int64_t begin_base, scan[NT / 32];
     uint32_t tmem;
-    Seg join[2];
+    Join join[2];
     int joins[2];
     int8_t par[sv::MAX_TREE];
 };
@@ -539,7 +556,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
         } else if (warp < 8) {
             // ---- queries and the tree's mask -----------------------------------------------
             const int t = tid - 192;
-            constexpr int CH = DP / 8, RPI = 64 / CH, PER = NQ / RPI;  // 16-byte chunks of a row; rows at a time
+            constexpr int CH = DP / 8, RPI = 64 / CH;  // 16-byte chunks of a row; rows at a time
             const int step_n = (int)((unsigned)RPI / (unsigned)P.G), step_h = RPI - step_n * P.G;  // RPI rows in nodes and heads
             const int64_t src_step = step_n * P.q_row + step_h * P.D, src_wrap = P.q_row - (int64_t)P.G * P.D;
             int seg = -1;
@@ -560,61 +577,52 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                     if (wrong) p = -1;
                 }
                 const int ch = t % CH, r0 = t / CH;
-                bool ok = true;
                 const unsigned gr = g.qt * NQ + r0;
                 int n = (int)(gr / (unsigned)P.G), h = (int)gr - n * P.G;
                 const uint16_t *src = P.q + ((int64_t)g.b * P.N + n) * P.q_row + (int64_t)(g.h * P.G + h) * P.D + ch * 8;
                 const bool wide = ch * 8 < P.D;
-#pragma unroll 1
-                for (int e0 = 0; e0 < PER; e0 += 8) {
-                    uint4 x[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (e0 + i >= PER) break;
-                        x[i] = make_uint4(0, 0, 0, 0);
-                        if (n < g.nn && wide && SV_INB(src - P.q, (int64_t)P.B * P.N * P.q_row, 1105))
-                            x[i] = *reinterpret_cast<const uint4 *>(src);
-                        // RPI rows on
-                        n += step_n;
-                        h += step_h;
-                        src += src_step;
-                        if (h >= P.G) h -= P.G, ++n, src += src_wrap;
-                    }
-                    if (e0 == 0) {
-                        if (seg >= 2) ok = tc::bar_wait(tc::smem_u32(&ms.qempty[buf]), ((seg >> 1) & 1) ^ 1, abort);
-                        ms.par[t] = (int8_t)p;
-                        if (t == 0) ms.code[buf] = ms.poison[buf] = 0;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (e0 + i >= PER) break;
-                        const int r = r0 + (e0 + i) * RPI;
-                        *reinterpret_cast<uint4 *>(smem + L::Q0 + buf * L::QSTEP + (ch >> 3) * NQ * 128 + r * 128 +
-                                                   (((ch & 7) ^ (r & 7)) << 4)) = x[i];
-                    }
+                bool ok = true;
+                if (seg >= 2) ok = tc::bar_wait(tc::smem_u32(&ms.qempty[buf]), ((seg >> 1) & 1) ^ 1, abort);
+                const uint32_t to = s0 + L::Q0 + buf * L::QSTEP + (ch >> 3) * NQ * 128;
+#pragma unroll 2
+                for (int r = r0; r < NQ; r += RPI) {
+                    const bool in = n < g.nn && wide && SV_INB(src - P.q, (int64_t)P.B * P.N * P.q_row, 1105);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                                 "l"(in ? src : P.q), "r"(in ? 16 : 0)
+                                 : "memory");
+                    // RPI rows on
+                    n += step_n;
+                    h += step_h;
+                    src += src_step;
+                    if (h >= P.G) h -= P.G, ++n, src += src_wrap;
                 }
-                tc::fence_async_smem();
+                ms.par[t] = (int8_t)p;
+                if (t == 0) ms.code[buf] = ms.poison[buf] = 0;
                 if (group_or(2, 64, !ok)) break;
                 if (wrong) ms.code[buf] = 1;
                 unsigned long long path = 0;
                 if (t < g.nn) {
                     if (P.parents)
-                        for (int n = t; n >= 0; n = ms.par[n]) path |= 1ull << n;
+                        for (int a = t; a >= 0; a = ms.par[a]) path |= 1ull << a;
                     else
                         path = ~0ull >> (63 - t);
                 }
                 ms.desc[buf][t] = path;
                 group_sync(2, 64);
-                // Of a node that sees this thread's, all columns: P.G of them from its first one on.
-                unsigned long long see = 0;
-                for (int n = t, c = t * P.G - g.qt * NQ; n < g.nn && c < NQ; ++n, c += P.G) {
-                    const int from = c > 0 ? c : 0, to = c + P.G < 64 ? c + P.G : 64;
-                    if (to > from && ((ms.desc[buf][n] >> t) & 1)) see |= ~0ull >> (64 - (to - from)) << from;
-                }
+                // A thread takes a column; its node's path says which nodes it sees.
+                const unsigned node = (g.qt * NQ + t) / (unsigned)P.G;
+                path = t < NQ && (int)node < g.nn ? ms.desc[buf][node] : 0;
                 group_sync(2, 64);
-                ms.desc[buf][t] = see;
+#pragma unroll 4
+                for (int a = 0; a < g.nn; ++a) {
+                    const unsigned see = __ballot_sync(0xffffffffu, (path >> a) & 1);
+                    if (lane == (a & 31)) reinterpret_cast<uint32_t *>(&ms.desc[buf][a])[warp & 1] = see;
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                tc::fence_async_smem();
                 tc::bar_arrive(tc::smem_u32(&ms.qfull[buf]));
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
             // ---- softmax: one position of a tile and half of its columns per thread ----------
             constexpr int CW = NQ / WG;
@@ -900,11 +908,14 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                     // The part that a run begins with is there early, so that it seldom joins two at its end.
                     group_sync(bar, 128);
                     if (t == 0 && !fail) {
+                        const int parts = g.c1 - g.c0 + 1, size = group_size(parts), first = (cta - g.c0) / size * size;
+                        const int n = parts - first < size ? parts - first : size;
+                        unsigned *count = &P.counters[first ? COUNTERS + g.c0 + first : g.c0];
                         __threadfence();
-                        unsigned *n = &P.counters[g.c0];
-                        if (atomicAdd(n, 1u) == (unsigned)(WG * (g.c1 - g.c0 + 1) - 1)) {
-                            *n = 0;
-                            ms.join[cta == g.c0] = g;
+                        if (atomicAdd(count, 1u) == (unsigned)(WG * n - 1)) {
+                            __threadfence();
+                            *count = 0;
+                            ms.join[cta == g.c0] = {g, first, n, 1};
                             ms.joins[cta == g.c0] = 1;
                         }
                     }
@@ -913,18 +924,45 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
             }
 
             // ---- the parts of which this CTA brought the last --------------------------------------
-            group_sync(3, 128 * WG);
-            if (!*abort)
-                for (int i = 0; i < 2; ++i) {
-                    if (!ms.joins[i]) continue;
-                    __threadfence();
-                    g = ms.join[i];
-                    // The parts' references and sums first, all read at once, into the ring (which is done with);
-                    // then a thread takes four dimensions of some columns.  The parts are added in their
-                    // order, so the result does not depend on who joins.
-                    const int parts = g.c1 - g.c0 + 1, t = tid - 256;
+            const bool off = group_or(3, 128 * WG, *abort != 0);
+            for (int i = 0; i < 2; ++i)
+                while (ms.joins[i] && !off) {
+                    // A thread takes four dimensions of IT columns, and one column's reference and sums; these
+                    // go through the ring, which is done with.  The parts are added in their order, so the
+                    // result does not depend on who joins.  A group's sum replaces its first part.
+                    constexpr int WARPS = 4 * WG, IT = NQ / WARPS;
+                    const Join &jn = ms.join[i];
+                    g = jn.g;
+                    const int parts = jn.n, t = tid - 256, d = (t & 31) * 4, c0 = t >> 5;  // columns c0, c0 + WARPS, ...
+                    const bool all = g.c1 - g.c0 + 1 == parts || jn.step > 1;
                     float *const jm = reinterpret_cast<float *>(smem), *const jl = jm + parts * NQ, *const jr = jl + parts * NQ;
-                    auto part_of = [&](int x) { return P.parts + (int64_t)(2 * (g.c0 + x) + (x == 0)) * part_floats<NQ>(); };
+                    uint32_t *const jrow = reinterpret_cast<uint32_t *>(jr + parts * NQ);  // columns' rows of the output (2^32 would be 550 GB)
+                    auto part_of = [&](int x) {
+                        const int y = jn.first + x * jn.step;
+                        return P.parts + (int64_t)(2 * (g.c0 + y) + (y == 0)) * part_floats<NQ>();
+                    };
+                    float4 y[2][IT], acc[IT];
+                    auto load = [&](int x, float4 (&y)[IT]) {
+                        if (x >= parts) return;
+                        const float *part = part_of(x) + c0 * MAXD + d;
+#pragma unroll
+                        for (int i = 0; i < IT; ++i) y[i] = __ldcg(reinterpret_cast<const float4 *>(part + WARPS * i * MAXD));
+                    };
+                    auto add = [&](int x, const float4 (&y)[IT]) {
+                        if (x >= parts) return;
+#pragma unroll
+                        for (int i = 0; i < IT; ++i) {
+                            const float f = jm[x * NQ + c0 + WARPS * i];
+                            if (f == 0.f) continue;
+                            acc[i].x += f * y[i].x;
+                            acc[i].y += f * y[i].y;
+                            acc[i].z += f * y[i].z;
+                            acc[i].w += f * y[i].w;
+                        }
+                    };
+                    load(0, y[0]);
+                    load(1, y[1]);
+#pragma unroll 1
                     for (int e = t; e < parts * NQ; e += 128 * WG) {
                         const float *r = part_of(e / NQ) + NQ * MAXD + e % NQ;
                         jm[e] = __ldcg(r);
@@ -934,7 +972,9 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                     group_sync(3, 128 * WG);
                     if (t < NQ) {
                         float top = -INFINITY, sum = 0.f, rsum = 0.f;
+#pragma unroll 1
                         for (int x = 0; x < parts; ++x) top = fmaxf(top, jm[x * NQ + t]);
+#pragma unroll 1
                         for (int x = 0; x < parts; ++x) {
                             const float m = jm[x * NQ + t], l = jl[x * NQ + t];
                             // 0: the part's positions have no weight in this row
@@ -942,54 +982,62 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                             if (l != 0.f) sum += f * l, rsum += f * jr[x * NQ + t];
                             jm[x * NQ + t] = f;
                         }
-                        const int gr = g.qt * NQ + t, n = gr / P.G;
-                        const bool bad = sum != sum;
-                        ms.fac[t] = n < g.nn || bad ? 1.f / rsum : 0.f;
-                        if (n < P.N && P.lse) {
+                        if (all) {
+                            const int gr = g.qt * NQ + t, n = (int)((unsigned)gr / (unsigned)P.G);
+                            const bool bad = sum != sum;
                             const int64_t row = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + gr - n * P.G;
-                            if (SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1111))
+                            ms.fac[t] = n < g.nn || bad ? 1.f / rsum : 0.f;
+                            jrow[t] = n < P.N ? (uint32_t)row : ~0u;
+                            if (n < P.N && P.lse && SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1111))
                                 P.lse[row] = n < g.nn || bad ? ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.69314718f
                                                              : -INFINITY;
+                        } else {
+                            float *r = part_of(0) + NQ * MAXD + t;
+                            r[0] = top;
+                            r[NQ] = sum;
+                            r[2 * NQ] = rsum;
                         }
                     }
                     group_sync(3, 128 * WG);
-                    constexpr int WARPS = 4 * WG, IT = NQ / WARPS < 4 ? NQ / WARPS : 4;
-                    const int d = (t & 31) * 4, c0 = t >> 5;  // columns c0, c0 + WARPS, ...
+#pragma unroll
+                    for (int i = 0; i < IT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-                    for (int b0 = c0; b0 < NQ; b0 += WARPS * IT) {
-                        float4 acc[IT];
+                    for (int x = 0; x < parts; x += 2) {
+                        add(x, y[0]);
+                        load(x + 2, y[0]);
+                        add(x + 1, y[1]);
+                        load(x + 3, y[1]);
+                    }
 #pragma unroll
-                        for (int i = 0; i < IT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-                        for (int x = 0; x < parts; ++x) {
-                            const float *part = part_of(x);
-                            float4 y[IT];
-#pragma unroll
-                            for (int i = 0; i < IT; ++i)
-                                y[i] = __ldcg(reinterpret_cast<const float4 *>(part + (b0 + WARPS * i) * MAXD + d));
-#pragma unroll
-                            for (int i = 0; i < IT; ++i) {
-                                const float f = jm[x * NQ + b0 + WARPS * i];
-                                if (f == 0.f) continue;
-                                acc[i].x += f * y[i].x;
-                                acc[i].y += f * y[i].y;
-                                acc[i].z += f * y[i].z;
-                                acc[i].w += f * y[i].w;
-                            }
+                    for (int i = 0; i < IT; ++i) {
+                        const int c = c0 + WARPS * i;
+                        if (!all) {
+                            *reinterpret_cast<float4 *>(part_of(0) + c * MAXD + d) = acc[i];
+                            continue;
                         }
-                        if (d >= P.D) continue;
-#pragma unroll
-                        for (int i = 0; i < IT; ++i) {
-                            const int c = b0 + WARPS * i, gr = g.qt * NQ + c, n = gr / P.G;
-                            if (n >= P.N) break;
-                            const int64_t row = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + gr - n * P.G;
-                            const float inv = ms.fac[c];
-                            uint2 y = make_uint2(0, 0);
-                            if (inv != 0.f)
-                                y = make_uint2(Half2<BF>::pack(acc[i].x * inv, acc[i].y * inv),
-                                               Half2<BF>::pack(acc[i].z * inv, acc[i].w * inv));
-                            if (SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1110))
-                                *reinterpret_cast<uint2 *>(P.out + row * P.D + d) = y;
+                        const float inv = ms.fac[c];
+                        uint2 y = make_uint2(0, 0);
+                        if (inv != 0.f)
+                            y = make_uint2(Half2<BF>::pack(acc[i].x * inv, acc[i].y * inv),
+                                           Half2<BF>::pack(acc[i].z * inv, acc[i].w * inv));
+                        const uint32_t row = jrow[c];
+                        if (row != ~0u && d < P.D && SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1110))
+                            *reinterpret_cast<uint2 *>(P.out + (int64_t)row * P.D + d) = y;
+                    }
+                    group_sync(3, 128 * WG);
+                    if (t == 0) {
+                        // The last group's CTA goes on to join the groups.
+                        ms.joins[i] = 0;
+                        if (!all) {
+                            const int size = group_size(g.c1 - g.c0 + 1), n = (g.c1 - g.c0) / size + 1;
+                            unsigned *count = &P.counters[2 * COUNTERS + g.c0];
+                            __threadfence();
+                            if (atomicAdd(count, 1u) == (unsigned)(n - 1)) {
+                                __threadfence();
+                                *count = 0;
+                                ms.join[i] = {g, 0, n, size};
+                                ms.joins[i] = 1;
+                            }
                         }
                     }
                     group_sync(3, 128 * WG);
