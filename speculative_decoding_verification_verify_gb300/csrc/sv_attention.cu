@@ -925,13 +925,13 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
 
             // ---- the parts of which this CTA brought the last --------------------------------------
             const bool off = group_or(3, 128 * WG, *abort != 0);
-            for (int i = 0; i < 2; ++i)
-                while (ms.joins[i] && !off) {
+            for (int end = 0; end < 2; ++end)  // the run's beginning, its end
+                while (ms.joins[end] && !off) {
                     // A thread takes four dimensions of IT columns, and one column's reference and sums; these
                     // go through the ring, which is done with.  The parts are added in their order, so the
                     // result does not depend on who joins.  A group's sum replaces its first part.
                     constexpr int WARPS = 4 * WG, IT = NQ / WARPS;
-                    const Join &jn = ms.join[i];
+                    const Join &jn = ms.join[end];
                     g = jn.g;
                     const int parts = jn.n, t = tid - 256, d = (t & 31) * 4, c0 = t >> 5;  // columns c0, c0 + WARPS, ...
                     const bool all = g.c1 - g.c0 + 1 == parts || jn.step > 1;
@@ -1027,7 +1027,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                     group_sync(3, 128 * WG);
                     if (t == 0) {
                         // The last group's CTA goes on to join the groups.
-                        ms.joins[i] = 0;
+                        ms.joins[end] = 0;
                         if (!all) {
                             const int size = group_size(g.c1 - g.c0 + 1), n = (g.c1 - g.c0) / size + 1;
                             unsigned *count = &P.counters[2 * COUNTERS + g.c0];
@@ -1035,8 +1035,8 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                             if (atomicAdd(count, 1u) == (unsigned)(n - 1)) {
                                 __threadfence();
                                 *count = 0;
-                                ms.join[i] = {g, 0, n, size};
-                                ms.joins[i] = 1;
+                                ms.join[end] = {g, 0, n, size};
+                                ms.joins[end] = 1;
                             }
                         }
                     }
