@@ -23,7 +23,8 @@
  *     count and shared memory per SM and raises the dynamic shared-memory limits of the kernels
  *     that take more than the default (cudaFuncSetAttribute: the finalising kernels, which size
  *     their request so that at most ceil(B / SMs) of their CTAs share an SM, and the top-k / top-p
- *     ring kernel's 109 KiB); make it before any stream capture on that device.  The library keeps
+ *     ring kernel's 109 KiB; attention and logprobs, up to 214 KiB); make it before any stream capture
+ *     on that device (spec_verify_attention and spec_verify_logprobs: the first call of each).  The library keeps
  *     this per device for the life of the process, so it must not be used again after
  *     cudaDeviceReset.
  *   - The return value is a host status, known when the call returns:
@@ -81,9 +82,12 @@ extern "C" {
 #define SPEC_VERIFY_DEV_BAD_TREE 3    /* parents[0] != -1, or parents[j] outside [0, j) */
 #define SPEC_VERIFY_DEV_DUP_SIBLING 4 /* two children of one node share a token (target-only) */
 #define SPEC_VERIFY_DEV_BAD_KV_POSITION 5 /* KV compaction: committed + N beyond the slot table,
-                                             accept_len >= N, or a path entry outside [0, N) */
-#define SPEC_VERIFY_DEV_BAD_KV_SLOT 6     /* KV compaction: a slot outside [0, num_slots) */
-#define SPEC_VERIFY_DEV_TIMEOUT 7      /* a bounded wait inside a kernel ran out: outputs undefined */
+                                             accept_len >= N, or a path entry outside [0, N); append,
+                                             attention: lengths or positions that do not fit */
+#define SPEC_VERIFY_DEV_BAD_KV_SLOT 6     /* KV cache: a slot outside [0, num_slots) */
+#define SPEC_VERIFY_DEV_TIMEOUT 7      /* attention, logprobs: a bounded wait inside the kernel ran out;
+                                          the outputs are undefined, and the workspace has to be
+                                          zero-filled again before its next use */
 
 /* Modes for spec_verify_workspace_bytes. */
 #define SPEC_VERIFY_MODE_GREEDY 0
@@ -343,8 +347,8 @@ int spec_verify_kv_append(const void *q, const void *k, const void *v, int dtype
  * included).  Arguments as for spec_verify_kv_append, and
  *   q              [B * N] rows of Hq heads of D elements, q_stride elements apart, rotated
  *   out            [B * N][Hq][D], contiguous, of q's type;  lse  [B * N][Hq] fp32 or NULL
- *   N <= 64, D a multiple of 16 from 64 to 128, Hq a multiple of Hkv, num_slots < 2^31,
- *   scale > 0 and finite
+ *   N <= 64, D a multiple of 16 from 64 to 128, Hq a multiple of Hkv, num_slots and the caches' slot
+ *   strides below 2^31, scale > 0 and finite
  *   workspace      spec_verify_attention_workspace_bytes(...) bytes, 256-byte aligned; zero-filled
  *                  before its first use, shared with the verifiers' (their counters' rules hold)
  * Sums and the softmax are in fp32; the weights are rounded to q's type for the product with v.

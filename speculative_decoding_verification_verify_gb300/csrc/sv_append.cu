@@ -11,6 +11,8 @@
 // chain runs under them.  A CTA takes one node: its unit of work is a pair of 16-byte vectors,
 // which under either pairing holds whole pairs (half-split: vectors rot/2 apart; adjacent: any
 // two), so a thread needs one unit's cosines and sines and no exchange with its neighbours.
+// Measured (GB300, copy rate 6.68 TB/s; 32 query and 8 key heads of 128, in a graph): 8194 rows 33.8 us for
+// 204 MB, 6.0 TB/s; 384 rows 4.0 us and one row 3.0 us, the chain's length.
 #include "sv_ops.cuh"
 
 namespace svapp {

@@ -12,7 +12,7 @@
 //   S^T [128 positions][rows] = K [128][D] . Q^T          both operands from shared memory
 //   O^T [128 dims][rows]     += V^T [dims][128] . P^T     V as it lies in the cache, read transposed
 //
-// One CTA per SM takes an equal run of the batch's work, whatever the lengths: tiles (128 positions of one
+// Each CTA takes an equal run of the batch's work, whatever the lengths: tiles (128 positions of one
 // request and key head) at COST_TILE each and segments (a request and key head) at COST_SEGMENT for
 // their beginning and end.  So one long request is split over all SMs and many short ones share them;
 // where a run cuts a request, the parts are joined by the CTA that finishes last.
@@ -21,12 +21,21 @@
 // TMA were tried first: four 128-byte rows took 61 clocks to issue, 8 bytes per clock, where an SM's
 // share of HBM is 23).  Warp 4 issues the products, warp 5 lists the run's segments (a segment: the
 // run's tiles of one request and key head) a few ahead of everybody, warps 6-7 stage the queries and
-// the tree's mask.  Warps 8-15 do the softmax, a position and half of the columns per thread: scores
-// come to them as columns, so the exponentials are spread evenly however few the query rows.
+// the tree's mask.  The warpgroups from warp 8 on do the softmax, a position and a share of the columns
+// per thread: scores come to them as columns, so the exponentials are spread evenly however few the
+// query rows.
 //
 // The softmax's reference moves only when a score passes it by more than 2^8 (a vote of 128 threads
 // per tile): weights are then at most 2^8, as exact in 16 bits as below 1, and the accumulators are
 // left alone in nearly every tile.
+//
+// Measured (GB300, copy rate 6.68 TB/s; 32 query and 8 key heads of 128 unless said): 64 chains of 8 over
+// 509 to 8192 positions 122-125 us for 742 MB, 5.9-6.1 TB/s; one tree of 16 over 131000 positions 100 us
+// for 537 MB, 5.3 TB/s (9 us until the first tile is there, 8 us for the joins); 96 requests of one token and 12
+// heads of 64 over 1 to 4001 positions 46 us for 148 MB, 3.2 TB/s; 48 trees of 8 over up to 504 positions 21 us.
+// Long segments are bound by HBM; short ones by the chain through a segment, some 5000 clocks (its
+// first scores 1000, references 600, weights and the last product 1300, what it writes 900), which is
+// all the SM does unless two CTAs share it.
 #include "sv_ops.cuh"
 #include "sv_tc.cuh"
 
@@ -43,12 +52,19 @@ constexpr int COUNTERS = 2 * MAX_SMS;
 constexpr int FLAGS = 16;     // bad-slot flags: more than the segments the ring can hold
 constexpr int SEGS = 8;       // segments listed ahead
 constexpr float SLACK = 8.f;  // log2 of the largest weight
+// In half tiles.  A segment at 3 or 5: 45.9 or 46.8 us against 45.8 for the 96 short requests above, 20.7 or 21.2
+// against 20.8 for the 48 trees; at 2 (with one CTA per SM) 63 against 56.
 constexpr int COST_TILE = 2, COST_SEGMENT = 4;
 
-// Warpgroups of the softmax: a position and a share of the columns per thread.
+// Warpgroups of the softmax: two hold 16 columns a thread at most, and so do four where there are 64 columns
+// (with 32 a thread: one tree of 16 over 131000 positions 105.6 us against 102.7).
 __host__ __device__ constexpr int groups(int nq) { return nq == 64 ? 4 : 2; }
 __host__ __device__ constexpr int threads(int nq) { return 256 + 128 * groups(nq); }
-// CTAs that an SM holds: see below.
+// CTAs that an SM holds.  With at most 8 columns a thread, 64 registers do, and one CTA works while the
+// other is between segments: 96 requests of 12 heads of 64 take 45.8 us against 54.6, 128 requests of up to
+// 504 positions (8 key heads of 128) 35 against 40.  Two units of 128 dimensions are then all that fit
+// in a ring, and long requests lose: 509 to 8192 positions 138 us against 136, one of 131000 111 against
+// 108.  At 32 columns 64 registers spill: 139 us against 125 for the 64 chains above.
 __host__ __device__ constexpr int ctas_per_sm(int nq) { return nq == 16 ? 2 : 1; }
 
 struct Params {
@@ -92,7 +108,8 @@ struct Join {
     int first, n, step;
 };
 
-// A segment's parts in groups: more than 8 are joined in two levels, for one CTA reads them at 50 bytes a clock.
+// A segment's parts in groups: more than 8 are joined in two levels, for one CTA reads them at 50 bytes a clock
+// (20 parts of 64 columns 116.5 us for the call against 118, 38 of 16 columns 111 against 117).
 __device__ __forceinline__ int group_size(int parts)
 {
     if (parts <= 8) return parts;
