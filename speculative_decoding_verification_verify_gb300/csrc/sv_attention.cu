@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
     const int cta = blockIdx.x;
     volatile int *abort = &ms.abort;
 
-    if (tid == 0) {
+    if (tid == NT - 32) {  // a warp that has no request to look at in a batch of ordinary size
         for (int s = 0; s < NU; ++s) {
             tc::bar_init(tc::smem_u32(&ms.full[s]), 128);
             tc::bar_init(tc::smem_u32(&ms.empty[s]), 1);
@@ -373,41 +373,42 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                 }
                 return slot;
             };
-            auto copy = [&](const unsigned char *base, uint32_t stride, int slots) {
-                if (u >= NU) {
-                    const bool free = tc::bar_wait(tc::smem_u32(&ms.empty[u % NU]), (u / NU + 1) & 1, abort);
-                    if (!__all_sync(0xffffffffu, free)) return false;
-                }
-                const uint32_t dst = s0 + (u % NU) * L::UNIT + to;
-                if (__all_sync(0xffffffffu, slots >= 0 && wide)) {
-#pragma unroll
-                    for (int i = 0; i < ITER; ++i) {
-                        const uint32_t s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 4 * RPI * 128),
-                                     "l"(base + (uint64_t)s * stride)
-                                     : "memory");
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < ITER; ++i) {  // zeros where there is nothing to copy
-                        const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 4 * RPI * 128),
-                                     "l"(s < 0 ? base : base + (uint64_t)(uint32_t)s * stride), "r"(s >= 0 && wide ? 16 : 0)
-                                     : "memory");
-                    }
-                }
-                // The unit's barrier hears of each thread's copies as they land; nobody waits for them here.
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&ms.full[u % NU]))
-                             : "memory");
-                ++u;
-                return true;
-            };
             for (int found = seek(true); found == 1 && ok;) {
                 const int slots = check(j * TILE + own >= g.c + g.nn);
                 const int64_t at = (int64_t)g.h * P.D + (wide ? chunk * 8 : 0);
+                const bool whole = __all_sync(0xffffffffu, slots >= 0 && wide);
                 found = seek(false);
-                ok = copy(reinterpret_cast<const unsigned char *>(P.k + at), (uint32_t)P.k_slot * 2, slots) &&
-                     copy(reinterpret_cast<const unsigned char *>(P.v + at), (uint32_t)P.v_slot * 2, slots);
+#pragma unroll 1
+                for (int kv = 0; kv < 2 && ok; ++kv, ++u) {
+                    if (u >= NU) {
+                        const bool free = tc::bar_wait(tc::smem_u32(&ms.empty[u % NU]), (u / NU + 1) & 1, abort);
+                        ok = __all_sync(0xffffffffu, free);
+                        if (!ok) break;
+                    }
+                    const uint32_t dst = s0 + (u % NU) * L::UNIT + to;
+                    const unsigned char *base = reinterpret_cast<const unsigned char *>((kv ? P.v : P.k) + at);
+                    const uint32_t stride = (uint32_t)(kv ? P.v_slot : P.k_slot) * 2;
+                    if (whole) {
+#pragma unroll
+                        for (int i = 0; i < ITER; ++i) {
+                            const uint32_t s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 4 * RPI * 128),
+                                         "l"(base + (uint64_t)s * stride)
+                                         : "memory");
+                        }
+                    } else {
+#pragma unroll 4
+                        for (int i = 0; i < ITER; ++i) {  // zeros where there is nothing to copy
+                            const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 4 * RPI * 128),
+                                         "l"(base + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride), "r"(s >= 0 && wide ? 16 : 0)
+                                         : "memory");
+                        }
+                    }
+                    // The unit's barrier hears of each thread's copies as they land; nobody waits for them here.
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&ms.full[u % NU]))
+                                 : "memory");
+                }
                 if (found == 2 && ok) found = seek(true);
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -551,7 +552,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                     first = false;
                 }
                 for (; item < HT && at < t1 && ok; ++item, at += cost) {
-                    g.h = item / P.QT;
+                    g.h = P.QT == 1 ? item : item / P.QT;
                     g.qt = item - g.h * P.QT;
                     g.j0 = cut_tile(t0 - at, ntile);
                     g.j1 = cut_tile(t1 - at, ntile);
