@@ -32,7 +32,7 @@
 // Measured (GB300, copy rate 6.68 TB/s; 32 query and 8 key heads of 128 unless said): 64 chains of 8 over
 // 509 to 8192 positions 122-125 us for 742 MB, 5.9-6.1 TB/s; one tree of 16 over 131000 positions 100 us
 // for 537 MB, 5.3 TB/s (9 us until the first tile is there, 8 us for the joins); 96 requests of one token and 12
-// heads of 64 over 1 to 4001 positions 46 us for 148 MB, 3.2 TB/s; 48 trees of 8 over up to 504 positions 21 us.
+// heads of 64 over 1 to 4001 positions 44 us for 148 MB, 3.4 TB/s; 48 trees of 8 over up to 504 positions 19 us.
 // Long segments are bound by HBM; short ones by the chain through a segment, some 5000 clocks (its
 // first scores 1000, references 600, weights and the last product 1300, what it writes 900), which is
 // all the SM does unless two CTAs share it.
