@@ -311,3 +311,36 @@ def test_long_rows_of_empty_requests_between_others():
     assert torch.isnan(got.out[bad].float()).all()
     keep = [b for b in range(len(nn)) if b not in bad]
     assert torch.equal(got.out[keep], want.out[keep])
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(1, 8, 2, 128), (1, 3, 3, 64), (8, 8, 2, 80), (16, 8, 2, 128)])
+def test_many_parts_of_a_request(N, Hq, Hkv, D):
+    """Requests cut into more parts than one join takes: every width of rows; the same bits from call to call;
+    counters left at zero; a wrong slot in one part reaches all the rows, and only this request's."""
+    s = make([30011, 17], N, Hq, Hkv, D, BF, seed=21, tree=N > 1)
+    want = check(s)
+    nbytes = sv.spec_verify_attention_workspace_bytes(2, N, Hq, Hkv, D, s["slot_table"].shape[1])
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device=DEV)
+    for _ in range(20):
+        got = call(s, workspace=ws)
+        assert torch.equal(got.out, want.out) and torch.equal(got.lse, want.lse)
+    torch.cuda.synchronize()
+    assert not ws[: 256 * 1024].any()
+    s["slot_table"][0, 20001] = -1
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = call(s, workspace=ws, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 6
+    assert torch.isnan(got.out[0].float()).all() and torch.isnan(got.lse[0]).all()
+    assert torch.equal(got.out[1], want.out[1]) and torch.equal(got.lse[1], want.lse[1])
+    assert not ws[: 256 * 1024].any()
+
+
+@pytest.mark.parametrize("N,G", [(16, 4), (8, 4), (3, 4)])
+def test_infinities_beside_a_path(N, G):
+    """Values that are not finite in one node's slot reach the nodes that see it, for every width of rows."""
+    s = make([129, 250], N, 2 * G, 2, 128, BF, seed=22, tree=True)
+    for b, c in enumerate([129, 250]):
+        s["v_cache"][int(s["slot_table"][b, c + 1]), 1, 5] = math.inf
+        s["v_cache"][int(s["slot_table"][b, c + N - 1]), 0, 100] = math.nan
+    check(s)
