@@ -344,3 +344,11 @@ def test_infinities_beside_a_path(N, G):
         s["v_cache"][int(s["slot_table"][b, c + 1]), 1, 5] = math.inf
         s["v_cache"][int(s["slot_table"][b, c + N - 1]), 0, 100] = math.nan
     check(s)
+
+
+@pytest.mark.parametrize("N", [1, 16])
+def test_more_requests_than_threads(N):
+    """Each thread of the prologue then counts several requests."""
+    rng = np.random.default_rng(23)
+    check(make([int(x) for x in rng.integers(0, 200, 1601)], N, 4, 1, 64, FP, seed=23, tree=N > 1),
+          num_nodes=[int(x) for x in rng.integers(0, N + 1, 1601)])

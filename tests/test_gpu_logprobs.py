@@ -249,3 +249,33 @@ def test_refusals():
             sv.spec_verify_logprobs(x, tok, **kw)
     with pytest.raises(sv.SpecVerifyError):
         sv.spec_verify_logprobs(x, torch.zeros((2, 4), dtype=torch.int32, device=DEV))  # more tokens than rows
+
+
+@pytest.mark.parametrize("dtype", [BF, FP32])
+def test_more_rows_than_are_listed_at_once(dtype):
+    """Hundreds of rows for every CTA and of entries for every thread, a third of them absent."""
+    B, T, V = 700, 64, 41
+    x, tok = rows(B, T, V, dtype, seed=12)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(13)
+    absent = torch.rand((B, T), generator=g, device=DEV) < 0.33
+    tok = tok.masked_fill(absent, -1)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = sv.spec_verify_logprobs(x, tok, top_n=3, temperature=0.9, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    raw = x.double()
+    d = raw / 0.9 - (raw / 0.9).amax(-1, keepdim=True)
+    lnz = d.exp().sum(-1).log()
+    at = tok.clamp(min=0).long()[..., None]
+    base = 2.0 ** -20 + (V / 4096 + 32) * 2.0 ** -23
+    w = d.gather(2, at)[..., 0]
+    near(got.logprobs, torch.where(absent, 0.0, w - lnz), base + 2.0 ** -22 * (w.abs() + lnz))
+    near(got.entropy, torch.where(absent, 0.0, lnz - (d.exp() * d).sum(-1) / lnz.exp()), base * (4 + 2 * lnz))
+    ranks = 1 + (raw > raw.gather(2, at)).sum(-1)
+    assert torch.equal(got.ranks.long(), torch.where(absent, 0, ranks))
+    order = torch.sort(raw, dim=-1, descending=True, stable=True).indices[..., :3]
+    assert torch.equal(got.top_ids.long(), torch.where(absent[..., None], -1, order))
+    y = d.gather(2, order)
+    near(got.top_logprobs, torch.where(absent[..., None], -math.inf, y - lnz[..., None]),
+         base + 2.0 ** -22 * (y.abs() + lnz[..., None]))
