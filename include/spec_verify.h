@@ -435,6 +435,14 @@ int spec_verify_debug_fault(uint64_t *fault);
 int spec_verify_wait_timeouts(uint64_t *count);
 
 /*
+ * The id of the graph capture that `stream` is under, 0 when it is under none.  For callers that keep
+ * workspaces: one that is to be used in a graph has to be zero-filled by the graph itself, or before any of
+ * its replays, and must live as long as the graph.  Enqueues nothing.  Returns SPEC_VERIFY_OK,
+ * SPEC_VERIFY_EINVAL for a NULL id, or SPEC_VERIFY_ECUDA (an invalidated capture among others).
+ */
+int spec_verify_capture_id(void *stream, uint64_t *id);
+
+/*
  * Allocation-free variant of spec_verify_rejection.  The pages have no counterpart: this entry
  * point exists for callers that cannot allocate device memory when they verify (a step running
  * under an allocator that forbids new allocations, an engine whose device memory is owned by

@@ -94,6 +94,8 @@ def _declare(lib):
     lib.spec_verify_logprobs.restype = i32
     lib.spec_verify_logprobs_workspace_bytes.argtypes = [i32] * 4
     lib.spec_verify_logprobs_workspace_bytes.restype = sz
+    lib.spec_verify_capture_id.argtypes = [vp, ctypes.POINTER(u64)]
+    lib.spec_verify_capture_id.restype = i32
     lib.spec_verify_debug_fault.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
     lib.spec_verify_debug_fault.restype = i32
     lib.spec_verify_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
@@ -173,21 +175,56 @@ class SpecVerifyError(RuntimeError):
 # --------------------------------------------------------------------------------------------
 # Marshalling helpers
 # --------------------------------------------------------------------------------------------
-_ws_cache: dict = {}
-_plan_ws_cache: dict = {}
+def _capture_id(stream: Optional[torch.cuda.Stream], raw: int) -> int:
+    """The id of the graph capture that a stream (None: the current one) is under; 0: none."""
+    if raw == 0 or (stream is None and not torch.cuda.is_current_stream_capturing()):
+        return 0  # (the default stream cannot be captured)
+    found = ctypes.c_uint64(0)
+    rc = load_library().spec_verify_capture_id(raw, ctypes.byref(found))
+    if rc != OK:
+        raise SpecVerifyError("spec_verify_capture_id", rc)
+    return found.value
+
+
+class _Workspaces:
+    """Device buffers kept per (device, stream).
+
+    A call under graph capture takes one that was made within that capture: its memory is the graph's, its
+    fill is a node ahead of the calls that need it, and every replay begins with it, whatever ran before and
+    in whatever order graphs are replayed.  So no graph holds a buffer that calls outside it use, or that is
+    given back when one of them needs a larger."""
+
+    def __init__(self, make):
+        self.make, self.kept, self.captured = make, {}, {}
+
+    def get(self, nbytes: int, device: int, stream: Optional[torch.cuda.Stream], raw: int) -> torch.Tensor:
+        key, capture = (device, raw), _capture_id(stream, raw)
+        if capture:
+            of, ws = self.captured.get(key, (0, None))
+            if of != capture:
+                ws = None
+        else:
+            ws = self.kept.get(key)
+        if ws is None or ws.numel() < nbytes:
+            with torch.cuda.stream(stream):  # the fill is in the order of the stream that uses it
+                ws = self.make(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+            if capture:
+                self.captured[key] = capture, ws
+            else:
+                self.kept[key] = ws
+        return ws
+
+
+# The library leaves a workspace's counters zero after each call, so one zero-fill suffices.
+_workspaces = _Workspaces(torch.zeros)
+# Not the verifiers' workspace: the planner overwrites its buffer, whose counter region the
+# verifiers need to stay zero.
+_plan_workspaces = _Workspaces(torch.empty)
 
 
 def workspace_for(nbytes: int, device: torch.device, stream: torch.cuda.Stream) -> torch.Tensor:
-    """A zero-filled uint8 device buffer of at least nbytes, kept per (device, stream).
-
-    The library leaves a workspace's counters zero after each call, so one zero-fill suffices.
-    """
-    key = (device.index, stream.cuda_stream)
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
-    return ws
+    """A uint8 device buffer of at least nbytes for calls on this stream, zero-filled when it was made."""
+    return _workspaces.get(nbytes, device.index, stream, stream.cuda_stream)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -548,13 +585,7 @@ def spec_verify_plan_budget(conf: torch.Tensor, cost: torch.Tensor, num_drafts=N
     nbytes = int(lib.spec_verify_plan_budget_workspace_bytes(B, K))
     if nbytes == 0:
         raise ValueError("the budget planner takes B * K <= 16384 slots and K <= 64")
-    # Not the verifiers' workspace: the planner overwrites its buffer, whose counter region the
-    # verifiers need to stay zero.
-    key = (dev.index, stream.cuda_stream)
-    ws = _plan_ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _plan_ws_cache[key] = ws
+    ws = _plan_workspaces.get(nbytes, dev.index, stream, stream.cuda_stream)
     rc = lib.spec_verify_plan_budget(_ptr(conf), _ptr(num_drafts), B, K, _ptr(cost), _ptr(admitted),
                                      _ptr(budget), _ptr(best_rate), _ptr(ws), ws.numel(),
                                      ctypes.c_void_p(stream.cuda_stream))
@@ -662,16 +693,6 @@ def _raw_stream(stream, device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
-def _workspace(nbytes: int, device: int, stream, raw: int) -> torch.Tensor:
-    """workspace_for, zero-filled on the stream that will use it."""
-    ws = _ws_cache.get((device, raw))
-    if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(stream):
-            ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _ws_cache[device, raw] = ws
-    return ws
-
-
 def spec_verify_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
                           v_cache: torch.Tensor, slot_table: torch.Tensor, committed: torch.Tensor,
                           cos_sin: Optional[torch.Tensor], *, parents=None, num_nodes=None,
@@ -746,7 +767,8 @@ def spec_verify_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
         lse = _result("lse", lse, (B, N, Hq), _FP32, dev, stream)
     raw = _raw_stream(stream, dev)
     if workspace is None:
-        workspace = _workspace(spec_verify_attention_workspace_bytes(B, N, Hq, Hkv, D, max_pos), dev, stream, raw)
+        nbytes = spec_verify_attention_workspace_bytes(B, N, Hq, Hkv, D, max_pos)
+        workspace = _workspaces.get(nbytes, dev, stream, raw)
     rc = lib.spec_verify_attention(
         q.data_ptr(), code, _row_stride("q", q, B, N, Hq, D), k_cache.data_ptr(), v_cache.data_ptr(), S,
         _slot_stride("k_cache", k_cache, Hkv, D), _slot_stride("v_cache", v_cache, Hkv, D),
@@ -792,7 +814,7 @@ def spec_verify_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, row_inde
         top_ids = top_logprobs = None
     raw = _raw_stream(stream, dev)
     if workspace is None:
-        workspace = _workspace(spec_verify_logprobs_workspace_bytes(B, T, V, top_n), dev, stream, raw)
+        workspace = _workspaces.get(spec_verify_logprobs_workspace_bytes(B, T, V, top_n), dev, stream, raw)
     rc = lib.spec_verify_logprobs(
         logits.data_ptr(), _logits_dtype(logits), _index("tokens", tokens, (B, T), dev),
         None if row_index is None else _index("row_index", row_index, (B, T), dev), B, rows, T, V,

@@ -1735,6 +1735,24 @@ extern "C" int spec_verify_wait_timeouts(uint64_t *count)
     return SPEC_VERIFY_OK;
 }
 
+// The capture that a stream is under; the legacy default stream (NULL) is never under one.
+extern "C" int spec_verify_capture_id(void *stream, uint64_t *id)
+{
+    if (!id) return SPEC_VERIFY_EINVAL;
+    *id = 0;
+    if (!stream) return SPEC_VERIFY_OK;
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long found = 0;
+    if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &found, nullptr, nullptr, nullptr, nullptr) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_VERIFY_ECUDA;
+    }
+    if (status == cudaStreamCaptureStatusInvalidated) return SPEC_VERIFY_ECUDA;
+    if (status == cudaStreamCaptureStatusActive) *id = found;
+    return SPEC_VERIFY_OK;
+}
+
 // ---------------------------------------------------------------------------------------------
 // Allocation-free entry point.
 //
