@@ -25,9 +25,12 @@
 // per thread: scores come to them as columns, so the exponentials are spread evenly however few the
 // query rows.
 //
-// The softmax's reference moves only when a score passes it by more than 2^8 (a vote of 128 threads
-// per tile): weights are then at most 2^8, as exact in 16 bits as below 1, and the accumulators are
-// left alone in nearly every tile.
+// The softmax's reference moves only when a score passes the largest that it was made for by more than
+// 2^8 (a vote of 128 threads per tile), so that the accumulators are left alone in nearly every tile.  A
+// weight keeps its digits at any size in bf16, whose exponents are fp32's.  In fp16 it does down to 2^-14,
+// then loses them one by one, and below 2^-25 it is 0: there the reference lies 2^7 below the maximum, so
+// that weights reach from 2^15 (of 65504) down to 2^-32 of an ordinary largest one.  131072 positions at
+// 2^-25.2 of one other, together 0.003 of the sum, were lost with the reference at the maximum.
 //
 // Measured (GB300, copy rate 6.68 TB/s; 32 query and 8 key heads of 128 unless said): 64 chains of 8 over
 // 509 to 8192 positions 122-125 us for 742 MB, 5.9-6.1 TB/s; one tree of 16 over 131000 positions 100 us
@@ -51,7 +54,9 @@ constexpr int MAX_SMS = 192;  // the workspace has room for two parts per CTA
 constexpr int COUNTERS = 2 * MAX_SMS;
 constexpr int FLAGS = 16;     // bad-slot flags: more than the segments the ring can hold
 constexpr int SEGS = 8;       // segments listed ahead
-constexpr float SLACK = 8.f;  // log2 of the largest weight
+constexpr float SLACK = 8.f;  // log2 of how far a score may pass the largest one that a reference was made for
+// log2 of the largest weight as a reference is made.
+__host__ __device__ constexpr float lift(bool bf16) { return bf16 ? 0.f : 7.f; }
 // In half tiles.  A segment at 3 or 5: 45.9 or 46.8 us against 45.8 for the 96 short requests above, 20.7 or 21.2
 // against 20.8 for the 48 trees; at 2 (with one CTA per SM) 63 against 56.
 constexpr int COST_TILE = 2, COST_SEGMENT = 4;
@@ -717,7 +722,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
 #pragma unroll
                         for (int c = 4; c < CW; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
                         move = group_or(bar, 128, fresh || fail ||
-                                                      fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > SLACK);
+                                                      fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > SLACK + lift(BF));
                     }
                     if (move) {
                         if (j > g.j0) {
@@ -726,7 +731,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                             tc::wait_ld(x);
                             mask();
                         }
-                        // Move the references to the columns' maxima.
+                        // Move the references to the columns' maxima, or below (lift).
                         float m = 0.f;
 #pragma unroll
                         for (int c = 0; c < CW; ++c) {
@@ -740,7 +745,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                             const int c = col0 + t;
                             m = fmaxf(fmaxf(ms.red[0][c], ms.red[1][c]), fmaxf(ms.red[2][c], ms.red[3][c]));
                             const float old = j == g.j0 ? -INFINITY : ms.ref[c];
-                            const float now = fmaxf(m, old);
+                            const float now = fmaxf(m - lift(BF), old);
                             ms.ref[c] = now;
                             ms.nref[c] = now == -INFINITY ? 0.f : -now;
                             ms.fac[c] = old == -INFINITY ? 0.f : ex2(old - now);
