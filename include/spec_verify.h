@@ -348,7 +348,7 @@ int spec_verify_kv_append(const void *q, const void *k, const void *v, int dtype
  *   q              [B * N] rows of Hq heads of D elements, q_stride elements apart, rotated
  *   out            [B * N][Hq][D], contiguous, of q's type;  lse  [B * N][Hq] fp32 or NULL
  *   N <= 64, D a multiple of 16 from 64 to 128, Hq a multiple of Hkv, num_slots and the caches' slot
- *   strides below 2^31, scale > 0 and finite
+ *   strides below 2^31, 0 < scale <= 2.3e38 (times log2(e) it has to be finite in fp32)
  *   workspace      spec_verify_attention_workspace_bytes(...) bytes, 256-byte aligned; zero-filled
  *                  before its first use, shared with the verifiers' (their counters' rules hold)
  * Sums and the softmax are in fp32; the weights are rounded to q's type for the product with v.

@@ -1147,6 +1147,7 @@ static const DevInfo *device_info()
 static int columns(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 constexpr size_t COUNTER_BYTES = 65536 * 4;  // the workspace's fixed region of counters
+constexpr float MAX_SCALE = 2.3e38f;         // times log2(e) it is still a number of fp32
 
 template <bool BF, int NQ, int DP>
 static cudaError_t launch(const Params &P, int grid, cudaStream_t s)
@@ -1215,7 +1216,7 @@ extern "C" int spec_verify_attention(const void *q, int dtype, int64_t q_stride,
     if (!q || !k_cache || !v_cache || !slot_table || !committed || !out || !workspace) return SPEC_VERIFY_EINVAL;
     if (dtype != SPEC_VERIFY_BF16 && dtype != SPEC_VERIFY_FP16) return SPEC_VERIFY_EINVAL;
     const size_t need = spec_verify_attention_workspace_bytes(B, N, Hq, Hkv, D, max_pos);
-    if (!need || num_slots < 1 || num_slots > 0x7fffffff || !(scale > 0.f) || scale > 3e38f) return SPEC_VERIFY_EINVAL;
+    if (!need || num_slots < 1 || num_slots > 0x7fffffff || !(scale > 0.f) || scale > MAX_SCALE) return SPEC_VERIFY_EINVAL;
     const int64_t qw = (int64_t)Hq * D, kw = (int64_t)Hkv * D;
     if (q_stride % 8 || k_slot_stride % 8 || v_slot_stride % 8 || q_stride < qw || k_slot_stride < kw || v_slot_stride < kw ||
         k_slot_stride >= (1ll << 31) || v_slot_stride >= (1ll << 31))
