@@ -50,6 +50,7 @@ constexpr int MAX_CTAS = 1024;
 constexpr int ROWS = 128;            // rows of its run that a CTA lists at a time
 constexpr float SLACK = 8.f;         // log2 of the largest term
 constexpr float LEAST = -0x1.92p99f;  // about -1e30, a bf16 value; logits below it count as it: 2^t is 0 and t stays finite
+constexpr float MOST_C = 1e8f, LEAST_C = 1e-26f;  // of log2(e) / T: LEAST c lies between -1e38 and -1e4
 constexpr float NEG_INF = -__builtin_huge_valf(), LOWEST = -0x1.fffffep127f;
 
 struct Params {
@@ -345,6 +346,46 @@ __device__ __forceinline__ int fault_of(const Params &P, int r)
     return temp >= 0.f && temp < 3.4e38f ? 0 : SPEC_VERIFY_DEV_BAD_ROW;
 }
 
+// The sums of a row for which the fold's fused product does not hold, by a warp, with differences before the
+// scale: a reference of such size is too coarse for the product (a row of nothing but finite masks; a
+// temperature close to 0), LEAST times c has left fp32, or comes so near to 0 that masks have weight.
+// 4 rows of 128256 at T = 1e-6 take 177 us in bf16 and 121 in fp32, against 35 and 50 at T = 1.  (Not called but
+// in place: what a call has to keep across it cost every row's end, 35.8 against 35.3 us for the 512 rows above.)
+template <typename T>
+__device__ __forceinline__ float2 sums_again(const T *row, int V, float top1, float temp)
+{
+    constexpr int FLY = 16;  // loads of a lane in flight
+    // log2(e) / T in two factors, so that no temperature takes it out of fp32.
+    const float a = temp < 1e-30f ? 0x1p64f : 1.f, b = 1.44269504f / (temp * a);
+    // One warp adds thousands of terms in a row, and equal ones are rounded the same way every time: what a
+    // sum loses is carried along.
+    float z = 0.f, s = 0.f, z_lost = 0.f, s_lost = 0.f;
+    auto add = [](float &sum, float &lost, float x) {
+        const float y = x - lost, now = sum + y;
+        lost = (now - sum) - y;
+        sum = now;
+    };
+    for (int i0 = threadIdx.x & 31; i0 < V; i0 += 32 * FLY) {
+        float x[FLY], zb = 0.f, sb = 0.f;
+#pragma unroll
+        for (int f = 0; f < FLY; ++f) x[f] = i0 + 32 * f < V ? Elt<T>::load(row, i0 + 32 * f) : NEG_INF;
+#pragma unroll
+        for (int f = 0; f < FLY; ++f) {
+            const float t = (x[f] - top1) * a * b, e = ex2(t);
+            zb += e;
+            if (e > 0.f) sb += e * t;
+        }
+        add(z, z_lost, zb);
+        add(s, s_lost, sb);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        z += __shfl_xor_sync(0xffffffffu, z, o);
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    }
+    return make_float2(z, s);
+}
+
 // The answers for a row's entry, by a warp; fin.top: its alternatives.
 template <typename T>
 __device__ __forceinline__ void answer(const Params &P, const Finish &fin, const Row &w, float m, float z, float s, int count)
@@ -355,20 +396,11 @@ __device__ __forceinline__ void answer(const Params &P, const Finish &fin, const
     const T *row = static_cast<const T *>(P.logits) + w.first;
     const float top1 = fin.top[0].v;
     const float c = 1.44269504f / temp;
-    // A reference of such size is too coarse for the fused product (a row of nothing but finite masks):
-    // differences are taken before the scale.
-    const bool low = fin.top[0].i >= 0 && !(fabsf(top1) * c < 1e7f);
-    if (low) {
-        z = s = 0.f;
-        for (int i = lane; i < P.V; i += 32) {
-            const float t = (Elt<T>::load(row, i) - top1) * c, e = ex2(t);
-            z += e;
-            if (e > 0.f) s += e * t;
-        }
-        for (int o = 16; o; o >>= 1) {
-            z += __shfl_xor_sync(0xffffffffu, z, o);
-            s += __shfl_xor_sync(0xffffffffu, s, o);
-        }
+    const bool low = fin.top[0].i >= 0 && !(fabsf(top1) * c < 1e7f && c < MOST_C && c > LEAST_C);
+    if (__builtin_expect(low, 0)) {
+        const float2 sums = sums_again<T>(row, P.V, top1, temp);
+        z = sums.x;
+        s = sums.y;
     }
     const bool bad = fin.top[0].i < 0 || !(z < __builtin_huge_valf());
     const float log_z = log2f(z);
