@@ -424,15 +424,25 @@ int spec_verify_philox(uint64_t seed, uint64_t offset, int n_slot, int n_req, ui
 int spec_verify_debug_fault(uint64_t *fault);
 
 /*
- * Waits that ran out of time in the top-k / top-p threshold kernel, read and cleared.  That
- * kernel streams rows through shared memory with asynchronous bulk copies and waits on each
- * copy's completion for at most 0.2 s; a wait that runs out (a copy should land in microseconds)
- * hands that CTA's remaining rows to the general threshold kernel, so the outputs are unaffected,
- * and adds one to this count.  *count = the waits that ran out since the last read (0 in normal
- * operation).  Synchronous (symbol copies after the work already enqueued on the legacy default
- * stream).  Returns SPEC_VERIFY_OK, SPEC_VERIFY_EINVAL for a NULL count, or SPEC_VERIFY_ECUDA.
+ * Waits that ran out of time, read and cleared.  The top-k / top-p threshold kernel streams rows
+ * through shared memory with asynchronous bulk copies and waits on each copy's completion for at
+ * most 0.2 s; a wait that runs out (a copy should land in microseconds) hands that CTA's remaining
+ * rows to the general threshold kernel, so the outputs are unaffected, and adds one to this count.
+ * So does each CTA of the log probabilities' kernel in which a wait ran out (about half a second),
+ * and these outputs are undefined (SPEC_VERIFY_DEV_TIMEOUT).  *count = the count since the last
+ * read (0 in normal operation).  Synchronous (symbol copies after the work already enqueued on the
+ * legacy default stream).  Returns SPEC_VERIFY_OK, SPEC_VERIFY_EINVAL for a NULL count, or
+ * SPEC_VERIFY_ECUDA.
  */
 int spec_verify_wait_timeouts(uint64_t *count);
+
+/*
+ * Debug builds: the limit, in SM clocks, of the waits that SPEC_VERIFY_DEV_TIMEOUT reports, on the
+ * current device; below 0 a wait that is not over at its first look runs out.  A test aid: with a
+ * small limit ordinary waits run out, and what follows can be looked at.  Synchronous.  Returns
+ * SPEC_VERIFY_OK, SPEC_VERIFY_ECUDA, or SPEC_VERIFY_EINVAL in a release build, whose limit is fixed.
+ */
+int spec_verify_debug_wait_clocks(int64_t clocks);
 
 /*
  * The id of the graph capture that `stream` is under, 0 when it is under none.  For callers that keep

@@ -94,6 +94,8 @@ def _declare(lib):
     lib.spec_verify_logprobs.restype = i32
     lib.spec_verify_logprobs_workspace_bytes.argtypes = [i32] * 4
     lib.spec_verify_logprobs_workspace_bytes.restype = sz
+    lib.spec_verify_debug_wait_clocks.argtypes = [ctypes.c_int64]
+    lib.spec_verify_debug_wait_clocks.restype = i32
     lib.spec_verify_capture_id.argtypes = [vp, ctypes.POINTER(u64)]
     lib.spec_verify_capture_id.restype = i32
     lib.spec_verify_debug_fault.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
@@ -148,14 +150,22 @@ def spec_verify_debug_fault(lib=None) -> int:
 
 
 def spec_verify_wait_timeouts(lib=None) -> int:
-    """Waits of the top-k / top-p ring kernel that ran out of time since the last read (0 in
-    normal operation; their rows were finished by the general threshold kernel)."""
+    """Waits inside kernels that ran out of time since the last read (0 in normal operation).  Rows of
+    the top-k / top-p ring kernel were then finished by the general threshold kernel; log probabilities
+    are undefined (device status 7)."""
     lib = lib or load_library()
     n = ctypes.c_uint64(0)
     rc = lib.spec_verify_wait_timeouts(ctypes.byref(n))
     if rc != OK:
         raise SpecVerifyError("spec_verify_wait_timeouts", rc)
     return int(n.value)
+
+
+def spec_verify_debug_wait_clocks(clocks: int, lib) -> None:
+    """The limit of waits inside a debug build's kernels, in SM clocks (a test aid; see the header)."""
+    rc = lib.spec_verify_debug_wait_clocks(clocks)
+    if rc != OK:
+        raise SpecVerifyError("spec_verify_debug_wait_clocks", rc)
 
 
 def spec_verify_strerror(code: int) -> str:

@@ -1700,6 +1700,8 @@ unsigned long long budget_debug_fault();
 unsigned long long append_debug_fault();
 unsigned long long attention_debug_fault();
 unsigned long long logprobs_debug_fault();
+bool logprobs_timeouts(unsigned long long &n);
+bool logprobs_wait_clocks(long long clocks);
 }  // namespace sv
 
 // The first out-of-range index the kernels met (debug builds), read and cleared across the
@@ -1723,16 +1725,27 @@ extern "C" int spec_verify_debug_fault(uint64_t *fault)
     return SPEC_VERIFY_OK;
 }
 
-// Stage waits of the threshold ring kernel that ran out of time, read and cleared; synchronous.
+// CTAs of the kernels with bounded waits in which one ran out, read and cleared; synchronous.
 extern "C" int spec_verify_wait_timeouts(uint64_t *count)
 {
     if (!count) return SPEC_VERIFY_EINVAL;
     unsigned long long n = 0, z = 0;
     if (cudaMemcpyFromSymbol(&n, sv::g_ring_timeouts, sizeof n) != cudaSuccess ||
-        cudaMemcpyToSymbol(sv::g_ring_timeouts, &z, sizeof z) != cudaSuccess)
+        cudaMemcpyToSymbol(sv::g_ring_timeouts, &z, sizeof z) != cudaSuccess || !sv::logprobs_timeouts(n))
         return SPEC_VERIFY_ECUDA;
     *count = n;
     return SPEC_VERIFY_OK;
+}
+
+// The limit of the bounded waits, in clocks, in a debug build; a release build keeps its own.
+extern "C" int spec_verify_debug_wait_clocks(int64_t clocks)
+{
+#ifdef SV_DEBUG
+    return sv::logprobs_wait_clocks(clocks) ? SPEC_VERIFY_OK : SPEC_VERIFY_ECUDA;
+#else
+    (void)clocks;
+    return SPEC_VERIFY_EINVAL;
+#endif
 }
 
 // The capture that a stream is under; the legacy default stream (NULL) is never under one.

@@ -700,7 +700,11 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
                         const int s = k % STAGES;
                         if (k >= STAGES)
                             ok = tc::bar_wait(tc::smem_u32(&sm.empty[s]), (k / STAGES + 1) & 1, abort);
-                        if (!ok) break;
+                        // (Warps that gave up on a copy release its stage all the same.)
+                        if (!ok || *abort) {
+                            ok = false;
+                            break;
+                        }
                         const uintptr_t t = first + (uintptr_t)j * TILE_VEC * 16;
                         uintptr_t a = t, z = t + TILE_VEC * 16;
                         if (z > first + (uintptr_t)nvec * 16) z = first + (uintptr_t)nvec * 16;
@@ -864,9 +868,11 @@ __global__ void __launch_bounds__(NT_ALL, CTAS_PER_SM) logprobs_kernel(const Par
             if (lane == 0) tc::bar_arrive(tc::smem_u32(&sm.folded[rr & 1]));
         }
     }
+    __syncthreads();  // any warp's wait may have been the one that ran out
     if (*abort && lane == 0) {
-        // A bounded wait ran out.  Copies land before the CTA ends, folded or not.
+        // Copies land before the CTA ends, folded or not.
         if (warp == NW) {
+            atomicAdd(&tc::g_timeouts, 1ull);
             const int64_t begin = clock64();
             for (int i = k > STAGES ? k - STAGES : 0; i < k; ++i)
                 while (!tc::bar_try(tc::smem_u32(&sm.full[i % STAGES]), (i / STAGES) & 1) &&
@@ -924,6 +930,9 @@ static cudaError_t launch(const Params &P, int grid, cudaStream_t s)
 }  // namespace svlp
 
 namespace sv {
+bool logprobs_timeouts(unsigned long long &n) { return tc::read_timeouts(n); }
+bool logprobs_wait_clocks(long long clocks) { return tc::set_wait_clocks(clocks); }
+
 // This module's first range violation (debug builds; 0 otherwise), cleared when read.
 unsigned long long logprobs_debug_fault()
 {

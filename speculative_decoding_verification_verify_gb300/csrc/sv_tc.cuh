@@ -15,6 +15,17 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)_
 // ---------------------------------------------------------------------------------------------
 constexpr int64_t WAIT_CLOCKS = 1000000000;  // about half a second
 
+// The limit of waits for other warps, copies and products; what a CTA waits for before it ends after that, its own
+// copies and products in flight, has WAIT_CLOCKS always.  In debug builds a test can lower it
+// (spec_verify_debug_wait_clocks); below 0 a wait that is not over at the first look runs out.
+#ifdef SV_DEBUG
+static __device__ long long g_wait_clocks = WAIT_CLOCKS;
+__device__ __forceinline__ int64_t wait_clocks() { return *(volatile long long *)&g_wait_clocks; }
+#else
+__device__ __forceinline__ constexpr int64_t wait_clocks() { return WAIT_CLOCKS; }
+#endif
+static __device__ unsigned long long g_timeouts;  // CTAs in which a wait ran out (spec_verify_wait_timeouts)
+
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -61,11 +72,18 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 // ran out of time.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort)
 {
+#ifdef SV_DEBUG
+    if (wait_clocks() < 0) {
+        if (bar_test(bar, parity)) return true;
+        *abort = 1;
+        return false;
+    }
+#endif
     if (bar_try(bar, parity)) return true;
     const int64_t t0 = clock64();
     while (!bar_try(bar, parity)) {
         if (*abort) return false;
-        if (clock64() - t0 > WAIT_CLOCKS) {
+        if (clock64() - t0 > wait_clocks()) {
             *abort = 1;
             return false;
         }
@@ -190,6 +208,25 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[32])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
                  : "memory");
+}
+
+// Host: this module's count of timeouts, read and cleared, and its limit of waits (debug builds).
+inline bool read_timeouts(unsigned long long &n)
+{
+    unsigned long long x = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&x, g_timeouts, sizeof x) != cudaSuccess || cudaMemcpyToSymbol(g_timeouts, &z, sizeof z) != cudaSuccess)
+        return false;
+    n += x;
+    return true;
+}
+
+inline bool set_wait_clocks([[maybe_unused]] long long clocks)
+{
+#ifdef SV_DEBUG
+    return cudaMemcpyToSymbol(g_wait_clocks, &clocks, sizeof clocks) == cudaSuccess;
+#else
+    return false;
+#endif
 }
 
 }  // namespace tc
