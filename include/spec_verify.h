@@ -428,8 +428,8 @@ int spec_verify_debug_fault(uint64_t *fault);
  * through shared memory with asynchronous bulk copies and waits on each copy's completion for at
  * most 0.2 s; a wait that runs out (a copy should land in microseconds) hands that CTA's remaining
  * rows to the general threshold kernel, so the outputs are unaffected, and adds one to this count.
- * So does each CTA of the log probabilities' kernel in which a wait ran out (about half a second),
- * and these outputs are undefined (SPEC_VERIFY_DEV_TIMEOUT).  *count = the count since the last
+ * So does each CTA of the attention and log probabilities' kernels in which a wait ran out (about
+ * half a second), and these outputs are undefined (SPEC_VERIFY_DEV_TIMEOUT).  *count = the count since the last
  * read (0 in normal operation).  Synchronous (symbol copies after the work already enqueued on the
  * legacy default stream).  Returns SPEC_VERIFY_OK, SPEC_VERIFY_EINVAL for a NULL count, or
  * SPEC_VERIFY_ECUDA.

@@ -151,8 +151,8 @@ def spec_verify_debug_fault(lib=None) -> int:
 
 def spec_verify_wait_timeouts(lib=None) -> int:
     """Waits inside kernels that ran out of time since the last read (0 in normal operation).  Rows of
-    the top-k / top-p ring kernel were then finished by the general threshold kernel; log probabilities
-    are undefined (device status 7)."""
+    the top-k / top-p ring kernel were then finished by the general threshold kernel; attention and log
+    probabilities are undefined (device status 7)."""
     lib = lib or load_library()
     n = ctypes.c_uint64(0)
     rc = lib.spec_verify_wait_timeouts(ctypes.byref(n))

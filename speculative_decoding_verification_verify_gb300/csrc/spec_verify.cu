@@ -1700,6 +1700,8 @@ unsigned long long budget_debug_fault();
 unsigned long long append_debug_fault();
 unsigned long long attention_debug_fault();
 unsigned long long logprobs_debug_fault();
+bool attention_timeouts(unsigned long long &n);
+bool attention_wait_clocks(long long clocks);
 bool logprobs_timeouts(unsigned long long &n);
 bool logprobs_wait_clocks(long long clocks);
 }  // namespace sv
@@ -1731,7 +1733,8 @@ extern "C" int spec_verify_wait_timeouts(uint64_t *count)
     if (!count) return SPEC_VERIFY_EINVAL;
     unsigned long long n = 0, z = 0;
     if (cudaMemcpyFromSymbol(&n, sv::g_ring_timeouts, sizeof n) != cudaSuccess ||
-        cudaMemcpyToSymbol(sv::g_ring_timeouts, &z, sizeof z) != cudaSuccess || !sv::logprobs_timeouts(n))
+        cudaMemcpyToSymbol(sv::g_ring_timeouts, &z, sizeof z) != cudaSuccess || !sv::attention_timeouts(n) ||
+        !sv::logprobs_timeouts(n))
         return SPEC_VERIFY_ECUDA;
     *count = n;
     return SPEC_VERIFY_OK;
@@ -1741,7 +1744,7 @@ extern "C" int spec_verify_wait_timeouts(uint64_t *count)
 extern "C" int spec_verify_debug_wait_clocks(int64_t clocks)
 {
 #ifdef SV_DEBUG
-    return sv::logprobs_wait_clocks(clocks) ? SPEC_VERIFY_OK : SPEC_VERIFY_ECUDA;
+    return sv::attention_wait_clocks(clocks) && sv::logprobs_wait_clocks(clocks) ? SPEC_VERIFY_OK : SPEC_VERIFY_ECUDA;
 #else
     (void)clocks;
     return SPEC_VERIFY_EINVAL;

@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
             // One thread does it all, and waits for nothing without weighing what is ready meanwhile.
             int64_t begin = 0;
             auto late = [&] {
-                if (!*abort && clock64() - begin <= tc::WAIT_CLOCKS) return false;
+                if (!*abort && clock64() - begin <= tc::wait_clocks()) return false;
                 *abort = 1;
                 return true;
             };
@@ -532,7 +532,8 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
             auto put = [&](const Seg &g) {
                 if (n >= SEGS) {
                     ok = tc::bar_wait(tc::smem_u32(&ms.segempty[n % SEGS]), (n / SEGS + 1) & 1, abort);
-                    if (!__all_sync(0xffffffffu, ok)) return false;
+                    ok = __all_sync(0xffffffffu, ok);  // the lanes stay together
+                    if (!ok) return;
                 }
                 if (lane == 0) {
                     ms.seg[n % SEGS] = g;
@@ -540,7 +541,6 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                 }
                 __syncwarp();
                 ++n;
-                return true;
             };
             Seg g = {};
             bool first = true;
@@ -1085,8 +1085,10 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
     tc::fence_after();
     if (ms.abort) {
         // A bounded wait ran out: what is written is not an answer.  The products in flight end
-        // (again with a limit) before their memory is given back; the copies were waited for.
-        if (tid == 128) {
+        // (again with a limit) before their memory is given back; the copies were waited for.  A commit is
+        // for the products of its own thread: the lane that issued them, which every election picks.
+        if (warp == 4 && tc::elect()) {
+            atomicAdd(&tc::g_timeouts, 1ull);
             const int64_t begin = clock64();
             tc::commit(tc::smem_u32(&ms.drain));
             while (!tc::bar_try(tc::smem_u32(&ms.drain), 0) && clock64() - begin < tc::WAIT_CLOCKS) {}
@@ -1181,6 +1183,9 @@ static cudaError_t dispatch(int nq, int dp, const Params &P, int grid,
 }  // namespace svatt
 
 namespace sv {
+bool attention_timeouts(unsigned long long &n) { return tc::read_timeouts(n); }
+bool attention_wait_clocks(long long clocks) { return tc::set_wait_clocks(clocks); }
+
 // This module's first range violation (debug builds; 0 otherwise), cleared when read.
 unsigned long long attention_debug_fault()
 {

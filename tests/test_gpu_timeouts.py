@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import speculative_decoding_verification_verify_gb300 as sv
+import test_gpu_attention as ta
 import test_gpu_logprobs as tl
 
 pytestmark = pytest.mark.gpu
@@ -69,3 +70,15 @@ def test_logprobs(lib, B, T, V):
         return sv.spec_verify_logprobs(x, tok, top_n=5, workspace=ws, dev_status=status)
 
     run_out(lib, call, sv.spec_verify_logprobs_workspace_bytes(B, T, V, 5))
+
+
+@pytest.mark.parametrize("committed,N,Hq,Hkv,D,dtype", [
+    ([700], 1, 4, 1, 128, torch.bfloat16), ([40000, 3], 8, 8, 2, 128, torch.bfloat16), ([30000], 16, 4, 1, 64, torch.float16),
+    ([0, 130, 700, 3, 128] * 40, 3, 8, 8, 80, torch.bfloat16), ([3000] * 64, 20, 4, 1, 128, torch.float16)])
+def test_attention(lib, committed, N, Hq, Hkv, D, dtype):
+    s = ta.make(committed, N, Hq, Hkv, D, dtype, seed=N, tree=N > 1)
+
+    def call(ws, status):
+        return ta.call(s, workspace=ws, dev_status=status)
+
+    run_out(lib, call, sv.spec_verify_attention_workspace_bytes(len(committed), N, Hq, Hkv, D, s["slot_table"].shape[1]))
