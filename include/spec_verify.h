@@ -86,8 +86,9 @@ extern "C" {
                                              attention: lengths or positions that do not fit */
 #define SPEC_VERIFY_DEV_BAD_KV_SLOT 6     /* KV cache: a slot outside [0, num_slots) */
 #define SPEC_VERIFY_DEV_TIMEOUT 7      /* attention, logprobs: a bounded wait inside the kernel ran out;
-                                          the outputs are undefined, and the workspace has to be
-                                          zero-filled again before its next use */
+                                          the outputs are undefined (nothing in them says so: the
+                                          event shows here and in spec_verify_wait_timeouts), and the
+                                          workspace has to be zero-filled again before its next use */
 
 /* Modes for spec_verify_workspace_bytes. */
 #define SPEC_VERIFY_MODE_GREEDY 0

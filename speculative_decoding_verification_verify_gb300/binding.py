@@ -224,6 +224,9 @@ class _Workspaces:
                 self.kept[key] = ws
         return ws
 
+    def forget(self):
+        self.kept.clear()
+
 
 # The library leaves a workspace's counters zero after each call, so one zero-fill suffices.
 _workspaces = _Workspaces(torch.zeros)
@@ -235,6 +238,14 @@ _plan_workspaces = _Workspaces(torch.empty)
 def workspace_for(nbytes: int, device: torch.device, stream: torch.cuda.Stream) -> torch.Tensor:
     """A uint8 device buffer of at least nbytes for calls on this stream, zero-filled when it was made."""
     return _workspaces.get(nbytes, device.index, stream, stream.cuda_stream)
+
+
+def spec_verify_reset_workspaces() -> None:
+    """Forget the buffers kept for calls without a workspace: the next call on each stream takes a new,
+    zero-filled one.  Needed after device status 7 (a wait inside a kernel ran out), which leaves counters
+    behind on which later calls would join too early.  A graph's calls begin with a fill and need it not;
+    a caller's own workspace is the caller's to zero."""
+    _workspaces.forget()
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -763,7 +774,9 @@ def spec_verify_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
 
     q [B, N, Hq, D] rotated, the cache and its tables as spec_verify_kv_append left them; scale
     defaults to D ** -0.5.  Returns out [B, N, Hq, D] and, when wanted or given, lse [B, N, Hq] fp32.
-    Without dev_status, faults in the data show in the returned rows alone (NaN)."""
+    Without dev_status, faults in the data show in the returned rows alone (NaN).  A wait inside the kernel
+    that runs out (status 7) does not show there but in dev_status and spec_verify_wait_timeouts;
+    spec_verify_reset_workspaces has to follow it."""
     lib = _lib or load_library()
     code, dt, dev = _half_dtype(q), q.dtype, _device_of("q", q)
     B, N, Hq, D = q.shape
@@ -804,7 +817,8 @@ def spec_verify_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, row_inde
     """Log probability, rank, entropy and top_n alternatives of given tokens: logits [B, rows, V] (bf16
     / fp32) as verified, tokens [B, T] int32 (verification's out_tokens; -1: nothing there), row_index
     [B, T] int32 (a tree's accept_index; None: token t belongs to row t), temperatures [B] fp32.
-    Without dev_status, faults in the data show in the returned entries alone (NaN, -1)."""
+    Without dev_status, faults in the data show in the returned entries alone (NaN, -1).  Status 7 as for
+    spec_verify_attention."""
     lib = _lib or load_library()
     dev = _device_of("logits", logits)
     if not logits.is_contiguous():

@@ -82,3 +82,23 @@ def test_attention(lib, committed, N, Hq, Hkv, D, dtype):
         return ta.call(s, workspace=ws, dev_status=status)
 
     run_out(lib, call, sv.spec_verify_attention_workspace_bytes(len(committed), N, Hq, Hkv, D, s["slot_table"].shape[1]))
+
+
+def test_after_a_reset_calls_without_a_workspace_are_right(lib):
+    s = ta.make([40000, 700], 8, 4, 1, 128, torch.bfloat16, seed=5, tree=True)
+    x, tok = tl.rows(1, 3, 40009, torch.bfloat16, seed=5)
+    with limit(lib, USUAL):
+        want, said = ta.call(s), sv.spec_verify_logprobs(x, tok, top_n=3)
+    for clocks in (-1, 2000, -1):
+        with limit(lib, clocks):
+            status = torch.zeros(1, dtype=torch.int32, device=DEV)
+            ta.call(s, dev_status=status)
+            sv.spec_verify_logprobs(x, tok, top_n=3, dev_status=status)
+            torch.cuda.synchronize()
+        assert clocks >= 0 or int(status) == 7
+        sv.spec_verify_reset_workspaces()
+        with limit(lib, USUAL):
+            got, again = ta.call(s), sv.spec_verify_logprobs(x, tok, top_n=3)
+            torch.cuda.synchronize()
+        assert torch.equal(got.out, want.out) and torch.equal(got.lse, want.lse)
+        assert all(torch.equal(a, b) for a, b in zip(again, said))

@@ -57,3 +57,14 @@ def test_capture_id_on_the_host(monkeypatch):
     _build.build()
     assert binding.load_library().spec_verify_capture_id(None, None) == binding.EINVAL
     assert binding._capture_id(None, 0) == 0
+
+
+def test_forgetting_gives_new_zeros(monkeypatch):
+    w, _ = kept(monkeypatch)
+    monkeypatch.setattr(binding, "_workspaces", w)
+    a = w.get(100, "cpu", None, 5)
+    a.fill_(1)  # what a wait that ran out leaves behind
+    assert w.get(100, "cpu", None, 5) is a
+    binding.spec_verify_reset_workspaces()
+    b = w.get(100, "cpu", None, 5)
+    assert b is not a and not b.any()
