@@ -185,12 +185,30 @@ class SpecVerifyError(RuntimeError):
 # --------------------------------------------------------------------------------------------
 # Marshalling helpers
 # --------------------------------------------------------------------------------------------
-def _capture_id(stream: Optional[torch.cuda.Stream], raw: int) -> int:
-    """The id of the graph capture that a stream (None: the current one) is under; 0: none."""
-    if raw == 0 or (stream is None and not torch.cuda.is_current_stream_capturing()):
+_current_device = torch._C._cuda_getDevice  # (torch.cuda.current_device looks first whether CUDA is set up)
+
+
+def _on(device: int, entry):
+    """An entry point of the library with that device current: it launches on, and keeps its kernels' attributes
+    for, the current one, and raw stream handles are that device's."""
+    if device == _current_device():
+        return entry
+
+    def call(*args):
+        with torch.cuda.device(device):
+            return entry(*args)
+
+    return call
+
+
+def _capture_id(device: int, stream: Optional[torch.cuda.Stream], raw: int) -> int:
+    """The id of the graph capture that a stream (None: the device's current one) is under; 0: none."""
+    if raw == 0:
         return 0  # (the default stream cannot be captured)
+    if stream is None and device == _current_device() and not torch.cuda.is_current_stream_capturing():
+        return 0
     found = ctypes.c_uint64(0)
-    rc = load_library().spec_verify_capture_id(raw, ctypes.byref(found))
+    rc = _on(device, load_library().spec_verify_capture_id)(raw, ctypes.byref(found))
     if rc != OK:
         raise SpecVerifyError("spec_verify_capture_id", rc)
     return found.value
@@ -208,7 +226,7 @@ class _Workspaces:
         self.make, self.kept, self.captured = make, {}, {}
 
     def get(self, nbytes: int, device: int, stream: Optional[torch.cuda.Stream], raw: int) -> torch.Tensor:
-        key, capture = (device, raw), _capture_id(stream, raw)
+        key, capture = (device, raw), _capture_id(device, stream, raw)
         if capture:
             of, ws = self.captured.get(key, (0, None))
             if of != capture:
@@ -304,7 +322,7 @@ def spec_verify_greedy(logits: torch.Tensor, draft_ids: torch.Tensor, *, out_tok
     accept_len = accept_len if accept_len is not None else torch.empty(B, dtype=torch.int32, device=dev)
     nbytes = spec_verify_workspace_bytes(MODE_GREEDY, B, k, V)
     workspace, dev_status = _ws_and_status(nbytes, dev, stream, workspace, dev_status)
-    rc = lib.spec_verify_greedy(_ptr(logits), _logits_dtype(logits), _ptr(draft_ids), B, k, V,
+    rc = _on(dev.index, lib.spec_verify_greedy)(_ptr(logits), _logits_dtype(logits), _ptr(draft_ids), B, k, V,
                                 _ptr(out_tokens), _ptr(accept_len), _ptr(workspace),
                                 workspace.numel(), _ptr(dev_status),
                                 ctypes.c_void_p(stream.cuda_stream))
@@ -338,7 +356,7 @@ def spec_verify_rejection(logits: torch.Tensor, draft_ids: torch.Tensor,
         out_probs = torch.empty((B, k1, 3), dtype=torch.float32, device=dev)
     nbytes = spec_verify_workspace_bytes(MODE_REJECTION, B, k, V)
     workspace, dev_status = _ws_and_status(nbytes, dev, stream, workspace, dev_status)
-    rc = lib.spec_verify_rejection(_ptr(logits), _logits_dtype(logits), _ptr(draft_ids),
+    rc = _on(dev.index, lib.spec_verify_rejection)(_ptr(logits), _logits_dtype(logits), _ptr(draft_ids),
                                    _ptr(draft_probs), B, k, V, float(temperature),
                                    int(seed) & (2**64 - 1), int(offset) & (2**64 - 1),
                                    _ptr(out_tokens), _ptr(accept_len), _ptr(out_probs),
@@ -371,7 +389,7 @@ def spec_verify_block(logits: torch.Tensor, draft_ids: torch.Tensor,
     accept_len = accept_len if accept_len is not None else torch.empty(B, dtype=torch.int32, device=dev)
     nbytes = spec_verify_workspace_bytes(MODE_BLOCK, B, k, V)
     workspace, dev_status = _ws_and_status(nbytes, dev, stream, workspace, dev_status)
-    rc = lib.spec_verify_block(_ptr(logits), _logits_dtype(logits), _ptr(draft_ids), _ptr(draft_probs),
+    rc = _on(dev.index, lib.spec_verify_block)(_ptr(logits), _logits_dtype(logits), _ptr(draft_ids), _ptr(draft_probs),
                                B, k, V, float(temperature), int(seed) & (2**64 - 1),
                                int(offset) & (2**64 - 1), _ptr(out_tokens), _ptr(accept_len),
                                _ptr(workspace), workspace.numel(), _ptr(dev_status),
@@ -400,7 +418,7 @@ def spec_verify_tree(logits: torch.Tensor, node_tokens: torch.Tensor, parents: t
     accept_len = accept_len if accept_len is not None else torch.empty(B, dtype=torch.int32, device=dev)
     nbytes = spec_verify_workspace_bytes(MODE_TREE, B, N, V)
     workspace, dev_status = _ws_and_status(nbytes, dev, stream, workspace, dev_status)
-    rc = lib.spec_verify_tree(_ptr(logits), _logits_dtype(logits), _ptr(node_tokens),
+    rc = _on(dev.index, lib.spec_verify_tree)(_ptr(logits), _logits_dtype(logits), _ptr(node_tokens),
                               _ptr(parents), B, N, V, int(mode), float(temperature),
                               int(seed) & (2**64 - 1), int(offset) & (2**64 - 1),
                               _ptr(out_tokens), _ptr(accept_index), _ptr(accept_len),
@@ -420,7 +438,7 @@ def spec_verify_philox(seed: int, offset: int, n_slot: int, n_req: int, out=None
     stream = stream or torch.cuda.current_stream(device)
     if out is None:
         out = torch.empty((n_slot, n_req, 4), dtype=torch.int32, device=device)
-    rc = lib.spec_verify_philox(int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), n_slot, n_req,
+    rc = _on(out.get_device(), lib.spec_verify_philox)(int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), n_slot, n_req,
                                 _ptr(out), ctypes.c_void_p(stream.cuda_stream))
     if rc != OK:
         raise SpecVerifyError("spec_verify_philox", rc)
@@ -445,7 +463,7 @@ def spec_verify_rejection_noalloc(logits: torch.Tensor, draft_ids: torch.Tensor,
     _check_dev("out_tokens", out_tokens, torch.int32)
     _check_dev("accept_len", accept_len, torch.int32)
     stream = stream or torch.cuda.current_stream(logits.device)
-    rc = lib.spec_verify_rejection_noalloc(_ptr(logits), _logits_dtype(logits), _ptr(draft_ids),
+    rc = _on(logits.device.index, lib.spec_verify_rejection_noalloc)(_ptr(logits), _logits_dtype(logits), _ptr(draft_ids),
                                            _ptr(draft_probs), B, k, V, float(temperature),
                                            int(seed) & (2**64 - 1), int(offset) & (2**64 - 1),
                                            _ptr(out_tokens), _ptr(accept_len), _ptr(out_probs),
@@ -496,7 +514,7 @@ def spec_verify_kv_compact(kv_pool: torch.Tensor, slot_table: torch.Tensor,
         committed_out = torch.empty(B, dtype=torch.int32, device=dev)
     if dev_status is None:
         dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
-    rc = lib.spec_verify_kv_compact(_ptr(kv_pool), int(num_slots), int(row_bytes), int(planes),
+    rc = _on(dev.index, lib.spec_verify_kv_compact)(_ptr(kv_pool), int(num_slots), int(row_bytes), int(planes),
                                     int(plane_stride), _ptr(slot_table), slot_table.shape[1],
                                     _ptr(committed), _ptr(committed_out), _ptr(accept_index),
                                     _ptr(accept_len), B, N, _ptr(dev_status),
@@ -543,7 +561,7 @@ def spec_verify_rejection_ex(logits: torch.Tensor, draft_ids: torch.Tensor,
     accept_len = accept_len if accept_len is not None else torch.empty(B, dtype=torch.int32, device=dev)
     nbytes = spec_verify_workspace_bytes(MODE_REJECTION, B, k, V)
     workspace, dev_status = _ws_and_status(nbytes, dev, stream, workspace, dev_status)
-    rc = lib.spec_verify_rejection_ex(_ptr(logits), _logits_dtype(logits), _ptr(draft_ids),
+    rc = _on(dev.index, lib.spec_verify_rejection_ex)(_ptr(logits), _logits_dtype(logits), _ptr(draft_ids),
                                       _ptr(draft_probs), B, k, V, ctypes.byref(opt),
                                       int(seed) & (2**64 - 1), int(offset) & (2**64 - 1),
                                       _ptr(out_tokens), _ptr(accept_len), _ptr(out_probs),
@@ -575,7 +593,7 @@ def spec_verify_tree_ex(logits: torch.Tensor, node_tokens: torch.Tensor, parents
     accept_len = accept_len if accept_len is not None else torch.empty(B, dtype=torch.int32, device=dev)
     nbytes = spec_verify_workspace_bytes(MODE_TREE, B, N, V)
     workspace, dev_status = _ws_and_status(nbytes, dev, stream, workspace, dev_status)
-    rc = lib.spec_verify_tree_ex(_ptr(logits), _logits_dtype(logits), _ptr(node_tokens),
+    rc = _on(dev.index, lib.spec_verify_tree_ex)(_ptr(logits), _logits_dtype(logits), _ptr(node_tokens),
                                  _ptr(parents), B, N, V, ctypes.byref(opt), int(seed) & (2**64 - 1),
                                  int(offset) & (2**64 - 1), _ptr(out_tokens), _ptr(accept_index),
                                  _ptr(accept_len), _ptr(workspace), workspace.numel(),
@@ -607,7 +625,7 @@ def spec_verify_plan_budget(conf: torch.Tensor, cost: torch.Tensor, num_drafts=N
     if nbytes == 0:
         raise ValueError("the budget planner takes B * K <= 16384 slots and K <= 64")
     ws = _plan_workspaces.get(nbytes, dev.index, stream, stream.cuda_stream)
-    rc = lib.spec_verify_plan_budget(_ptr(conf), _ptr(num_drafts), B, K, _ptr(cost), _ptr(admitted),
+    rc = _on(dev.index, lib.spec_verify_plan_budget)(_ptr(conf), _ptr(num_drafts), B, K, _ptr(cost), _ptr(admitted),
                                      _ptr(budget), _ptr(best_rate), _ptr(ws), ws.numel(),
                                      ctypes.c_void_p(stream.cuda_stream))
     if rc != OK:
@@ -745,7 +763,7 @@ def spec_verify_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_c
         cs = cos_sin.data_ptr()
     max_pos = slot_table.shape[-1]
     q_out = _result("q_out", q_out, (B, N, Hq, D), dt, dev, stream)
-    rc = lib.spec_verify_kv_append(
+    rc = _on(dev, lib.spec_verify_kv_append)(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), code, _row_stride("q", q, B, N, Hq, D),
         _row_stride("k", k, B, N, Hkv, D), _row_stride("v", v, B, N, Hkv, D), q_out.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), S, _slot_stride("k_cache", k_cache, Hkv, D),
@@ -792,7 +810,7 @@ def spec_verify_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     if workspace is None:
         nbytes = spec_verify_attention_workspace_bytes(B, N, Hq, Hkv, D, max_pos)
         workspace = _workspaces.get(nbytes, dev, stream, raw)
-    rc = lib.spec_verify_attention(
+    rc = _on(dev, lib.spec_verify_attention)(
         q.data_ptr(), code, _row_stride("q", q, B, N, Hq, D), k_cache.data_ptr(), v_cache.data_ptr(), S,
         _slot_stride("k_cache", k_cache, Hkv, D), _slot_stride("v_cache", v_cache, Hkv, D),
         _index("slot_table", slot_table, (B, max_pos), dev), max_pos, _index("committed", committed, (B,), dev),
@@ -839,7 +857,7 @@ def spec_verify_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, row_inde
     raw = _raw_stream(stream, dev)
     if workspace is None:
         workspace = _workspaces.get(spec_verify_logprobs_workspace_bytes(B, T, V, top_n), dev, stream, raw)
-    rc = lib.spec_verify_logprobs(
+    rc = _on(dev, lib.spec_verify_logprobs)(
         logits.data_ptr(), _logits_dtype(logits), _index("tokens", tokens, (B, T), dev),
         None if row_index is None else _index("row_index", row_index, (B, T), dev), B, rows, T, V,
         None if temperatures is None else temperatures.data_ptr(), temperature, top_n, logprobs.data_ptr(),

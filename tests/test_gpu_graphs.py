@@ -83,14 +83,14 @@ def test_replays_in_any_order():
 
 def test_capture_ids():
     side = torch.cuda.Stream()
-    assert sv.binding._capture_id(side, side.cuda_stream) == 0 and sv.binding._capture_id(None, 0) == 0
+    assert sv.binding._capture_id(0, side, side.cuda_stream) == 0 and sv.binding._capture_id(0, None, 0) == 0
     x, seen = torch.zeros(4, device=DEV), []
     for _ in range(2):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             cur = torch.cuda.current_stream()
             x.add_(1)
-            seen.append(sv.binding._capture_id(None, cur.cuda_stream))
-            assert sv.binding._capture_id(cur, cur.cuda_stream) == seen[-1]
-            assert sv.binding._capture_id(side, side.cuda_stream) == 0
+            seen.append(sv.binding._capture_id(0, None, cur.cuda_stream))
+            assert sv.binding._capture_id(0, cur, cur.cuda_stream) == seen[-1]
+            assert sv.binding._capture_id(0, side, side.cuda_stream) == 0
     assert 0 not in seen and seen[0] != seen[1]

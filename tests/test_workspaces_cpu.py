@@ -7,7 +7,7 @@ from speculative_decoding_verification_verify_gb300 import binding
 
 def kept(monkeypatch, make=torch.zeros):
     now = dict(capture=0)
-    monkeypatch.setattr(binding, "_capture_id", lambda stream, raw: now["capture"])
+    monkeypatch.setattr(binding, "_capture_id", lambda device, stream, raw: now["capture"])
     return binding._Workspaces(make), now
 
 
@@ -56,7 +56,7 @@ def test_capture_id_on_the_host(monkeypatch):
 
     _build.build()
     assert binding.load_library().spec_verify_capture_id(None, None) == binding.EINVAL
-    assert binding._capture_id(None, 0) == 0
+    assert binding._capture_id(0, None, 0) == 0
 
 
 def test_forgetting_gives_new_zeros(monkeypatch):
