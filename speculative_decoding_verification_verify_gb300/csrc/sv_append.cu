@@ -65,6 +65,8 @@ __global__ void __launch_bounds__(NT) append_kernel(const Params P)
     const int hv = P.D / 8, hu = hv / 2;  // a head's vectors and units
     const int units = (P.Hq + 2 * P.Hkv) * hu;
     const int rv = P.rot / 8;  // rotated vectors of a head (even)
+    const int c = SV_INB(b, P.B, 1001) ? P.committed[b] : 0;
+    const int nn = P.num_nodes && SV_INB(b, P.B, 1002) ? P.num_nodes[b] : P.N;
 
     // A unit's two vectors: (j, j + rv/2) among the rotated ones when pairs are half a rotation
     // apart, else neighbours.
@@ -86,19 +88,19 @@ __global__ void __launch_bounds__(NT) append_kernel(const Params P)
         const uint4 *base = is_q ? P.q : is_k ? P.k : P.v;
         const int64_t stride = is_q ? P.q_row : is_k ? P.k_row : P.v_row;
         const int64_t at = row * stride + (x.head - (is_q ? 0 : is_k ? P.Hq : P.Hq + P.Hkv)) * hv;
-        if (!SV_INB(at + x.i1, (rows - 1) * stride + (is_q ? P.Hq : P.Hkv) * hv, 1006)) return;
+        if (!SV_INB(n, nn, 1007) || !SV_INB(at + x.i1, (rows - 1) * stride + (is_q ? P.Hq : P.Hkv) * hv, 1006)) return;
         a = base[at + x.i0];
         c = base[at + x.i1];
     };
 
-    // The row's first vectors, before anything is known of where they go.
+    // The row's first vectors, before anything is known of where they go; a row that the caller says is not
+    // there is not read.
     uint4 va[UNROLL], vb[UNROLL];
+    if (n < nn)
 #pragma unroll
-    for (int i = 0; i < UNROLL; ++i)
-        if (tid + i * NT < units) load(unit(tid + i * NT), va[i], vb[i]);
+        for (int i = 0; i < UNROLL; ++i)
+            if (tid + i * NT < units) load(unit(tid + i * NT), va[i], vb[i]);
 
-    const int c = SV_INB(b, P.B, 1001) ? P.committed[b] : 0;
-    const int nn = P.num_nodes && SV_INB(b, P.B, 1002) ? P.num_nodes[b] : P.N;
     int code = 0;
     if (nn < 0 || nn > P.N || c < 0 || (int64_t)c + nn > P.max_pos) code = SPEC_VERIFY_DEV_BAD_KV_POSITION;
     const bool here = n < nn;
