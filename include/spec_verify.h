@@ -314,7 +314,7 @@ int spec_verify_kv_compact(void *kv_pool, int64_t num_slots, size_t row_bytes, i
  *   q, k, v        [B * N] rows of Hq, Hkv, Hkv heads of D elements, *_stride elements apart (so the
  *                  three may be parts of one projection's rows); dtype SPEC_VERIFY_BF16 or _FP16;
  *                  bases 16-byte aligned, strides multiples of 8, D a multiple of 16, at most 1024
- *   q_out          [B * N][Hq][D], contiguous; must not overlap q
+ *   q_out          [B * N][Hq][D], contiguous; must not overlap q, from its first row to its last
  *   k_cache, v_cache  [num_slots] slots of [Hkv][D], *_slot_stride elements apart (multiples of 8)
  *   slot_table, committed  as for spec_verify_kv_compact: the slots and the lengths that it takes
  *   parents        [B][N] as for spec_verify_tree (N <= 64), or NULL

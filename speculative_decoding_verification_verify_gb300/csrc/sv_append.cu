@@ -214,6 +214,8 @@ extern "C" int spec_verify_kv_append(const void *q, const void *k, const void *v
     if (((uintptr_t)slot_table | (uintptr_t)committed | (uintptr_t)parents | (uintptr_t)num_nodes |
          (uintptr_t)dev_status) % 4)
         return SPEC_VERIFY_EINVAL;
+    const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)q_out, rows = (uintptr_t)B * N;
+    if (q0 < o0 + rows * qw * 2 && o0 < q0 + ((rows - 1) * q_stride + qw) * 2) return SPEC_VERIFY_EINVAL;
     svapp::Params P;
     P.q = static_cast<const uint4 *>(q);
     P.k = static_cast<const uint4 *>(k);
