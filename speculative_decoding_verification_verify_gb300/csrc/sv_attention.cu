@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
-            // ---- softmax: one position of a tile and half of its columns per thread ----------
+            // ---- softmax: one position of a tile and a share of its columns per thread -------
             constexpr int CW = NQ / WG;
             const int t = tid & 127, wq = warp & 3, wg = (warp - 8) >> 2, bar = 4 + wg;
             const int col0 = wg * CW;
@@ -842,29 +842,19 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                 }
 
                 // ---- the segment's end: join the columns' sums, write rows or a part -----------
-                constexpr int W = CW < 16 ? CW : 16;
+                auto column_totals = [&](const uint64_t (&pairs)[CW / 2], float *to) {
+                    float y[CW];
 #pragma unroll
-                for (int c0 = 0; c0 < CW; c0 += W) {
-                    float y[W];
-#pragma unroll
-                    for (int c = 0; c < W; c += 2) {
-                        const float2 f = sv::f2_split(raw[(c0 + c) / 2]);
+                    for (int c = 0; c < CW; c += 2) {
+                        const float2 f = sv::f2_split(pairs[c / 2]);
                         y[c] = f.x;
                         y[c + 1] = f.y;
                     }
-                    const float a = column_sum<W>(y, lane);
-#pragma unroll
-                    for (int c = 0; c < W; c += 2) {
-                        const float2 f = sv::f2_split(rnd[(c0 + c) / 2]);
-                        y[c] = f.x;
-                        y[c + 1] = f.y;
-                    }
-                    const float b = column_sum<W>(y, lane);
-                    if (lane < W) {
-                        ms.red[wq][col0 + c0 + lane] = a;
-                        ms.red2[wq][col0 + c0 + lane] = b;
-                    }
-                }
+                    const float total = column_sum<CW>(y, lane);
+                    if (lane < CW) to[lane] = total;
+                };
+                column_totals(raw, &ms.red[wq][col0]);
+                column_totals(rnd, &ms.red2[wq][col0]);
                 group_sync(bar, 128);
                 // While the last products run, a thread t < CW says what there is to say of column t.
                 const int raise = *(volatile int *)&ms.bad[wg][seg % FLAGS] ? SPEC_VERIFY_DEV_BAD_KV_SLOT
@@ -940,7 +930,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                 } else {
 #pragma unroll
                     for (int c = 0; c < CW; ++c) part[(col0 + c) * MAXD + t] = o[c];
-                    // Both warpgroups of every CTA come to the segment's counter; the last one's CTA joins the parts.
+                    // Every warpgroup of every CTA comes to the segment's counter; the last one's CTA joins the parts.
                     // The part that a run begins with is there early, so that it seldom joins two at its end.
                     group_sync(bar, 128);
                     if (t == 0 && !fail) {
