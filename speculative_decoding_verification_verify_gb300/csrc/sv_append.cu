@@ -11,16 +11,20 @@
 // chain runs under them.  A CTA takes one node: its unit of work is a pair of 16-byte vectors,
 // which under either pairing holds whole pairs (half-split: vectors rot/2 apart; adjacent: any
 // two), so a thread needs one unit's cosines and sines and no exchange with its neighbours.
-// Measured (GB300, copy rate 6.68 TB/s; 32 query and 8 key heads of 128, in a graph): 8194 rows 33.8 us for
-// 204 MB, 6.0 TB/s; 384 rows 4.0 us and one row 3.0 us, the chain's length.
+// Measured (GB300, copy rate 6.68 TB/s; 32 query and 8 key heads of 128, in a graph): 8194 rows 33 us for
+// 204 MB, 6.2 TB/s; 384 rows 3.6 us and one row 2.9 us, the chain's length.  Narrow rows are bound by the CTAs
+// that come and go, one for each: 8194 rows of 3 + 2 heads of 64 take 9.5 us for 13 MB, of 4 + 2 heads of 128
+// 10.9 us for 29 MB.
 #include "sv_ops.cuh"
 
 namespace svapp {
 
 using sv::Half2;
 
-constexpr int NT = 128;    // threads per CTA
-constexpr int UNROLL = 3;  // units of a thread in flight: a row of 48 heads of 128
+// Threads per CTA.  A thread has one unit in flight, whatever the row's width: with three, 8194 rows of 5 heads of
+// 64 took 12.6 us against 9.5, of 12 heads of 128 15.4 against 12.9, of 48 35.4 against 33.2, of 80 52.3 against
+// 52.7; a single row of 48 heads 2.75 against 2.87.
+constexpr int NT = 128;
 
 struct Params {
     const uint4 *q, *k, *v;            // rows of heads * D elements, row_*  vectors apart
@@ -93,13 +97,10 @@ __global__ void __launch_bounds__(NT) append_kernel(const Params P)
         c = base[at + x.i1];
     };
 
-    // The row's first vectors, before anything is known of where they go; a row that the caller says is not
+    // The thread's first vectors, before anything is known of where they go; a row that the caller says is not
     // there is not read.
-    uint4 va[UNROLL], vb[UNROLL];
-    if (n < nn)
-#pragma unroll
-        for (int i = 0; i < UNROLL; ++i)
-            if (tid + i * NT < units) load(unit(tid + i * NT), va[i], vb[i]);
+    uint4 va, vb;
+    if (n < nn && tid < units) load(unit(tid), va, vb);
 
     int code = 0;
     if (nn < 0 || nn > P.N || c < 0 || (int64_t)c + nn > P.max_pos) code = SPEC_VERIFY_DEV_BAD_KV_POSITION;
@@ -141,31 +142,24 @@ __global__ void __launch_bounds__(NT) append_kernel(const Params P)
         return;
     }
     const float *cs = P.cos_sin + ((int64_t)c + depth) * P.rot;
-    for (int u0 = 0; u0 < units; u0 += UNROLL * NT) {
-        if (u0 > 0)
-#pragma unroll
-            for (int i = 0; i < UNROLL; ++i)
-                if (u0 + tid + i * NT < units) load(unit(u0 + tid + i * NT), va[i], vb[i]);
-#pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
-            if (u0 + tid + i * NT >= units) break;
-            const Unit x = unit(u0 + tid + i * NT);
-            const bool is_q = x.head < P.Hq, is_k = x.head < P.Hq + P.Hkv;
-            if (x.turned && is_k) {
-                const float4 *pc = reinterpret_cast<const float4 *>(cs + 8 * x.j);
-                const float4 *ps = reinterpret_cast<const float4 *>(cs + 8 * x.j + P.rot / 2);
-                const float4 c0 = __ldg(pc), c1 = __ldg(pc + 1), s0 = __ldg(ps), s1 = __ldg(ps + 1);
-                const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-                const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-                rotate<BF, ADJ>(va[i], vb[i], cc, ss);
-            }
-            uint4 *const dst = (is_q    ? P.q_out + row * P.q_out_row
-                                : is_k ? P.k_cache + (int64_t)slot * P.k_slot - P.Hq * hv
-                                       : P.v_cache + (int64_t)slot * P.v_slot - (P.Hq + P.Hkv) * hv) +
-                               x.head * hv;
-            dst[x.i0] = va[i];
-            dst[x.i1] = vb[i];
+    for (int u = tid; u < units; u += NT) {
+        const Unit x = unit(u);
+        if (u != tid) load(x, va, vb);
+        const bool is_q = x.head < P.Hq, is_k = x.head < P.Hq + P.Hkv;
+        if (x.turned && is_k) {
+            const float4 *pc = reinterpret_cast<const float4 *>(cs + 8 * x.j);
+            const float4 *ps = reinterpret_cast<const float4 *>(cs + 8 * x.j + P.rot / 2);
+            const float4 c0 = __ldg(pc), c1 = __ldg(pc + 1), s0 = __ldg(ps), s1 = __ldg(ps + 1);
+            const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+            const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+            rotate<BF, ADJ>(va, vb, cc, ss);
         }
+        uint4 *const dst = (is_q    ? P.q_out + row * P.q_out_row
+                            : is_k ? P.k_cache + (int64_t)slot * P.k_slot - P.Hq * hv
+                                   : P.v_cache + (int64_t)slot * P.v_slot - (P.Hq + P.Hkv) * hv) +
+                           x.head * hv;
+        dst[x.i0] = va;
+        dst[x.i1] = vb;
     }
 }
 
