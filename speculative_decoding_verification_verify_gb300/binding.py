@@ -709,11 +709,14 @@ def _index(name: str, t: torch.Tensor, shape, device: int) -> int:
 
 
 def _result(name: str, t: Optional[torch.Tensor], shape, dtype, device: int, stream) -> torch.Tensor:
-    """A caller's output checked, or a new one that the stream's work may write."""
+    """A caller's output checked, or a new one that the stream's work may write at once: from memory that its
+    earlier work has had, kept until the current stream's work of the time it is dropped is done."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        if stream is not None:
-            t.record_stream(stream)
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        t.record_stream(torch.cuda.current_stream(device))
     elif t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{device}")
     return t
