@@ -39,6 +39,8 @@
 // 509 to 8192 positions 122-125 us for 742 MB, 5.9-6.1 TB/s; one tree of 16 over 131000 positions 100 us
 // for 537 MB, 5.3 TB/s (9 us until the first tile is there, 8 us for the joins); 96 requests of one token and 12
 // heads of 64 over 1 to 4001 positions 44 us for 148 MB, 3.4 TB/s; 48 trees of 8 over up to 504 positions 19 us.
+// One token of each of 64 requests over 8192 positions 320 us for 2.15 GB, 6.7 TB/s.  Heads of 80, 96 and 112 are padded
+// to 128 by the copies' zero-filling form: the 64 chains 138, 138 and 164 us for 464, 557 and 649 MB.
 // Long segments are bound by HBM; short ones by the chain through a segment, some 5000 clocks (its
 // first scores 1000, references 600, weights and the last product 1300, what it writes 900), which is
 // all the SM does unless two CTAs share it.
@@ -69,11 +71,12 @@ constexpr int COST_TILE = 2, COST_SEGMENT = 4;
 // (with 32 a thread: one tree of 16 over 131000 positions 105.6 us against 102.7).
 __host__ __device__ constexpr int groups(int nq) { return nq == 64 ? 4 : 2; }
 __host__ __device__ constexpr int threads(int nq) { return 256 + 128 * groups(nq); }
-// CTAs that an SM holds.  With at most 8 columns a thread, 64 registers do, and one CTA works while the
-// other is between segments: 96 requests of 12 heads of 64 take 45.8 us against 54.6, 128 requests of up to
-// 504 positions (8 key heads of 128) 35 against 40.  Two units of 128 dimensions are then all that fit
-// in a ring, and long requests lose: 509 to 8192 positions 138 us against 136, one of 131000 111 against
-// 108.  At 32 columns 64 registers spill: 139 us against 125 for the 64 chains above.
+// CTAs that an SM holds.  With at most 8 columns a thread, 64 registers nearly do (32 bytes spilled), and one CTA
+// works while the other is between segments: 96 requests of 12 heads of 64 take 44.4 us against 52.4, 128
+// requests of up to 504 positions (8 key heads of 128) 30.2 against 30.7.  Two units of 128 dimensions are then all
+// that fit in a ring, and longer requests lose: 64 requests of 509 to 8192 positions 122.5 us against 118.6, of
+// 8192 320 against 315, one of 131000 93.2 against 89.7.  At 32 columns 64 registers spill 260 bytes: 139 us
+// against 125 for the 64 chains above.
 __host__ __device__ constexpr int ctas_per_sm(int nq) { return nq == 16 ? 2 : 1; }
 
 struct Params {
