@@ -1,4 +1,6 @@
 """spec_verify_attention with scores of any size that fp32 holds."""
+import math
+
 import pytest
 import torch
 
@@ -48,3 +50,28 @@ def test_the_largest_score_takes_all(dtype, size, N, Hq, order):
         got = call({**s, **{k: s[k][b:b + 1] for k in ("q", "slot_table", "committed")}})
         assert torch.equal(got.out[0], s["v_cache"][slot[at], 0].expand(N, Hq, 64))
         assert float((got.lse.double() - score[at]).abs().max()) <= 2.0 ** -21 * float(score[at].abs())
+
+
+@pytest.mark.parametrize("dtype,size", [(BF, 17), (BF, 24), (BF, 35), (BF, 57), (BF, 110), (FP, 24), (FP, 27)])
+@pytest.mark.parametrize("N,Hq", [(1, 2), (16, 4)])
+def test_parts_of_a_request(dtype, size, N, Hq):
+    """The same over a request that many CTAs share: parts whose references lie whole exponents apart, and one
+    score that two parts hold alike, whose values then count half each."""
+    c = 40000
+    s = make([c], N, Hq, 1, 64, dtype, seed=size)
+    up = (size + 3) // 2
+    s["q"].zero_()
+    s["q"][..., 0] = 2.0 ** up
+    g = torch.Generator(device=DEV)
+    g.manual_seed(size)
+    grid = torch.randint(-100, 100, (c + N,), generator=g, device=DEV).float() / 128
+    grid[1234], grid[38000] = 101 / 128, 101 / 128
+    slot = s["slot_table"][0, : c + N].long()
+    s["k_cache"][slot, 0, 0] = (grid * 2.0 ** (size + 3 - up)).to(dtype)
+    got = call(s)
+    a, b = s["v_cache"][slot[1234], 0].double(), s["v_cache"][slot[38000], 0].double()
+    # The weights are alike and exact, so is their sum; a product with its reciprocal and the rounding of the row.
+    tol = (2.0 ** -8 if dtype is BF else 2.0 ** -11) * ((a + b) / 2).abs() + 2.0 ** -21 * (a.abs() + b.abs()) + 2.0 ** -24
+    assert bool(((got.out[0].double() - (a + b) / 2).abs() <= tol).all())
+    lse = float(s["k_cache"][slot[1234], 0, 0].double() * 2.0 ** up / 8) + math.log(2.0)
+    assert float((got.lse.double() - lse).abs().max()) <= 2.0 ** -21 * abs(lse)
