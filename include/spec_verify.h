@@ -67,6 +67,7 @@ extern "C" {
 #define SPEC_VERIFY_BF16 0
 #define SPEC_VERIFY_FP32 1
 #define SPEC_VERIFY_FP16 2 /* queries, keys and values only */
+#define SPEC_VERIFY_E4M3 3 /* the cache's rows only: spec_verify_kv_append_ex */
 
 /* Host return codes. */
 #define SPEC_VERIFY_OK 0
@@ -364,6 +365,57 @@ int spec_verify_attention(const void *q, int dtype, int64_t q_stride, const void
                           const int32_t *committed, const int32_t *parents, const int32_t *num_nodes,
                           int B, int N, int Hq, int Hkv, int D, float scale, void *out, float *lse,
                           void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * spec_verify_kv_append with the heads' norms in the same pass and the cache's rows in 16 or in 8 bits.  Arguments,
+ * rotation, faults and the rows past num_nodes as there, and
+ *   q_norm, k_norm  [D] of q's type, 16-byte aligned, or NULL (no norm): a head of q or k is first
+ *                  x * w / sqrt(mean(x^2) + eps), its sum of squares in fp32; eps finite, >= 0
+ *   cache_dtype    dtype: a slot is [Hkv][D] of it, and the slot strides count its elements; or
+ *                  SPEC_VERIFY_E4M3: a slot is a row of spec_verify_kv_e4m3_row_bytes(Hkv, D) bytes: [Hkv][D] e4m3,
+ *                  then a byte 127 + e for each head, then zeros; it stands for e4m3 * 2^e.  The slot strides
+ *                  count bytes and are multiples of 16
+ *   D              a multiple of 16, at most 512
+ * e is the smallest exponent with which the head's largest magnitude is at most 448 * 2^e, from -126 (q bf16) or
+ * -15 (fp16) to 7; values are rounded once, to nearest even, after norm and rotation in fp32; those beyond
+ * 448 * 2^7 = 57344 become that, NaN stays NaN (and does not count for e).  A cache is read with queries of the type
+ * that it was written with.  spec_verify_kv_compact moves such rows as any others.
+ */
+size_t spec_verify_kv_e4m3_row_bytes(int Hkv, int D); /* 0 for unsupported sizes */
+int spec_verify_kv_append_ex(const void *q, const void *k, const void *v, int dtype, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, void *q_out, void *k_cache, void *v_cache,
+                             int cache_dtype, int64_t num_slots, int64_t k_slot_stride, int64_t v_slot_stride,
+                             const int32_t *slot_table, int max_pos, const int32_t *committed,
+                             const int32_t *parents, const int32_t *num_nodes, const float *cos_sin,
+                             int rot_positions, int rotary_dim, int interleaved, const void *q_norm,
+                             const void *k_norm, float eps, int B, int N, int Hq, int Hkv, int D,
+                             int32_t *dev_status, void *stream);
+
+/*
+ * Positions of the paged cache as contiguous rows of 16 bits (for a caller's own attention, for moving a request to
+ * another cache): k_out[b][n] and v_out[b][n] [Hkv][D] = the rows of position first[b] + n, n < num_rows[b] (NULL:
+ * all N); the rows past num_rows are 0.  From a cache of 8-bit rows the values are exact (in fp16: where fp16 holds
+ * them; what append_ex wrote from fp16 it does).  Arguments as for spec_verify_kv_append_ex; dtype is the outputs' and, where its rows
+ * have 16 bits, the cache's.  Device status codes: 5 (num_rows outside [0, N], first below 0, or first + num_rows
+ * beyond max_pos): the request's rows are NaN; 6 (a slot outside the pool): that row is NaN.  One launch, no workspace.
+ */
+int spec_verify_kv_read(const void *k_cache, const void *v_cache, int cache_dtype, int64_t num_slots,
+                        int64_t k_slot_stride, int64_t v_slot_stride, const int32_t *slot_table, int max_pos,
+                        const int32_t *first, const int32_t *num_rows, int B, int N, int Hkv, int D,
+                        void *k_out, void *v_out, int dtype, int32_t *dev_status, void *stream);
+
+/*
+ * spec_verify_attention over a cache of 8-bit rows (spec_verify_kv_append_ex).  Arguments, outputs, faults and workspace
+ * rules as there, but for the caches' layout: slot strides in bytes, multiples of 16 below 2^31.  The keys and values
+ * that enter are what the rows stand for, exactly.
+ */
+size_t spec_verify_attention_e4m3_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int max_pos);
+int spec_verify_attention_e4m3(const void *q, int dtype, int64_t q_stride, const void *k_cache,
+                               const void *v_cache, int64_t num_slots, int64_t k_slot_stride,
+                               int64_t v_slot_stride, const int32_t *slot_table, int max_pos,
+                               const int32_t *committed, const int32_t *parents, const int32_t *num_nodes,
+                               int B, int N, int Hq, int Hkv, int D, float scale, void *out, float *lse,
+                               void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream);
 
 /*
  * Log probabilities of given tokens, with the distribution's entropy and its most likely

@@ -1,4 +1,4 @@
-// sv_attention.cu -- attention of a verification step's nodes over the paged cache.
+// sv_attention.cuh -- attention of a verification step's nodes over the paged cache.
 //
 //   s_j = scale * q . k_j over the positions j that node n sees: j < committed, and the positions
 //   committed + a of the nodes a on the path from the root to n (a chain: a <= n)
@@ -44,7 +44,9 @@
 // Long segments are bound by HBM; short ones by the chain through a segment, some 5000 clocks (its
 // first scores 1000, references 600, weights and the last product 1300, what it writes 900), which is
 // all the SM does unless two CTAs share it.
-#include "sv_ops.cuh"
+#pragma once
+
+#include "sv_e4m3.cuh"
 #include "sv_tc.cuh"
 
 #include <mutex>
@@ -77,13 +79,14 @@ __host__ __device__ constexpr int threads(int nq) { return 256 + 128 * groups(nq
 // that fit in a ring, and longer requests lose: 64 requests of 509 to 8192 positions 122.5 us against 118.6, of
 // 8192 320 against 315, one of 131000 93.2 against 89.7.  At 32 columns 64 registers spill 260 bytes: 139 us
 // against 125 for the 64 chains above.
-__host__ __device__ constexpr int ctas_per_sm(int nq) { return nq == 16 ? 2 : 1; }
+__host__ __device__ constexpr int ctas_per_sm(int nq, bool e4) { return nq == 16 && !e4 ? 2 : 1; }
 
 struct Params {
-    const uint16_t *q, *k, *v;
+    const uint16_t *q;
+    const unsigned char *k, *v;
     uint16_t *out;
     float *lse;
-    int64_t q_row, k_slot, v_slot, num_slots;
+    int64_t q_row, k_slot, v_slot, num_slots;  // the slots' strides in elements of the cache
     const int32_t *slot_table, *committed, *parents, *num_nodes;
     int max_pos, B, N, Hq, Hkv, D, G, QT;  // G query heads per key head, QT column blocks
     float scale_log2;
@@ -95,11 +98,11 @@ struct Params {
 
 // Shared memory: a ring of units (a K or V tile each; tile k's K is unit 2 k, its V unit 2 k + 1),
 // two query buffers, the weights, then Misc.  All bases are multiples of 1024 bytes.
-template <int NQ, int DP>
+template <int NQ, int DP, bool E4>
 struct Layout {
     static constexpr int HALVES = DP / 64;
     static constexpr int UNIT = TILE * DP * 2;
-    static constexpr int NU = ctas_per_sm(NQ) == 2 ? (DP == 64 ? 5 : 2) : 5 * 128 / DP;
+    static constexpr int NU = ctas_per_sm(NQ, E4) == 2 ? (DP == 64 ? 5 : 2) : 5 * 128 / DP;
     static constexpr int QBYTES = NQ * DP * 2;
     static constexpr int QSTEP = QBYTES < 1024 ? 1024 : QBYTES;
     static constexpr int PBYTES = TILE * 128;  // a row of 64 columns per position
@@ -213,7 +216,7 @@ __host__ __device__ constexpr int part_floats()
 // tiles before `cut_tile` to the run before; cuts are at least COST_TILE apart, so no run between two
 // cuts of a segment is empty.
 // (Quotients in 32 bits wherever they fit: 64-bit division is a hundred instructions.)
-__device__ __noinline__ int64_t quotient64(int64_t a, int64_t b) { return a / b; }
+static __device__ __noinline__ int64_t quotient64(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 {
     return (uint64_t)(a | b) >> 32 ? quotient64(a, b) : (int64_t)((unsigned)a / (unsigned)b);
@@ -240,10 +243,10 @@ __device__ __forceinline__ void lengths(const Params &P, int b, int &c, int &nn)
     nn = P.num_nodes ? (SV_INB(b, P.B, 1102) ? P.num_nodes[b] : 0) : P.N;
 }
 
-template <bool BF, int NQ, int DP>
-__global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel(const Params P)
+template <bool BF, int NQ, int DP, bool E4>
+__global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_kernel(const Params P)
 {
-    using L = Layout<NQ, DP>;
+    using L = Layout<NQ, DP, E4>;
     using M = Misc<NQ, L::NU>;
     constexpr int NU = L::NU, HALVES = L::HALVES, NT = threads(NQ), WG = groups(NQ);
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -345,12 +348,11 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
             // ---- tiles into shared memory -------------------------------------------------
             // A row's CPR chunks go to CPR lanes, 32 / CPR rows to a warp's copy.  A lane keeps the
             // slot of one of its warp's 32 rows; they are read one tile ahead of the copies.
-            constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
+            constexpr int CPR = E4 ? DP / 16 : DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
             const int chunk = lane % CPR, sub = lane / CPR;
             const int own = warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot it keeps
             const int first = warp * RPI + sub;                                // its row of the first copy
-            const uint32_t to = (chunk >> 3) * TILE * 128 + first * 128 + (((chunk & 7) ^ (first & 7)) << 4);
-            const bool wide = chunk * 8 < P.D;
+            const bool wide = chunk * (E4 ? 16 : 8) < P.D;
             Seg g = {};
             int seg = -1, j = 0, slot = -1, u = 0;
             bool ok = true;
@@ -386,43 +388,115 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                 }
                 return slot;
             };
-            for (int found = seek(true); found == 1 && ok;) {
-                const int slots = check(j * TILE + own >= g.c + g.nn);
-                const int64_t at = (int64_t)g.h * P.D + (wide ? chunk * 8 : 0);
-                const bool whole = __all_sync(0xffffffffu, slots >= 0 && wide);
-                found = seek(false);
-#pragma unroll 1
-                for (int kv = 0; kv < 2 && ok; ++kv, ++u) {
-                    if (u >= NU) {
-                        const bool free = tc::bar_wait(tc::smem_u32(&ms.empty[u % NU]), (u / NU + 1) & 1, abort);
-                        ok = __all_sync(0xffffffffu, free);
-                        if (!ok) break;
-                    }
-                    const uint32_t dst = s0 + (u % NU) * L::UNIT + to;
-                    const unsigned char *base = reinterpret_cast<const unsigned char *>((kv ? P.v : P.k) + at);
-                    const uint32_t stride = (uint32_t)(kv ? P.v_slot : P.k_slot) * 2;
-                    if (whole) {
-#pragma unroll
-                        for (int i = 0; i < ITER; ++i) {
-                            const uint32_t s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 4 * RPI * 128),
-                                         "l"(base + (uint64_t)s * stride)
-                                         : "memory");
-                        }
-                    } else {
-#pragma unroll 4
-                        for (int i = 0; i < ITER; ++i) {  // zeros where there is nothing to copy
-                            const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 4 * RPI * 128),
-                                         "l"(base + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride), "r"(s >= 0 && wide ? 16 : 0)
-                                         : "memory");
-                        }
-                    }
-                    // The unit's barrier hears of each thread's copies as they land; nobody waits for them here.
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&ms.full[u % NU]))
-                                 : "memory");
+            // A unit of the ring may be written again once its products are done.
+            auto room = [&] {
+                if (u >= NU) {
+                    const bool free = tc::bar_wait(tc::smem_u32(&ms.empty[u % NU]), (u / NU + 1) & 1, abort);
+                    ok = __all_sync(0xffffffffu, free);
                 }
-                if (found == 2 && ok) found = seek(true);
+                return ok;
+            };
+            if constexpr (!E4) {
+                const uint32_t to = (chunk >> 3) * TILE * 128 + first * 128 + (((chunk & 7) ^ (first & 7)) << 4);
+                for (int found = seek(true); found == 1 && ok;) {
+                    const int slots = check(j * TILE + own >= g.c + g.nn);
+                    const int64_t at = (int64_t)g.h * P.D + (wide ? chunk * 8 : 0);
+                    const bool whole = __all_sync(0xffffffffu, slots >= 0 && wide);
+                    found = seek(false);
+    #pragma unroll 1
+                    for (int kv = 0; kv < 2 && ok; ++kv, ++u) {
+                        if (!room()) break;
+                        const uint32_t dst = s0 + (u % NU) * L::UNIT + to;
+                        const unsigned char *base = (kv ? P.v : P.k) + 2 * at;
+                        const uint32_t stride = (uint32_t)(kv ? P.v_slot : P.k_slot) * 2;
+                        if (whole) {
+    #pragma unroll
+                            for (int i = 0; i < ITER; ++i) {
+                                const uint32_t s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 4 * RPI * 128),
+                                             "l"(base + (uint64_t)s * stride)
+                                             : "memory");
+                            }
+                        } else {
+    #pragma unroll 4
+                            for (int i = 0; i < ITER; ++i) {  // zeros where there is nothing to copy
+                                const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 4 * RPI * 128),
+                                             "l"(base + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride), "r"(s >= 0 && wide ? 16 : 0)
+                                             : "memory");
+                            }
+                        }
+                        // The unit's barrier hears of each thread's copies as they land; nobody waits for them here.
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&ms.full[u % NU]))
+                                     : "memory");
+                    }
+                    if (found == 2 && ok) found = seek(true);
+                }
+            } else {
+                // 8-bit rows pass through registers: 16 values per load, widened to two of the unit's chunks.  A
+                // tile's keys and values are asked for while the tile before is widened.
+                uint4 raw[2][ITER];
+                int es[2] = {0, 0};  // the exponents of the row whose slot the lane keeps
+                const uint32_t to = s0 + (chunk >> 2) * TILE * 128 + first * 128;
+                const uint32_t c0 = ((2 * chunk & 7) ^ (first & 7)) << 4, c1 = c0 ^ 16;
+                auto ask = [&](int slots, int kv) {
+                    const uint32_t stride = (uint32_t)(kv ? P.v_slot : P.k_slot);
+                    const unsigned char *base = kv ? P.v : P.k;
+                    es[kv] = 127;
+                    if (slots >= 0) es[kv] = __ldg(base + (uint64_t)(uint32_t)slots * stride + P.Hkv * P.D + g.h);
+                    base += g.h * P.D + chunk * 16;
+#pragma unroll
+                    for (int i = 0; i < ITER; ++i) {
+                        const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
+                        raw[kv][i] = make_uint4(0, 0, 0, 0);
+                        if (s >= 0 && wide) raw[kv][i] = __ldg(reinterpret_cast<const uint4 *>(base + (uint64_t)(uint32_t)s * stride));
+                    }
+                };
+                auto widen = [&](int kv) {
+                    const uint32_t dst = to + (u % NU) * L::UNIT;
+                    const bool odd = DP == 128 && chunk >= 4;  // lanes 4 apart write the other chunk: no bank twice
+                    const uint32_t a0 = dst + (odd ? c1 : c0), a1 = dst + (odd ? c0 : c1);
+#pragma unroll
+                    for (int i = 0; i < ITER; ++i) {
+                        const sv::E4m3Scale<BF> f(__shfl_sync(0xffffffffu, es[kv], i * RPI + sub));
+                        const uint4 w = raw[kv][i];
+                        const uint4 lo = make_uint4(f(w.x), f(w.x >> 16), f(w.y), f(w.y >> 16));
+                        const uint4 hi = make_uint4(f(w.z), f(w.z >> 16), f(w.w), f(w.w >> 16));
+                        const uint4 x = odd ? hi : lo, y = odd ? lo : hi;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0 + i * 4 * RPI * 128), "r"(x.x), "r"(x.y),
+                                     "r"(x.z), "r"(x.w)
+                                     : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1 + i * 4 * RPI * 128), "r"(y.x), "r"(y.y),
+                                     "r"(y.z), "r"(y.w)
+                                     : "memory");
+                    }
+                    tc::fence_async_smem();
+                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));
+                    ++u;
+                };
+                int found = seek(true);
+                int slots = found == 1 ? check(j * TILE + own >= g.c + g.nn) : -1;
+                if (found == 1) ask(slots, 0), ask(slots, 1);
+                while (found == 1) {
+                    const int next = seek(false);
+                    if (!room()) break;
+                    widen(0);
+                    if (next == 1) {
+                        slots = check(j * TILE + own >= g.c + g.nn);
+                        ask(slots, 0);
+                    }
+                    if (!room()) break;
+                    widen(1);
+                    if (next == 1) {
+                        ask(slots, 1);
+                    } else if (next == 2) {
+                        found = seek(true);
+                        slots = found == 1 ? check(j * TILE + own >= g.c + g.nn) : -1;
+                        if (found == 1) ask(slots, 0), ask(slots, 1);
+                        continue;
+                    }
+                    found = next;
+                }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp == 4) {
@@ -898,7 +972,13 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ)) attention_kernel
                         const int64_t st = (int64_t)g.b * P.max_pos + y;
                         const int slot = SV_INB(st, (int64_t)P.B * P.max_pos, 1107) ? P.slot_table[st] : -1;
                         if (slot < 0 || slot >= P.num_slots) continue;
-                        const uint32_t bits = P.v[(int64_t)slot * P.v_slot + g.h * P.D + t];
+                        uint32_t bits;
+                        if constexpr (E4) {
+                            const unsigned char *at = P.v + (int64_t)slot * P.v_slot;
+                            bits = sv::E4m3Scale<BF>(at[P.Hkv * P.D + g.h])(at[g.h * P.D + t]) & 0xffffu;
+                        } else {
+                            bits = reinterpret_cast<const uint16_t *>(P.v)[(int64_t)slot * P.v_slot + g.h * P.D + t];
+                        }
                         if ((bits & Half2<BF>::EXP_MASK) != Half2<BF>::EXP_MASK) continue;
                         const float val = Half2<BF>::unpack(bits).x;
                         const unsigned see = (unsigned)(ms.desc[buf][y - g.c] >> col0);
@@ -1101,22 +1181,23 @@ struct DevInfo {
 static std::mutex g_mu;
 static DevInfo g_dev[64];
 
-template <bool BF, int NQ, int DP>
+template <bool BF, int NQ, int DP, bool E4>
 constexpr size_t smem_bytes()
 {
-    using L = Layout<NQ, DP>;
+    using L = Layout<NQ, DP, E4>;
     return L::M0 + sizeof(Misc<NQ, L::NU>);
 }
 
-template <bool BF, int NQ, int DP>
+template <bool BF, int NQ, int DP, bool E4>
 static bool allow()
 {
-    static_assert(smem_bytes<BF, NQ, DP>() <= 232448, "shared memory of a CTA");
-    return cudaFuncSetAttribute((const void *)attention_kernel<BF, NQ, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)smem_bytes<BF, NQ, DP>()) == cudaSuccess;
+    static_assert(smem_bytes<BF, NQ, DP, E4>() <= 232448, "shared memory of a CTA");
+    return cudaFuncSetAttribute((const void *)attention_kernel<BF, NQ, DP, E4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)smem_bytes<BF, NQ, DP, E4>()) == cudaSuccess;
 }
 
 // Once per device: the kernels' shared memory, the SM count.
+template <bool E4>
 static const DevInfo *device_info()
 {
     int dev = 0;
@@ -1126,9 +1207,9 @@ static const DevInfo *device_info()
     if (d.sms == 0) {
         int sms = 0;
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            !(allow<true, 16, 64>() && allow<true, 32, 64>() && allow<true, 64, 64>() && allow<true, 16, 128>() &&
-              allow<true, 32, 128>() && allow<true, 64, 128>() && allow<false, 16, 64>() && allow<false, 32, 64>() &&
-              allow<false, 64, 64>() && allow<false, 16, 128>() && allow<false, 32, 128>() && allow<false, 64, 128>())) {
+            !(allow<true, 16, 64, E4>() && allow<true, 32, 64, E4>() && allow<true, 64, 64, E4>() && allow<true, 16, 128, E4>() &&
+              allow<true, 32, 128, E4>() && allow<true, 64, 128, E4>() && allow<false, 16, 64, E4>() && allow<false, 32, 64, E4>() &&
+              allow<false, 64, 64, E4>() && allow<false, 16, 128, E4>() && allow<false, 32, 128, E4>() && allow<false, 64, 128, E4>())) {
             cudaGetLastError();
             return nullptr;
         }
@@ -1144,79 +1225,57 @@ static int columns(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 constexpr size_t COUNTER_BYTES = 65536 * 4;  // the workspace's fixed region of counters
 constexpr float MAX_SCALE = 2.3e38f;         // times log2(e) it is still a number of fp32
 
-template <bool BF, int NQ, int DP>
+template <bool BF, int NQ, int DP, bool E4>
 static cudaError_t launch(const Params &P, int grid, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(threads(NQ));
-    cfg.dynamicSmemBytes = smem_bytes<BF, NQ, DP>();
+    cfg.dynamicSmemBytes = smem_bytes<BF, NQ, DP, E4>();
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_kernel<BF, NQ, DP>, P);
+    return cudaLaunchKernelEx(&cfg, attention_kernel<BF, NQ, DP, E4>, P);
 }
 
-template <bool BF>
+template <bool BF, bool E4>
 static cudaError_t dispatch(int nq, int dp, const Params &P, int grid,
                             cudaStream_t s)
 {
     if (dp == 64)
-        return nq == 16 ? launch<BF, 16, 64>(P, grid, s)
-               : nq == 32 ? launch<BF, 32, 64>(P, grid, s)
-                          : launch<BF, 64, 64>(P, grid, s);
-    return nq == 16 ? launch<BF, 16, 128>(P, grid, s)
-           : nq == 32 ? launch<BF, 32, 128>(P, grid, s)
-                      : launch<BF, 64, 128>(P, grid, s);
+        return nq == 16 ? launch<BF, 16, 64, E4>(P, grid, s)
+               : nq == 32 ? launch<BF, 32, 64, E4>(P, grid, s)
+                          : launch<BF, 64, 64, E4>(P, grid, s);
+    return nq == 16 ? launch<BF, 16, 128, E4>(P, grid, s)
+           : nq == 32 ? launch<BF, 32, 128, E4>(P, grid, s)
+                      : launch<BF, 64, 128, E4>(P, grid, s);
 }
 
-}  // namespace svatt
-
-namespace sv {
-bool attention_timeouts(unsigned long long &n) { return tc::read_timeouts(n); }
-bool attention_wait_clocks(long long clocks) { return tc::set_wait_clocks(clocks); }
-
-// This module's first range violation (debug builds; 0 otherwise), cleared when read.
-unsigned long long attention_debug_fault()
-{
-#ifdef SV_DEBUG
-    unsigned long long w = 0, z = 0;
-    if (cudaMemcpyFromSymbol(&w, g_sv_debug_fault, sizeof w) != cudaSuccess ||
-        cudaMemcpyToSymbol(g_sv_debug_fault, &z, sizeof z) != cudaSuccess)
-        return ~0ull;
-    return w;
-#else
-    return 0;
-#endif
-}
-}  // namespace sv
-
-extern "C" size_t spec_verify_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int max_pos)
+// The workspace: two parts per CTA behind the counters.
+static size_t workspace_bytes(int B, int N, int Hq, int Hkv, int D, int max_pos, bool e4)
 {
     if (B < 1 || B > 65536 || N < 1 || N > sv::MAX_TREE || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq > (1 << 16) || D < 64 ||
-        D > svatt::MAXD || D % 16 || max_pos < 1)
+        D > MAXD || D % 16 || max_pos < 1)
         return 0;
-    const size_t nq = (size_t)svatt::columns(N * (Hq / Hkv));
-    return svatt::COUNTER_BYTES + 2 * svatt::MAX_SMS * svatt::ctas_per_sm((int)nq) * (nq * svatt::MAXD + 3 * nq) * sizeof(float);
+    const size_t nq = (size_t)columns(N * (Hq / Hkv));
+    return COUNTER_BYTES + 2 * MAX_SMS * ctas_per_sm((int)nq, e4) * (nq * MAXD + 3 * nq) * sizeof(float);
 }
 
-extern "C" int spec_verify_attention(const void *q, int dtype, int64_t q_stride, const void *k_cache,
-                                     const void *v_cache, int64_t num_slots, int64_t k_slot_stride,
-                                     int64_t v_slot_stride, const int32_t *slot_table, int max_pos,
-                                     const int32_t *committed, const int32_t *parents, const int32_t *num_nodes, int B,
-                                     int N, int Hq, int Hkv, int D, float scale, void *out, float *lse, void *workspace,
-                                     size_t ws_bytes, int32_t *dev_status, void *stream)
+template <bool E4>
+static int run(const void *q, int dtype, int64_t q_stride, const void *k_cache, const void *v_cache, int64_t num_slots,
+               int64_t k_slot_stride, int64_t v_slot_stride, const int32_t *slot_table, int max_pos,
+               const int32_t *committed, const int32_t *parents, const int32_t *num_nodes, int B, int N, int Hq, int Hkv,
+               int D, float scale, void *out, float *lse, void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream)
 {
-    using namespace svatt;
     if (!q || !k_cache || !v_cache || !slot_table || !committed || !out || !workspace) return SPEC_VERIFY_EINVAL;
     if (dtype != SPEC_VERIFY_BF16 && dtype != SPEC_VERIFY_FP16) return SPEC_VERIFY_EINVAL;
-    const size_t need = spec_verify_attention_workspace_bytes(B, N, Hq, Hkv, D, max_pos);
+    const size_t need = workspace_bytes(B, N, Hq, Hkv, D, max_pos, E4);
     if (!need || num_slots < 1 || num_slots > 0x7fffffff || !(scale > 0.f) || scale > MAX_SCALE) return SPEC_VERIFY_EINVAL;
-    const int64_t qw = (int64_t)Hq * D, kw = (int64_t)Hkv * D;
-    if (q_stride % 8 || k_slot_stride % 8 || v_slot_stride % 8 || q_stride < qw || k_slot_stride < kw || v_slot_stride < kw ||
+    const int64_t qw = (int64_t)Hq * D, kw = E4 ? sv::e4m3_row_bytes(Hkv, D) : (int64_t)Hkv * D;
+    if (q_stride % 8 || k_slot_stride % (E4 ? 16 : 8) || v_slot_stride % (E4 ? 16 : 8) || q_stride < qw || k_slot_stride < kw || v_slot_stride < kw ||
         k_slot_stride >= (1ll << 31) || v_slot_stride >= (1ll << 31))
         return SPEC_VERIFY_EINVAL;
     if (((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out) % 16) return SPEC_VERIFY_EINVAL;
@@ -1224,13 +1283,13 @@ extern "C" int spec_verify_attention(const void *q, int dtype, int64_t q_stride,
          (uintptr_t)dev_status) % 4)
         return SPEC_VERIFY_EINVAL;
     if (ws_bytes < need || (uintptr_t)workspace % 256) return SPEC_VERIFY_EWORKSPACE;
-    const DevInfo *dev = device_info();
+    const DevInfo *dev = device_info<E4>();
     if (!dev) return SPEC_VERIFY_ECUDA;
     const bool bf = dtype == SPEC_VERIFY_BF16;
     Params P;
     P.q = static_cast<const uint16_t *>(q);
-    P.k = static_cast<const uint16_t *>(k_cache);
-    P.v = static_cast<const uint16_t *>(v_cache);
+    P.k = static_cast<const unsigned char *>(k_cache);
+    P.v = static_cast<const unsigned char *>(v_cache);
     P.out = static_cast<uint16_t *>(out);
     P.lse = lse;
     P.q_row = q_stride;
@@ -1254,15 +1313,17 @@ extern "C" int spec_verify_attention(const void *q, int dtype, int64_t q_stride,
     P.dev_status = dev_status;
     P.counters = static_cast<unsigned *>(workspace);
     P.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + COUNTER_BYTES);
-    int grid = (dev->sms < MAX_SMS ? dev->sms : MAX_SMS) * ctas_per_sm(nq);
+    int grid = (dev->sms < MAX_SMS ? dev->sms : MAX_SMS) * ctas_per_sm(nq, E4);
     const int64_t most = (int64_t)B * Hkv * P.QT * ((max_pos + TILE - 1) / TILE);
     if (most < grid) grid = (int)most;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int dp = D <= 64 ? 64 : 128;
-    const cudaError_t e = bf ? dispatch<true>(nq, dp, P, grid, s) : dispatch<false>(nq, dp, P, grid, s);
+    const cudaError_t e = bf ? dispatch<true, E4>(nq, dp, P, grid, s) : dispatch<false, E4>(nq, dp, P, grid, s);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return SPEC_VERIFY_ECUDA;
     }
     return SPEC_VERIFY_OK;
 }
+
+}  // namespace svatt

@@ -192,7 +192,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[16])
 }
 
 // Host: this module's count of timeouts, read and cleared, and its limit of waits (debug builds).
-inline bool read_timeouts(unsigned long long &n)
+[[maybe_unused]] static bool read_timeouts(unsigned long long &n)
 {
     unsigned long long x = 0, z = 0;
     if (cudaMemcpyFromSymbol(&x, g_timeouts, sizeof x) != cudaSuccess || cudaMemcpyToSymbol(g_timeouts, &z, sizeof z) != cudaSuccess)
@@ -201,7 +201,7 @@ inline bool read_timeouts(unsigned long long &n)
     return true;
 }
 
-inline bool set_wait_clocks([[maybe_unused]] long long clocks)
+[[maybe_unused]] static bool set_wait_clocks([[maybe_unused]] long long clocks)
 {
 #ifdef SV_DEBUG
     return cudaMemcpyToSymbol(g_wait_clocks, &clocks, sizeof clocks) == cudaSuccess;
