@@ -418,6 +418,27 @@ int spec_verify_attention_e4m3(const void *q, int dtype, int64_t q_stride, const
                                void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream);
 
 /*
+ * Attention of a chunk of a prompt over one layer's paged cache, causal: node n of request b sees the positions
+ * j <= committed + n, its own included (append first).  A whole prompt is a chunk with committed = 0; requests of
+ * different lengths come as one padded batch with num_nodes.  Arguments as for spec_verify_attention, without a tree
+ * and with any N (B * N and N * Hq / Hkv below 2^31), and
+ *   cache_dtype    dtype: 16-bit rows; SPEC_VERIFY_E4M3: 8-bit rows, slot strides in bytes (spec_verify_kv_append_ex)
+ *   workspace      spec_verify_attention_chunk_workspace_bytes(...) bytes, 256-byte aligned; rules as for the verifiers'
+ *                  (their counters are not touched)
+ * Sums and the softmax are in fp32; the weights are rounded to q's type for the product with v.  What a node does not
+ * see has no part in its row, whatever is stored there.  Rows of nodes past num_nodes are 0 with lse -inf.  Device
+ * status codes: 5 (lengths that do not fit): the request's rows are NaN; 6 (a slot outside the pool): the rows that
+ * see its position are NaN.  The same inputs give the same bits.  Two launches.
+ */
+size_t spec_verify_attention_chunk_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int max_pos);
+int spec_verify_attention_chunk(const void *q, int dtype, int64_t q_stride, const void *k_cache,
+                                const void *v_cache, int cache_dtype, int64_t num_slots, int64_t k_slot_stride,
+                                int64_t v_slot_stride, const int32_t *slot_table, int max_pos,
+                                const int32_t *committed, const int32_t *num_nodes, int B, int N, int Hq,
+                                int Hkv, int D, float scale, void *out, float *lse, void *workspace,
+                                size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/*
  * Log probabilities of given tokens, with the distribution's entropy and its most likely
  * alternatives: what a server answers beside the tokens that verification emitted.  With
  * x = logits / T of a row:

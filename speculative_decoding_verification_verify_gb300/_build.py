@@ -12,7 +12,7 @@ LIB_PATH = os.path.join(PKG, "libspecverify.so")
 DEBUG_LIB_PATH = os.path.join(PKG, "libspecverify_debug.so")  # range-checked build (-DSV_DEBUG)
 SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "sv_kv.cu", "sv_budget.cu", "sv_append.cu",
                                               "sv_attention.cu", "sv_logprobs.cu", "sv_cache.cu",
-                                              "sv_attention_e4m3.cu")]
+                                              "sv_attention_e4m3.cu", "sv_chunk.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("sv_device.cuh", "sv_draw.cuh", "sv_stream.cuh", "sv_rescan.cuh",
                                                   "sv_decide.cuh", "sv_topkp.cuh", "sv_topkp_ring.cuh",
                                                   "sv_check.cuh", "sv_ops.cuh", "sv_tc.cuh", "sv_e4m3.cuh",

@@ -102,6 +102,11 @@ def _declare(lib):
     lib.spec_verify_attention_e4m3.restype = i32
     lib.spec_verify_attention_e4m3_workspace_bytes.argtypes = [i32] * 6
     lib.spec_verify_attention_e4m3_workspace_bytes.restype = sz
+    lib.spec_verify_attention_chunk.argtypes = [vp, i32, i64, vp, vp, i32, i64, i64, i64, vp, i32, vp, vp, i32, i32,
+                                                i32, i32, i32, f32, vp, vp, vp, sz, vp, vp]
+    lib.spec_verify_attention_chunk.restype = i32
+    lib.spec_verify_attention_chunk_workspace_bytes.argtypes = [i32] * 6
+    lib.spec_verify_attention_chunk_workspace_bytes.restype = sz
     lib.spec_verify_logprobs.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, vp, f32, i32, vp, vp, vp,
                                          vp, vp, vp, sz, vp, vp]
     lib.spec_verify_logprobs.restype = i32
@@ -985,6 +990,42 @@ def spec_verify_attention_e4m3(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         workspace.data_ptr(), workspace.numel(), _status(dev_status, dev), raw)
     if rc != OK:
         raise SpecVerifyError("spec_verify_attention_e4m3", rc)
+    return Attention(out, lse)
+
+
+@functools.lru_cache(maxsize=256)
+def spec_verify_attention_chunk_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int, max_pos: int) -> int:
+    return int(load_library().spec_verify_attention_chunk_workspace_bytes(B, N, Hq, Hkv, D, max_pos))
+
+
+def spec_verify_attention_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                slot_table: torch.Tensor, committed: torch.Tensor, *,
+                                kv_heads: Optional[int] = None, num_nodes=None, scale: Optional[float] = None,
+                                out=None, lse=None, want_lse: bool = False, workspace=None, dev_status=None,
+                                stream=None) -> Attention:
+    """Causal attention of a chunk of a prompt: q [B, N, Hq, D] rotated, node n at position committed + n, over
+    one layer's paged cache that holds the chunk's own rows too.  k_cache and v_cache are 16-bit rows [num_slots,
+    Hkv, D] or, with kv_heads, 8-bit ones (uint8 [num_slots, row bytes]); the rest as for spec_verify_attention."""
+    lib = _lib or load_library()
+    code, dt, dev = _half_dtype(q), q.dtype, _device_of("q", q)
+    B, N, Hq, D = q.shape
+    rows, S, Hkv, ks, vs = _caches(k_cache, v_cache, kv_heads, D, dt, dev)
+    max_pos = slot_table.shape[-1]
+    out = _result("out", out, (B, N, Hq, D), dt, dev, stream)
+    if lse is not None or want_lse:
+        lse = _result("lse", lse, (B, N, Hq), _FP32, dev, stream)
+    raw = _raw_stream(stream, dev)
+    if workspace is None:
+        nbytes = spec_verify_attention_chunk_workspace_bytes(B, N, Hq, Hkv, D, max_pos)
+        workspace = _workspaces.get(nbytes, dev, stream, raw)
+    rc = _on(dev, lib.spec_verify_attention_chunk)(
+        q.data_ptr(), code, _row_stride("q", q, B, N, Hq, D), k_cache.data_ptr(), v_cache.data_ptr(), rows, S, ks, vs,
+        _index("slot_table", slot_table, (B, max_pos), dev), max_pos, _index("committed", committed, (B,), dev),
+        None if num_nodes is None else _index("num_nodes", num_nodes, (B,), dev), B, N, Hq, Hkv, D,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _status(dev_status, dev), raw)
+    if rc != OK:
+        raise SpecVerifyError("spec_verify_attention_chunk", rc)
     return Attention(out, lse)
 
 

@@ -1702,10 +1702,13 @@ unsigned long long attention_debug_fault();
 unsigned long long logprobs_debug_fault();
 unsigned long long cache_debug_fault();
 unsigned long long attention_e4m3_debug_fault();
+unsigned long long chunk_debug_fault();
 bool attention_timeouts(unsigned long long &n);
 bool attention_wait_clocks(long long clocks);
 bool attention_e4m3_timeouts(unsigned long long &n);
 bool attention_e4m3_wait_clocks(long long clocks);
+bool chunk_timeouts(unsigned long long &n);
+bool chunk_wait_clocks(long long clocks);
 bool logprobs_timeouts(unsigned long long &n);
 bool logprobs_wait_clocks(long long clocks);
 }  // namespace sv
@@ -1724,7 +1727,7 @@ extern "C" int spec_verify_debug_fault(uint64_t *fault)
 #endif
     for (unsigned long long x : {sv::kv_debug_fault(), sv::budget_debug_fault(), sv::append_debug_fault(),
                                  sv::attention_debug_fault(), sv::logprobs_debug_fault(), sv::cache_debug_fault(),
-                                 sv::attention_e4m3_debug_fault()}) {
+                                 sv::attention_e4m3_debug_fault(), sv::chunk_debug_fault()}) {
         if (x == ~0ull) return SPEC_VERIFY_ECUDA;
         if (!w) w = x;
     }
@@ -1739,7 +1742,8 @@ extern "C" int spec_verify_wait_timeouts(uint64_t *count)
     unsigned long long n = 0, z = 0;
     if (cudaMemcpyFromSymbol(&n, sv::g_ring_timeouts, sizeof n) != cudaSuccess ||
         cudaMemcpyToSymbol(sv::g_ring_timeouts, &z, sizeof z) != cudaSuccess || !sv::attention_timeouts(n) ||
-        !sv::logprobs_timeouts(n) || !sv::attention_e4m3_timeouts(n))
+        !sv::logprobs_timeouts(n) || !sv::attention_e4m3_timeouts(n) ||
+        !sv::chunk_timeouts(n))
         return SPEC_VERIFY_ECUDA;
     *count = n;
     return SPEC_VERIFY_OK;
@@ -1749,7 +1753,9 @@ extern "C" int spec_verify_wait_timeouts(uint64_t *count)
 extern "C" int spec_verify_debug_wait_clocks(int64_t clocks)
 {
 #ifdef SV_DEBUG
-    return sv::attention_wait_clocks(clocks) && sv::logprobs_wait_clocks(clocks) && sv::attention_e4m3_wait_clocks(clocks) ? SPEC_VERIFY_OK : SPEC_VERIFY_ECUDA;
+    return sv::attention_wait_clocks(clocks) && sv::logprobs_wait_clocks(clocks) && sv::attention_e4m3_wait_clocks(clocks) &&
+                   sv::chunk_wait_clocks(clocks)
+               ? SPEC_VERIFY_OK : SPEC_VERIFY_ECUDA;
 #else
     (void)clocks;
     return SPEC_VERIFY_EINVAL;

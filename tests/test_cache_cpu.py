@@ -77,6 +77,33 @@ def test_nodes(lib):
     assert nodes(lib, ws=0x10080) == binding.EWORKSPACE
 
 
+def chunk(lib, **bad):
+    a = dict(q=A, dtype=0, qs=32 * 128, kc=A, vc=A, cache=E, slots=100, kss=1040, vss=1040, table=A, max_pos=64,
+             committed=A, num_nodes=None, B=2, N=800, Hq=32, Hkv=8, D=128, scale=0.1, out=A, lse=None, ws=A,
+             nbytes=1 << 30, status=None, stream=None)
+    assert set(bad) <= set(a)
+    return lib.spec_verify_attention_chunk(*{**a, **bad}.values())
+
+
+def test_chunk(lib):
+    for bad in (dict(q=None), dict(kc=None), dict(vc=None), dict(table=None), dict(committed=None), dict(out=None),
+                dict(ws=None), dict(dtype=1), dict(dtype=E), dict(cache=1), dict(cache=2), dict(cache=-1), dict(B=0),
+                dict(B=65537), dict(N=0), dict(B=65536, N=65536), dict(Hq=0), dict(Hkv=0), dict(Hkv=5), dict(D=48),
+                dict(D=72), dict(D=144), dict(max_pos=0), dict(max_pos=(1 << 31) - 1), dict(slots=0), dict(slots=1 << 31),
+                dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(qs=4088),
+                dict(qs=4100), dict(kss=1024), dict(vss=1048), dict(kss=1 << 31), dict(cache=0, kss=1016),
+                dict(cache=0, vss=1028), dict(q=ODD), dict(kc=ODD), dict(vc=ODD), dict(out=ODD), dict(table=ODD4),
+                dict(committed=ODD4), dict(num_nodes=ODD4), dict(lse=ODD4), dict(status=ODD4),
+                dict(B=60000, N=30000, Hq=64, Hkv=64, max_pos=1 << 30)):
+        assert chunk(lib, **bad) == binding.EINVAL, bad
+    assert chunk(lib, nbytes=16) == binding.EWORKSPACE
+    assert chunk(lib, ws=0x10080) == binding.EWORKSPACE
+    need = binding.spec_verify_attention_chunk_workspace_bytes
+    assert need(2, 800, 32, 8, 128, 64) > 0 and need(1, 1 << 20, 64, 8, 64, 1 << 20) > 0
+    for bad in ((0, 8, 32, 8, 128, 64), (2, 8, 32, 5, 128, 64), (2, 8, 32, 8, 130, 64), (2, 8, 32, 8, 128, 0)):
+        assert need(*bad) == 0
+
+
 def test_row_bytes(lib):
     for Hkv, D in ((1, 16), (8, 128), (3, 80), (5, 112), (16, 512)):
         assert binding.spec_verify_kv_e4m3_row_bytes(Hkv, D) == pc.row_bytes(Hkv, D)
@@ -94,6 +121,8 @@ def test_tensors_on_the_host_are_refused(lib):
         binding.spec_verify_kv_read(c, c, i, i[0, :1], 2, kv_heads=2, head_dim=64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         binding.spec_verify_attention_e4m3(h, c, c, i, i[0, :1], kv_heads=2)
+    with pytest.raises(ValueError):
+        binding.spec_verify_attention_chunk(h, c, c, i, i[0, :1], kv_heads=2)
 
 
 def test_the_plain_form_of_the_rows():
