@@ -72,7 +72,8 @@ constexpr int COST_TILE = 2, COST_SEGMENT = 4;
 // Warpgroups of the softmax: two hold 16 columns a thread at most, and so do four where there are 64 columns
 // (with 32 a thread: one tree of 16 over 131000 positions 105.6 us against 102.7).
 __host__ __device__ constexpr int groups(int nq) { return nq == 64 ? 4 : 2; }
-__host__ __device__ constexpr int threads(int nq) { return 256 + 128 * groups(nq); }
+// (8-bit rows: a warpgroup more of copies, behind the softmax's.)
+__host__ __device__ constexpr int threads(int nq, bool e4) { return 256 + 128 * groups(nq) + (e4 ? 128 : 0); }
 // CTAs that an SM holds.  With at most 8 columns a thread, 64 registers nearly do (32 bytes spilled), and one CTA
 // works while the other is between segments: 96 requests of 12 heads of 64 take 44.4 us against 52.4, 128
 // requests of up to 504 positions (8 key heads of 128) 30.2 against 30.7.  Two units of 128 dimensions are then all
@@ -114,7 +115,7 @@ struct Layout {
 struct __align__(16) Seg {
     int b, h, qt, kind;        // kind 0: to attend; 1: no nodes; 2: lengths are wrong; 3: no more segments
     int c, nn, j0, j1;
-    int part, c0, c1, pad;     // part: the workspace part it writes (-1: it is the whole); the CTAs it spans
+    int part, c0, c1, pad;     // part: the workspace part it writes (-1: it is the whole); the runs it spans
 };
 
 // Parts to be joined: of segment g, `n` from the `first` on, `step` apart.
@@ -133,10 +134,11 @@ __device__ __forceinline__ int group_size(int parts)
     return s;
 }
 
-template <int NQ, int NU>
+template <bool BF, int NQ, int DP, bool E4>
 struct Misc {
+    static constexpr int NU = Layout<NQ, DP, E4>::NU;
     uint64_t full[NU], empty[NU];
-    static constexpr int NT = threads(NQ), WG = groups(NQ);
+    static constexpr int NT = threads(NQ, E4), WG = groups(NQ);
     uint64_t sfull[2], sempty[2], qfull[2], qempty[2], segfull[SEGS], segempty[SEGS], pfull, pvdone, drain;
     Seg seg[SEGS];
     unsigned long long desc[2][sv::MAX_TREE];  // columns that see node a, of the staged queries
@@ -150,6 +152,7 @@ struct Misc {
     Join join[2];
     int joins[2];
     int8_t par[sv::MAX_TREE];
+    typename sv::E4m3FeedSmem<BF, DP, E4>::type feed[8];
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -244,11 +247,11 @@ __device__ __forceinline__ void lengths(const Params &P, int b, int &c, int &nn)
 }
 
 template <bool BF, int NQ, int DP, bool E4>
-__global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_kernel(const Params P)
+__global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attention_kernel(const Params P)
 {
     using L = Layout<NQ, DP, E4>;
-    using M = Misc<NQ, L::NU>;
-    constexpr int NU = L::NU, HALVES = L::HALVES, NT = threads(NQ), WG = groups(NQ);
+    using M = Misc<BF, NQ, DP, E4>;
+    constexpr int NU = L::NU, HALVES = L::HALVES, NT = threads(NQ, E4), WG = groups(NQ);
     extern __shared__ __align__(1024) unsigned char smem[];
     M &ms = *reinterpret_cast<M *>(smem + L::M0);
     const uint32_t s0 = tc::smem_u32(smem);
@@ -284,14 +287,20 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_ke
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // The batch's cost, and the request that this CTA's run begins in.
+    // 8-bit rows: each key head (and column block) has the axis for itself, and as many CTAs; so all heads read the
+    // same positions at a time, whose rows are too short for memory's sectors to be a head's own.
     const int HT = P.Hkv * P.QT;
+    const int LN = E4 && HT <= (int)gridDim.x ? HT : 1, IT = LN > 1 ? 1 : HT;
+    const int run = E4 ? (unsigned)cta / (unsigned)LN : cta, own_item = E4 ? cta - run * LN : 0;
+    auto cta_of = [&](int r) { return E4 ? r * LN + own_item : r; };  // of this axis' run r
+    const int most_runs = E4 ? gridDim.x / LN : gridDim.x;
     const int per = (P.B + NT - 1) / NT;
     int64_t mine = 0;
 #pragma unroll 1
     for (int i = 0; i < per && tid * per + i < P.B; ++i) {
         int c, nn;
         lengths(P, tid * per + i, c, nn);
-        mine += cost_of(tiles_of(kind_of(P, c, nn), c, nn)) * HT;
+        mine += cost_of(tiles_of(kind_of(P, c, nn), c, nn)) * IT;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -308,9 +317,9 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_ke
     };
     const int64_t before = incl - mine + sum(lane < warp ? in : 0), total = sum(in);
     // Small batches leave the last CTAs out: a run costs COST_TILE at least.
-    const int G = total / COST_TILE < (int64_t)gridDim.x ? (int)(total / COST_TILE) : (int)gridDim.x;
+    const int G = total / COST_TILE < (int64_t)most_runs ? (int)(total / COST_TILE) : most_runs;
     // Odd lanes work out the run's end, even ones its beginning.
-    const int64_t edge = cta + (lane & 1) <= G ? run_begin(cta + (lane & 1), total, G) : total;
+    const int64_t edge = run + (lane & 1) <= G ? run_begin(run + (lane & 1), total, G) : total;
     const int64_t t0 = __shfl_sync(0xffffffffu, edge, 0), t1 = __shfl_sync(0xffffffffu, edge, 1);
     if (t0 >= before && t0 < before + mine) {
         int64_t at = before;
@@ -319,7 +328,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_ke
         for (; per > 1 && b < P.B; ++b) {
             int c, nn;
             lengths(P, b, c, nn);
-            const int64_t n = cost_of(tiles_of(kind_of(P, c, nn), c, nn)) * HT;
+            const int64_t n = cost_of(tiles_of(kind_of(P, c, nn), c, nn)) * IT;
             if (t0 < at + n) break;
             at += n;
         }
@@ -344,15 +353,17 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_ke
     };
 
     if (t1 > t0) {
-        if (warp < 4) {
+        if (warp < 4 || (E4 && warp >= 8 + 4 * WG)) {
+            const int cw = E4 ? warp & 3 : warp;  // the warp of its warpgroup
             // ---- tiles into shared memory -------------------------------------------------
             // A row's CPR chunks go to CPR lanes, 32 / CPR rows to a warp's copy.  A lane keeps the
             // slot of one of its warp's 32 rows; they are read one tile ahead of the copies.
-            constexpr int CPR = E4 ? DP / 16 : DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
+            [[maybe_unused]] constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
+            sv::E4m3Feed<BF, DP> feed(&ms.feed[warp < 4 ? warp : 4 + cw], cw, lane, P.D);
             const int chunk = lane % CPR, sub = lane / CPR;
-            const int own = warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot it keeps
-            const int first = warp * RPI + sub;                                // its row of the first copy
-            const bool wide = chunk * (E4 ? 16 : 8) < P.D;
+            const int own = E4 ? feed.own : cw * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot it keeps
+            const int first = cw * RPI + sub;                                  // its row of the first copy
+            const bool wide = chunk * 8 < P.D;
             Seg g = {};
             int seg = -1, j = 0, slot = -1, u = 0;
             bool ok = true;
@@ -388,6 +399,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_ke
                 }
                 return slot;
             };
+            if constexpr (E4) u = warp < 4 ? 0 : 1;
             // A unit of the ring may be written again once its products are done.
             auto room = [&] {
                 if (u >= NU) {
@@ -433,69 +445,60 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_ke
                     if (found == 2 && ok) found = seek(true);
                 }
             } else {
-                // 8-bit rows pass through registers: 16 values per load, widened to two of the unit's chunks.  A
-                // tile's keys and values are asked for while the tile before is widened.
-                uint4 raw[2][ITER];
-                int es[2] = {0, 0};  // the exponents of the row whose slot the lane keeps
-                const uint32_t to = s0 + (chunk >> 2) * TILE * 128 + first * 128;
-                const uint32_t c0 = ((2 * chunk & 7) ^ (first & 7)) << 4, c1 = c0 ^ 16;
-                auto ask = [&](int slots, int kv) {
-                    const uint32_t stride = (uint32_t)(kv ? P.v_slot : P.k_slot);
-                    const unsigned char *base = kv ? P.v : P.k;
-                    es[kv] = 127;
-                    if (slots >= 0) es[kv] = __ldg(base + (uint64_t)(uint32_t)slots * stride + P.Hkv * P.D + g.h);
-                    base += g.h * P.D + chunk * 16;
-#pragma unroll
-                    for (int i = 0; i < ITER; ++i) {
-                        const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
-                        raw[kv][i] = make_uint4(0, 0, 0, 0);
-                        if (s >= 0 && wide) raw[kv][i] = __ldg(reinterpret_cast<const uint4 *>(base + (uint64_t)(uint32_t)s * stride));
+                // One warpgroup has the keys, the other the values.  Of the tiles ahead one has its rows under way while
+                // a tile is widened, the next is asked of L2 and has its powers of two under way, the third its slots.
+                const int kv = u;
+                const unsigned char *const cache = kv ? P.v : P.k;
+                const uint32_t stride = (uint32_t)(kv ? P.v_slot : P.k_slot);
+                bool sought = false, placed = false, loaded = false, last = false;
+                int es = 127, b = 0;  // buffer b: the loaded tile's; the other: the placed one's
+                auto look = [&](bool block) {
+                    if (sought || last) return;
+                    const int found = seek(block);
+                    sought = found == 1;
+                    last = found == 0;
+                };
+                auto place = [&] {
+                    if (!sought || placed) return;
+                    sought = false;
+                    placed = true;
+                    const int s = check(j * TILE + own >= g.c + g.nn);
+                    const unsigned char *const row = cache + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride, *const at = row + g.h * P.D;
+                    feed.put_row(b ^ 1, s < 0 ? sv::e4m3_none(false) : at);
+                    es = 127;
+                    if (s >= 0) {
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + P.D - 1));
+                        es = __ldg(row + P.Hkv * P.D + g.h);
                     }
                 };
-                auto widen = [&](int kv) {
-                    const uint32_t dst = to + (u % NU) * L::UNIT;
-                    const bool odd = DP == 128 && chunk >= 4;  // lanes 4 apart write the other chunk: no bank twice
-                    const uint32_t a0 = dst + (odd ? c1 : c0), a1 = dst + (odd ? c0 : c1);
-#pragma unroll
-                    for (int i = 0; i < ITER; ++i) {
-                        const sv::E4m3Scale<BF> f(__shfl_sync(0xffffffffu, es[kv], i * RPI + sub));
-                        const uint4 w = raw[kv][i];
-                        const uint4 lo = make_uint4(f(w.x), f(w.x >> 16), f(w.y), f(w.y >> 16));
-                        const uint4 hi = make_uint4(f(w.z), f(w.z >> 16), f(w.w), f(w.w >> 16));
-                        const uint4 x = odd ? hi : lo, y = odd ? lo : hi;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0 + i * 4 * RPI * 128), "r"(x.x), "r"(x.y),
-                                     "r"(x.z), "r"(x.w)
-                                     : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1 + i * 4 * RPI * 128), "r"(y.x), "r"(y.y),
-                                     "r"(y.z), "r"(y.w)
-                                     : "memory");
-                    }
-                    tc::fence_async_smem();
-                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));
-                    ++u;
-                };
-                int found = seek(true);
-                int slots = found == 1 ? check(j * TILE + own >= g.c + g.nn) : -1;
-                if (found == 1) ask(slots, 0), ask(slots, 1);
-                while (found == 1) {
-                    const int next = seek(false);
-                    if (!room()) break;
-                    widen(0);
-                    if (next == 1) {
-                        slots = check(j * TILE + own >= g.c + g.nn);
-                        ask(slots, 0);
+                for (;;) {
+                    if (!loaded) {
+                        look(true);
+                        place();
+                        if (!placed) break;
+                        feed.put_scale(b ^ 1, es);
+                        __syncwarp();
+                        b ^= 1;
+                        feed.load_all(b);
+                        loaded = true;
+                        placed = false;
+                        look(false);
+                        place();
+                        look(false);
                     }
                     if (!room()) break;
-                    widen(1);
-                    if (next == 1) {
-                        ask(slots, 1);
-                    } else if (next == 2) {
-                        found = seek(true);
-                        slots = found == 1 ? check(j * TILE + own >= g.c + g.nn) : -1;
-                        if (found == 1) ask(slots, 0), ask(slots, 1);
-                        continue;
-                    }
-                    found = next;
+                    const bool more = placed;
+                    if (more) feed.put_scale(b ^ 1, es);
+                    __syncwarp();
+                    feed.widen(s0 + (u % NU) * L::UNIT, b, more, b ^ 1);
+                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
+                    u += 2;
+                    loaded = more;
+                    placed = false;
+                    if (more) b ^= 1;
+                    place();
+                    look(false);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -638,19 +641,20 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_ke
                     at += item * cost;
                     first = false;
                 }
-                for (; item < HT && at < t1 && ok; ++item, at += cost) {
-                    g.h = P.QT == 1 ? item : item / P.QT;
-                    g.qt = item - g.h * P.QT;
+                for (; item < IT && at < t1 && ok; ++item, at += cost) {
+                    const int x = item + own_item;
+                    g.h = P.QT == 1 ? x : x / P.QT;
+                    g.qt = x - g.h * P.QT;
                     g.j0 = cut_tile(t0 - at, ntile);
                     g.j1 = cut_tile(t1 - at, ntile);
                     if (g.j0 >= g.j1) continue;
                     g.part = -1;
                     if (g.j0 > 0 || g.j1 < ntile) {
                         // The runs that hold its first and its last tile, and all between.
-                        const int run = run_before(at + (lane & 1 ? cost - COST_TILE / 2 : COST_SEGMENT + COST_TILE / 2), total, G);
-                        g.c0 = __shfl_sync(0xffffffffu, run, 0);
-                        g.c1 = __shfl_sync(0xffffffffu, run, 1);
-                        g.part = 2 * cta + (cta == g.c0);
+                        const int ends = run_before(at + (lane & 1 ? cost - COST_TILE / 2 : COST_SEGMENT + COST_TILE / 2), total, G);
+                        g.c0 = __shfl_sync(0xffffffffu, ends, 0);
+                        g.c1 = __shfl_sync(0xffffffffu, ends, 1);
+                        g.part = 2 * cta + (run == g.c0);
                     }
                     put(g);
                 }
@@ -975,7 +979,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_ke
                         uint32_t bits;
                         if constexpr (E4) {
                             const unsigned char *at = P.v + (int64_t)slot * P.v_slot;
-                            bits = sv::E4m3Scale<BF>(at[P.Hkv * P.D + g.h])(at[g.h * P.D + t]) & 0xffffu;
+                            bits = sv::E4m3Scale<BF>(sv::E4m3Scale<BF>::bits(at[P.Hkv * P.D + g.h]))(at[g.h * P.D + t]) & 0xffffu;
                         } else {
                             bits = reinterpret_cast<const uint16_t *>(P.v)[(int64_t)slot * P.v_slot + g.h * P.D + t];
                         }
@@ -1017,15 +1021,15 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_ke
                     // The part that a run begins with is there early, so that it seldom joins two at its end.
                     group_sync(bar, 128);
                     if (t == 0 && !fail) {
-                        const int parts = g.c1 - g.c0 + 1, size = group_size(parts), first = (cta - g.c0) / size * size;
+                        const int parts = g.c1 - g.c0 + 1, size = group_size(parts), first = (run - g.c0) / size * size;
                         const int n = parts - first < size ? parts - first : size;
-                        unsigned *count = &P.counters[first ? COUNTERS + g.c0 + first : g.c0];
+                        unsigned *count = &P.counters[first ? COUNTERS + cta_of(g.c0 + first) : cta_of(g.c0)];
                         __threadfence();
                         if (atomicAdd(count, 1u) == (unsigned)(WG * n - 1)) {
                             __threadfence();
                             *count = 0;
-                            ms.join[cta == g.c0] = {g, first, n, 1};
-                            ms.joins[cta == g.c0] = 1;
+                            ms.join[run == g.c0] = {g, first, n, 1};
+                            ms.joins[run == g.c0] = 1;
                         }
                     }
                 }
@@ -1048,7 +1052,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_ke
                     uint32_t *const jrow = reinterpret_cast<uint32_t *>(jr + parts * NQ);  // columns' rows of the output (2^32 would be 550 GB)
                     auto part_of = [&](int x) {
                         const int y = jn.first + x * jn.step;
-                        return P.parts + (int64_t)(2 * (g.c0 + y) + (y == 0)) * part_floats<NQ>();
+                        return P.parts + (int64_t)(2 * cta_of(g.c0 + y) + (y == 0)) * part_floats<NQ>();
                     };
                     float4 y[2][IT], acc[IT];
                     auto load = [&](int x, float4 (&y)[IT]) {
@@ -1139,7 +1143,7 @@ __global__ void __launch_bounds__(threads(NQ), ctas_per_sm(NQ, E4)) attention_ke
                         ms.joins[end] = 0;
                         if (!all) {
                             const int size = group_size(g.c1 - g.c0 + 1), n = (g.c1 - g.c0) / size + 1;
-                            unsigned *count = &P.counters[2 * COUNTERS + g.c0];
+                            unsigned *count = &P.counters[2 * COUNTERS + cta_of(g.c0)];
                             __threadfence();
                             if (atomicAdd(count, 1u) == (unsigned)(n - 1)) {
                                 __threadfence();
@@ -1185,7 +1189,7 @@ template <bool BF, int NQ, int DP, bool E4>
 constexpr size_t smem_bytes()
 {
     using L = Layout<NQ, DP, E4>;
-    return L::M0 + sizeof(Misc<NQ, L::NU>);
+    return L::M0 + sizeof(Misc<BF, NQ, DP, E4>);
 }
 
 template <bool BF, int NQ, int DP, bool E4>
@@ -1230,7 +1234,7 @@ static cudaError_t launch(const Params &P, int grid, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(threads(NQ));
+    cfg.blockDim = dim3(threads(NQ, E4));
     cfg.dynamicSmemBytes = smem_bytes<BF, NQ, DP, E4>();
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

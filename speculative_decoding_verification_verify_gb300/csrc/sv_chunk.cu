@@ -79,15 +79,19 @@ struct Layout {
     static constexpr int Q0 = NU * UNIT, M0 = Q0 + 2 * QHALF;
 };
 
-template <int NU>
+template <int NU, class Feed, int FEEDS>
 struct Misc {
     uint64_t full[NU], empty[NU];
     uint64_t sfull[2], pfull[2], odone[2], qfull, qempty, segfull[SEGS], segempty[SEGS], drain;
-    Seg seg[SEGS];
-    int64_t scan[NT / 32], begin_base;
+    union {
+        Seg seg[SEGS];
+        int64_t scan[NT / 32];  // (before any segment is listed)
+    };
+    int64_t begin_base;
     int begin_b, abort;
     int poison[4];  // a segment's number: its values have some that are not finite behind the block's first row
     uint32_t tmem;
+    Feed feed[FEEDS];
 };
 
 // Floats of a part: the weighted values [dimensions / 4][row][4], references and sums of the rows.
@@ -141,12 +145,15 @@ __device__ __forceinline__ int64_t run_begin(int64_t r, int64_t total, int runs)
 __device__ __forceinline__ int run_before(int64_t x, int64_t total, int runs) { return (int)((x * runs + total - 1) / total) - 1; }
 
 template <bool BF, int DP, bool E4>
+using MiscOf = Misc<Layout<DP>::NU, typename sv::E4m3FeedSmem<BF, DP, E4>::type, 4>;
+
+template <bool BF, int DP, bool E4>
 __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Params P)
 {
     using L = Layout<DP>;
     constexpr int NU = L::NU;
     extern __shared__ __align__(1024) unsigned char smem[];
-    Misc<NU> &ms = *reinterpret_cast<Misc<NU> *>(smem + L::M0);
+    auto &ms = *reinterpret_cast<MiscOf<BF, DP, E4> *>(smem + L::M0);
     const uint32_t s0 = tc::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
     volatile int *abort = &ms.abort;
@@ -231,15 +238,16 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
 
     // (The registers of a launch, 128 a thread, go to those who hold a row of scores.)
     if (warp < 4) {
-        if constexpr (E4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if constexpr (E4) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         // ---- queries and tiles into shared memory ---------------------------------------------
         constexpr int QCPR = DP / 8, QRPI = 32 / QCPR;            // 16-byte chunks of a query row; rows of a warp's copy
-        constexpr int CPR = E4 ? DP / 16 : DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
+        [[maybe_unused]] constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
+        sv::E4m3Feed<BF, DP> feed(&ms.feed[warp], warp, lane, P.D);
         const int chunk = lane % CPR, sub = lane / CPR;
-        const int own = warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot the lane keeps
-        const int first = warp * RPI + sub;                                // its row of the first copy
-        const bool wide = chunk * (E4 ? 16 : 8) < P.D;
+        const int own = E4 ? feed.own : warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot the lane keeps
+        const int first = warp * RPI + sub;                                                // its row of the first copy
+        const bool wide = chunk * 8 < P.D;
         Seg g;
         int u = 0, seg = 0;
         bool ok = true;
@@ -320,63 +328,42 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                     }
                 }
             } else {
-                // 16 values per load, widened to two of the unit's chunks; a tile's keys and values are asked for while
-                // the tile before is widened.
-                uint4 raw[2][ITER];
-                int es[2];
-                const uint32_t to = s0 + (chunk >> 2) * TILE * 128 + first * 128;
-                const uint32_t c0 = ((2 * chunk & 7) ^ (first & 7)) << 4, c1 = c0 ^ 16;
-                auto ask = [&](int slots, int kv) {
-                    const int64_t stride = kv ? P.v_slot : P.k_slot;
-                    const unsigned char *base = kv ? P.v : P.k;
-                    es[kv] = 127;
-                    if (slots >= 0) es[kv] = __ldg(base + slots * stride + P.Hkv * P.D + g.h);
-                    base += g.h * P.D + chunk * 16;
-                    const uint32_t none = kv == 0 ? 0x7f7f7f7fu : 0u;
-#pragma unroll
-                    for (int i = 0; i < ITER; ++i) {
-                        const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
-                        const uint32_t w = s == -2 ? none : 0u;
-                        raw[kv][i] = make_uint4(w, w, w, w);
-                        if (s >= 0 && wide) raw[kv][i] = __ldg(reinterpret_cast<const uint4 *>(base + s * stride));
-                    }
+                // A unit is widened as the rows of the next one are asked for.  Buffer 0 is the keys', 1 the values'.
+                auto row = [&](int slot, int kv) {
+                    return slot < 0 ? sv::e4m3_none(slot == -2 && kv == 0) : (kv ? P.v + slot * P.v_slot : P.k + slot * P.k_slot) + g.h * P.D;
                 };
-                auto widen = [&](int kv) {
-                    const uint32_t dst = to + (u % NU) * L::UNIT;
-                    const bool odd = DP == 128 && chunk >= 4;  // lanes 4 apart write the other chunk: no bank twice
-                    const uint32_t a0 = dst + (odd ? c1 : c0), a1 = dst + (odd ? c0 : c1);
-#pragma unroll
-                    for (int i = 0; i < ITER; ++i) {
-                        const sv::E4m3Scale<BF> f(__shfl_sync(0xffffffffu, es[kv], i * RPI + sub));
-                        const uint4 w = raw[kv][i];
-                        const uint4 lo = make_uint4(f(w.x), f(w.x >> 16), f(w.y), f(w.y >> 16));
-                        const uint4 hi = make_uint4(f(w.z), f(w.z >> 16), f(w.w), f(w.w >> 16));
-                        const uint4 x = odd ? hi : lo, y = odd ? lo : hi;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0 + i * 4 * RPI * 128), "r"(x.x), "r"(x.y),
-                                     "r"(x.z), "r"(x.w)
-                                     : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1 + i * 4 * RPI * 128), "r"(y.x), "r"(y.y),
-                                     "r"(y.z), "r"(y.w)
-                                     : "memory");
-                    }
-                    tc::fence_async_smem();
-                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));
+                auto exponent = [&](int slot, int kv) {
+                    return slot < 0 ? 127 : (int)__ldg((kv ? P.v + slot * P.v_slot : P.k + slot * P.k_slot) + P.Hkv * P.D + g.h);
+                };
+                auto unit = [&](int b, bool more) {
+                    if (!room()) return false;
+                    feed.widen(s0 + (u % NU) * L::UNIT, b, more, b ^ 1);
+                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
                     ++u;
+                    return true;
                 };
-                int slots = check(g.j0, ahead);
-                ask(slots, 0);
-                ask(slots, 1);
+                int slot = check(g.j0, ahead), es[2] = {exponent(slot, 0), exponent(slot, 1)};
+                __syncwarp();
+                feed.put_row(0, row(slot, 0));
+                feed.put_row(1, row(slot, 1));
+                __syncwarp();
+                feed.load_all(0);
                 for (int j = g.j0; j < g.j1; ++j) {
+                    const bool more = j + 1 < g.j1;
+                    feed.put_scale(0, es[0]);
                     ahead = look(j + 1);
-                    if (!room()) break;
-                    widen(0);
-                    if (j + 1 < g.j1) {
-                        slots = check(j + 1, ahead);
-                        ask(slots, 0);
+                    __syncwarp();
+                    if (!unit(0, true)) break;
+                    feed.put_scale(1, es[1]);
+                    if (more) {
+                        slot = check(j + 1, ahead);
+                        feed.put_row(0, row(slot, 0));
+                        es[0] = exponent(slot, 0);
+                        es[1] = exponent(slot, 1);
                     }
-                    if (!room()) break;
-                    widen(1);
-                    if (j + 1 < g.j1) ask(slots, 1);
+                    __syncwarp();
+                    if (!unit(1, more)) break;
+                    if (more) feed.put_row(1, row(slot, 1));
                 }
             }
         }
@@ -510,7 +497,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
             if (lane == 0) P.joins[cta] = jn;
         }
     } else {
-        if constexpr (E4) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        if constexpr (E4) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         // ---- softmax: a row per thread ---------------------------------------------------------
         const int half = (warp - 8) >> 2, wq = warp & 3, t = tid & 127;
@@ -663,7 +650,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                     for (int i = 0; i < 32; ++i) {
                         if (32 * d + i >= P.D) continue;
                         uint32_t bits;
-                        if constexpr (E4) bits = sv::E4m3Scale<BF>(src[P.Hkv * P.D + g.h])(src[g.h * P.D + 32 * d + i]) & 0xffffu;
+                        if constexpr (E4) bits = sv::E4m3Scale<BF>(sv::E4m3Scale<BF>::bits(src[P.Hkv * P.D + g.h]))(src[g.h * P.D + 32 * d + i]) & 0xffffu;
                         else bits = reinterpret_cast<const uint16_t *>(src)[g.h * P.D + 32 * d + i];
                         if ((bits & Half2<BF>::EXP_MASK) == Half2<BF>::EXP_MASK) o[i] += Half2<BF>::unpack(bits).x;
                     }
@@ -823,18 +810,18 @@ __global__ void __launch_bounds__(JT) finish_kernel(const __grid_constant__ Para
 static std::mutex g_mu;
 static int g_sms[64];
 
-template <int DP>
+template <bool BF, int DP, bool E4>
 constexpr size_t smem_bytes()
 {
-    return Layout<DP>::M0 + sizeof(Misc<Layout<DP>::NU>);
+    return Layout<DP>::M0 + sizeof(MiscOf<BF, DP, E4>);
 }
 
 template <bool BF, int DP, bool E4>
 static bool allow()
 {
-    static_assert(smem_bytes<DP>() <= 232448, "shared memory of a CTA");
+    static_assert(smem_bytes<BF, DP, E4>() <= 232448, "shared memory of a CTA");
     return cudaFuncSetAttribute((const void *)chunk_kernel<BF, DP, E4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)smem_bytes<DP>()) == cudaSuccess;
+                                (int)smem_bytes<BF, DP, E4>()) == cudaSuccess;
 }
 
 // Once per device: the kernels' shared memory; the SM count, 0 when it cannot be had.
@@ -889,8 +876,8 @@ static cudaError_t launch(F *kernel, const Params &P, int grid, int threads, siz
 template <bool BF, bool E4>
 static cudaError_t dispatch(const Params &P, int sms, cudaStream_t s)
 {
-    const cudaError_t e = P.D <= 64 ? launch(chunk_kernel<BF, 64, E4>, P, P.ctas, NT, smem_bytes<64>(), s)
-                                    : launch(chunk_kernel<BF, 128, E4>, P, P.ctas, NT, smem_bytes<128>(), s);
+    const cudaError_t e = P.D <= 64 ? launch(chunk_kernel<BF, 64, E4>, P, P.ctas, NT, smem_bytes<BF, 64, E4>(), s)
+                                    : launch(chunk_kernel<BF, 128, E4>, P, P.ctas, NT, smem_bytes<BF, 128, E4>(), s);
     return e != cudaSuccess ? e : launch(finish_kernel<BF>, P, 2 * sms, JT, 0, s);
 }
 

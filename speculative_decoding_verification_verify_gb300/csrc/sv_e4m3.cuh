@@ -49,41 +49,122 @@ __device__ __forceinline__ uint32_t e4m3_half2(uint32_t bits)
 
 __device__ __forceinline__ float2 e4m3_unpack(uint32_t bits) { return Half2<false>::unpack(e4m3_half2(bits)); }
 
-// Pairs of values (the low 16 bits) in 16 bits, times their head's power of two, from its byte: exact.
+// Values in 16 bits, times their head's power of two: exact, NaN too.  `bits` of a head are the factor in the type.  (Shifting the bits to where bf16 has them and one product is as many instructions, but knows no NaN.)
 template <bool BF>
 struct E4m3Scale;
 
 template <>
 struct E4m3Scale<true> {
     uint64_t f;
-    __device__ __forceinline__ explicit E4m3Scale(int byte)
+    static __device__ __forceinline__ uint16_t bits(int byte) { return (uint16_t)(byte << 7); }
+    __device__ __forceinline__ explicit E4m3Scale(uint16_t bits)
     {
-        const float x = __uint_as_float((uint32_t)byte << 23);
+        const float x = __uint_as_float((uint32_t)bits << 16);
         f = f2(x, x);
     }
-    __device__ __forceinline__ uint32_t operator()(uint32_t bits) const
+    // Two values, of the low 16 bits.  (The product's low half is zeros: four digits.  bf16's subnormals lose some.)
+    __device__ __forceinline__ uint32_t operator()(uint32_t two) const
     {
-        const float2 x = e4m3_unpack(bits), y = f2_split(f2_mul(f2(x.x, x.y), f));
-        return Half2<true>::pack(y.x, y.y);
+        const float2 x = e4m3_unpack(two), y = f2_split(f2_mul(f2(x.x, x.y), f));
+        return __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
     }
 };
 
-// (2^e in two factors that fp16 holds, the first of them exact on every value: rounded once, where 2^e is below -15.)
+// (2^e is a number of fp16, subnormal below -14, for all exponents that append writes from fp16.)
 template <>
 struct E4m3Scale<false> {
-    __half2 f, g;
-    __device__ __forceinline__ explicit E4m3Scale(int byte)
+    __half2 f;
+    static __device__ __forceinline__ uint16_t bits(int byte)
     {
-        const int e = byte - 127, a = e < -14 ? -14 : e > 15 ? 15 : e, b = e - a < -24 ? -25 : e - a > 15 ? 15 : e - a;
-        f = __float2half2_rn(exp2_int(a));
-        g = __float2half2_rn(exp2_int(b));
+        return __half_as_ushort(__float2half_rn(__uint_as_float((uint32_t)byte << 23)));
     }
-    __device__ __forceinline__ uint32_t operator()(uint32_t bits) const
+    __device__ __forceinline__ explicit E4m3Scale(uint16_t bits) { f = __half2half2(__ushort_as_half(bits)); }
+    __device__ __forceinline__ uint32_t operator()(uint32_t two) const
     {
-        const uint32_t h = e4m3_half2(bits);
-        const __half2 y = __hmul2(__hmul2(*reinterpret_cast<const __half2 *>(&h), f), g);
+        const uint32_t h = e4m3_half2(two);
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), f);
         return *reinterpret_cast<const uint32_t *>(&y);
     }
+};
+
+// What a lane reads where a row is not there: zeros, or NaN.
+#define SV_NAN4 {0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu}
+static __device__ const uint4 g_e4m3_none[2][8] = {{}, {SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4}};
+#undef SV_NAN4
+__device__ __forceinline__ const unsigned char *e4m3_none(bool nan) { return reinterpret_cast<const unsigned char *>(g_e4m3_none[nan]); }
+
+// A warpgroup's tiles of 128 rows from 8-bit rows to 16-bit units in shared memory (128-byte swizzle, halves of 64
+// values), through registers.  A warp has 32 rows of a tile, in ITER loads of RPI rows; each row's address and power
+// of two are worked out by one lane, and come to the lanes that read it through shared memory: a load is then two
+// additions.  (With a shuffle and a test for each, a tile's widening took half as long again.)
+template <bool BF, int DP>
+struct E4m3Feed {
+    static constexpr int CPR = DP / 16, RPI = 32 / CPR, ITER = CPR;
+    struct __align__(16) Smem {
+        const unsigned char *row[2][RPI][ITER];
+        uint16_t scale[2][RPI][ITER];
+    };
+    Smem &sm;
+    int own, sub, mine_sub, mine_i;  // the row whose slot the lane keeps, of a warp's tile; its place
+    uint32_t to;
+    int offset;  // of the lane's chunk in a row; below 0: beyond the head
+    uint4 raw[ITER];
+
+    // `warp` of the warpgroup.  Eight lanes that store together have chunks of two rows: no bank twice.
+    __device__ __forceinline__ E4m3Feed(void *s, int warp, int lane, int D) : sm(*static_cast<Smem *>(s))
+    {
+        const int chunk = DP == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
+        sub = DP == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2;
+        mine_sub = lane % RPI;
+        mine_i = lane / RPI;
+        own = warp * RPI + mine_sub + 4 * RPI * mine_i;
+        const int first = warp * RPI + sub;
+        to = (chunk >> 2) * 128 * 128 + first * 128 + (((2 * chunk & 7) ^ (first & 7)) << 4);
+        offset = chunk * 16 < D ? chunk * 16 : -1;
+    }
+    // The address of the lane's own row of a tile in buffer b: a head's values; its power of two.
+    __device__ __forceinline__ void put_row(int b, const unsigned char *at) { sm.row[b][mine_sub][mine_i] = at; }
+    __device__ __forceinline__ void put_scale(int b, int byte) { sm.scale[b][mine_sub][mine_i] = E4m3Scale<BF>::bits(byte); }
+    __device__ __forceinline__ void load(int b, int i)
+    {
+        const unsigned char *at = sm.row[b][sub][i];
+        const unsigned char *const p = offset < 0 ? e4m3_none(false) : at + offset;
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(raw[i].x), "=r"(raw[i].y), "=r"(raw[i].z), "=r"(raw[i].w)
+                     : "l"(p));
+    }
+    __device__ __forceinline__ void load_all(int b)
+    {
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) load(b, i);
+    }
+    // The loaded rows, with buffer b's powers of two, to a unit; where `more`, the rows of buffer `next` are asked for.
+    __device__ __forceinline__ void widen(uint32_t unit, int b, bool more, int next)
+    {
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const uint4 w = raw[i];
+            const E4m3Scale<BF> f(sm.scale[b][sub][i]);
+            if (more) load(next, i);
+            const uint32_t at = unit + to + i * 4 * RPI * 128;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(f(w.x)), "r"(f(w.x >> 16)), "r"(f(w.y)),
+                         "r"(f(w.y >> 16))
+                         : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16), "r"(f(w.z)), "r"(f(w.z >> 16)), "r"(f(w.w)),
+                         "r"(f(w.w >> 16))
+                         : "memory");
+        }
+    }
+};
+
+// What a warp of it has in shared memory; nothing in a kernel of 16-bit rows.
+template <bool BF, int DP, bool E4>
+struct E4m3FeedSmem {
+    using type = typename E4m3Feed<BF, DP>::Smem;
+};
+template <bool BF, int DP>
+struct E4m3FeedSmem<BF, DP, false> {
+    struct type {};
 };
 
 }  // namespace sv
