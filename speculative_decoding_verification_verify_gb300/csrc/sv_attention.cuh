@@ -103,11 +103,13 @@ template <int NQ, int DP, bool E4>
 struct Layout {
     static constexpr int HALVES = DP / 64;
     static constexpr int UNIT = TILE * DP * 2;
-    static constexpr int NU = ctas_per_sm(NQ, E4) == 2 ? (DP == 64 ? 5 : 2) : 5 * 128 / DP;
+    // (8-bit rows: a unit of keys and one of values are enough, the rings before them have the tiles under way.)
+    static constexpr int NU = E4 ? 2 * 128 / DP : ctas_per_sm(NQ, E4) == 2 ? (DP == 64 ? 5 : 2) : 5 * 128 / DP;
+    static constexpr int AHEAD = 3 * 128 / DP, RING = E4 ? AHEAD * (128 * DP + 512) : 0;  // of keys, of values
     static constexpr int QBYTES = NQ * DP * 2;
     static constexpr int QSTEP = QBYTES < 1024 ? 1024 : QBYTES;
     static constexpr int PBYTES = TILE * 128;  // a row of 64 columns per position
-    static constexpr int Q0 = NU * UNIT, P0 = Q0 + 2 * QSTEP, M0 = P0 + PBYTES;
+    static constexpr int Q0 = NU * UNIT, P0 = Q0 + 2 * QSTEP, R0 = P0 + PBYTES, M0 = R0 + 2 * RING;
     static constexpr int COLS = 3 * NQ <= 64 ? 64 : 3 * NQ <= 128 ? 128 : 256;  // TMEM columns
 };
 
@@ -152,7 +154,7 @@ struct Misc {
     Join join[2];
     int joins[2];
     int8_t par[sv::MAX_TREE];
-    typename sv::E4m3FeedSmem<BF, DP, E4>::type feed[8];
+    typename sv::E4m3FeedSmem<BF, DP, Layout<NQ, DP, E4>::AHEAD, E4>::type feed[8];
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -359,7 +361,8 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             // A row's CPR chunks go to CPR lanes, 32 / CPR rows to a warp's copy.  A lane keeps the
             // slot of one of its warp's 32 rows; they are read one tile ahead of the copies.
             [[maybe_unused]] constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
-            sv::E4m3Feed<BF, DP> feed(&ms.feed[warp < 4 ? warp : 4 + cw], cw, lane, P.D);
+            constexpr int AHEAD = L::AHEAD;
+            sv::E4m3Feed<BF, DP, AHEAD> feed(&ms.feed[warp < 4 ? warp : 4 + cw], s0 + L::R0 + (warp < 4 ? 0 : L::RING), cw, lane, P.D);
             const int chunk = lane % CPR, sub = lane / CPR;
             const int own = E4 ? feed.own : cw * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot it keeps
             const int first = cw * RPI + sub;                                  // its row of the first copy
@@ -386,6 +389,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 slot = -1;
                 if (pos < g.c + g.nn) {
                     const int64_t at = (int64_t)g.b * P.max_pos + pos;
+                    if (E4 && pos + 2 * TILE < g.c + g.nn) asm volatile("prefetch.global.L2 [%0];" ::"l"(P.slot_table + at + 2 * TILE));
                     slot = SV_INB(at, (int64_t)P.B * P.max_pos, 1103) ? P.slot_table[at] : -1;
                 }
                 return 1;
@@ -445,59 +449,55 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                     if (found == 2 && ok) found = seek(true);
                 }
             } else {
-                // One warpgroup has the keys, the other the values.  Of the tiles ahead one has its rows under way while
-                // a tile is widened, the next is asked of L2 and has its powers of two under way, the third its slots.
+                // One warpgroup has the keys, the other the values.  While a tile is widened its place in the ring is
+                // filled with the one AHEAD tiles on, whose slots were read the tile before.
                 const int kv = u;
                 const unsigned char *const cache = kv ? P.v : P.k;
-                const uint32_t stride = (uint32_t)(kv ? P.v_slot : P.k_slot);
-                bool sought = false, placed = false, loaded = false, last = false;
-                int es = 127, b = 0;  // buffer b: the loaded tile's; the other: the placed one's
+                const uint64_t stride = kv ? P.v_slot : P.k_slot;
+                bool sought = false, last = false;
+                int r = 0, count = 0;  // the oldest tile's place; tiles under way
                 auto look = [&](bool block) {
                     if (sought || last) return;
                     const int found = seek(block);
                     sought = found == 1;
                     last = found == 0;
                 };
-                auto place = [&] {
-                    if (!sought || placed) return;
-                    sought = false;
-                    placed = true;
-                    const int s = check(j * TILE + own >= g.c + g.nn);
-                    const unsigned char *const row = cache + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride, *const at = row + g.h * P.D;
-                    feed.put_row(b ^ 1, s < 0 ? sv::e4m3_none(false) : at);
-                    es = 127;
-                    if (s >= 0) {
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + P.D - 1));
-                        es = __ldg(row + P.Hkv * P.D + g.h);
-                    }
-                };
                 for (;;) {
-                    if (!loaded) {
-                        look(true);
-                        place();
-                        if (!placed) break;
-                        feed.put_scale(b ^ 1, es);
-                        __syncwarp();
-                        b ^= 1;
-                        feed.load_all(b);
-                        loaded = true;
-                        placed = false;
-                        look(false);
-                        place();
-                        look(false);
+                    // The places without a tile: all at the beginning, later where a segment was not listed in time.
+                    while (count < AHEAD) {
+                        look(count == 0);
+                        if (!sought) break;
+                        sought = false;
+                        const int s = check(j * TILE + own >= g.c + g.nn), at = (r + count) % AHEAD;
+#pragma unroll
+                        for (int i = 0; i < feed.ITER; ++i) feed.ask(at, i, s, cache, stride, g.h * P.D);
+                        feed.asked(at, count++, s, cache, stride, P.Hkv * P.D + g.h);
                     }
+                    if (count == 0) break;
+                    for (int i = count; i < AHEAD; ++i) feed.commit();  // (what is waited for is counted in groups)
+                    look(false);
+                    const bool more = sought && count == AHEAD;
+                    const int s = more ? check(j * TILE + own >= g.c + g.nn) : -1;
+                    feed.wait();
                     if (!room()) break;
-                    const bool more = placed;
-                    if (more) feed.put_scale(b ^ 1, es);
-                    __syncwarp();
-                    feed.widen(s0 + (u % NU) * L::UNIT, b, more, b ^ 1);
+                    feed.scales(r, lane);
+                    const uint32_t unit = s0 + (u % NU) * L::UNIT;
+                    if (more) {
+#pragma unroll
+                        for (int i = 0; i < feed.ITER; ++i) {
+                            feed.widen(unit, r, i);
+                            feed.ask(r, i, s, cache, stride, g.h * P.D);
+                        }
+                        feed.asked(r, AHEAD - 1, s, cache, stride, P.Hkv * P.D + g.h);
+                        sought = false;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < feed.ITER; ++i) feed.widen(unit, r, i);
+                        --count;
+                    }
                     tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
                     u += 2;
-                    loaded = more;
-                    placed = false;
-                    if (more) b ^= 1;
-                    place();
+                    r = r + 1 == AHEAD ? 0 : r + 1;
                     look(false);
                 }
             }

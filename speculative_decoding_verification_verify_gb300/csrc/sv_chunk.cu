@@ -71,12 +71,13 @@ struct __align__(16) Seg {
     int nt[2], part, pad;
 };
 
-template <int DP>
+template <int DP, bool E4>
 struct Layout {
     static constexpr int UNIT = TILE * DP * 2;      // a tile's keys or values
     static constexpr int QHALF = HALF * DP * 2;
-    static constexpr int NU = DP == 64 ? 10 : 5;    // units in the ring
-    static constexpr int Q0 = NU * UNIT, M0 = Q0 + 2 * QHALF;
+    // Units in the ring; 8-bit rows have one of their own before it, of AHEAD tiles' keys or values in turn.
+    static constexpr int NU = (E4 ? 3 : 5) * 128 / DP, AHEAD = 3 * 128 / DP;
+    static constexpr int Q0 = NU * UNIT, R0 = Q0 + 2 * QHALF, M0 = R0 + (E4 ? AHEAD * (128 * DP + 512) : 0);
 };
 
 template <int NU, class Feed, int FEEDS>
@@ -145,12 +146,12 @@ __device__ __forceinline__ int64_t run_begin(int64_t r, int64_t total, int runs)
 __device__ __forceinline__ int run_before(int64_t x, int64_t total, int runs) { return (int)((x * runs + total - 1) / total) - 1; }
 
 template <bool BF, int DP, bool E4>
-using MiscOf = Misc<Layout<DP>::NU, typename sv::E4m3FeedSmem<BF, DP, E4>::type, 4>;
+using MiscOf = Misc<Layout<DP, E4>::NU, typename sv::E4m3FeedSmem<BF, DP, Layout<DP, E4>::AHEAD, E4>::type, 4>;
 
 template <bool BF, int DP, bool E4>
 __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Params P)
 {
-    using L = Layout<DP>;
+    using L = Layout<DP, E4>;
     constexpr int NU = L::NU;
     extern __shared__ __align__(1024) unsigned char smem[];
     auto &ms = *reinterpret_cast<MiscOf<BF, DP, E4> *>(smem + L::M0);
@@ -243,7 +244,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
         // ---- queries and tiles into shared memory ---------------------------------------------
         constexpr int QCPR = DP / 8, QRPI = 32 / QCPR;            // 16-byte chunks of a query row; rows of a warp's copy
         [[maybe_unused]] constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
-        sv::E4m3Feed<BF, DP> feed(&ms.feed[warp], warp, lane, P.D);
+        constexpr int AHEAD = L::AHEAD;
+        sv::E4m3Feed<BF, DP, AHEAD> feed(&ms.feed[warp], s0 + L::R0, warp, lane, P.D);
         const int chunk = lane % CPR, sub = lane / CPR;
         const int own = E4 ? feed.own : warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot the lane keeps
         const int first = warp * RPI + sub;                                                // its row of the first copy
@@ -328,42 +330,50 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                     }
                 }
             } else {
-                // A unit is widened as the rows of the next one are asked for.  Buffer 0 is the keys', 1 the values'.
-                auto row = [&](int slot, int kv) {
-                    return slot < 0 ? sv::e4m3_none(slot == -2 && kv == 0) : (kv ? P.v + slot * P.v_slot : P.k + slot * P.k_slot) + g.h * P.D;
+                // The segment's units (keys and values of a tile in turn): while one is widened its place in the ring is
+                // filled with the one AHEAD units on.
+                const int units = 2 * (g.j1 - g.j0);
+                int slot = -1, x = 0;  // the slots of the unit to be asked for next, the x-th
+                auto next = [&] {
+                    if (x & 1) return;
+                    slot = check(g.j0 + x / 2, ahead);
+                    ahead = look(g.j0 + x / 2 + 1);
                 };
-                auto exponent = [&](int slot, int kv) {
-                    return slot < 0 ? 127 : (int)__ldg((kv ? P.v + slot * P.v_slot : P.k + slot * P.k_slot) + P.Hkv * P.D + g.h);
+                auto place = [&](int i) { feed.ask(x % AHEAD, i, x & 1 && slot == -2 ? -1 : slot, x & 1 ? P.v : P.k, x & 1 ? P.v_slot : P.k_slot, g.h * P.D); };
+                auto placed = [&](int count) {
+                    feed.asked(x % AHEAD, count, slot, x & 1 ? P.v : P.k, x & 1 ? P.v_slot : P.k_slot, P.Hkv * P.D + g.h);
+                    ++x;
                 };
-                auto unit = [&](int b, bool more) {
-                    if (!room()) return false;
-                    feed.widen(s0 + (u % NU) * L::UNIT, b, more, b ^ 1);
-                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
-                    ++u;
-                    return true;
-                };
-                int slot = check(g.j0, ahead), es[2] = {exponent(slot, 0), exponent(slot, 1)};
-                __syncwarp();
-                feed.put_row(0, row(slot, 0));
-                feed.put_row(1, row(slot, 1));
-                __syncwarp();
-                feed.load_all(0);
-                for (int j = g.j0; j < g.j1; ++j) {
-                    const bool more = j + 1 < g.j1;
-                    feed.put_scale(0, es[0]);
-                    ahead = look(j + 1);
-                    __syncwarp();
-                    if (!unit(0, true)) break;
-                    feed.put_scale(1, es[1]);
-                    if (more) {
-                        slot = check(j + 1, ahead);
-                        feed.put_row(0, row(slot, 0));
-                        es[0] = exponent(slot, 0);
-                        es[1] = exponent(slot, 1);
+                for (int a = 0; a < AHEAD; ++a) {
+                    if (x >= units) {
+                        feed.commit();
+                        continue;
                     }
-                    __syncwarp();
-                    if (!unit(1, more)) break;
-                    if (more) feed.put_row(1, row(slot, 1));
+                    next();
+#pragma unroll
+                    for (int i = 0; i < feed.ITER; ++i) place(i);
+                    placed(a);
+                }
+                for (int y = 0; y < units; ++y, ++u) {
+                    const bool more = x < units;
+                    if (more) next();
+                    feed.wait();
+                    if (!room()) break;
+                    feed.scales(y % AHEAD, lane);
+                    const uint32_t unit = s0 + (u % NU) * L::UNIT;
+                    if (more) {
+#pragma unroll
+                        for (int i = 0; i < feed.ITER; ++i) {
+                            feed.widen(unit, y % AHEAD, i);
+                            place(i);
+                        }
+                        placed(AHEAD - 1);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < feed.ITER; ++i) feed.widen(unit, y % AHEAD, i);
+                        feed.commit();
+                    }
+                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
                 }
             }
         }
@@ -813,7 +823,7 @@ static int g_sms[64];
 template <bool BF, int DP, bool E4>
 constexpr size_t smem_bytes()
 {
-    return Layout<DP>::M0 + sizeof(MiscOf<BF, DP, E4>);
+    return Layout<DP, E4>::M0 + sizeof(MiscOf<BF, DP, E4>);
 }
 
 template <bool BF, int DP, bool E4>

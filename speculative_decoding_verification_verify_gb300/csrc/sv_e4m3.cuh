@@ -87,83 +87,102 @@ struct E4m3Scale<false> {
     }
 };
 
-// What a lane reads where a row is not there: zeros, or NaN.
+// NaN's bits, a row of them.
 #define SV_NAN4 {0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu}
-static __device__ const uint4 g_e4m3_none[2][8] = {{}, {SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4}};
+static __device__ const uint4 g_e4m3_nan[8] = {SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN4};
 #undef SV_NAN4
-__device__ __forceinline__ const unsigned char *e4m3_none(bool nan) { return reinterpret_cast<const unsigned char *>(g_e4m3_none[nan]); }
 
-// A warpgroup's tiles of 128 rows from 8-bit rows to 16-bit units in shared memory (128-byte swizzle, halves of 64
-// values), through registers.  A warp has 32 rows of a tile, in ITER loads of RPI rows; each row's address and power
-// of two are worked out by one lane, and come to the lanes that read it through shared memory: a load is then two
-// additions.  (With a shuffle and a test for each, a tile's widening took half as long again.)
-template <bool BF, int DP>
+// A warpgroup's tiles of 128 rows, from the cache's 8-bit rows to 16-bit units in shared memory (128-byte swizzle,
+// halves of 64 values).  Rows come by asynchronous copies into a ring of R tiles and are widened from there: a thread
+// reads what it copied itself, so the ring needs no barriers, and R tiles are under way whatever the memory's latency.
+// (Rows loaded to registers a tile ahead: 430 us where this takes a fraction; a copy's arrival cannot be waited for
+// without waiting for those after it.)  A warp has 32 rows of a tile, in ITER copies of RPI rows; a row's slot and power
+// of two are one lane's.
+template <bool BF, int DP, int R>
 struct E4m3Feed {
     static constexpr int CPR = DP / 16, RPI = 32 / CPR, ITER = CPR;
+    static constexpr int TILE_BYTES = 128 * DP + 128 * 4;  // a tile of the ring: rows, then a word with each row's power of two
+    static constexpr int BYTES = R * TILE_BYTES;
     struct __align__(16) Smem {
-        const unsigned char *row[2][RPI][ITER];
-        uint16_t scale[2][RPI][ITER];
+        uint16_t scale[RPI][ITER];  // a warp's
     };
     Smem &sm;
-    int own, sub, mine_sub, mine_i;  // the row whose slot the lane keeps, of a warp's tile; its place
-    uint32_t to;
-    int offset;  // of the lane's chunk in a row; below 0: beyond the head
-    uint4 raw[ITER];
+    int own, sub, tid;  // the row whose slot the lane keeps, of a tile
+    uint32_t to, ring;
+    int offset;         // of the lane's chunk in a row; below 0: beyond the head
+    uint32_t shifts;    // where in their words the powers of two are, two bits for each tile under way, the oldest first
 
-    // `warp` of the warpgroup.  Eight lanes that store together have chunks of two rows: no bank twice.
-    __device__ __forceinline__ E4m3Feed(void *s, int warp, int lane, int D) : sm(*static_cast<Smem *>(s))
+    // `warp` of the warpgroup, whose ring it is.  Eight lanes that store together have chunks of two rows: no bank twice.
+    __device__ __forceinline__ E4m3Feed(void *s, uint32_t ring_at, int warp, int lane, int D)
+        : sm(*static_cast<Smem *>(s)), tid(warp * 32 + lane), ring(ring_at), shifts(0)
     {
         const int chunk = DP == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
         sub = DP == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2;
-        mine_sub = lane % RPI;
-        mine_i = lane / RPI;
-        own = warp * RPI + mine_sub + 4 * RPI * mine_i;
+        own = warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);
         const int first = warp * RPI + sub;
         to = (chunk >> 2) * 128 * 128 + first * 128 + (((2 * chunk & 7) ^ (first & 7)) << 4);
         offset = chunk * 16 < D ? chunk * 16 : -1;
     }
-    // The address of the lane's own row of a tile in buffer b: a head's values; its power of two.
-    __device__ __forceinline__ void put_row(int b, const unsigned char *at) { sm.row[b][mine_sub][mine_i] = at; }
-    __device__ __forceinline__ void put_scale(int b, int byte) { sm.scale[b][mine_sub][mine_i] = E4m3Scale<BF>::bits(byte); }
-    __device__ __forceinline__ void load(int b, int i)
+    static __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
     {
-        const unsigned char *at = sm.row[b][sub][i];
-        const unsigned char *const p = offset < 0 ? e4m3_none(false) : at + offset;
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(raw[i].x), "=r"(raw[i].y), "=r"(raw[i].z), "=r"(raw[i].w)
-                     : "l"(p));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
     }
-    __device__ __forceinline__ void load_all(int b)
+    // One of the copies of a tile into place r: `slot` is that of the lane's own row, below 0 where it is not there (zeros;
+    // -2: NaN), `head` the offset of the head's values in a row.
+    __device__ __forceinline__ void ask(int r, int i, int slot, const unsigned char *cache, uint64_t stride, int head)
     {
-#pragma unroll
-        for (int i = 0; i < ITER; ++i) load(b, i);
+        const int s = __shfl_sync(0xffffffffu, slot, i * RPI + sub);
+        const unsigned char *at = cache + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride + head;
+        if (s == -2) at = reinterpret_cast<const unsigned char *>(g_e4m3_nan);
+        copy16(ring + r * TILE_BYTES + i * 2048 + tid * 16, at + (offset < 0 ? 0 : offset), s != -1 && offset >= 0);
     }
-    // The loaded rows, with buffer b's powers of two, to a unit; where `more`, the rows of buffer `next` are asked for.
-    __device__ __forceinline__ void widen(uint32_t unit, int b, bool more, int next)
+    // Its powers of two, and the end of its copies; `count`: tiles under way before it.
+    __device__ __forceinline__ void asked(int r, int count, int slot, const unsigned char *cache, uint64_t stride, int at)
     {
-#pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const uint4 w = raw[i];
-            const E4m3Scale<BF> f(sm.scale[b][sub][i]);
-            if (more) load(next, i);
-            const uint32_t at = unit + to + i * 4 * RPI * 128;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(f(w.x)), "r"(f(w.x >> 16)), "r"(f(w.y)),
-                         "r"(f(w.y >> 16))
-                         : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16), "r"(f(w.z)), "r"(f(w.z >> 16)), "r"(f(w.w)),
-                         "r"(f(w.w >> 16))
-                         : "memory");
-        }
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ring + r * TILE_BYTES + 128 * DP + tid * 4),
+                     "l"(cache + (uint64_t)(uint32_t)(slot < 0 ? 0 : slot) * stride + (at & ~3)), "r"(slot < 0 ? 0 : 4)
+                     : "memory");
+        shifts |= (uint32_t)(at & 3) << 2 * count;
+        commit();
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // The oldest of the R tiles (or empty groups) is there.
+    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory"); }
+    // The powers of two of the tile in place r, before `widen`.
+    __device__ __forceinline__ void scales(int r, int lane)
+    {
+        uint32_t w;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(ring + r * TILE_BYTES + 128 * DP + tid * 4) : "memory");
+        __syncwarp();
+        sm.scale[lane % RPI][lane / RPI] = E4m3Scale<BF>::bits(w >> 8 * (shifts & 3) & 0xff);
+        shifts >>= 2;
+        __syncwarp();
+    }
+    __device__ __forceinline__ void widen(uint32_t unit, int r, int i)
+    {
+        uint4 w;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "r"(ring + r * TILE_BYTES + i * 2048 + tid * 16)
+                     : "memory");
+        const E4m3Scale<BF> f(sm.scale[sub][i]);
+        const uint32_t at = unit + to + i * 4 * RPI * 128;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(f(w.x)), "r"(f(w.x >> 16)), "r"(f(w.y)),
+                     "r"(f(w.y >> 16))
+                     : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16), "r"(f(w.z)), "r"(f(w.z >> 16)), "r"(f(w.w)),
+                     "r"(f(w.w >> 16))
+                     : "memory");
     }
 };
 
 // What a warp of it has in shared memory; nothing in a kernel of 16-bit rows.
-template <bool BF, int DP, bool E4>
+template <bool BF, int DP, int R, bool E4>
 struct E4m3FeedSmem {
-    using type = typename E4m3Feed<BF, DP>::Smem;
+    using type = typename E4m3Feed<BF, DP, R>::Smem;
 };
-template <bool BF, int DP>
-struct E4m3FeedSmem<BF, DP, false> {
+template <bool BF, int DP, int R>
+struct E4m3FeedSmem<BF, DP, R, false> {
     struct type {};
 };
 
