@@ -103,12 +103,14 @@ template <int NQ, int DP, bool E4>
 struct Layout {
     static constexpr int HALVES = DP / 64;
     static constexpr int UNIT = TILE * DP * 2;
-    // (8-bit rows: a unit of keys and one of values are enough, the rings before them have the tiles under way.)
-    static constexpr int NU = E4 ? 2 * 128 / DP : ctas_per_sm(NQ, E4) == 2 ? (DP == 64 ? 5 : 2) : 5 * 128 / DP;
-    static constexpr int AHEAD = 3 * 128 / DP, RING = E4 ? AHEAD * (128 * DP + 512) : 0;  // of keys, of values
+    // (8-bit rows: two units of keys and two of values, an even number for the two warpgroups that fill them; with one of
+    // each 195 us where two take 140.  The rings before them have the tiles under way.)
+    static constexpr int NU = E4 ? 4 * 128 / DP : ctas_per_sm(NQ, E4) == 2 ? (DP == 64 ? 5 : 2) : 5 * 128 / DP;
+    static constexpr int AHEAD = NQ == 64 ? (DP == 64 ? 3 : 1) : 2 * 128 / DP, RING = E4 ? AHEAD * (128 * DP + 512) : 0;  // of keys, of values
     static constexpr int QBYTES = NQ * DP * 2;
     static constexpr int QSTEP = QBYTES < 1024 ? 1024 : QBYTES;
-    static constexpr int PBYTES = TILE * 128;  // a row of 64 columns per position
+    static constexpr int PROW = E4 && NQ <= 32 ? 64 : 128;  // a row of 32 or 64 columns per position
+    static constexpr int PBYTES = TILE * PROW;
     static constexpr int Q0 = NU * UNIT, P0 = Q0 + 2 * QSTEP, R0 = P0 + PBYTES, M0 = R0 + 2 * RING;
     static constexpr int COLS = 3 * NQ <= 64 ? 64 : 3 * NQ <= 128 ? 128 : 256;  // TMEM columns
 };
@@ -482,20 +484,16 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                     if (!room()) break;
                     feed.scales(r, lane);
                     const uint32_t unit = s0 + (u % NU) * L::UNIT;
+                    feed.widen(unit, r);
+                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
                     if (more) {
 #pragma unroll
-                        for (int i = 0; i < feed.ITER; ++i) {
-                            feed.widen(unit, r, i);
-                            feed.ask(r, i, s, cache, stride, g.h * P.D);
-                        }
+                        for (int i = 0; i < feed.ITER; ++i) feed.ask(r, i, s, cache, stride, g.h * P.D);
                         feed.asked(r, AHEAD - 1, s, cache, stride, P.Hkv * P.D + g.h);
                         sought = false;
                     } else {
-#pragma unroll
-                        for (int i = 0; i < feed.ITER; ++i) feed.widen(unit, r, i);
                         --count;
                     }
-                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
                     u += 2;
                     r = r + 1 == AHEAD ? 0 : r + 1;
                     look(false);
@@ -508,7 +506,8 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             constexpr uint32_t ID_O = tc::instr_desc(BF, true, true, 128, NQ);
             const int dsteps = P.D / 16;
             const uint64_t kd = tc::smem_desc(s0, 0, 1024), qd = tc::smem_desc(s0 + L::Q0, 0, 1024);
-            const uint64_t vd = tc::smem_desc(s0, HALVES > 1 ? TILE * 128 : 0, 1024), pd = tc::smem_desc(s0 + L::P0, 0, 1024);
+            const uint64_t vd = tc::smem_desc(s0, HALVES > 1 ? TILE * 128 : 0, 1024), pd = L::PROW == 64 ? tc::smem_desc64(s0 + L::P0, 0, 512) : tc::smem_desc(s0 + L::P0, 0, 1024);
+            constexpr int PSTEP = L::PROW;  // 16 positions
             int k = 0, seg = -1;       // tiles whose scores are under way
             int wk = 0, wsteps = 0, wstart = 0;  // tiles weighed; the waiting one's
             bool ok = true;
@@ -525,10 +524,10 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 if (wsteps == 8) {  // straight-line code for whole tiles
                     tc::mma_f16(tmem + 2 * NQ, a, pd, ID_O, !wstart);
 #pragma unroll
-                    for (int i = 1; i < 8; ++i) tc::mma_f16(tmem + 2 * NQ, a + i * 128, pd + i * 128, ID_O, true);
+                    for (int i = 1; i < 8; ++i) tc::mma_f16(tmem + 2 * NQ, a + i * 128, pd + i * PSTEP, ID_O, true);
                 } else {
                     for (int i = 0; i < wsteps; ++i)
-                        tc::mma_f16(tmem + 2 * NQ, a + i * 128, pd + i * 128, ID_O, !wstart || i > 0);
+                        tc::mma_f16(tmem + 2 * NQ, a + i * 128, pd + i * PSTEP, ID_O, !wstart || i > 0);
                 }
                 tc::commit(tc::smem_u32(&ms.empty[u % NU]));
                 tc::commit(tc::smem_u32(&ms.pvdone));
@@ -886,7 +885,8 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                             raw[c / 2] = sv::f2_add(raw[c / 2], sv::f2(a, b));
                             rnd[c / 2] = sv::f2_add(rnd[c / 2], sv::f2(r.x, r.y));
                         }
-                        *reinterpret_cast<uint4 *>(smem + L::P0 + t * 128 + (((col0 / 8 + ch) ^ (t & 7)) << 4)) =
+                        *reinterpret_cast<uint4 *>(smem + L::P0 + t * L::PROW +
+                                                    (((col0 / 8 + ch) ^ (L::PROW == 64 ? t >> 1 & 3 : t & 7)) << 4)) =
                             make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
                     if (wg < 2 && special && pos >= g.c && pos < len) {

@@ -361,19 +361,15 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                     if (!room()) break;
                     feed.scales(y % AHEAD, lane);
                     const uint32_t unit = s0 + (u % NU) * L::UNIT;
+                    feed.widen(unit, y % AHEAD);
+                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
                     if (more) {
 #pragma unroll
-                        for (int i = 0; i < feed.ITER; ++i) {
-                            feed.widen(unit, y % AHEAD, i);
-                            place(i);
-                        }
+                        for (int i = 0; i < feed.ITER; ++i) place(i);
                         placed(AHEAD - 1);
                     } else {
-#pragma unroll
-                        for (int i = 0; i < feed.ITER; ++i) feed.widen(unit, y % AHEAD, i);
                         feed.commit();
                     }
-                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
                 }
             }
         }

@@ -158,21 +158,33 @@ struct E4m3Feed {
         shifts >>= 2;
         __syncwarp();
     }
-    __device__ __forceinline__ void widen(uint32_t unit, int r, int i)
+    // (All of a thread's rows are read before the first is stored: the reads' latency is paid once.)
+    __device__ __forceinline__ void widen(uint32_t unit, int r)
     {
-        uint4 w;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                     : "r"(ring + r * TILE_BYTES + i * 2048 + tid * 16)
-                     : "memory");
-        const E4m3Scale<BF> f(sm.scale[sub][i]);
-        const uint32_t at = unit + to + i * 4 * RPI * 128;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(f(w.x)), "r"(f(w.x >> 16)), "r"(f(w.y)),
-                     "r"(f(w.y >> 16))
-                     : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16), "r"(f(w.z)), "r"(f(w.z >> 16)), "r"(f(w.w)),
-                     "r"(f(w.w >> 16))
-                     : "memory");
+        uint4 w[ITER];
+#pragma unroll
+        for (int i = 0; i < ITER; ++i)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                         : "r"(ring + r * TILE_BYTES + i * 2048 + tid * 16)
+                         : "memory");
+        union {
+            uint16_t s[ITER];
+            uint32_t w[ITER / 2];
+        } f;
+#pragma unroll
+        for (int i = 0; i < ITER / 2; ++i) f.w[i] = reinterpret_cast<const uint32_t *>(sm.scale[sub])[i];
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const E4m3Scale<BF> g(f.s[i]);
+            const uint32_t at = unit + to + i * 4 * RPI * 128;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(g(w[i].x)), "r"(g(w[i].x >> 16)), "r"(g(w[i].y)),
+                         "r"(g(w[i].y >> 16))
+                         : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16), "r"(g(w[i].z)), "r"(g(w[i].z >> 16)), "r"(g(w[i].w)),
+                         "r"(g(w[i].w >> 16))
+                         : "memory");
+        }
     }
 };
 

@@ -163,6 +163,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
            2ull << 61;
 }
 
+// The same under the 64-byte swizzle: rows of 64 bytes, blocks of 32 elements.
+__device__ __forceinline__ uint64_t smem_desc64(uint32_t addr, uint32_t lbo, uint32_t sbo)
+{
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 |
+           4ull << 61;
+}
+
 // fp32 accumulators, A and B of one 16-bit type; *_mn: contiguous along M / N instead of K.
 __device__ __forceinline__ constexpr uint32_t instr_desc(bool bf16, bool a_mn, bool b_mn, int m, int n)
 {
