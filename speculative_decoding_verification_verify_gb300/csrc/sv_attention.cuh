@@ -61,6 +61,7 @@ constexpr int MAX_SMS = 192;  // the workspace has room for two parts per CTA
 constexpr int COUNTERS = 2 * MAX_SMS;
 constexpr int FLAGS = 16;     // bad-slot flags: more than the segments the ring can hold
 constexpr int SEGS = 8;       // segments listed ahead
+constexpr int SLOTS = 4;      // tiles whose slots are listed ahead (8-bit rows)
 constexpr float SLACK = 8.f;  // log2 of how much a weight may pass the reference's
 constexpr float FAR = 0x1p24f;  // of a reference times the scale
 // log2 of the reference's weight.
@@ -156,6 +157,12 @@ struct Misc {
     Join join[2];
     int joins[2];
     int8_t par[sv::MAX_TREE];
+    // 8-bit rows: of the tiles ahead, the rows' slots, the key head (-1: no more), the rows that there are, the segment.
+    struct __align__(16) Slots {
+        int slot[TILE];
+        int h, left, seg, pad;
+    } slots[E4 ? SLOTS : 1];
+    uint64_t slotfull[SLOTS], slotempty[SLOTS];
     typename sv::E4m3FeedSmem<BF, DP, Layout<NQ, DP, E4>::AHEAD, E4>::type feed[8];
 };
 
@@ -277,7 +284,11 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
         }
         for (int i = 0; i < SEGS; ++i) {
             tc::bar_init(tc::smem_u32(&ms.segfull[i]), 1);
-            tc::bar_init(tc::smem_u32(&ms.segempty[i]), NT / 32 - 1);  // warps but the one that lists
+            tc::bar_init(tc::smem_u32(&ms.segempty[i]), NT / 32 - (E4 ? 9 : 1));  // warps but the one that lists; 8-bit copies have the slots' list
+        }
+        for (int i = 0; E4 && i < SLOTS; ++i) {
+            tc::bar_init(tc::smem_u32(&ms.slotfull[i]), 33);
+            tc::bar_init(tc::smem_u32(&ms.slotempty[i]), 8);
         }
         tc::bar_init(tc::smem_u32(&ms.pfull), 128 * WG);
         tc::bar_init(tc::smem_u32(&ms.pvdone), 1);
@@ -357,16 +368,74 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
     };
 
     if (t1 > t0) {
-        if (warp < 4 || (E4 && warp >= 8 + 4 * WG)) {
-            const int cw = E4 ? warp & 3 : warp;  // the warp of its warpgroup
+        if (E4 && (warp < 4 || warp >= 8 + 4 * WG)) {
+            // ---- 8-bit tiles into shared memory ---------------------------------------------
+            // One warpgroup has the keys, the other the values.  While a tile is widened its place in the ring is
+            // filled with the one AHEAD tiles on, whose slots are listed.
+            constexpr int AHEAD = L::AHEAD;
+            using Feed = sv::E4m3Feed<BF, DP, AHEAD>;
+            const int cw = warp & 3, kv = warp < 4 ? 0 : 1;
+            Feed feed(&ms.feed[4 * kv + cw], s0 + L::R0 + kv * L::RING, cw, lane, P.D);
+            const unsigned char *const cache = kv ? P.v : P.k;
+            const uint64_t stride = kv ? P.v_slot : P.k_slot;
+            int r = 0, count = 0, n = 0, u = kv;  // the oldest tile's place; tiles under way; tiles asked for; its unit
+            bool ok = true, last = false;
+            // The next tile's slots, into a place: 1, or 0 when there are none, 2 when they are not listed yet.
+            auto ask = [&](int at, bool block) {
+                if (last) return 0;
+                const uint32_t bar = tc::smem_u32(&ms.slotfull[n % SLOTS]);
+                const bool there = block ? tc::bar_wait(bar, (n / SLOTS) & 1, abort) : tc::bar_test(bar, (n / SLOTS) & 1);
+                if (!__all_sync(0xffffffffu, there)) return block ? 0 : 2;
+                const auto &list = ms.slots[n % SLOTS];
+                const int h = list.h, left = list.left;
+                last = h < 0;
+                if (last) return 0;
+                int slot[Feed::ITER];
+                const int mine = list.slot[feed.own];
+#pragma unroll
+                for (int i = 0; i < Feed::ITER; ++i) slot[i] = list.slot[feed.row(i)];
+                const bool fine = (unsigned)mine < (unsigned)P.num_slots;
+                if (feed.own < left && !fine)
+#pragma unroll
+                    for (int i = 0; i < WG; ++i) *(volatile int *)&ms.bad[i][list.seg % FLAGS] = 1;
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(tc::smem_u32(&ms.slotempty[n % SLOTS]));
+#pragma unroll
+                for (int i = 0; i < Feed::ITER; ++i) {
+                    const bool in = feed.row(i) < left && (unsigned)slot[i] < (unsigned)P.num_slots;
+                    feed.ask(at, i, in ? slot[i] : -1, cache, stride, h * P.D);
+                }
+                feed.asked(at, count, feed.own < left && fine ? mine : -1, cache, stride, P.Hkv * P.D + h);
+                ++n;
+                ++count;
+                return 1;
+            };
+            for (;;) {
+                // The places without a tile: all at the beginning, later where slots were not listed in time.
+                while (count < AHEAD && ask((r + count) % AHEAD, count == 0) == 1) {}
+                if (count == 0) break;
+                for (int i = count; i < AHEAD; ++i) feed.commit();  // (what is waited for is counted in groups)
+                feed.wait();
+                if (u >= NU) ok = __all_sync(0xffffffffu, tc::bar_wait(tc::smem_u32(&ms.empty[u % NU]), (u / NU + 1) & 1, abort));
+                if (!ok) break;
+                feed.scales(r, lane);
+                feed.widen(s0 + (u % NU) * L::UNIT, r);
+                tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
+                u += 2;
+                --count;
+                const int at = r;
+                r = r + 1 == AHEAD ? 0 : r + 1;
+                if (count == AHEAD - 1) ask(at, false);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (!E4 && warp < 4) {
+            const int cw = warp;
             // ---- tiles into shared memory -------------------------------------------------
             // A row's CPR chunks go to CPR lanes, 32 / CPR rows to a warp's copy.  A lane keeps the
             // slot of one of its warp's 32 rows; they are read one tile ahead of the copies.
             [[maybe_unused]] constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
-            constexpr int AHEAD = L::AHEAD;
-            sv::E4m3Feed<BF, DP, AHEAD> feed(&ms.feed[warp < 4 ? warp : 4 + cw], s0 + L::R0 + (warp < 4 ? 0 : L::RING), cw, lane, P.D);
             const int chunk = lane % CPR, sub = lane / CPR;
-            const int own = E4 ? feed.own : cw * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot it keeps
+            const int own = cw * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot it keeps
             const int first = cw * RPI + sub;                                  // its row of the first copy
             const bool wide = chunk * 8 < P.D;
             Seg g = {};
@@ -391,7 +460,6 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 slot = -1;
                 if (pos < g.c + g.nn) {
                     const int64_t at = (int64_t)g.b * P.max_pos + pos;
-                    if (E4 && pos + 2 * TILE < g.c + g.nn) asm volatile("prefetch.global.L2 [%0];" ::"l"(P.slot_table + at + 2 * TILE));
                     slot = SV_INB(at, (int64_t)P.B * P.max_pos, 1103) ? P.slot_table[at] : -1;
                 }
                 return 1;
@@ -405,7 +473,6 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 }
                 return slot;
             };
-            if constexpr (E4) u = warp < 4 ? 0 : 1;
             // A unit of the ring may be written again once its products are done.
             auto room = [&] {
                 if (u >= NU) {
@@ -414,7 +481,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 }
                 return ok;
             };
-            if constexpr (!E4) {
+            {
                 const uint32_t to = (chunk >> 3) * TILE * 128 + first * 128 + (((chunk & 7) ^ (first & 7)) << 4);
                 for (int found = seek(true); found == 1 && ok;) {
                     const int slots = check(j * TILE + own >= g.c + g.nn);
@@ -449,54 +516,6 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                                      : "memory");
                     }
                     if (found == 2 && ok) found = seek(true);
-                }
-            } else {
-                // One warpgroup has the keys, the other the values.  While a tile is widened its place in the ring is
-                // filled with the one AHEAD tiles on, whose slots were read the tile before.
-                const int kv = u;
-                const unsigned char *const cache = kv ? P.v : P.k;
-                const uint64_t stride = kv ? P.v_slot : P.k_slot;
-                bool sought = false, last = false;
-                int r = 0, count = 0;  // the oldest tile's place; tiles under way
-                auto look = [&](bool block) {
-                    if (sought || last) return;
-                    const int found = seek(block);
-                    sought = found == 1;
-                    last = found == 0;
-                };
-                for (;;) {
-                    // The places without a tile: all at the beginning, later where a segment was not listed in time.
-                    while (count < AHEAD) {
-                        look(count == 0);
-                        if (!sought) break;
-                        sought = false;
-                        const int s = check(j * TILE + own >= g.c + g.nn), at = (r + count) % AHEAD;
-#pragma unroll
-                        for (int i = 0; i < feed.ITER; ++i) feed.ask(at, i, s, cache, stride, g.h * P.D);
-                        feed.asked(at, count++, s, cache, stride, P.Hkv * P.D + g.h);
-                    }
-                    if (count == 0) break;
-                    for (int i = count; i < AHEAD; ++i) feed.commit();  // (what is waited for is counted in groups)
-                    look(false);
-                    const bool more = sought && count == AHEAD;
-                    const int s = more ? check(j * TILE + own >= g.c + g.nn) : -1;
-                    feed.wait();
-                    if (!room()) break;
-                    feed.scales(r, lane);
-                    const uint32_t unit = s0 + (u % NU) * L::UNIT;
-                    feed.widen(unit, r);
-                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
-                    if (more) {
-#pragma unroll
-                        for (int i = 0; i < feed.ITER; ++i) feed.ask(r, i, s, cache, stride, g.h * P.D);
-                        feed.asked(r, AHEAD - 1, s, cache, stride, P.Hkv * P.D + g.h);
-                        sought = false;
-                    } else {
-                        --count;
-                    }
-                    u += 2;
-                    r = r + 1 == AHEAD ? 0 : r + 1;
-                    look(false);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -605,6 +624,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             // ---- the run's segments ----------------------------------------------------------
             // The lengths of 32 requests are read at a time.
             int b = ms.begin_b, base = b, c = 0, nn = 0, n = 0;
+            [[maybe_unused]] int seg = -1, tiles = 0;
             if (b + lane < P.B) lengths(P, b + lane, c, nn);
             int64_t at = ms.begin_base;  // the cost before the item
             bool ok = true;
@@ -620,6 +640,30 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 }
                 __syncwarp();
                 ++n;
+            };
+            // 8-bit rows: a tile's slots, ahead of its copies.
+            auto list = [&](int h, int left, int64_t at) {
+                if (tiles >= SLOTS)
+                    ok = __all_sync(0xffffffffu, tc::bar_wait(tc::smem_u32(&ms.slotempty[tiles % SLOTS]), (tiles / SLOTS + 1) & 1, abort));
+                if (!ok) return;
+                auto &list = ms.slots[tiles % SLOTS];
+                const uint32_t bar = tc::smem_u32(&ms.slotfull[tiles % SLOTS]);
+#pragma unroll
+                for (int i = 0; i < TILE / 32; ++i) {
+                    const int row = lane + 32 * i;
+                    const bool in = row < left && SV_INB(at + row, (int64_t)P.B * P.max_pos, 1103);
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(&list.slot[row])),
+                                 "l"(P.slot_table + (in ? at + row : 0)), "r"(in ? 4 : 0)
+                                 : "memory");
+                }
+                if (lane == 0) {
+                    list.h = h;
+                    list.left = left;
+                    list.seg = seg;
+                    tc::bar_arrive(bar);
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+                ++tiles;
             };
             Seg g = {};
             bool first = true;
@@ -656,11 +700,18 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                         g.part = 2 * cta + (run == g.c0);
                     }
                     put(g);
+                    if (E4 && !g.kind) {
+                        ++seg;
+                        for (int y = g.j0; y < g.j1 && ok; ++y)
+                            list(g.h, g.c + g.nn - y * TILE, (int64_t)g.b * P.max_pos + (int64_t)y * TILE);
+                    }
                 }
                 ++b;
             }
             g.kind = 3;
             if (ok) put(g);
+            if (E4 && ok) list(-1, 0, 0);
+            if (E4) asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp < 8) {
             // ---- queries and the tree's mask -----------------------------------------------
             const int t = tid - 192;

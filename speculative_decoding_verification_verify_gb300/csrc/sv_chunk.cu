@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                     slot = check(g.j0 + x / 2, ahead);
                     ahead = look(g.j0 + x / 2 + 1);
                 };
-                auto place = [&](int i) { feed.ask(x % AHEAD, i, x & 1 && slot == -2 ? -1 : slot, x & 1 ? P.v : P.k, x & 1 ? P.v_slot : P.k_slot, g.h * P.D); };
+                auto place = [&](int i) { const int s = __shfl_sync(0xffffffffu, slot, i * feed.RPI + feed.sub); feed.ask(x % AHEAD, i, x & 1 && s == -2 ? -1 : s, x & 1 ? P.v : P.k, x & 1 ? P.v_slot : P.k_slot, g.h * P.D); };
                 auto placed = [&](int count) {
                     feed.asked(x % AHEAD, count, slot, x & 1 ? P.v : P.k, x & 1 ? P.v_slot : P.k_slot, P.Hkv * P.D + g.h);
                     ++x;

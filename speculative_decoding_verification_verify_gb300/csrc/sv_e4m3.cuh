@@ -127,14 +127,15 @@ struct E4m3Feed {
     {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
     }
-    // One of the copies of a tile into place r: `slot` is that of the lane's own row, below 0 where it is not there (zeros;
-    // -2: NaN), `head` the offset of the head's values in a row.
+    // The tile's row of the lane's i-th copy.
+    __device__ __forceinline__ int row(int i) const { return (to >> 7 & 127) + 4 * RPI * i; }
+    // A copy of a tile into place r: `slot` is its row's, below 0 where it is not there (zeros; -2: NaN), `head` the offset of
+    // the head's values in a row.
     __device__ __forceinline__ void ask(int r, int i, int slot, const unsigned char *cache, uint64_t stride, int head)
     {
-        const int s = __shfl_sync(0xffffffffu, slot, i * RPI + sub);
-        const unsigned char *at = cache + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride + head;
-        if (s == -2) at = reinterpret_cast<const unsigned char *>(g_e4m3_nan);
-        copy16(ring + r * TILE_BYTES + i * 2048 + tid * 16, at + (offset < 0 ? 0 : offset), s != -1 && offset >= 0);
+        const unsigned char *at = cache + (uint64_t)(uint32_t)(slot < 0 ? 0 : slot) * stride + head;
+        if (slot == -2) at = reinterpret_cast<const unsigned char *>(g_e4m3_nan);
+        copy16(ring + r * TILE_BYTES + i * 2048 + tid * 16, at + (offset < 0 ? 0 : offset), slot != -1 && offset >= 0);
     }
     // Its powers of two, and the end of its copies; `count`: tiles under way before it.
     __device__ __forceinline__ void asked(int r, int count, int slot, const unsigned char *cache, uint64_t stride, int at)
