@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             const int cw = warp & 3, kv = warp < 4 ? 0 : 1;
             Feed feed(&ms.feed[4 * kv + cw], s0 + L::R0 + kv * L::RING, cw, lane, P.D);
             const unsigned char *const cache = kv ? P.v : P.k;
-            const uint64_t stride = kv ? P.v_slot : P.k_slot;
+            const uint32_t stride = kv ? P.v_slot : P.k_slot;
             int r = 0, count = 0, n = 0, u = kv;  // the oldest tile's place; tiles under way; tiles asked for; its unit
             bool ok = true, last = false;
             // The next tile's slots, into a place: 1, or 0 when there are none, 2 when they are not listed yet.
@@ -390,22 +390,19 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 const int h = list.h, left = list.left;
                 last = h < 0;
                 if (last) return 0;
-                int slot[Feed::ITER];
                 const int mine = list.slot[feed.own];
-#pragma unroll
-                for (int i = 0; i < Feed::ITER; ++i) slot[i] = list.slot[feed.row(i)];
-                const bool fine = (unsigned)mine < (unsigned)P.num_slots;
-                if (feed.own < left && !fine)
+                const bool fine = (unsigned)mine < (unsigned)P.num_slots, in = feed.own < left;
+                if (in && !fine)
 #pragma unroll
                     for (int i = 0; i < WG; ++i) *(volatile int *)&ms.bad[i][list.seg % FLAGS] = 1;
+                const bool whole = __all_sync(0xffffffffu, in && fine);
+                feed.ask(at, whole, cache + h * P.D, stride, [&](int i) {
+                    const int s = list.slot[feed.row(i)];
+                    return whole || (feed.row(i) < left && (unsigned)s < (unsigned)P.num_slots) ? s : -1;
+                });
+                feed.asked(at, count, in && fine ? mine : -1, cache, stride, P.Hkv * P.D + h);
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem_u32(&ms.slotempty[n % SLOTS]));
-#pragma unroll
-                for (int i = 0; i < Feed::ITER; ++i) {
-                    const bool in = feed.row(i) < left && (unsigned)slot[i] < (unsigned)P.num_slots;
-                    feed.ask(at, i, in ? slot[i] : -1, cache, stride, h * P.D);
-                }
-                feed.asked(at, count, feed.own < left && fine ? mine : -1, cache, stride, P.Hkv * P.D + h);
                 ++n;
                 ++count;
                 return 1;

@@ -339,7 +339,13 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                     slot = check(g.j0 + x / 2, ahead);
                     ahead = look(g.j0 + x / 2 + 1);
                 };
-                auto place = [&](int i) { const int s = __shfl_sync(0xffffffffu, slot, i * feed.RPI + feed.sub); feed.ask(x % AHEAD, i, x & 1 && s == -2 ? -1 : s, x & 1 ? P.v : P.k, x & 1 ? P.v_slot : P.k_slot, g.h * P.D); };
+                auto place = [&] {
+                    const bool whole = __all_sync(0xffffffffu, slot >= 0);
+                    feed.ask(x % AHEAD, whole, (x & 1 ? P.v : P.k) + g.h * P.D, (uint32_t)(x & 1 ? P.v_slot : P.k_slot), [&](int i) {
+                        const int s = __shfl_sync(0xffffffffu, slot, i * feed.RPI + feed.sub);
+                        return x & 1 && s == -2 ? -1 : s;
+                    });
+                };
                 auto placed = [&](int count) {
                     feed.asked(x % AHEAD, count, slot, x & 1 ? P.v : P.k, x & 1 ? P.v_slot : P.k_slot, P.Hkv * P.D + g.h);
                     ++x;
@@ -350,8 +356,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                         continue;
                     }
                     next();
-#pragma unroll
-                    for (int i = 0; i < feed.ITER; ++i) place(i);
+                    place();
                     placed(a);
                 }
                 for (int y = 0; y < units; ++y, ++u) {
@@ -364,8 +369,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                     feed.widen(unit, y % AHEAD);
                     tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
                     if (more) {
-#pragma unroll
-                        for (int i = 0; i < feed.ITER; ++i) place(i);
+                        place();
                         placed(AHEAD - 1);
                     } else {
                         feed.commit();

@@ -110,6 +110,7 @@ struct E4m3Feed {
     int own, sub, tid;  // the row whose slot the lane keeps, of a tile
     uint32_t to, ring;
     int offset;         // of the lane's chunk in a row; below 0: beyond the head
+    bool full;          // no lane's is
     uint32_t shifts;    // where in their words the powers of two are, two bits for each tile under way, the oldest first
 
     // `warp` of the warpgroup, whose ring it is.  Eight lanes that store together have chunks of two rows: no bank twice.
@@ -122,26 +123,41 @@ struct E4m3Feed {
         const int first = warp * RPI + sub;
         to = (chunk >> 2) * 128 * 128 + first * 128 + (((2 * chunk & 7) ^ (first & 7)) << 4);
         offset = chunk * 16 < D ? chunk * 16 : -1;
-    }
-    static __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
-    {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+        full = D == DP;
     }
     // The tile's row of the lane's i-th copy.
     __device__ __forceinline__ int row(int i) const { return (to >> 7 & 127) + 4 * RPI * i; }
-    // A copy of a tile into place r: `slot` is its row's, below 0 where it is not there (zeros; -2: NaN), `head` the offset of
-    // the head's values in a row.
-    __device__ __forceinline__ void ask(int r, int i, int slot, const unsigned char *cache, uint64_t stride, int head)
+    // The copies of a tile into place r, of rows whose slots are `slots(i)`: `whole` where all of the warp's 32 rows are
+    // there, else below 0 where one is not (zeros; -2: NaN).  `cache` is where the head's values of slot 0 are.
+    template <class Slots>
+    __device__ __forceinline__ void ask(int r, bool whole, const unsigned char *cache, uint32_t stride, Slots slots)
     {
-        const unsigned char *at = cache + (uint64_t)(uint32_t)(slot < 0 ? 0 : slot) * stride + head;
-        if (slot == -2) at = reinterpret_cast<const unsigned char *>(g_e4m3_nan);
-        copy16(ring + r * TILE_BYTES + i * 2048 + tid * 16, at + (offset < 0 ? 0 : offset), slot != -1 && offset >= 0);
+        const uint32_t dst = ring + r * TILE_BYTES + tid * 16;
+        // (The same way for all lanes of a warp: `slots` may exchange them.)
+        if (whole && full) {
+            const unsigned char *const at = cache + offset;
+#pragma unroll
+            for (int i = 0; i < ITER; ++i)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 2048), "l"(at + (uint64_t)(uint32_t)slots(i) * stride)
+                             : "memory");
+        } else {
+#pragma unroll 2
+            for (int i = 0; i < ITER; ++i) {
+                const int s = slots(i);
+                const unsigned char *at = s == -2 ? reinterpret_cast<const unsigned char *>(g_e4m3_nan)
+                                                  : cache + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 2048), "l"(at + (offset < 0 ? 0 : offset)),
+                             "r"(s != -1 && offset >= 0 ? 16 : 0)
+                             : "memory");
+            }
+        }
     }
-    // Its powers of two, and the end of its copies; `count`: tiles under way before it.
-    __device__ __forceinline__ void asked(int r, int count, int slot, const unsigned char *cache, uint64_t stride, int at)
+    // Its powers of two (`slot`: the lane's own row's, below 0 where it is not there), `at` bytes into a slot of `cache`, and
+    // the end of its copies; `count`: tiles under way before it.
+    __device__ __forceinline__ void asked(int r, int count, int slot, const unsigned char *cache, uint32_t stride, int at)
     {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ring + r * TILE_BYTES + 128 * DP + tid * 4),
-                     "l"(cache + (uint64_t)(uint32_t)(slot < 0 ? 0 : slot) * stride + (at & ~3)), "r"(slot < 0 ? 0 : 4)
+                     "l"(cache + (at & ~3) + (uint64_t)(uint32_t)(slot < 0 ? 0 : slot) * stride), "r"(slot < 0 ? 0 : 4)
                      : "memory");
         shifts |= (uint32_t)(at & 3) << 2 * count;
         commit();
