@@ -73,8 +73,11 @@ constexpr int COST_TILE = 2, COST_SEGMENT = 4;
 // Warpgroups of the softmax: two hold 16 columns a thread at most, and so do four where there are 64 columns
 // (with 32 a thread: one tree of 16 over 131000 positions 105.6 us against 102.7).
 __host__ __device__ constexpr int groups(int nq) { return nq == 64 ? 4 : 2; }
-// (8-bit rows: a warpgroup more of copies, behind the softmax's.)
-__host__ __device__ constexpr int threads(int nq, bool e4) { return 256 + 128 * groups(nq) + (e4 ? 128 : 0); }
+// (8-bit rows: a warpgroup for keys and one for values in a team, the first of them where the 16-bit copies are, the
+// others behind the softmax's.  A warp's way through a tile is some 3500 clocks; two teams are all the threads that there
+// are registers for.)
+__host__ __device__ constexpr int teams(int nq) { return nq == 64 ? 1 : 2; }
+__host__ __device__ constexpr int threads(int nq, bool e4) { return 256 + 128 * groups(nq) + (e4 ? 256 * teams(nq) - 128 : 0); }
 // CTAs that an SM holds.  With at most 8 columns a thread, 64 registers nearly do (32 bytes spilled), and one CTA
 // works while the other is between segments: 96 requests of 12 heads of 64 take 44.4 us against 52.4, 128
 // requests of up to 504 positions (8 key heads of 128) 30.2 against 30.7.  Two units of 128 dimensions are then all
@@ -107,12 +110,12 @@ struct Layout {
     // (8-bit rows: two units of keys and two of values, an even number for the two warpgroups that fill them; with one of
     // each 195 us where two take 140.  The rings before them have the tiles under way.)
     static constexpr int NU = E4 ? 4 * 128 / DP : ctas_per_sm(NQ, E4) == 2 ? (DP == 64 ? 5 : 2) : 5 * 128 / DP;
-    static constexpr int AHEAD = NQ == 64 ? (DP == 64 ? 3 : 1) : 2 * 128 / DP, RING = E4 ? AHEAD * (128 * DP + 512) : 0;  // of keys, of values
+    static constexpr int AHEAD = NQ == 64 ? (DP == 64 ? 3 : 1) : 128 / DP, RING = E4 ? AHEAD * (128 * DP + 512) : 0;  // of keys, of values
     static constexpr int QBYTES = NQ * DP * 2;
     static constexpr int QSTEP = QBYTES < 1024 ? 1024 : QBYTES;
     static constexpr int PROW = E4 && NQ <= 32 ? 64 : 128;  // a row of 32 or 64 columns per position
     static constexpr int PBYTES = TILE * PROW;
-    static constexpr int Q0 = NU * UNIT, P0 = Q0 + 2 * QSTEP, R0 = P0 + PBYTES, M0 = R0 + 2 * RING;
+    static constexpr int Q0 = NU * UNIT, P0 = Q0 + 2 * QSTEP, R0 = P0 + PBYTES, M0 = R0 + 2 * teams(NQ) * RING;
     static constexpr int COLS = 3 * NQ <= 64 ? 64 : 3 * NQ <= 128 ? 128 : 256;  // TMEM columns
 };
 
@@ -163,7 +166,7 @@ struct Misc {
         int h, left, seg, pad;
     } slots[E4 ? SLOTS : 1];
     uint64_t slotfull[SLOTS], slotempty[SLOTS];
-    typename sv::E4m3FeedSmem<BF, DP, Layout<NQ, DP, E4>::AHEAD, E4>::type feed[8];
+    typename sv::E4m3FeedSmem<BF, DP, Layout<NQ, DP, E4>::AHEAD, E4>::type feed[8 * teams(NQ)];
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
         }
         for (int i = 0; i < SEGS; ++i) {
             tc::bar_init(tc::smem_u32(&ms.segfull[i]), 1);
-            tc::bar_init(tc::smem_u32(&ms.segempty[i]), NT / 32 - (E4 ? 9 : 1));  // warps but the one that lists; 8-bit copies have the slots' list
+            tc::bar_init(tc::smem_u32(&ms.segempty[i]), NT / 32 - (E4 ? 8 * teams(NQ) + 1 : 1));  // warps but the one that lists; 8-bit copies have the slots' list
         }
         for (int i = 0; E4 && i < SLOTS; ++i) {
             tc::bar_init(tc::smem_u32(&ms.slotfull[i]), 33);
@@ -370,15 +373,16 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
     if (t1 > t0) {
         if (E4 && (warp < 4 || warp >= 8 + 4 * WG)) {
             // ---- 8-bit tiles into shared memory ---------------------------------------------
-            // One warpgroup has the keys, the other the values.  While a tile is widened its place in the ring is
-            // filled with the one AHEAD tiles on, whose slots are listed.
+            // Warpgroups have the keys and the values in turn, two teams of two every other tile.  While a tile is widened
+            // its place in the warpgroup's ring is filled with its next.
             constexpr int AHEAD = L::AHEAD;
             using Feed = sv::E4m3Feed<BF, DP, AHEAD>;
-            const int cw = warp & 3, kv = warp < 4 ? 0 : 1;
-            Feed feed(&ms.feed[4 * kv + cw], s0 + L::R0 + kv * L::RING, cw, lane, P.D);
+            constexpr int TEAMS = teams(NQ);
+            const int cw = warp & 3, wg = warp < 4 ? 0 : (warp - 4 - 4 * WG) >> 2, kv = wg & 1;
+            Feed feed(&ms.feed[4 * wg + cw], s0 + L::R0 + wg * L::RING, cw, lane, P.D);
             const unsigned char *const cache = kv ? P.v : P.k;
             const uint32_t stride = kv ? P.v_slot : P.k_slot;
-            int r = 0, count = 0, n = 0, u = kv;  // the oldest tile's place; tiles under way; tiles asked for; its unit
+            int r = 0, count = 0, n = wg >> 1, u = wg;  // the oldest tile's place; tiles under way; the next to ask for; the oldest's unit
             bool ok = true, last = false;
             // The next tile's slots, into a place: 1, or 0 when there are none, 2 when they are not listed yet.
             auto ask = [&](int at, bool block) {
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 feed.asked(at, count, in && fine ? mine : -1, cache, stride, P.Hkv * P.D + h);
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem_u32(&ms.slotempty[n % SLOTS]));
-                ++n;
+                n += TEAMS;
                 ++count;
                 return 1;
             };
@@ -413,16 +417,17 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 if (count == 0) break;
                 for (int i = count; i < AHEAD; ++i) feed.commit();  // (what is waited for is counted in groups)
                 feed.wait();
-                if (u >= NU) ok = __all_sync(0xffffffffu, tc::bar_wait(tc::smem_u32(&ms.empty[u % NU]), (u / NU + 1) & 1, abort));
-                if (!ok) break;
-                feed.scales(r, lane);
-                feed.widen(s0 + (u % NU) * L::UNIT, r);
-                tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
-                u += 2;
+                typename Feed::Tile tile;
+                feed.read(r, lane, tile);
                 --count;
                 const int at = r;
                 r = r + 1 == AHEAD ? 0 : r + 1;
                 if (count == AHEAD - 1) ask(at, false);
+                if (u >= NU) ok = __all_sync(0xffffffffu, tc::bar_wait(tc::smem_u32(&ms.empty[u % NU]), (u / NU + 1) & 1, abort));
+                if (!ok) break;
+                feed.write(s0 + (u % NU) * L::UNIT, tile);
+                tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
+                u += 2 * TEAMS;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (!E4 && warp < 4) {
@@ -707,7 +712,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             }
             g.kind = 3;
             if (ok) put(g);
-            if (E4 && ok) list(-1, 0, 0);
+            for (int i = 0; E4 && ok && i < teams(NQ); ++i) list(-1, 0, 0);  // each team comes to one
             if (E4) asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp < 8) {
             // ---- queries and the tree's mask -----------------------------------------------

@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
         constexpr int QCPR = DP / 8, QRPI = 32 / QCPR;            // 16-byte chunks of a query row; rows of a warp's copy
         [[maybe_unused]] constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
         constexpr int AHEAD = L::AHEAD;
-        sv::E4m3Feed<BF, DP, AHEAD> feed(&ms.feed[warp], s0 + L::R0, warp, lane, P.D);
+        using Feed = sv::E4m3Feed<BF, DP, AHEAD>;
+        Feed feed(&ms.feed[warp], s0 + L::R0, warp, lane, P.D);
         const int chunk = lane % CPR, sub = lane / CPR;
         const int own = E4 ? feed.own : warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot the lane keeps
         const int first = warp * RPI + sub;                                                // its row of the first copy
@@ -363,17 +364,17 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                     const bool more = x < units;
                     if (more) next();
                     feed.wait();
-                    if (!room()) break;
-                    feed.scales(y % AHEAD, lane);
-                    const uint32_t unit = s0 + (u % NU) * L::UNIT;
-                    feed.widen(unit, y % AHEAD);
-                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
+                    typename Feed::Tile tile;
+                    feed.read(y % AHEAD, lane, tile);
                     if (more) {
                         place();
                         placed(AHEAD - 1);
                     } else {
                         feed.commit();
                     }
+                    if (!room()) break;
+                    feed.write(s0 + (u % NU) * L::UNIT, tile);
+                    tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
                 }
             }
         }

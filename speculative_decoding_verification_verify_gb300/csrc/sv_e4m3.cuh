@@ -165,41 +165,42 @@ struct E4m3Feed {
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
     // The oldest of the R tiles (or empty groups) is there.
     static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory"); }
-    // The powers of two of the tile in place r, before `widen`.
-    __device__ __forceinline__ void scales(int r, int lane)
-    {
-        uint32_t w;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(ring + r * TILE_BYTES + 128 * DP + tid * 4) : "memory");
-        __syncwarp();
-        sm.scale[lane % RPI][lane / RPI] = E4m3Scale<BF>::bits(w >> 8 * (shifts & 3) & 0xff);
-        shifts >>= 2;
-        __syncwarp();
-    }
-    // (All of a thread's rows are read before the first is stored: the reads' latency is paid once.)
-    __device__ __forceinline__ void widen(uint32_t unit, int r)
-    {
+    // A tile is read whole before it is stored: its place in the ring is free for the next copies meanwhile.
+    struct Tile {
         uint4 w[ITER];
+        uint32_t scale[ITER / 2];  // two rows' in each
+    };
+    // The tile in place r.  (Copies into it may follow: a warp's accesses of shared memory are carried out in their order,
+    // and a copy's write comes a trip to memory later.)
+    __device__ __forceinline__ void read(int r, int lane, Tile &t)
+    {
+        uint32_t power;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(power) : "r"(ring + r * TILE_BYTES + 128 * DP + tid * 4) : "memory");
 #pragma unroll
         for (int i = 0; i < ITER; ++i)
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                         : "=r"(t.w[i].x), "=r"(t.w[i].y), "=r"(t.w[i].z), "=r"(t.w[i].w)
                          : "r"(ring + r * TILE_BYTES + i * 2048 + tid * 16)
                          : "memory");
-        union {
-            uint16_t s[ITER];
-            uint32_t w[ITER / 2];
-        } f;
+        __syncwarp();
+        sm.scale[lane % RPI][lane / RPI] = E4m3Scale<BF>::bits(power >> 8 * (shifts & 3) & 0xff);
+        shifts >>= 2;
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < ITER / 2; ++i) f.w[i] = reinterpret_cast<const uint32_t *>(sm.scale[sub])[i];
+        for (int i = 0; i < ITER / 2; ++i) t.scale[i] = reinterpret_cast<const uint32_t *>(sm.scale[sub])[i];
+    }
+    __device__ __forceinline__ void write(uint32_t unit, const Tile &t)
+    {
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            const E4m3Scale<BF> g(f.s[i]);
+            const E4m3Scale<BF> g((uint16_t)(t.scale[i / 2] >> 16 * (i & 1)));
             const uint32_t at = unit + to + i * 4 * RPI * 128;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(g(w[i].x)), "r"(g(w[i].x >> 16)), "r"(g(w[i].y)),
-                         "r"(g(w[i].y >> 16))
+            const uint4 &w = t.w[i];
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(g(w.x)), "r"(g(w.x >> 16)), "r"(g(w.y)),
+                         "r"(g(w.y >> 16))
                          : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16), "r"(g(w[i].z)), "r"(g(w[i].z >> 16)), "r"(g(w[i].w)),
-                         "r"(g(w[i].w >> 16))
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16), "r"(g(w.z)), "r"(g(w.z >> 16)), "r"(g(w.w)),
+                         "r"(g(w.w >> 16))
                          : "memory");
         }
     }
