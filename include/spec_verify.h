@@ -395,7 +395,7 @@ int spec_verify_kv_append_ex(const void *q, const void *k, const void *v, int dt
  * Positions of the paged cache as contiguous rows of 16 bits (for a caller's own attention, for moving a request to
  * another cache): k_out[b][n] and v_out[b][n] [Hkv][D] = the rows of position first[b] + n, n < num_rows[b] (NULL:
  * all N); the rows past num_rows are 0.  From a cache of 8-bit rows the values are exact (in fp16: where fp16 holds
- * them; what append_ex wrote from fp16 it does).  Arguments as for spec_verify_kv_append_ex; dtype is the outputs' and, where its rows
+ * them; what append_ex wrote from fp16 it does).  k_out and v_out are 32-byte aligned.  Arguments as for spec_verify_kv_append_ex; dtype is the outputs' and, where its rows
  * have 16 bits, the cache's.  Device status codes: 5 (num_rows outside [0, N], first below 0, or first + num_rows
  * beyond max_pos): the request's rows are NaN; 6 (a slot outside the pool): that row is NaN.  One launch, no workspace.
  */

@@ -160,13 +160,12 @@ struct Misc {
     Join join[2];
     int joins[2];
     int8_t par[sv::MAX_TREE];
-    // 8-bit rows: of the tiles ahead, the rows' slots, the key head (-1: no more), the rows that there are, the segment.
+    // 8-bit rows: of the tiles ahead, the rows' slots (in the order of the copies), the key head (-1: no more), the rows that there are, the segment.
     struct __align__(16) Slots {
         int slot[TILE];
         int h, left, seg, pad;
     } slots[E4 ? SLOTS : 1];
     uint64_t slotfull[SLOTS], slotempty[SLOTS];
-    typename sv::E4m3FeedSmem<BF, DP, Layout<NQ, DP, E4>::AHEAD, E4>::type feed[8 * teams(NQ)];
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -379,7 +378,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             using Feed = sv::E4m3Feed<BF, DP, AHEAD>;
             constexpr int TEAMS = teams(NQ);
             const int cw = warp & 3, wg = warp < 4 ? 0 : (warp - 4 - 4 * WG) >> 2, kv = wg & 1;
-            Feed feed(&ms.feed[4 * wg + cw], s0 + L::R0 + wg * L::RING, cw, lane, P.D);
+            Feed feed(s0 + L::R0 + wg * L::RING, cw, lane, P.D);
             const unsigned char *const cache = kv ? P.v : P.k;
             const uint32_t stride = kv ? P.v_slot : P.k_slot;
             int r = 0, count = 0, n = wg >> 1, u = wg;  // the oldest tile's place; tiles under way; the next to ask for; the oldest's unit
@@ -394,16 +393,23 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 const int h = list.h, left = list.left;
                 last = h < 0;
                 if (last) return 0;
-                const int mine = list.slot[feed.own];
+                const int mine = list.slot[Feed::place(feed.own)];
+                int slot[Feed::ITER];
+#pragma unroll
+                for (int i = 0; i < Feed::ITER; i += 4) {
+                    const int4 four = *reinterpret_cast<const int4 *>(&list.slot[feed.first() + i]);
+                    slot[i] = four.x, slot[i + 1] = four.y, slot[i + 2] = four.z, slot[i + 3] = four.w;
+                }
                 const bool fine = (unsigned)mine < (unsigned)P.num_slots, in = feed.own < left;
                 if (in && !fine)
 #pragma unroll
                     for (int i = 0; i < WG; ++i) *(volatile int *)&ms.bad[i][list.seg % FLAGS] = 1;
                 const bool whole = __all_sync(0xffffffffu, in && fine);
-                feed.ask(at, whole, cache + h * P.D, stride, [&](int i) {
-                    const int s = list.slot[feed.row(i)];
-                    return whole || (feed.row(i) < left && (unsigned)s < (unsigned)P.num_slots) ? s : -1;
-                });
+                if (!whole)
+#pragma unroll
+                    for (int i = 0; i < Feed::ITER; ++i)
+                        if (feed.row(i) >= left || (unsigned)slot[i] >= (unsigned)P.num_slots) slot[i] = -1;
+                feed.ask(at, whole, cache + h * P.D, stride, slot);
                 feed.asked(at, count, in && fine ? mine : -1, cache, stride, P.Hkv * P.D + h);
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem_u32(&ms.slotempty[n % SLOTS]));
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 for (int i = count; i < AHEAD; ++i) feed.commit();  // (what is waited for is counted in groups)
                 feed.wait();
                 typename Feed::Tile tile;
-                feed.read(r, lane, tile);
+                feed.read(r, tile);
                 --count;
                 const int at = r;
                 r = r + 1 == AHEAD ? 0 : r + 1;
@@ -654,7 +660,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 for (int i = 0; i < TILE / 32; ++i) {
                     const int row = lane + 32 * i;
                     const bool in = row < left && SV_INB(at + row, (int64_t)P.B * P.max_pos, 1103);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(&list.slot[row])),
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(&list.slot[sv::E4m3Feed<BF, DP, 1>::place(row)])),
                                  "l"(P.slot_table + (in ? at + row : 0)), "r"(in ? 4 : 0)
                                  : "memory");
                 }

@@ -147,14 +147,12 @@ __global__ void __launch_bounds__(NT) append_kernel(const Append P)
     for (int h0 = 0; h0 < heads; h0 += per) {
         const int head = h0 + first;
         const bool mine = live && head < heads;
-        if (h0 > 0) {
-            va = vb = make_uint4(0, 0, 0, 0);
-            if (mine) load(head, va, vb);
-        }
         const bool is_q = head < P.Hq, is_k = !is_q && head < P.Hq + P.Hkv;
         float x[8], y[8];
         to_float<BF>(va, x);
         to_float<BF>(vb, y);
+        if (live && head + per < heads) load(head + per, va, vb);  // the next ones' while these are worked on
+        else va = vb = make_uint4(0, 0, 0, 0);
         const uint4 *weight = is_q ? P.q_norm : is_k ? P.k_norm : nullptr;
         if (P.q_norm || P.k_norm) {
             float sum = 0.f;
@@ -230,77 +228,88 @@ struct Read {
     int64_t k_slot, v_slot, num_slots;  // strides in bytes
     const int32_t *slot_table, *first, *num_rows;
     int B, N, Hkv, D, max_pos;
-    int units;  // of a row of k and v together, 16 values each
+    int units;  // of a row of k or v, 16 values each
     int32_t *dev_status;
 };
 
-constexpr int READ_NT = 256, READ_U = 4;  // units of a thread, all under way at once
+// A warp takes the keys and the values of two rows, so that its lanes have their places with few divisions, and 16
+// values of them a lane at a time, READ_U of those under way.  Stores of 32 bytes fill a sector each.
+constexpr int READ_NT = 256, READ_SIDES = 4, READ_U = 4;
+
+__device__ __forceinline__ void store32(void *at, const uint4 &x, const uint4 &y)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(y.x),
+                 "r"(y.y), "r"(y.z), "r"(y.w)
+                 : "memory");
+}
 
 template <bool BF, bool E4>
 __global__ void __launch_bounds__(READ_NT) read_kernel(const Read P)
 {
-    const int64_t total = (int64_t)P.B * P.N * P.units, u0 = (int64_t)blockIdx.x * (READ_NT * READ_U) + threadIdx.x;
-    const int half = P.units / 2;
-    uint4 x[READ_U], y[READ_U];
-    float f[READ_U];
-    int bad = 0;
-#pragma unroll
-    for (int i = 0; i < READ_U; ++i) {
-        const int64_t u = u0 + i * READ_NT;
-        x[i] = y[i] = make_uint4(0, 0, 0, 0);
-        f[i] = 1.f;
-        if (u >= total) continue;
-        const int64_t row = u / P.units;
-        const int at = (int)(u - row * P.units), b = (int)((unsigned)row / (unsigned)P.N), n = (int)(row - (int64_t)b * P.N);
+    const int lane = threadIdx.x & 31, U = P.units;
+    const int64_t sides = 2 * (int64_t)P.B * P.N;
+    const int64_t side0 = ((int64_t)blockIdx.x * (READ_NT / 32) + (threadIdx.x >> 5)) * READ_SIDES;
+    // The first lanes find the sides' rows: where they are (0: nowhere), and what is there instead.
+    const unsigned char *from = nullptr;
+    uint32_t fill = 0;
+    if (lane < READ_SIDES && side0 + lane < sides) {
+        const int64_t row = (side0 + lane) >> 1;
+        const int b = (int)((unsigned)row / (unsigned)P.N), n = (int)(row - (int64_t)b * P.N);
         const int c = SV_INB(b, P.B, 1211) ? P.first[b] : 0;
         const int nn = P.num_rows && SV_INB(b, P.B, 1212) ? P.num_rows[b] : P.N;
-        int code = 0, slot = -1;
+        int code = 0;
         if (nn < 0 || nn > P.N || c < 0 || (int64_t)c + nn > P.max_pos) {
             code = SPEC_VERIFY_DEV_BAD_KV_POSITION;
         } else if (n < nn) {
             const int64_t s = (int64_t)b * P.max_pos + c + n;
-            slot = SV_INB(s, (int64_t)P.B * P.max_pos, 1213) ? P.slot_table[s] : -1;
+            const int slot = SV_INB(s, (int64_t)P.B * P.max_pos, 1213) ? P.slot_table[s] : -1;
             if (slot < 0 || slot >= P.num_slots) code = SPEC_VERIFY_DEV_BAD_KV_SLOT;
+            else from = lane & 1 ? P.v + (int64_t)slot * P.v_slot : P.k + (int64_t)slot * P.k_slot;
         }
         if (code) {
-            f[i] = NAN;
-            bad = code > bad ? code : bad;
-        } else if (n < nn) {
-            const bool is_v = at >= half;
-            const unsigned char *src = is_v ? P.v + (int64_t)slot * P.v_slot : P.k + (int64_t)slot * P.k_slot;
-            const int v = is_v ? at - half : at;
-            if (E4) {
-                x[i] = __ldg(reinterpret_cast<const uint4 *>(src) + v);
-                const unsigned head = (unsigned)v * 16u / (unsigned)P.D;
-                f[i] = __uint_as_float((uint32_t)src[P.Hkv * P.D + head] << 23);
-            } else {
-                x[i] = __ldg(reinterpret_cast<const uint4 *>(src) + 2 * v);
-                y[i] = __ldg(reinterpret_cast<const uint4 *>(src) + 2 * v + 1);
-            }
+            fill = Half2<BF>::NAN2;
+            if (P.dev_status) atomicMax(P.dev_status, code);
         }
     }
-    if (bad && P.dev_status) atomicMax(P.dev_status, bad);
+    const int total = (int)(sides - side0 < READ_SIDES ? (sides > side0 ? sides - side0 : 0) : READ_SIDES) * U;
+    for (int i0 = 0; i0 < total; i0 += 32 * READ_U) {
+        uint4 x[READ_U], y[READ_U];
+        uint32_t scale[READ_U];
+        unsigned char *to[READ_U];
 #pragma unroll
-    for (int i = 0; i < READ_U; ++i) {
-        const int64_t u = u0 + i * READ_NT;
-        if (u >= total) continue;
-        if (f[i] != f[i]) {
-            x[i] = y[i] = make_uint4(Half2<BF>::NAN2, Half2<BF>::NAN2, Half2<BF>::NAN2, Half2<BF>::NAN2);
-        } else if (E4) {
-            auto two = [&](uint32_t bits) {
-                const float2 z = sv::e4m3_unpack(bits & 0xffffu);
-                return Half2<BF>::pack(z.x * f[i], z.y * f[i]);
-            };
-            const uint4 z = x[i];
-            x[i] = make_uint4(two(z.x), two(z.x >> 16), two(z.y), two(z.y >> 16));
-            y[i] = make_uint4(two(z.z), two(z.z >> 16), two(z.w), two(z.w >> 16));
+        for (int i = 0; i < READ_U; ++i) {
+            const int at = i0 + 32 * i + lane, s = min((unsigned)at / (unsigned)U, (unsigned)(READ_SIDES - 1)), u = at - s * U;
+            const unsigned char *src = reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, (unsigned long long)from, s));
+            const uint32_t f = __shfl_sync(0xffffffffu, fill, s);
+            to[i] = nullptr;
+            if (at >= total) continue;
+            x[i] = y[i] = make_uint4(f, f, f, f);
+            scale[i] = 0;
+            to[i] = reinterpret_cast<unsigned char *>((s & 1 ? P.v_out : P.k_out) + 2 * (((side0 + s) >> 1) * U + u));
+            if (!src) continue;
+            if (E4) {
+                x[i] = __ldg(reinterpret_cast<const uint4 *>(src) + u);
+                scale[i] = 1u << 31 | src[P.Hkv * P.D + (unsigned)u * 16u / (unsigned)P.D];
+            } else {
+                x[i] = __ldg(reinterpret_cast<const uint4 *>(src) + 2 * u);
+                y[i] = __ldg(reinterpret_cast<const uint4 *>(src) + 2 * u + 1);
+            }
         }
-        const int64_t row = u / P.units;
-        const int at = (int)(u - row * P.units);
-        const bool is_v = at >= half;
-        uint4 *const dst = (is_v ? P.v_out : P.k_out) + 2 * (row * half + (is_v ? at - half : at));
-        dst[0] = x[i];
-        dst[1] = y[i];
+#pragma unroll
+        for (int i = 0; i < READ_U; ++i) {
+            if (!to[i]) continue;
+            if (E4 && scale[i]) {
+                const float f = __uint_as_float(scale[i] << 23);
+                auto two = [&](uint32_t bits) {
+                    const float2 z = sv::e4m3_unpack(bits & 0xffffu);
+                    return Half2<BF>::pack(z.x * f, z.y * f);
+                };
+                const uint4 z = x[i];
+                x[i] = make_uint4(two(z.x), two(z.x >> 16), two(z.y), two(z.y >> 16));
+                y[i] = make_uint4(two(z.z), two(z.z >> 16), two(z.w), two(z.w >> 16));
+            }
+            store32(to[i], x[i], y[i]);
+        }
     }
 }
 
@@ -431,7 +440,7 @@ extern "C" int spec_verify_kv_read(const void *k_cache, const void *v_cache, int
     if (B < 1 || N < 1 || (int64_t)B * N > 0x7fffffff || max_pos < 1) return SPEC_VERIFY_EINVAL;
     if (Hkv < 1 || D < 16 || D % 16 || D > 512 || (int64_t)Hkv * D > (1 << 23)) return SPEC_VERIFY_EINVAL;
     if (!cache_ok(cache_dtype, num_slots, k_slot_stride, v_slot_stride, Hkv, D)) return SPEC_VERIFY_EINVAL;
-    if (!aligned({k_cache, v_cache, k_out, v_out}, 16) || !aligned({slot_table, first, num_rows, dev_status}, 4))
+    if (!aligned({k_cache, v_cache}, 16) || !aligned({k_out, v_out}, 32) || !aligned({slot_table, first, num_rows, dev_status}, 4))
         return SPEC_VERIFY_EINVAL;
     const int elt = cache_dtype == SPEC_VERIFY_E4M3 ? 1 : 2;
     Read P;
@@ -450,9 +459,10 @@ extern "C" int spec_verify_kv_read(const void *k_cache, const void *v_cache, int
     P.Hkv = Hkv;
     P.D = D;
     P.max_pos = max_pos;
-    P.units = 2 * Hkv * (D / 16);
+    P.units = Hkv * (D / 16);
     P.dev_status = dev_status;
-    const int64_t total = (int64_t)B * N * P.units, grid = (total + READ_NT * READ_U - 1) / (READ_NT * READ_U);
+    constexpr int PER = READ_SIDES * (READ_NT / 32);
+    const int64_t grid = (2 * (int64_t)B * N + PER - 1) / PER;
     if (grid > 0x7fffffff) return SPEC_VERIFY_EINVAL;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool e4 = cache_dtype == SPEC_VERIFY_E4M3;

@@ -80,7 +80,7 @@ struct Layout {
     static constexpr int Q0 = NU * UNIT, R0 = Q0 + 2 * QHALF, M0 = R0 + (E4 ? AHEAD * (128 * DP + 512) : 0);
 };
 
-template <int NU, class Feed, int FEEDS>
+template <int NU>
 struct Misc {
     uint64_t full[NU], empty[NU];
     uint64_t sfull[2], pfull[2], odone[2], qfull, qempty, segfull[SEGS], segempty[SEGS], drain;
@@ -92,7 +92,6 @@ struct Misc {
     int begin_b, abort;
     int poison[4];  // a segment's number: its values have some that are not finite behind the block's first row
     uint32_t tmem;
-    Feed feed[FEEDS];
 };
 
 // Floats of a part: the weighted values [dimensions / 4][row][4], references and sums of the rows.
@@ -146,7 +145,7 @@ __device__ __forceinline__ int64_t run_begin(int64_t r, int64_t total, int runs)
 __device__ __forceinline__ int run_before(int64_t x, int64_t total, int runs) { return (int)((x * runs + total - 1) / total) - 1; }
 
 template <bool BF, int DP, bool E4>
-using MiscOf = Misc<Layout<DP, E4>::NU, typename sv::E4m3FeedSmem<BF, DP, Layout<DP, E4>::AHEAD, E4>::type, 4>;
+using MiscOf = Misc<Layout<DP, E4>::NU>;
 
 template <bool BF, int DP, bool E4>
 __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Params P)
@@ -246,7 +245,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
         [[maybe_unused]] constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
         constexpr int AHEAD = L::AHEAD;
         using Feed = sv::E4m3Feed<BF, DP, AHEAD>;
-        Feed feed(&ms.feed[warp], s0 + L::R0, warp, lane, P.D);
+        Feed feed(s0 + L::R0, warp, lane, P.D);
         const int chunk = lane % CPR, sub = lane / CPR;
         const int own = E4 ? feed.own : warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot the lane keeps
         const int first = warp * RPI + sub;                                                // its row of the first copy
@@ -342,10 +341,10 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                 };
                 auto place = [&] {
                     const bool whole = __all_sync(0xffffffffu, slot >= 0);
-                    feed.ask(x % AHEAD, whole, (x & 1 ? P.v : P.k) + g.h * P.D, (uint32_t)(x & 1 ? P.v_slot : P.k_slot), [&](int i) {
-                        const int s = __shfl_sync(0xffffffffu, slot, i * feed.RPI + feed.sub);
-                        return x & 1 && s == -2 ? -1 : s;
-                    });
+                    int slots[Feed::ITER];
+#pragma unroll
+                    for (int i = 0; i < Feed::ITER; ++i) slots[i] = __shfl_sync(0xffffffffu, x & 1 && slot == -2 ? -1 : slot, i * Feed::RPI + feed.sub);
+                    feed.ask(x % AHEAD, whole, (x & 1 ? P.v : P.k) + g.h * P.D, (uint32_t)(x & 1 ? P.v_slot : P.k_slot), slots);
                 };
                 auto placed = [&](int count) {
                     feed.asked(x % AHEAD, count, slot, x & 1 ? P.v : P.k, x & 1 ? P.v_slot : P.k_slot, P.Hkv * P.D + g.h);
@@ -365,7 +364,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                     if (more) next();
                     feed.wait();
                     typename Feed::Tile tile;
-                    feed.read(y % AHEAD, lane, tile);
+                    feed.read(y % AHEAD, tile);
                     if (more) {
                         place();
                         placed(AHEAD - 1);

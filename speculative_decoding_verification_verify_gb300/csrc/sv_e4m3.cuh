@@ -103,10 +103,6 @@ struct E4m3Feed {
     static constexpr int CPR = DP / 16, RPI = 32 / CPR, ITER = CPR;
     static constexpr int TILE_BYTES = 128 * DP + 128 * 4;  // a tile of the ring: rows, then a word with each row's power of two
     static constexpr int BYTES = R * TILE_BYTES;
-    struct __align__(16) Smem {
-        uint16_t scale[RPI][ITER];  // a warp's
-    };
-    Smem &sm;
     int own, sub, tid;  // the row whose slot the lane keeps, of a tile
     uint32_t to, ring;
     int offset;         // of the lane's chunk in a row; below 0: beyond the head
@@ -114,8 +110,7 @@ struct E4m3Feed {
     uint32_t shifts;    // where in their words the powers of two are, two bits for each tile under way, the oldest first
 
     // `warp` of the warpgroup, whose ring it is.  Eight lanes that store together have chunks of two rows: no bank twice.
-    __device__ __forceinline__ E4m3Feed(void *s, uint32_t ring_at, int warp, int lane, int D)
-        : sm(*static_cast<Smem *>(s)), tid(warp * 32 + lane), ring(ring_at), shifts(0)
+    __device__ __forceinline__ E4m3Feed(uint32_t ring_at, int warp, int lane, int D) : tid(warp * 32 + lane), ring(ring_at), shifts(0)
     {
         const int chunk = DP == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
         sub = DP == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2;
@@ -125,25 +120,25 @@ struct E4m3Feed {
         offset = chunk * 16 < D ? chunk * 16 : -1;
         full = D == DP;
     }
-    // The tile's row of the lane's i-th copy.
+    // The tile's row of the lane's i-th copy; where a list in the order of lanes' copies has a row, and the lane's first.
     __device__ __forceinline__ int row(int i) const { return (to >> 7 & 127) + 4 * RPI * i; }
-    // The copies of a tile into place r, of rows whose slots are `slots(i)`: `whole` where all of the warp's 32 rows are
+    static __device__ __forceinline__ int place(int row) { return row % (4 * RPI) * ITER + row / (4 * RPI); }
+    __device__ __forceinline__ int first() const { return (to >> 7 & 127) * ITER; }
+    // The copies of a tile into place r, of rows whose slots are given: `whole` where all of the warp's 32 rows are
     // there, else below 0 where one is not (zeros; -2: NaN).  `cache` is where the head's values of slot 0 are.
-    template <class Slots>
-    __device__ __forceinline__ void ask(int r, bool whole, const unsigned char *cache, uint32_t stride, Slots slots)
+    __device__ __forceinline__ void ask(int r, bool whole, const unsigned char *cache, uint32_t stride, const int (&slot)[ITER])
     {
         const uint32_t dst = ring + r * TILE_BYTES + tid * 16;
-        // (The same way for all lanes of a warp: `slots` may exchange them.)
         if (whole && full) {
             const unsigned char *const at = cache + offset;
 #pragma unroll
             for (int i = 0; i < ITER; ++i)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 2048), "l"(at + (uint64_t)(uint32_t)slots(i) * stride)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 2048), "l"(at + (uint64_t)(uint32_t)slot[i] * stride)
                              : "memory");
         } else {
-#pragma unroll 2
+#pragma unroll
             for (int i = 0; i < ITER; ++i) {
-                const int s = slots(i);
+                const int s = slot[i];
                 const unsigned char *at = s == -2 ? reinterpret_cast<const unsigned char *>(g_e4m3_nan)
                                                   : cache + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride;
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 2048), "l"(at + (offset < 0 ? 0 : offset)),
@@ -156,7 +151,7 @@ struct E4m3Feed {
     // the end of its copies; `count`: tiles under way before it.
     __device__ __forceinline__ void asked(int r, int count, int slot, const unsigned char *cache, uint32_t stride, int at)
     {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ring + r * TILE_BYTES + 128 * DP + tid * 4),
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ring + r * TILE_BYTES + 128 * DP + place(own) * 4),
                      "l"(cache + (at & ~3) + (uint64_t)(uint32_t)(slot < 0 ? 0 : slot) * stride), "r"(slot < 0 ? 0 : 4)
                      : "memory");
         shifts |= (uint32_t)(at & 3) << 2 * count;
@@ -164,36 +159,42 @@ struct E4m3Feed {
     }
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
     // The oldest of the R tiles (or empty groups) is there.
-    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory"); }
+    static __device__ __forceinline__ void wait()
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
+        __syncwarp();  // (the powers of two were copied by other lanes)
+    }
     // A tile is read whole before it is stored: its place in the ring is free for the next copies meanwhile.
     struct Tile {
         uint4 w[ITER];
-        uint32_t scale[ITER / 2];  // two rows' in each
+        uint32_t power[ITER];  // the words that have the rows' powers of two, at `shift`
+        int shift;
     };
-    // The tile in place r.  (Copies into it may follow: a warp's accesses of shared memory are carried out in their order,
-    // and a copy's write comes a trip to memory later.)
-    __device__ __forceinline__ void read(int r, int lane, Tile &t)
+    // The tile in place r.  (Copies into it may follow once the warp's lanes are past this: a warp's accesses of shared
+    // memory are carried out in their order, and a copy's write comes a trip to memory later.)
+    __device__ __forceinline__ void read(int r, Tile &t)
     {
-        uint32_t power;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(power) : "r"(ring + r * TILE_BYTES + 128 * DP + tid * 4) : "memory");
+#pragma unroll
+        for (int i = 0; i < ITER; i += 4)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(t.power[i]), "=r"(t.power[i + 1]), "=r"(t.power[i + 2]), "=r"(t.power[i + 3])
+                         : "r"(ring + r * TILE_BYTES + 128 * DP + (first() + i) * 4)
+                         : "memory");
 #pragma unroll
         for (int i = 0; i < ITER; ++i)
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(t.w[i].x), "=r"(t.w[i].y), "=r"(t.w[i].z), "=r"(t.w[i].w)
                          : "r"(ring + r * TILE_BYTES + i * 2048 + tid * 16)
                          : "memory");
-        __syncwarp();
-        sm.scale[lane % RPI][lane / RPI] = E4m3Scale<BF>::bits(power >> 8 * (shifts & 3) & 0xff);
+        t.shift = 8 * (shifts & 3);
         shifts >>= 2;
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < ITER / 2; ++i) t.scale[i] = reinterpret_cast<const uint32_t *>(sm.scale[sub])[i];
     }
     __device__ __forceinline__ void write(uint32_t unit, const Tile &t)
     {
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            const E4m3Scale<BF> g((uint16_t)(t.scale[i / 2] >> 16 * (i & 1)));
+            const E4m3Scale<BF> g(E4m3Scale<BF>::bits(t.power[i] >> t.shift & 0xff));
             const uint32_t at = unit + to + i * 4 * RPI * 128;
             const uint4 &w = t.w[i];
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(g(w.x)), "r"(g(w.x >> 16)), "r"(g(w.y)),
@@ -204,16 +205,6 @@ struct E4m3Feed {
                          : "memory");
         }
     }
-};
-
-// What a warp of it has in shared memory; nothing in a kernel of 16-bit rows.
-template <bool BF, int DP, int R, bool E4>
-struct E4m3FeedSmem {
-    using type = typename E4m3Feed<BF, DP, R>::Smem;
-};
-template <bool BF, int DP, int R>
-struct E4m3FeedSmem<BF, DP, R, false> {
-    struct type {};
 };
 
 }  // namespace sv

@@ -52,7 +52,7 @@ def test_read(lib):
                 dict(cache=1), dict(cache=2), dict(dtype=1), dict(dtype=E), dict(slots=0), dict(slots=1 << 31),
                 dict(kss=1024), dict(vss=1048), dict(max_pos=0), dict(B=0), dict(N=0), dict(B=1 << 16, N=1 << 16),
                 dict(Hkv=0), dict(D=8), dict(D=24), dict(D=528), dict(kc=ODD), dict(vc=ODD), dict(k_out=ODD),
-                dict(v_out=ODD), dict(table=ODD4), dict(first=ODD4), dict(num=ODD4), dict(status=ODD4)):
+                dict(v_out=ODD), dict(k_out=A + 16), dict(v_out=A + 16), dict(table=ODD4), dict(first=ODD4), dict(num=ODD4), dict(status=ODD4)):
         assert read(lib, **bad) == binding.EINVAL, bad
 
 
