@@ -83,7 +83,7 @@ struct Layout {
 template <int NU>
 struct Misc {
     uint64_t full[NU], empty[NU];
-    uint64_t sfull[2], pfull[2], odone[2], qfull, qempty, segfull[SEGS], segempty[SEGS], drain;
+    uint64_t sfull[2], pfull[2][2], odone[2], qfull, qempty, segfull[SEGS], segempty[SEGS], drain;
     union {
         Seg seg[SEGS];
         int64_t scan[NT / 32];  // (before any segment is listed)
@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
         }
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(tc::smem_u32(&ms.sfull[i]), 1);
-            tc::bar_init(tc::smem_u32(&ms.pfull[i]), 128);
+            tc::bar_init(tc::smem_u32(&ms.pfull[i][0]), 128);
+            tc::bar_init(tc::smem_u32(&ms.pfull[i][1]), 128);
             tc::bar_init(tc::smem_u32(&ms.odone[i]), 1);
         }
         tc::bar_init(tc::smem_u32(&ms.qfull), 128);
@@ -412,14 +413,21 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                         for (int h = 0; h < 2 && ok; ++h) {
                             if (j >= g.j0 && j < e[h]) {
                                 wait(ms.full[uv % NU], uv / NU);
-                                wait(ms.pfull[h], k[h]);
+                                wait(ms.pfull[h][0], k[h]);
                                 if (!ok) break;
                                 tc::fence_after();
                                 tc::fence_async_smem();
                                 const uint64_t b = vd + (uint64_t)((uv % NU) * (L::UNIT >> 4));
                                 const uint32_t a = tmem + h * TILE, d = tmem + 256 + h * MAXD;
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) tc::mma_f16_ts(d, a + i * 8, b + i * 128, id_o, j > g.j0 || i > 0);
+                                for (int i = 0; i < 4; ++i) tc::mma_f16_ts(d, a + i * 8, b + i * 128, id_o, j > g.j0 || i > 0);
+                                if constexpr (!E4) {
+                                    wait(ms.pfull[h][1], k[h]);
+                                    if (!ok) break;
+                                    tc::fence_after();
+                                }
+#pragma unroll
+                                for (int i = 4; i < 8; ++i) tc::mma_f16_ts(d, a + i * 8, b + i * 128, id_o, true);
                                 if (j + 1 == e[h]) tc::commit(tc::smem_u32(&ms.odone[h]));
                                 ++k[h];
                             }
@@ -581,30 +589,14 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
 #pragma unroll
                     for (int i = 0; i < TILE; ++i) x[i] -= off;
                 }
-                const uint64_t bias2 = sv::f2(bias, bias);
-                uint64_t acc[2] = {0, 0};
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) {
-                        const float2 e = sv::f2_split(sv::f2_fma(sv::f2(x[64 * i + 2 * y], x[64 * i + 2 * y + 1]), scale2, bias2));
-                        const float a = ex2(e.x), b = ex2(e.y);
-                        acc[y & 1] = sv::f2_add(acc[y & 1], sv::f2(a, b));
-                        p[y] = Half2<BF>::pack(a, b);
-                    }
-                    tc::tmem_st32(st + 32 * i, p);
-                }
-                const float2 s = sv::f2_split(sv::f2_add(acc[0], acc[1]));
-                sum += s.x + s.y;
-                const int pos = j * TILE + t;
-                if ((j + 1) * TILE - 1 > front) {
+                auto set_aside = [&] {
+                    if ((j + 1) * TILE - 1 <= front) return;
+                    const int pos = j * TILE + t;
                     // A weight of 0 does not undo an infinity or a NaN: what is not finite in values that the block's
                     // first row does not see is set aside, and the rows that do see it get it at the segment's end.
                     // (Both halves do so, each before its own products; what the other has set aside reads as 0.)
                     const int uv = units + 2 * (j - g.j0) + 1;
                     ok = __all_sync(0xffffffffu, tc::bar_wait(tc::smem_u32(&ms.full[uv % NU]), (uv / NU) & 1, abort));
-                    if (!ok) break;
                     if (pos > front && pos < g.c + g.nn) {
                         // An exponent of all ones carries into the sign's place.
                         constexpr uint32_t EXP2 = Half2<BF>::EXP_MASK * 0x10001u;
@@ -630,10 +622,37 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                     }
                     tc::fence_async_smem();
                     __syncwarp();
+                };
+                if (!E4) set_aside();
+                const uint64_t bias2 = sv::f2(bias, bias);
+                uint64_t acc[2] = {0, 0};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) {
+                        const float2 e = sv::f2_split(sv::f2_fma(sv::f2(x[64 * i + 2 * y], x[64 * i + 2 * y + 1]), scale2, bias2));
+                        const float a = ex2(e.x), b = ex2(e.y);
+                        acc[y & 1] = sv::f2_add(acc[y & 1], sv::f2(a, b));
+                        p[y] = Half2<BF>::pack(a, b);
+                    }
+                    tc::tmem_st32(st + 32 * i, p);
+                    // The first half's products start while the second half's weights are made.  (Not with 8-bit rows: beside
+                    // the widening a look at one more barrier costs more than that, 2180 us against 1690 below.)
+                    if constexpr (!E4) {
+                        tc::wait_st();
+                        tc::fence_before();
+                        tc::bar_arrive(tc::smem_u32(&ms.pfull[half][i]));
+                    }
                 }
-                tc::wait_st();
-                tc::fence_before();
-                tc::bar_arrive(tc::smem_u32(&ms.pfull[half]));
+                const float2 s = sv::f2_split(sv::f2_add(acc[0], acc[1]));
+                sum += s.x + s.y;
+                if constexpr (E4) {
+                    set_aside();
+                    tc::wait_st();
+                    tc::fence_before();
+                    tc::bar_arrive(tc::smem_u32(&ms.pfull[half][0]));
+                }
             }
             units += 2 * (g.j1 - g.j0);
             if (!ok) break;
@@ -725,8 +744,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
     if (warp == 4) tc::tmem_free(tmem, 512);
 }
 
-// The second kernel: rows of nodes that are not there, requests whose lengths are wrong, and the blocks in parts.  A
-// slice is 4 rows of a block; 4 groups of threads take every fourth part, a thread 4 dimensions of a row.
+// The second kernel: rows of nodes that are not there, requests whose lengths are wrong, and the blocks in parts.  (The
+// first has two warps with nothing to do, but no registers for them: 8-bit rows 1690 us against 1990 below.)  A slice is 4 rows of a block; 4 groups of threads take every fourth part, a thread 4 dimensions of a row.
 constexpr int JT = 512, SLICES = ROWS / 4;
 
 template <bool BF>
