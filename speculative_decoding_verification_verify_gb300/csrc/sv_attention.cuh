@@ -108,14 +108,13 @@ struct Layout {
     static constexpr int HALVES = DP / 64;
     static constexpr int UNIT = TILE * DP * 2;
     // (8-bit rows: two units of keys and two of values, an even number for the two warpgroups that fill them; with one of
-    // each 195 us where two take 140.  The rings before them have the tiles under way.)
+    // each 195 us where two take 140.)
     static constexpr int NU = E4 ? 4 * 128 / DP : ctas_per_sm(NQ, E4) == 2 ? (DP == 64 ? 5 : 2) : 5 * 128 / DP;
-    static constexpr int AHEAD = NQ == 64 ? (DP == 64 ? 3 : 1) : 128 / DP, RING = E4 ? AHEAD * (128 * DP + 512) : 0;  // of keys, of values
     static constexpr int QBYTES = NQ * DP * 2;
     static constexpr int QSTEP = QBYTES < 1024 ? 1024 : QBYTES;
     static constexpr int PROW = E4 && NQ <= 32 ? 64 : 128;  // a row of 32 or 64 columns per position
     static constexpr int PBYTES = TILE * PROW;
-    static constexpr int Q0 = NU * UNIT, P0 = Q0 + 2 * QSTEP, R0 = P0 + PBYTES, M0 = R0 + 2 * teams(NQ) * RING;
+    static constexpr int Q0 = NU * UNIT, P0 = Q0 + 2 * QSTEP, M0 = P0 + PBYTES;
     static constexpr int COLS = 3 * NQ <= 64 ? 64 : 3 * NQ <= 128 ? 128 : 256;  // TMEM columns
 };
 
@@ -166,6 +165,7 @@ struct Misc {
         int h, left, seg, pad;
     } slots[E4 ? SLOTS : 1];
     uint64_t slotfull[SLOTS], slotempty[SLOTS];
+    uint16_t powers[E4 ? 8 * teams(NQ) : 1][32];  // of a warp's rows
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -372,70 +372,65 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
     if (t1 > t0) {
         if (E4 && (warp < 4 || warp >= 8 + 4 * WG)) {
             // ---- 8-bit tiles into shared memory ---------------------------------------------
-            // Warpgroups have the keys and the values in turn, two teams of two every other tile.  While a tile is widened
-            // its place in the warpgroup's ring is filled with its next.
-            constexpr int AHEAD = L::AHEAD;
-            using Feed = sv::E4m3Feed<BF, DP, AHEAD>;
+            // Warpgroups have the keys and the values in turn, two teams of two every other tile.  As a row of a tile is
+            // stored, that of the warpgroup's next tile is loaded in its place.
+            using Rows = sv::E4m3Rows<BF, DP>;
             constexpr int TEAMS = teams(NQ);
             const int cw = warp & 3, wg = warp < 4 ? 0 : (warp - 4 - 4 * WG) >> 2, kv = wg & 1;
-            Feed feed(s0 + L::R0 + wg * L::RING, cw, lane, P.D);
+            Rows rows(&ms.powers[4 * wg + cw], cw, lane, P.D);
             const unsigned char *const cache = kv ? P.v : P.k;
             const uint32_t stride = kv ? P.v_slot : P.k_slot;
-            int r = 0, count = 0, n = wg >> 1, u = wg;  // the oldest tile's place; tiles under way; the next to ask for; the oldest's unit
-            bool ok = true, last = false;
-            // The next tile's slots, into a place: 1, or 0 when there are none, 2 when they are not listed yet.
-            auto ask = [&](int at, bool block) {
+            int n = wg >> 1, u = wg;  // the next tile to be looked for; the unit of the one at hand
+            bool ok = true, last = false, whole = false;
+            int slot[Rows::ITER], power = 0, h = 0;  // of the next tile; its powers of two are asked for as it is found
+            // 1: its slots are here, 0: there are no more tiles, 2: they are not listed yet.
+            auto find = [&](bool block) {
                 if (last) return 0;
                 const uint32_t bar = tc::smem_u32(&ms.slotfull[n % SLOTS]);
                 const bool there = block ? tc::bar_wait(bar, (n / SLOTS) & 1, abort) : tc::bar_test(bar, (n / SLOTS) & 1);
                 if (!__all_sync(0xffffffffu, there)) return block ? 0 : 2;
                 const auto &list = ms.slots[n % SLOTS];
-                const int h = list.h, left = list.left;
+                const int left = list.left;
+                h = list.h;
                 last = h < 0;
                 if (last) return 0;
-                const int mine = list.slot[Feed::place(feed.own)];
-                int slot[Feed::ITER];
+                const int mine = list.slot[Rows::place(rows.own)];
 #pragma unroll
-                for (int i = 0; i < Feed::ITER; i += 4) {
-                    const int4 four = *reinterpret_cast<const int4 *>(&list.slot[feed.first() + i]);
+                for (int i = 0; i < Rows::ITER; i += 4) {
+                    const int4 four = *reinterpret_cast<const int4 *>(&list.slot[rows.first() + i]);
                     slot[i] = four.x, slot[i + 1] = four.y, slot[i + 2] = four.z, slot[i + 3] = four.w;
                 }
-                const bool fine = (unsigned)mine < (unsigned)P.num_slots, in = feed.own < left;
+                const bool fine = (unsigned)mine < (unsigned)P.num_slots, in = rows.own < left;
                 if (in && !fine)
 #pragma unroll
                     for (int i = 0; i < WG; ++i) *(volatile int *)&ms.bad[i][list.seg % FLAGS] = 1;
-                const bool whole = __all_sync(0xffffffffu, in && fine);
+                whole = __all_sync(0xffffffffu, in && fine);
                 if (!whole)
 #pragma unroll
-                    for (int i = 0; i < Feed::ITER; ++i)
-                        if (feed.row(i) >= left || (unsigned)slot[i] >= (unsigned)P.num_slots) slot[i] = -1;
-                feed.ask(at, whole, cache + h * P.D, stride, slot);
-                feed.asked(at, count, in && fine ? mine : -1, cache, stride, P.Hkv * P.D + h);
+                    for (int i = 0; i < Rows::ITER; ++i)
+                        if (rows.row(i) >= left || (unsigned)slot[i] >= (unsigned)P.num_slots) slot[i] = -1;
+                power = 127;
+                if (in && fine) power = __ldg(cache + (uint64_t)(uint32_t)mine * stride + P.Hkv * P.D + h);
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem_u32(&ms.slotempty[n % SLOTS]));
                 n += TEAMS;
-                ++count;
                 return 1;
             };
+            bool loaded = false;
             for (;;) {
-                // The places without a tile: all at the beginning, later where slots were not listed in time.
-                while (count < AHEAD && ask((r + count) % AHEAD, count == 0) == 1) {}
-                if (count == 0) break;
-                for (int i = count; i < AHEAD; ++i) feed.commit();  // (what is waited for is counted in groups)
-                feed.wait();
-                typename Feed::Tile tile;
-                feed.read(r, tile);
-                --count;
-                const int at = r;
-                r = r + 1 == AHEAD ? 0 : r + 1;
-                if (count == AHEAD - 1) ask(at, false);
+                if (!loaded) {
+                    if (find(true) != 1) break;
+                    rows.load(whole, cache + h * P.D, stride, slot);
+                }
+                const int mine = power;
+                loaded = find(false) == 1;
+                rows.powers(mine, lane);
                 if (u >= NU) ok = __all_sync(0xffffffffu, tc::bar_wait(tc::smem_u32(&ms.empty[u % NU]), (u / NU + 1) & 1, abort));
                 if (!ok) break;
-                feed.write(s0 + (u % NU) * L::UNIT, tile);
+                rows.store(s0 + (u % NU) * L::UNIT, loaded, whole, cache + h * P.D, stride, slot);
                 tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
                 u += 2 * TEAMS;
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (!E4 && warp < 4) {
             const int cw = warp;
             // ---- tiles into shared memory -------------------------------------------------
@@ -532,8 +527,9 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             constexpr uint32_t ID_S = tc::instr_desc(BF, false, false, 128, NQ);
             constexpr uint32_t ID_O = tc::instr_desc(BF, true, true, 128, NQ);
             const int dsteps = P.D / 16;
-            const uint64_t kd = tc::smem_desc(s0, 0, 1024), qd = tc::smem_desc(s0 + L::Q0, 0, 1024);
-            const uint64_t vd = tc::smem_desc(s0, HALVES > 1 ? TILE * 128 : 0, 1024), pd = L::PROW == 64 ? tc::smem_desc64(s0 + L::P0, 0, 512) : tc::smem_desc(s0 + L::P0, 0, 1024);
+            constexpr uint32_t HIGH = tc::desc_high(1024), HIGH_P = tc::desc_high(L::PROW == 64 ? 512 : 1024, L::PROW == 64);
+            const uint32_t kd = tc::desc_low(s0, 0), qd = tc::desc_low(s0 + L::Q0, 0);
+            const uint32_t vd = tc::desc_low(s0, HALVES > 1 ? TILE * 128 : 0), pd = tc::desc_low(s0 + L::P0, 0);
             constexpr int PSTEP = L::PROW;  // 16 positions
             int k = 0, seg = -1;       // tiles whose scores are under way
             int wk = 0, wsteps = 0, wstart = 0;  // tiles weighed; the waiting one's
@@ -547,20 +543,22 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 const int u = 2 * wk + 1;
                 tc::fence_after();
                 tc::fence_async_smem();  // the copies are ordinary writes; this thread has seen them land
-                const uint64_t a = vd + (uint64_t)((u % NU) * (L::UNIT >> 4));
+                const uint32_t a = vd + (u % NU) * (L::UNIT >> 4);
                 if (wsteps == 8) {  // straight-line code for whole tiles
-                    tc::mma_f16(tmem + 2 * NQ, a, pd, ID_O, !wstart);
+                    tc::mma_f16<HIGH, HIGH_P>(tmem + 2 * NQ, a, pd, ID_O, !wstart);
 #pragma unroll
-                    for (int i = 1; i < 8; ++i) tc::mma_f16(tmem + 2 * NQ, a + i * 128, pd + i * PSTEP, ID_O, true);
+                    for (int i = 1; i < 8; ++i) tc::mma_f16<HIGH, HIGH_P>(tmem + 2 * NQ, a + i * 128, pd + i * PSTEP, ID_O, true);
                 } else {
                     for (int i = 0; i < wsteps; ++i)
-                        tc::mma_f16(tmem + 2 * NQ, a + i * 128, pd + i * PSTEP, ID_O, !wstart || i > 0);
+                        tc::mma_f16<HIGH, HIGH_P>(tmem + 2 * NQ, a + i * 128, pd + i * PSTEP, ID_O, !wstart || i > 0);
                 }
                 tc::commit(tc::smem_u32(&ms.empty[u % NU]));
                 tc::commit(tc::smem_u32(&ms.pvdone));
                 ++wk;
             };
             // One thread does it all, and waits for nothing without weighing what is ready meanwhile.
+            constexpr int LOOKS = 64;  // between looks at the clock and the abort word, which take as long as a barrier's
+            unsigned looks = 0;
             int64_t begin = 0;
             auto late = [&] {
                 if (!*abort && clock64() - begin <= tc::wait_clocks()) return false;
@@ -588,20 +586,20 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                     begin = clock64();
                     while (!scored || wk < k) {
                         if (!scored && tc::bar_test(tc::smem_u32(&ms.full[u % NU]), (u / NU) & 1) &&
-                            tc::bar_test(tc::smem_u32(&ms.qfull[seg & 1]), (seg >> 1) & 1) &&
+                            (j > g.j0 || tc::bar_test(tc::smem_u32(&ms.qfull[seg & 1]), (seg >> 1) & 1)) &&
                             (k < 2 || tc::bar_test(tc::smem_u32(&ms.sempty[sb]), ((k >> 1) & 1) ^ 1))) {
                             tc::fence_after();
                             tc::fence_async_smem();
-                            const uint64_t a = kd + (uint64_t)((u % NU) * (L::UNIT >> 4));
-                            const uint64_t b = qd + (uint64_t)((seg & 1) * (L::QSTEP >> 4));
+                            const uint32_t a = kd + (u % NU) * (L::UNIT >> 4);
+                            const uint32_t b = qd + (seg & 1) * (L::QSTEP >> 4);
                             if (dsteps == DP / 16) {
 #pragma unroll
                                 for (int d = 0; d < DP / 16; ++d)
-                                    tc::mma_f16(tmem + sb * NQ, a + (d >> 2) * (TILE * 8) + (d & 3) * 2,
+                                    tc::mma_f16<HIGH, HIGH>(tmem + sb * NQ, a + (d >> 2) * (TILE * 8) + (d & 3) * 2,
                                                 b + (d >> 2) * (NQ * 8) + (d & 3) * 2, ID_S, d > 0);
                             } else {
                                 for (int d = 0; d < dsteps; ++d)
-                                    tc::mma_f16(tmem + sb * NQ, a + (d >> 2) * (TILE * 8) + (d & 3) * 2,
+                                    tc::mma_f16<HIGH, HIGH>(tmem + sb * NQ, a + (d >> 2) * (TILE * 8) + (d & 3) * 2,
                                                 b + (d >> 2) * (NQ * 8) + (d & 3) * 2, ID_S, d > 0);
                             }
                             tc::commit(tc::smem_u32(&ms.empty[u % NU]));
@@ -610,7 +608,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                             scored = true;
                         }
                         if (wk < k && ready_p()) weigh();
-                        if (late()) {
+                        if (++looks % LOOKS == 0 && late()) {
                             ok = false;
                             break;
                         }
@@ -660,7 +658,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 for (int i = 0; i < TILE / 32; ++i) {
                     const int row = lane + 32 * i;
                     const bool in = row < left && SV_INB(at + row, (int64_t)P.B * P.max_pos, 1103);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(&list.slot[sv::E4m3Feed<BF, DP, 1>::place(row)])),
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(&list.slot[sv::E4m3Rows<BF, DP>::place(row)])),
                                  "l"(P.slot_table + (in ? at + row : 0)), "r"(in ? 4 : 0)
                                  : "memory");
                 }

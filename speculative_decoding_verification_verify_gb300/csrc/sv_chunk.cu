@@ -38,7 +38,7 @@ constexpr int MAX_SMS = 192;
 constexpr int NT = 512;
 constexpr int SEGS = 4;         // segments listed ahead
 constexpr int SEGMENT = 384;    // the cost of a block's beginning and end, in positions
-constexpr int MIN_TILES = 2;    // of a run
+constexpr int MIN_TILES = 4;    // of a run (2: 16 tokens behind 30000, one key head, 53 us for a call waited for, against 45.5; 6: 3 x 67 tokens 50 against 44)
 constexpr float SLACK = 8.f;    // log2 of how much a weight may pass the reference's
 constexpr float FAR = 0x1p24f;  // of a reference times the scale: its rounding is whole exponents from here on
 // log2 of the reference's weight: fp16 keeps a long tail of small weights below 2^15 (as in sv_attention.cuh).
@@ -46,7 +46,8 @@ __host__ __device__ constexpr float lift(bool bf16) { return bf16 ? 0.f : 7.f; }
 
 // A block in parts: of CTA c0's run the second part, of c0 + 1 .. c1's the first.
 struct __align__(16) Join {
-    int b, h, qb, c0, c1, nn, pad0, pad1;  // c1 = c0: nothing to join
+    int b, h, qb, c0;  // (read as two vectors)
+    int c1, nn, pad0, pad1;  // c1 = c0: nothing to join
 };
 
 struct Params {
@@ -386,18 +387,19 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
             // ---- products ----------------------------------------------------------------------
             const uint32_t id_s = tc::instr_desc(BF, false, false, 128, TILE), id_o = tc::instr_desc(BF, false, true, 128, P.D);
             const int dsteps = P.D / 16;
-            const uint64_t kd = tc::smem_desc(s0, 0, 1024), qd = tc::smem_desc(s0 + L::Q0, 0, 1024);
-            const uint64_t vd = tc::smem_desc(s0, DP > 64 ? TILE * 128 : 0, 1024);
+            constexpr uint32_t HIGH = tc::desc_high(1024);
+            const uint32_t kd = tc::desc_low(s0, 0), qd = tc::desc_low(s0 + L::Q0, 0);
+            const uint32_t vd = tc::desc_low(s0, DP > 64 ? TILE * 128 : 0);
             Seg g;
             int u = 0, seg = 0, k[2] = {0, 0};  // units, segments and the halves' tiles so far
             bool ok = true;
             const bool me = tc::elect();
             auto wait = [&](uint64_t &bar, int n) { ok = ok && tc::bar_wait(tc::smem_u32(&bar), n & 1, abort); };
             auto score = [&](int h, int unit) {
-                const uint64_t a = qd + (uint64_t)(h * (L::QHALF >> 4)), b = kd + (uint64_t)((unit % NU) * (L::UNIT >> 4));
+                const uint32_t a = qd + h * (L::QHALF >> 4), b = kd + (unit % NU) * (L::UNIT >> 4);
 #pragma unroll 4
                 for (int d = 0; d < dsteps; ++d)
-                    tc::mma_f16(tmem + h * TILE, a + (d >> 2) * (HALF * 8) + (d & 3) * 2, b + (d >> 2) * (TILE * 8) + (d & 3) * 2, id_s,
+                    tc::mma_f16<HIGH, HIGH>(tmem + h * TILE, a + (d >> 2) * (HALF * 8) + (d & 3) * 2, b + (d >> 2) * (TILE * 8) + (d & 3) * 2, id_s,
                                 d > 0);
                 tc::commit(tc::smem_u32(&ms.sfull[h]));
             };
@@ -417,17 +419,17 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                                 if (!ok) break;
                                 tc::fence_after();
                                 tc::fence_async_smem();
-                                const uint64_t b = vd + (uint64_t)((uv % NU) * (L::UNIT >> 4));
+                                const uint32_t b = vd + (uv % NU) * (L::UNIT >> 4);
                                 const uint32_t a = tmem + h * TILE, d = tmem + 256 + h * MAXD;
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) tc::mma_f16_ts(d, a + i * 8, b + i * 128, id_o, j > g.j0 || i > 0);
+                                for (int i = 0; i < 4; ++i) tc::mma_f16_ts<HIGH>(d, a + i * 8, b + i * 128, id_o, j > g.j0 || i > 0);
                                 if constexpr (!E4) {
                                     wait(ms.pfull[h][1], k[h]);
                                     if (!ok) break;
                                     tc::fence_after();
                                 }
 #pragma unroll
-                                for (int i = 4; i < 8; ++i) tc::mma_f16_ts(d, a + i * 8, b + i * 128, id_o, true);
+                                for (int i = 4; i < 8; ++i) tc::mma_f16_ts<HIGH>(d, a + i * 8, b + i * 128, id_o, true);
                                 if (j + 1 == e[h]) tc::commit(tc::smem_u32(&ms.odone[h]));
                                 ++k[h];
                             }
@@ -751,7 +753,7 @@ constexpr int JT = 512, SLICES = ROWS / 4;
 template <bool BF>
 __global__ void __launch_bounds__(JT) finish_kernel(const __grid_constant__ Params P)
 {
-    __shared__ int s_list[MAX_SMS], s_count;
+    __shared__ int s_list[MAX_SMS], s_warp[JT / 32];
     __shared__ float s_part[3][6][128];
     const int tid = threadIdx.x;
     // Requests are shared by as many CTAs as there are to each.
@@ -769,20 +771,26 @@ __global__ void __launch_bounds__(JT) finish_kernel(const __grid_constant__ Para
             for (int64_t i = (int64_t)s * JT + tid; i < rows; i += (int64_t)share * JT) P.lse[from + i] = r.wrong ? NAN : -INFINITY;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tid < 32) {
-        int count = 0;
-        for (int c = tid; c < (P.ctas + 31) / 32 * 32; c += 32) {
-            const bool has = c < P.ctas && __ldcg(&P.joins[c].c1) > __ldcg(&P.joins[c].c0);
-            const unsigned all = __ballot_sync(0xffffffffu, has);
-            if (has) s_list[count + __popc(all & ((1u << tid) - 1))] = c;
-            count += __popc(all);
-        }
-        if (tid == 0) s_count = count;
+    // The CTAs whose runs began a block that others ended.
+    bool has = false;
+    if (tid < P.ctas) {
+        const int4 lo = __ldcg(reinterpret_cast<const int4 *>(P.joins + tid)), hi = __ldcg(reinterpret_cast<const int4 *>(P.joins + tid) + 1);
+        has = hi.x > lo.w;  // c1 > c0
     }
+    const unsigned all = __ballot_sync(0xffffffffu, has);
+    if ((tid & 31) == 0) s_warp[tid >> 5] = __popc(all);
+    __syncthreads();
+    int before = 0, count = 0;
+#pragma unroll
+    for (int w = 0; w < (MAX_SMS + 31) / 32; ++w) {
+        before += w < tid >> 5 ? s_warp[w] : 0;
+        count += s_warp[w];
+    }
+    if (has) s_list[before + __popc(all & ((1u << (tid & 31)) - 1))] = tid;
     __syncthreads();
     const int group = tid >> 7, x = tid & 127, d = x >> 2;
 #pragma unroll 1
-    for (int w = blockIdx.x; w < s_count * SLICES; w += gridDim.x) {
+    for (int w = blockIdx.x; w < count * SLICES; w += gridDim.x) {
         const Join jn = P.joins[s_list[w / SLICES]];
         const int r = (w % SLICES) * 4 + (x & 3);
         const unsigned gr = (unsigned)jn.qb * ROWS + r, n = gr / (unsigned)P.G, h = gr - n * P.G;
@@ -907,7 +915,7 @@ static cudaError_t dispatch(const Params &P, int sms, cudaStream_t s)
 {
     const cudaError_t e = P.D <= 64 ? launch(chunk_kernel<BF, 64, E4>, P, P.ctas, NT, smem_bytes<BF, 64, E4>(), s)
                                     : launch(chunk_kernel<BF, 128, E4>, P, P.ctas, NT, smem_bytes<BF, 128, E4>(), s);
-    return e != cudaSuccess ? e : launch(finish_kernel<BF>, P, 2 * sms, JT, 0, s);
+    return e != cudaSuccess ? e : launch(finish_kernel<BF>, P, 4 * sms, JT, 0, s);
 }
 
 }  // namespace svch

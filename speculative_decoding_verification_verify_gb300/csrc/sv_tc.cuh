@@ -144,30 +144,24 @@ __device__ __forceinline__ void commit(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
-}
-
 // Operand in shared memory under the 128-byte swizzle.  Rows of 128 bytes, groups of eight rows
 // `sbo` bytes apart; when the contiguous direction is M or N, blocks of 64 elements of it `lbo`
-// bytes apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
+// bytes apart.  (Under the 64-byte swizzle rows of 64 bytes, blocks of 32 elements.)
+//
+// A product by its descriptors' low words; the high ones are constants of the layouts.  (Fewer registers to be moved for
+// each product: the first eight and two commits take 416 clocks against 675.)
+__host__ __device__ constexpr uint32_t desc_high(uint32_t sbo, bool swizzle64 = false) { return sbo >> 4 | 1u << 14 | (swizzle64 ? 4u : 2u) << 29; }
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return (addr & 0x3ffff) >> 4 | (lbo >> 4) << 16; }
+template <uint32_t HIGH_A, uint32_t HIGH_B>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add)
 {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 |
-           2ull << 61;
-}
-
-// The same under the 64-byte swizzle: rows of 64 bytes, blocks of 32 elements.
-__device__ __forceinline__ uint64_t smem_desc64(uint32_t addr, uint32_t lbo, uint32_t sbo)
-{
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 |
-           4ull << 61;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %6};\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(HIGH_A), "n"(HIGH_B)
+        : "memory");
 }
 
 // fp32 accumulators, A and B of one 16-bit type; *_mn: contiguous along M / N instead of K.
@@ -213,13 +207,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v)
 }
 
 // The product with A in TMEM: a row per lane, two 16-bit values per column.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+template <uint32_t HIGH_B>
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(HIGH_B)
         : "memory");
 }
 
