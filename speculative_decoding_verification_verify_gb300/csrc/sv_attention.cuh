@@ -73,11 +73,9 @@ constexpr int COST_TILE = 2, COST_SEGMENT = 4;
 // Warpgroups of the softmax: two hold 16 columns a thread at most, and so do four where there are 64 columns
 // (with 32 a thread: one tree of 16 over 131000 positions 105.6 us against 102.7).
 __host__ __device__ constexpr int groups(int nq) { return nq == 64 ? 4 : 2; }
-// (8-bit rows: a warpgroup for keys and one for values in a team, the first of them where the 16-bit copies are, the
-// others behind the softmax's.  A warp's way through a tile is some 3500 clocks; two teams are all the threads that there
-// are registers for.)
-__host__ __device__ constexpr int teams(int nq) { return nq == 64 ? 1 : 2; }
-__host__ __device__ constexpr int threads(int nq, bool e4) { return 256 + 128 * groups(nq) + (e4 ? 256 * teams(nq) - 128 : 0); }
+// (8-bit rows: a warpgroup more of copies, behind the softmax's.  With two for keys and two for values, every other tile
+// each, 64 requests of one token over 8192 positions took 407 us against 367.)
+__host__ __device__ constexpr int threads(int nq, bool e4) { return 256 + 128 * groups(nq) + (e4 ? 128 : 0); }
 // CTAs that an SM holds.  With at most 8 columns a thread, 64 registers nearly do (32 bytes spilled), and one CTA
 // works while the other is between segments: 96 requests of 12 heads of 64 take 44.4 us against 52.4, 128
 // requests of up to 504 positions (8 key heads of 128) 30.2 against 30.7.  Two units of 128 dimensions are then all
@@ -110,11 +108,12 @@ struct Layout {
     // (8-bit rows: two units of keys and two of values, an even number for the two warpgroups that fill them; with one of
     // each 195 us where two take 140.)
     static constexpr int NU = E4 ? 4 * 128 / DP : ctas_per_sm(NQ, E4) == 2 ? (DP == 64 ? 5 : 2) : 5 * 128 / DP;
+    static constexpr int AHEAD = NQ == 64 ? (DP == 64 ? 3 : 1) : 2 * 128 / DP, RING = E4 ? AHEAD * (128 * DP + 512) : 0;  // of keys, of values
     static constexpr int QBYTES = NQ * DP * 2;
     static constexpr int QSTEP = QBYTES < 1024 ? 1024 : QBYTES;
     static constexpr int PROW = E4 && NQ <= 32 ? 64 : 128;  // a row of 32 or 64 columns per position
     static constexpr int PBYTES = TILE * PROW;
-    static constexpr int Q0 = NU * UNIT, P0 = Q0 + 2 * QSTEP, M0 = P0 + PBYTES;
+    static constexpr int Q0 = NU * UNIT, P0 = Q0 + 2 * QSTEP, R0 = P0 + PBYTES, M0 = R0 + 2 * RING;
     static constexpr int COLS = 3 * NQ <= 64 ? 64 : 3 * NQ <= 128 ? 128 : 256;  // TMEM columns
 };
 
@@ -165,7 +164,6 @@ struct Misc {
         int h, left, seg, pad;
     } slots[E4 ? SLOTS : 1];
     uint64_t slotfull[SLOTS], slotempty[SLOTS];
-    uint16_t powers[E4 ? 8 * teams(NQ) : 1][32];  // of a warp's rows
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -286,7 +284,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
         }
         for (int i = 0; i < SEGS; ++i) {
             tc::bar_init(tc::smem_u32(&ms.segfull[i]), 1);
-            tc::bar_init(tc::smem_u32(&ms.segempty[i]), NT / 32 - (E4 ? 8 * teams(NQ) + 1 : 1));  // warps but the one that lists; 8-bit copies have the slots' list
+            tc::bar_init(tc::smem_u32(&ms.segempty[i]), NT / 32 - (E4 ? 9 : 1));  // warps but the one that lists; 8-bit copies have the slots' list
         }
         for (int i = 0; E4 && i < SLOTS; ++i) {
             tc::bar_init(tc::smem_u32(&ms.slotfull[i]), 33);
@@ -372,65 +370,69 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
     if (t1 > t0) {
         if (E4 && (warp < 4 || warp >= 8 + 4 * WG)) {
             // ---- 8-bit tiles into shared memory ---------------------------------------------
-            // Warpgroups have the keys and the values in turn, two teams of two every other tile.  As a row of a tile is
-            // stored, that of the warpgroup's next tile is loaded in its place.
-            using Rows = sv::E4m3Rows<BF, DP>;
-            constexpr int TEAMS = teams(NQ);
-            const int cw = warp & 3, wg = warp < 4 ? 0 : (warp - 4 - 4 * WG) >> 2, kv = wg & 1;
-            Rows rows(&ms.powers[4 * wg + cw], cw, lane, P.D);
+            // One warpgroup has the keys, the other the values.  When a tile has been read its place in the ring is filled
+            // with the one AHEAD tiles on, whose slots are listed, while it is widened.
+            constexpr int AHEAD = L::AHEAD;
+            using Feed = sv::E4m3Feed<BF, DP, AHEAD>;
+            const int cw = warp & 3, kv = warp < 4 ? 0 : 1;
+            Feed feed(s0 + L::R0 + kv * L::RING, cw, lane, P.D);
             const unsigned char *const cache = kv ? P.v : P.k;
             const uint32_t stride = kv ? P.v_slot : P.k_slot;
-            int n = wg >> 1, u = wg;  // the next tile to be looked for; the unit of the one at hand
-            bool ok = true, last = false, whole = false;
-            int slot[Rows::ITER], power = 0, h = 0;  // of the next tile; its powers of two are asked for as it is found
-            // 1: its slots are here, 0: there are no more tiles, 2: they are not listed yet.
-            auto find = [&](bool block) {
+            int r = 0, count = 0, n = 0, u = kv;  // the oldest tile's place; tiles under way; the next to ask for; the oldest's unit
+            bool ok = true, last = false;
+            // The next tile's slots, into a place: 1, or 0 when there are none, 2 when they are not listed yet.
+            auto ask = [&](int at, bool block) {
                 if (last) return 0;
                 const uint32_t bar = tc::smem_u32(&ms.slotfull[n % SLOTS]);
                 const bool there = block ? tc::bar_wait(bar, (n / SLOTS) & 1, abort) : tc::bar_test(bar, (n / SLOTS) & 1);
                 if (!__all_sync(0xffffffffu, there)) return block ? 0 : 2;
                 const auto &list = ms.slots[n % SLOTS];
-                const int left = list.left;
-                h = list.h;
+                const int h = list.h, left = list.left;
                 last = h < 0;
                 if (last) return 0;
-                const int mine = list.slot[Rows::place(rows.own)];
+                const int mine = list.slot[Feed::place(feed.own)];
+                int slot[Feed::ITER];
 #pragma unroll
-                for (int i = 0; i < Rows::ITER; i += 4) {
-                    const int4 four = *reinterpret_cast<const int4 *>(&list.slot[rows.first() + i]);
+                for (int i = 0; i < Feed::ITER; i += 4) {
+                    const int4 four = *reinterpret_cast<const int4 *>(&list.slot[feed.first() + i]);
                     slot[i] = four.x, slot[i + 1] = four.y, slot[i + 2] = four.z, slot[i + 3] = four.w;
                 }
-                const bool fine = (unsigned)mine < (unsigned)P.num_slots, in = rows.own < left;
+                const bool fine = (unsigned)mine < (unsigned)P.num_slots, in = feed.own < left;
                 if (in && !fine)
 #pragma unroll
                     for (int i = 0; i < WG; ++i) *(volatile int *)&ms.bad[i][list.seg % FLAGS] = 1;
-                whole = __all_sync(0xffffffffu, in && fine);
+                const bool whole = __all_sync(0xffffffffu, in && fine);
                 if (!whole)
 #pragma unroll
-                    for (int i = 0; i < Rows::ITER; ++i)
-                        if (rows.row(i) >= left || (unsigned)slot[i] >= (unsigned)P.num_slots) slot[i] = -1;
-                power = 127;
-                if (in && fine) power = __ldg(cache + (uint64_t)(uint32_t)mine * stride + P.Hkv * P.D + h);
+                    for (int i = 0; i < Feed::ITER; ++i)
+                        if (feed.row(i) >= left || (unsigned)slot[i] >= (unsigned)P.num_slots) slot[i] = -1;
+                feed.ask(at, whole, cache + h * P.D, stride, slot);
+                feed.asked(at, count, in && fine ? mine : -1, cache, stride, P.Hkv * P.D + h);
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem_u32(&ms.slotempty[n % SLOTS]));
-                n += TEAMS;
+                ++n;
+                ++count;
                 return 1;
             };
-            bool loaded = false;
             for (;;) {
-                if (!loaded) {
-                    if (find(true) != 1) break;
-                    rows.load(whole, cache + h * P.D, stride, slot);
-                }
-                const int mine = power;
-                loaded = find(false) == 1;
-                rows.powers(mine, lane);
+                // The places without a tile: all at the beginning, later where slots were not listed in time.
+                while (count < AHEAD && ask((r + count) % AHEAD, count == 0) == 1) {}
+                if (count == 0) break;
+                for (int i = count; i < AHEAD; ++i) feed.commit();  // (what is waited for is counted in groups)
+                feed.wait();
+                typename Feed::Tile tile;
+                feed.read(r, tile);
+                --count;
+                const int at = r;
+                r = r + 1 == AHEAD ? 0 : r + 1;
+                if (count == AHEAD - 1) ask(at, false);
                 if (u >= NU) ok = __all_sync(0xffffffffu, tc::bar_wait(tc::smem_u32(&ms.empty[u % NU]), (u / NU + 1) & 1, abort));
                 if (!ok) break;
-                rows.store(s0 + (u % NU) * L::UNIT, loaded, whole, cache + h * P.D, stride, slot);
+                feed.write(s0 + (u % NU) * L::UNIT, tile);
                 tc::bar_arrive(tc::smem_u32(&ms.full[u % NU]));  // (the products' thread fences what it sees)
-                u += 2 * TEAMS;
+                u += 2;
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (!E4 && warp < 4) {
             const int cw = warp;
             // ---- tiles into shared memory -------------------------------------------------
@@ -658,7 +660,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 for (int i = 0; i < TILE / 32; ++i) {
                     const int row = lane + 32 * i;
                     const bool in = row < left && SV_INB(at + row, (int64_t)P.B * P.max_pos, 1103);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(&list.slot[sv::E4m3Rows<BF, DP>::place(row)])),
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(&list.slot[sv::E4m3Feed<BF, DP, 1>::place(row)])),
                                  "l"(P.slot_table + (in ? at + row : 0)), "r"(in ? 4 : 0)
                                  : "memory");
                 }
@@ -716,7 +718,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             }
             g.kind = 3;
             if (ok) put(g);
-            for (int i = 0; E4 && ok && i < teams(NQ); ++i) list(-1, 0, 0);  // each team comes to one
+            if (E4 && ok) list(-1, 0, 0);
             if (E4) asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp < 8) {
             // ---- queries and the tree's mask -----------------------------------------------

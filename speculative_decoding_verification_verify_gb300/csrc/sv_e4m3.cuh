@@ -207,71 +207,4 @@ struct E4m3Feed {
     }
 };
 
-// The same through registers: a warpgroup's tile of 128 rows is loaded as the one before it is stored.
-template <bool BF, int DP>
-struct E4m3Rows {
-    static constexpr int CPR = DP / 16, RPI = 32 / CPR, ITER = CPR;
-    uint16_t *const power;  // the warp's rows' powers of two
-    int own, sub;           // the row whose slot the lane keeps, of a tile
-    uint32_t to;
-    int offset;             // of the lane's chunk in a row; below 0: beyond the head
-    bool full;              // no lane's is
-    uint4 w[ITER];
-    uint32_t scale[ITER / 2];  // two rows' in each
-
-    __device__ __forceinline__ E4m3Rows(uint16_t (*p)[32], int warp, int lane, int D) : power(*p)
-    {
-        const int chunk = DP == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
-        sub = DP == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2;
-        own = warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);
-        const int first = warp * RPI + sub;
-        to = (chunk >> 2) * 128 * 128 + first * 128 + (((2 * chunk & 7) ^ (first & 7)) << 4);
-        offset = chunk * 16 < D ? chunk * 16 : -1;
-        full = D == DP;
-    }
-    __device__ __forceinline__ int row(int i) const { return (to >> 7 & 127) + 4 * RPI * i; }
-    static __device__ __forceinline__ int place(int row) { return row % (4 * RPI) * ITER + row / (4 * RPI); }
-    __device__ __forceinline__ int first() const { return (to >> 7 & 127) * ITER; }
-    __device__ __forceinline__ void load_row(int i, bool whole, const unsigned char *cache, uint32_t stride, int slot)
-    {
-        const unsigned char *const at = cache + (uint64_t)(uint32_t)slot * stride + offset;
-        if ((whole && full) || (slot >= 0 && offset >= 0))
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                         : "l"(at));
-        else
-            w[i] = make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ void load(bool whole, const unsigned char *cache, uint32_t stride, const int (&slot)[ITER])
-    {
-#pragma unroll
-        for (int i = 0; i < ITER; ++i) load_row(i, whole, cache, stride, slot[i]);
-    }
-    // The loaded tile's powers of two, of which the lane has its own row's.
-    __device__ __forceinline__ void powers(int mine, int lane)
-    {
-        power[lane % RPI * ITER + lane / RPI] = E4m3Scale<BF>::bits(mine);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < ITER / 2; ++i) scale[i] = reinterpret_cast<const uint32_t *>(power + sub * ITER)[i];
-        __syncwarp();
-    }
-    // The loaded tile to a unit; where `more`, the next one's rows in its place.
-    __device__ __forceinline__ void store(uint32_t unit, bool more, bool whole, const unsigned char *cache, uint32_t stride, const int (&slot)[ITER])
-    {
-#pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const E4m3Scale<BF> g((uint16_t)(scale[i / 2] >> 16 * (i & 1)));
-            const uint32_t at = unit + to + i * 4 * RPI * 128;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(g(w[i].x)), "r"(g(w[i].x >> 16)), "r"(g(w[i].y)),
-                         "r"(g(w[i].y >> 16))
-                         : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16), "r"(g(w[i].z)), "r"(g(w[i].z >> 16)), "r"(g(w[i].w)),
-                         "r"(g(w[i].w >> 16))
-                         : "memory");
-            if (more) load_row(i, whole, cache, stride, slot[i]);
-        }
-    }
-};
-
 }  // namespace sv
