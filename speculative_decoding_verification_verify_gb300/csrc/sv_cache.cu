@@ -234,7 +234,7 @@ struct Read {
 
 // A warp takes the keys and the values of two rows, so that its lanes have their places with few divisions, and 16
 // values of them a lane at a time, READ_U of those under way.  Stores of 32 bytes fill a sector each.
-constexpr int READ_NT = 256, READ_SIDES = 4, READ_U = 4;
+constexpr int READ_NT = 256, READ_SIDES = 4, READ_U = 2;
 
 __device__ __forceinline__ void store32(void *at, const uint4 &x, const uint4 &y)
 {
