@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             // with the one AHEAD tiles on, whose slots are listed, while it is widened.
             constexpr int AHEAD = L::AHEAD;
             using Feed = sv::E4m3Feed<BF, DP, AHEAD>;
-            const int cw = warp & 3, kv = warp < 4 ? 0 : 1;
+            const int cw = warp & 3, kv = warp < 4 ? 0 : (warp - 4 - 4 * WG) >> 2;
             Feed feed(s0 + L::R0 + kv * L::RING, cw, lane, P.D);
             const unsigned char *const cache = kv ? P.v : P.k;
             const uint32_t stride = kv ? P.v_slot : P.k_slot;
