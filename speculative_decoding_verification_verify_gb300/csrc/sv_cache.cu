@@ -10,6 +10,9 @@
 // magnitude are a few exchanges, and a row passes through registers once.
 #include "sv_e4m3.cuh"
 
+#include <initializer_list>
+#include <type_traits>
+
 namespace svc {
 
 using sv::Half2;
@@ -51,11 +54,29 @@ __device__ __forceinline__ uint4 to_half(const float (&x)[8])
                       Half2<BF>::pack(x[6], x[7]));
 }
 
+// a * b + c * d to half a unit or so: the second product's rounding is made good.
+__device__ __forceinline__ float sum2(float a, float b, float c, float d)
+{
+    const float p = c * d, e = fmaf(c, d, -p);
+    return fmaf(a, b, p) + e;
+}
+
+// What is rounded to four digits is worked out more exactly than what keeps eight: each of fp32's roundings that is saved
+// is as many fewer values next to a border that fall on its other side.
+template <bool FINE>
 __device__ __forceinline__ void turn(float &x, float &y, float c, float s)
 {
-    const float a = x * c - y * s, b = y * c + x * s;
+    const float a = FINE ? sum2(x, c, -y, s) : x * c - y * s, b = FINE ? sum2(y, c, x, s) : y * c + x * s;
     x = a;
     y = b;
+}
+
+template <bool FINE>
+__device__ __forceinline__ float scaled(float x, float r, float w)
+{
+    if (!FINE) return x * (r * w);
+    const float p = r * w, e = fmaf(r, w, -p);
+    return fmaf(x, p, x * e);
 }
 
 template <bool BF, bool ADJ, bool E4>
@@ -155,31 +176,37 @@ __global__ void __launch_bounds__(NT) append_kernel(const Append P)
         else va = vb = make_uint4(0, 0, 0, 0);
         const uint4 *weight = is_q ? P.q_norm : is_k ? P.k_norm : nullptr;
         if (P.q_norm || P.k_norm) {
-            float sum = 0.f;
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += x[i] * x[i] + y[i] * y[i];
+            for (int i = 0; i < 8; ++i) part[i & 3] += x[i] * x[i] + y[i] * y[i];
+            float sum = (part[0] + part[1]) + (part[2] + part[3]);
             for (int o = P.lanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (weight && mine) {
-                const float r = rsqrtf(sum / (float)P.D + P.eps);
+                const float r = __frsqrt_rn(sum / (float)P.D + P.eps);
                 float w[8];
                 to_float<BF>(__ldg(weight + i0), w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
+                for (int i = 0; i < 8; ++i) x[i] = E4 && is_k ? scaled<true>(x[i], r, w[i]) : scaled<false>(x[i], r, w[i]);
                 to_float<BF>(__ldg(weight + i1), w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= r * w[i];
+                for (int i = 0; i < 8; ++i) y[i] = E4 && is_k ? scaled<true>(y[i], r, w[i]) : scaled<false>(y[i], r, w[i]);
             }
         }
-        if (live && turned && (is_q || is_k)) {
+        auto rotate = [&](auto fine) {
+            constexpr bool F = decltype(fine)::value;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (!ADJ) {
-                    turn(x[i], y[i], cs[i], sn[i]);
+                    turn<F>(x[i], y[i], cs[i], sn[i]);
                 } else if (i < 4) {
-                    turn(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
-                    turn(y[2 * i], y[2 * i + 1], cs[4 + i], sn[4 + i]);
+                    turn<F>(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
+                    turn<F>(y[2 * i], y[2 * i + 1], cs[4 + i], sn[4 + i]);
                 }
             }
+        };
+        if (live && turned) {
+            if (E4 && is_k) rotate(std::true_type());
+            else if (is_q || is_k) rotate(std::false_type());
         }
         if (is_q) {
             if (mine) {
