@@ -23,8 +23,8 @@
  *     count and shared memory per SM and raises the dynamic shared-memory limits of the kernels
  *     that take more than the default (cudaFuncSetAttribute: the finalising kernels, which size
  *     their request so that at most ceil(B / SMs) of their CTAs share an SM, and the top-k / top-p
- *     ring kernel's 109 KiB; attention and logprobs, up to 214 KiB); make it before any stream capture
- *     on that device (spec_verify_attention and spec_verify_logprobs: the first call of each).  The library keeps
+ *     ring kernel's 109 KiB; attention and logprobs, up to 227 KiB); make it before any stream capture
+ *     on that device (the attention entry points and spec_verify_logprobs: the first call of each).  The library keeps
  *     this per device for the life of the process, so it must not be used again after
  *     cudaDeviceReset.
  *   - The return value is a host status, known when the call returns:
@@ -86,7 +86,7 @@ extern "C" {
                                              accept_len >= N, or a path entry outside [0, N); append,
                                              attention: lengths or positions that do not fit */
 #define SPEC_VERIFY_DEV_BAD_KV_SLOT 6     /* KV cache: a slot outside [0, num_slots) */
-#define SPEC_VERIFY_DEV_TIMEOUT 7      /* attention, logprobs: a bounded wait inside the kernel ran out;
+#define SPEC_VERIFY_DEV_TIMEOUT 7      /* attention (every form), logprobs: a bounded wait inside the kernel ran out;
                                           the outputs are undefined (nothing in them says so: the
                                           event shows here and in spec_verify_wait_timeouts), and the
                                           workspace has to be zero-filled again before its next use */

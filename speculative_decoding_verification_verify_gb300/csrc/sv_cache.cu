@@ -8,6 +8,11 @@
 // Bytes bound both.  A thread of append has two 16-byte vectors of a head, which under either pairing hold whole
 // pairs (as in sv_append.cu); the lanes that share a head are neighbours, so that a norm's sum and a head's largest
 // magnitude are a few exchanges, and a row passes through registers once.
+//
+// Measured (GB300, copy rate 6.68 TB/s; 32 query and 8 key heads of 128): append of 8194 rows of fp16 with norms to 8-bit
+// rows 42 us for 185 MB, 4.4 TB/s, its instructions at 70% of the issue slots; with the rows read back 58 us for 237 MB.
+// 384 rows 4.5 us, one row 3 us.  Read of 48 requests' 24 thousand 8-bit rows 27 us for 127 MB, 4.7 TB/s; of 60001 rows of 4
+// heads of 80 28 us for 116 MB, 4.1 TB/s: the chain slot table, slot, row at 48 warps an SM.
 #include "sv_e4m3.cuh"
 
 #include <initializer_list>

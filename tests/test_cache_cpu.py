@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import plain64_cache as pc
-from speculative_decoding_verification_verify_gb300 import _build, binding
+from speculative_decoding_verification_verify_gb300 import _build, binding, binding_cache
 
 A, ODD, ODD4 = 0x10000, 0x10008, 0x10002  # never dereferenced
 E = binding.E4M3
@@ -98,7 +98,7 @@ def test_chunk(lib):
         assert chunk(lib, **bad) == binding.EINVAL, bad
     assert chunk(lib, nbytes=16) == binding.EWORKSPACE
     assert chunk(lib, ws=0x10080) == binding.EWORKSPACE
-    need = binding.spec_verify_attention_chunk_workspace_bytes
+    need = binding_cache.spec_verify_attention_chunk_workspace_bytes
     assert need(2, 800, 32, 8, 128, 64) > 0 and need(1, 1 << 20, 64, 8, 64, 1 << 20) > 0
     for bad in ((0, 8, 32, 8, 128, 64), (2, 8, 32, 5, 128, 64), (2, 8, 32, 8, 130, 64), (2, 8, 32, 8, 128, 0)):
         assert need(*bad) == 0
@@ -106,9 +106,9 @@ def test_chunk(lib):
 
 def test_row_bytes(lib):
     for Hkv, D in ((1, 16), (8, 128), (3, 80), (5, 112), (16, 512)):
-        assert binding.spec_verify_kv_e4m3_row_bytes(Hkv, D) == pc.row_bytes(Hkv, D)
+        assert binding_cache.spec_verify_kv_e4m3_row_bytes(Hkv, D) == pc.row_bytes(Hkv, D)
     for Hkv, D in ((0, 64), (1, 0), (1, 24), (1, 528), (1 << 20, 64)):
-        assert binding.spec_verify_kv_e4m3_row_bytes(Hkv, D) == 0
+        assert binding_cache.spec_verify_kv_e4m3_row_bytes(Hkv, D) == 0
 
 
 def test_tensors_on_the_host_are_refused(lib):
@@ -116,13 +116,13 @@ def test_tensors_on_the_host_are_refused(lib):
     c = torch.zeros((9, pc.row_bytes(2, 64)), dtype=torch.uint8)
     i = torch.zeros((1, 8), dtype=torch.int32)
     with pytest.raises(ValueError):
-        binding.spec_verify_kv_append_ex(h, h[:, :, :2], h[:, :, :2], c, c, i, i[0, :1], None)
+        binding_cache.spec_verify_kv_append_ex(h, h[:, :, :2], h[:, :, :2], c, c, i, i[0, :1], None)
     with pytest.raises(ValueError):
-        binding.spec_verify_kv_read(c, c, i, i[0, :1], 2, kv_heads=2, head_dim=64, dtype=torch.bfloat16)
+        binding_cache.spec_verify_kv_read(c, c, i, i[0, :1], 2, kv_heads=2, head_dim=64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
-        binding.spec_verify_attention_e4m3(h, c, c, i, i[0, :1], kv_heads=2)
+        binding_cache.spec_verify_attention_e4m3(h, c, c, i, i[0, :1], kv_heads=2)
     with pytest.raises(ValueError):
-        binding.spec_verify_attention_chunk(h, c, c, i, i[0, :1], kv_heads=2)
+        binding_cache.spec_verify_attention_chunk(h, c, c, i, i[0, :1], kv_heads=2)
 
 
 def test_the_plain_form_of_the_rows():
