@@ -91,6 +91,13 @@ def test_ragged_nodes_many_requests_and_long_ones():
     check(make([131072 - 5], 5, 8, 2, 128, BF, seed=5, tree=True))
 
 
+@pytest.mark.parametrize("Hkv", [5, 76, 77, 160])
+def test_more_heads_than_runs(Hkv):
+    """A key head has CTAs of its own while there are enough of them."""
+    check(make([100, 0, 300], 1, Hkv, Hkv, 64, BF, seed=Hkv))
+    check(make([9000, 700], 3, 2 * Hkv, Hkv, 64, FP, seed=Hkv))
+
+
 def test_magnitudes_of_the_whole_range():
     """Values of heads from 2^-60 to beyond the largest that a row holds."""
     for dtype, lo, hi in ((BF, -60, 14), (FP, -14, 13)):

@@ -235,6 +235,19 @@ def test_faults(e4m3):
     run(nodes, 5, {(b, n) for b in (1, 3) for n in range(80)})
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_heads_and_two_calls_at_once(e4m3):
+    s, t = make([0, 400], 90, 160, 160, 64, BF, e4m3, seed=14), make([2000], 70, 8, 1, 128, BF, e4m3, seed=15)
+    one, two = check(s), check(t)
+    side = [torch.cuda.Stream() for _ in range(2)]
+    for x in side:
+        x.wait_stream(torch.cuda.current_stream())
+    got = [(call(s, stream=side[0]), call(t, stream=side[1])) for _ in range(5)]
+    torch.cuda.synchronize()
+    for a, c in got:
+        assert torch.equal(a.out, one.out) and torch.equal(c.out, two.out) and torch.equal(c.lse, two.lse)
+
+
 def test_slots_past_a_request_are_not_followed():
     s = make([33, 129], 70, 4, 1, 128, BF, seed=12)
     want = call(s)
