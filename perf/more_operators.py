@@ -173,11 +173,6 @@ def _parents(B, N, g):
     return p.int()
 
 
-def _two_to(e):
-    """2^e in 32 bits, -127 < e < 128, by its bits (a library's power need not be exact)."""
-    return (e.int() + 127 << 23).view(torch.float32)
-
-
 def _powers(x, dtype):
     """The exponents of heads' powers of two: the smallest with which the largest value fits e4m3."""
     m, e = torch.frexp(x.abs().amax(-1))
@@ -187,7 +182,7 @@ def _powers(x, dtype):
 def _rounded(x, dtype):
     """x [..., D] in 32 bits as e4m3, and the exponents."""
     e = _powers(x, dtype)
-    y = (x * _two_to(-e[..., None])).clamp(-LARGEST, LARGEST)
+    y = torch.ldexp(x, -e[..., None]).clamp(-LARGEST, LARGEST)
     return y.to(torch.float8_e4m3fn), e
 
 
@@ -304,7 +299,7 @@ def _values(s, cache, slot):
     Hkv, D = s["Hkv"], s["D"]
     rows = cache[slot]
     x = rows[..., : Hkv * D].contiguous().view(torch.float8_e4m3fn).float().unflatten(-1, (Hkv, D))
-    return x * _two_to(rows[..., Hkv * D: Hkv * (D + 1)].int()[..., None] - 127)
+    return torch.ldexp(x, rows[..., Hkv * D: Hkv * (D + 1)].int()[..., None] - 127)
 
 
 def _depth(parents):
@@ -443,8 +438,8 @@ def _nearest(x, dtype):
     grid = _e4m3_grid()
     mid = (grid[1:] + grid[:-1]) / 2
     m, e = torch.frexp(x.abs().amax(-1, keepdim=True) / grid[-1])
-    p = (e - (m == 0.5).int()).clamp(EXP_LO[dtype], EXP_HI)  # the smallest power that is no smaller
-    step = (p.long() + 1023 << 52).view(torch.float64)
+    p = (e - (m == 0.5).int()).double()  # the smallest power that is no smaller
+    step = 2.0 ** p.clamp(EXP_LO[dtype], EXP_HI)
     y = (x.abs() / step).clamp(max=float(grid[-1]))
     lower, upper = torch.bucketize(y, mid), torch.bucketize(y, mid, right=True)
     at = torch.where(lower % 2 == 0, lower, upper)  # they differ at a tie: the even one
@@ -459,8 +454,7 @@ def _exact_rows(s, cache, slot):
     bits = rows[:, : Hkv * D].long()
     x = grid[(bits & 127).clamp(max=126)] * (1 - 2 * (bits >> 7))
     x = torch.where(bits & 127 == 127, math.nan, x)
-    step = (rows[:, Hkv * D: Hkv * (D + 1)].long() + (1023 - 127) << 52).view(torch.float64)
-    return x.view(-1, Hkv, D) * step[:, :, None]
+    return x.view(-1, Hkv, D) * 2.0 ** (rows[:, Hkv * D: Hkv * (D + 1)].double() - 127)[:, :, None]
 
 
 def _exact_append(s):
