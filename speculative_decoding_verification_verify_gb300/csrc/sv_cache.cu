@@ -59,11 +59,12 @@ __device__ __forceinline__ uint4 to_half(const float (&x)[8])
                       Half2<BF>::pack(x[6], x[7]));
 }
 
-// a * b + c * d to half a unit or so: the second product's rounding is made good.
+// a * b + c * d, the second product's rounding made good: two roundings are left, of the sum and of what makes it good.
+// (An infinite product has no rounding: the difference is NaN, the sum is what it is.)
 __device__ __forceinline__ float sum2(float a, float b, float c, float d)
 {
-    const float p = c * d, e = fmaf(c, d, -p);
-    return fmaf(a, b, p) + e;
+    const float p = c * d, e = fmaf(c, d, -p), s = fmaf(a, b, p), y = s + e;
+    return y == y ? y : s;
 }
 
 // What is rounded to four digits is worked out more exactly than what keeps eight: each of fp32's roundings that is saved

@@ -1,0 +1,52 @@
+"""The 8-bit cache at the ends of the types' ranges."""
+import math
+
+import pytest
+import torch
+
+import plain64_cache as pc
+import test_gpu_cache as tc
+from plain64 import rotate
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from speculative_decoding_verification_verify_gb300 import _build
+
+    _build.build()
+    torch.cuda.set_device(DEV)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot", [64, 32])
+def test_infinite_keys_saturate(dtype, interleaved, rot):
+    """An infinity in either place of a pair, in both, and where nothing is rotated: what is infinite after the rotation
+    is 57344 with its sign, and only an infinity less another is NaN."""
+    s = tc.setup(1, 1, 2, 6, 64, rot, dtype, True, seed=rot, norm=False, committed=[3])
+    i = torch.arange(rot // 2, device=DEV)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
+    k = s["k"][0, 0]
+    k[0, a[3]], k[1, b[5]], k[2, a[0]], k[2, b[0]] = math.inf, -math.inf, math.inf, math.inf
+    k[3, a[1]], k[3, b[2]], k[3, 63] = -math.inf, math.inf, math.nan
+    k[4, 62] = -math.inf
+    tc.call(s, interleaved=interleaved)
+    cs = s["cos_sin"][3].double()
+    assert (cs != 0).all()
+    y, size = rotate(k.double(), cs[: rot // 2], cs[rot // 2:], rot, interleaved)
+    row = s["k_cache"][int(s["slot_table"][0, 3])]
+    got = pc.decode(row, 6, 64)
+    infinite, fine = torch.isinf(y), torch.isfinite(y)
+    assert int(infinite[:4].sum()) >= 6
+    assert torch.equal(torch.isnan(got), torch.isnan(y))
+    assert torch.equal(got[infinite], pc.LARGEST * 2.0 ** pc.HI * y[infinite].sign())
+    e = row[6 * 64: 6 * 65].int() - 127
+    assert torch.equal(e[infinite.any(1)], torch.full_like(e[infinite.any(1)], pc.HI))
+    # Half a step of four digits, the smallest step 2^(e - 9); three roundings of fp32 before.
+    half = torch.maximum(y.abs() * 2.0 ** -4, 2.0 ** (e.double()[:, None] - 10)) + 2.0 ** -22 * size
+    assert ((got - y).abs() <= half)[fine].all()
