@@ -369,7 +369,7 @@ int spec_verify_attention(const void *q, int dtype, int64_t q_stride, const void
 /*
  * spec_verify_kv_append with the heads' norms in the same pass and the cache's rows in 16 or in 8 bits.  Arguments,
  * rotation, faults and the rows past num_nodes as there, and
- *   q_norm, k_norm  [D] of q's type, 16-byte aligned, or NULL (no norm): a head of q or k is first
+ *   q_norm, k_norm  [D] of q's type, finite, 16-byte aligned, or NULL (no norm): a head of q or k is first
  *                  x * w / sqrt(mean(x^2) + eps), its sum of squares in fp32; eps finite, >= 0
  *   cache_dtype    dtype: a slot is [Hkv][D] of it, and the slot strides count its elements; or
  *                  SPEC_VERIFY_E4M3: a slot is a row of spec_verify_kv_e4m3_row_bytes(Hkv, D) bytes: [Hkv][D] e4m3,

@@ -77,12 +77,14 @@ __device__ __forceinline__ void turn(float &x, float &y, float c, float s)
     y = b;
 }
 
+// x * r * w, r the reciprocal of a root of x's head: x * r is a number of modest size, r * w may pass fp32.
 template <bool FINE>
 __device__ __forceinline__ float scaled(float x, float r, float w)
 {
-    if (!FINE) return x * (r * w);
-    const float p = r * w, e = fmaf(r, w, -p);
-    return fmaf(x, p, x * e);
+    const float p = x * r;
+    if (!FINE) return p * w;
+    const float e = fmaf(x, r, -p);
+    return fmaf(p, w, e * w);
 }
 
 template <bool BF, bool ADJ, bool E4>

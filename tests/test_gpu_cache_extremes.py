@@ -50,3 +50,16 @@ def test_infinite_keys_saturate(dtype, interleaved, rot):
     # Half a step of four digits, the smallest step 2^(e - 9); three roundings of fp32 before.
     half = torch.maximum(y.abs() * 2.0 ** -4, 2.0 ** (e.double()[:, None] - 10)) + 2.0 ** -22 * size
     assert ((got - y).abs() <= half)[fine].all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_norms_whose_factors_pass_fp32(e4m3):
+    """The root's reciprocal times the weight is beyond fp32; the values are not."""
+    for seed, up in ((1, 100), (2, 66)):
+        s = tc.setup(2, 2, 4, 2, 64, 64, BF, e4m3, seed=seed)
+        for x in ("q", "k"):
+            s[x].mul_(2.0 ** -60)
+            s[x][..., 5::16] *= 2.0 ** -60
+            s[x + "_norm"].mul_(2.0 ** up)
+        got = tc.check(s, eps=0.0)
+        assert torch.isfinite(got.float()).all() and got.float().abs().max() > 2.0 ** (up - 2)
