@@ -15,7 +15,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "sv_kv.cu", "sv_bud
                                               "sv_attention_e4m3.cu", "sv_chunk.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("sv_device.cuh", "sv_draw.cuh", "sv_stream.cuh", "sv_rescan.cuh",
                                                   "sv_decide.cuh", "sv_topkp.cuh", "sv_topkp_ring.cuh",
-                                                  "sv_check.cuh", "sv_ops.cuh", "sv_tc.cuh", "sv_e4m3.cuh",
+                                                  "sv_check.cuh", "sv_ops.cuh", "sv_tc.cuh", "sv_e4m3.cuh", "sv_reference.cuh",
                                                   "sv_attention.cuh")] + [
     os.path.join(INCLUDE, "spec_verify.h")]
 

@@ -57,13 +57,17 @@
 #pragma once
 
 #include "sv_e4m3.cuh"
+#include "sv_reference.cuh"
 #include "sv_tc.cuh"
 
 #include <mutex>
 
 namespace svatt {
 
+using sv::ex2;
+using sv::FAR;
 using sv::Half2;
+using sv::lift;
 
 constexpr int TILE = 128;     // positions per tile
 constexpr int MAXD = 128;
@@ -73,9 +77,6 @@ constexpr int FLAGS = 16;     // bad-slot flags: more than the segments the ring
 constexpr int SEGS = 8;       // segments listed ahead
 constexpr int SLOTS = 4;      // tiles whose slots are listed ahead (8-bit rows)
 constexpr float SLACK = 8.f;  // log2 of how much a weight may pass the reference's
-constexpr float FAR = 0x1p24f;  // of a reference times the scale
-// log2 of the reference's weight.
-__host__ __device__ constexpr float lift(bool bf16) { return bf16 ? 0.f : 7.f; }
 // In half tiles.  A segment at 3 or 5: 45.9 or 46.8 us against 45.8 for the 96 short requests above, 20.7 or 21.2
 // against 20.8 for the 48 trees; at 2 (with one CTA per SM) 63 against 56.
 constexpr int COST_TILE = 2, COST_SEGMENT = 4;
@@ -175,13 +176,6 @@ struct Misc {
     } slots[E4 ? SLOTS : 1];
     uint64_t slotfull[SLOTS], slotempty[SLOTS];
 };
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ float warp_max(float x)
 {
@@ -807,7 +801,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             const int col0 = wg * CW;
             const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16) + col0;
             // A reference's exponent, negated: what is added to a score times the scale.
-            auto minus = [&](float ref) { return ref == -INFINITY ? 0.f : fmaf(-ref, P.scale_log2, lift(BF)); };
+            auto minus = [&](float ref) { return sv::reference_add<BF>(ref, P.scale_log2); };
             const uint64_t scale2 = sv::f2(P.scale_log2, P.scale_log2);
             uint64_t raw[CW / 2], rnd[CW / 2];  // this position's share of the columns' sums
             int k = 0, seg = -1;
@@ -906,7 +900,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                             ms.ref[c] = now;
                             ms.off[c] = far ? now : 0.f;
                             ms.nref[c] = far ? lift(BF) : add;
-                            ms.fac[c] = old == -INFINITY ? 0.f : ex2(add - minus(old));
+                            ms.fac[c] = sv::reference_factor<BF>(old, now, P.scale_log2);
                             slow = far || now == -INFINITY;
                         }
                         fresh = group_or(bar, 128, slow);
@@ -1028,7 +1022,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                         }
                     } else {
                         float *r = part + NQ * MAXD + col0 + t;
-                        r[0] = ms.ref[col0 + t] == -INFINITY ? -INFINITY : -minus(ms.ref[col0 + t]);
+                        r[0] = ms.ref[col0 + t];
                         r[NQ] = raise ? NAN : sum;
                         r[2 * NQ] = raise ? NAN : rsum;
                     }
@@ -1160,7 +1154,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                         for (int x = 0; x < parts; ++x) {
                             const float m = jm[x * NQ + t], l = jl[x * NQ + t];
                             // 0: the part's positions have no weight in this row
-                            const float f = l == 0.f ? 0.f : ex2(m == -INFINITY ? 0.f : m - top);
+                            const float f = l == 0.f ? 0.f : sv::reference_factor<BF>(m, top, P.scale_log2);
                             if (l != 0.f) sum += f * l, rsum += f * jr[x * NQ + t];
                             jm[x * NQ + t] = f;
                         }
@@ -1171,7 +1165,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                             ms.fac[t] = n < g.nn || bad ? 1.f / rsum : 0.f;
                             jrow[t] = n < P.N ? (uint32_t)row : ~0u;
                             if (n < P.N && P.lse && SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1111))
-                                P.lse[row] = n < g.nn || bad ? ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.69314718f
+                                P.lse[row] = n < g.nn || bad ? (log2f(sum) - minus(top)) * 0.69314718f
                                                              : -INFINITY;
                         } else {
                             float *r = part_of(0) + NQ * MAXD + t;
