@@ -33,13 +33,17 @@
 // are half of that and the softmax the same; scores issued before the weights' products (there are columns of TMEM
 // for both) took 364 us against 350, for the halves' softmax then runs in step.
 #include "sv_e4m3.cuh"
+#include "sv_reference.cuh"
 #include "sv_tc.cuh"
 
 #include <mutex>
 
 namespace svch {
 
+using sv::ex2;
+using sv::FAR;
 using sv::Half2;
+using sv::lift;
 
 constexpr int TILE = 128, ROWS = 256, HALF = 128, MAXD = 128;
 constexpr int MAX_SMS = 192;
@@ -48,9 +52,6 @@ constexpr int SEGS = 4;         // segments listed ahead
 constexpr int SEGMENT = 384;    // the cost of a block's beginning and end, in positions
 constexpr int MIN_TILES = 4;    // of a run (2: 16 tokens behind 30000, one key head, 53 us for a call waited for, against 45.5; 6: 3 x 67 tokens 50 against 44)
 constexpr float SLACK = 8.f;    // log2 of how much a weight may pass the reference's
-constexpr float FAR = 0x1p24f;  // of a reference times the scale: its rounding is whole exponents from here on
-// log2 of the reference's weight: fp16 keeps a long tail of small weights below 2^15 (as in sv_attention.cuh).
-__host__ __device__ constexpr float lift(bool bf16) { return bf16 ? 0.f : 7.f; }
 
 // A block in parts: of CTA c0's run the second part, of c0 + 1 .. c1's the first.
 struct __align__(16) Join {
@@ -108,13 +109,6 @@ constexpr int PART = ROWS * MAXD + 2 * ROWS;
 
 // The keys of a slot outside the pool: NaN of either type.
 static __device__ const uint4 g_nan = {0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu};
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // ---------------------------------------------------------------------------------------------
 // The axis of costs.  A block sees c + 256 (i + 1) / G positions at most; times G that is a whole number, and so
@@ -532,7 +526,6 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
         const uint32_t lanes = (uint32_t)(wq * 32) << 16;
         const uint32_t st = tmem + lanes + half * TILE, ot = tmem + lanes + 256 + half * MAXD;
         const int dsteps = (P.D + 31) / 32;  // in blocks of 32 columns
-        auto minus = [&](float ref) { return ref == -INFINITY ? 0.f : fmaf(-ref, P.scale_log2, lift(BF)); };
         const uint64_t scale2 = sv::f2(P.scale_log2, P.scale_log2);
         int k = 0, seg = 0, ends = 0, units = 0;
         bool ok = true;
@@ -571,8 +564,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
                 const bool move = far || ref == -INFINITY || fmaf(m, P.scale_log2, add) > SLACK + lift(BF);
                 if (__any_sync(0xffffffffu, move)) {
                     const float now = fmaxf(m, ref), was = add;
-                    add = minus(now);
-                    const float fac = ref == -INFINITY ? 0.f : now == ref ? 1.f : ex2(add - was);
+                    add = sv::reference_add<BF>(now, P.scale_log2);
+                    const float fac = sv::reference_factor<BF>(ref, was, now, add, P.scale_log2);
                     ref = now;
                     far = fabsf(add) >= FAR;
                     sum *= fac;
@@ -701,7 +694,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
             float *const part = P.parts + (int64_t)g.part * PART;
             const int r = half * HALF + t;
             if (g.part >= 0) {
-                part[ROWS * MAXD + r] = ref == -INFINITY ? -INFINITY : -add;
+                part[ROWS * MAXD + r] = ref;
                 part[ROWS * MAXD + ROWS + r] = sum;
             } else if (mine && P.lse && SV_INB(row, (int64_t)P.B * P.N * P.Hq, 1305)) {
                 P.lse[row] = (log2f(sum) - add) * 0.69314718f;
@@ -806,11 +799,11 @@ __global__ void __launch_bounds__(JT) finish_kernel(const __grid_constant__ Para
         const int parts = jn.c1 - jn.c0 + 1;
         float top = -INFINITY, sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        // Sums with weights up to 2^(their reference) join; a part without weight has none (NaN has).
+        // Sums join at the higher reference; a part without weight has none (NaN has).
         auto join = [&](float m, float l, const float4 &o) {
             if (l == 0.f) return;
             const float now = fmaxf(top, m);
-            const float f0 = sum == 0.f ? 0.f : ex2(top == now ? 0.f : top - now), f1 = ex2(m == now ? 0.f : m - now);
+            const float f0 = sv::reference_factor<BF>(top, now, P.scale_log2), f1 = sv::reference_factor<BF>(m, now, P.scale_log2);
             top = now;
             sum = sum * f0 + l * f1;
             acc.x = (f0 == 0.f ? 0.f : acc.x * f0) + (f1 == 0.f ? 0.f : o.x * f1);
@@ -843,7 +836,7 @@ __global__ void __launch_bounds__(JT) finish_kernel(const __grid_constant__ Para
                 const float inv = 1.f / sum;
                 reinterpret_cast<uint2 *>(P.out + row * P.D)[d] =
                     make_uint2(Half2<BF>::pack(acc.x * inv, acc.y * inv), Half2<BF>::pack(acc.z * inv, acc.w * inv));
-                if (d == 0 && P.lse) P.lse[row] = ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.69314718f;
+                if (d == 0 && P.lse) P.lse[row] = (log2f(sum) - sv::reference_add<BF>(top, P.scale_log2)) * 0.69314718f;
             }
         }
     }

@@ -31,18 +31,23 @@ __device__ __forceinline__ float reference_add(float ref, float scale)
     return ref == -INFINITY ? 0.f : fmaf(-ref, scale, lift(BF));
 }
 
-// The factor that takes a sum from reference `old` to `now`, which is no lower.
+// The factor that takes a sum from reference `old` to `now`, which is no lower (`was`, `is`: what they add).
 template <bool BF>
-__device__ __forceinline__ float reference_factor(float old, float now, float scale)
+__device__ __forceinline__ float reference_factor(float old, float was, float now, float is, float scale)
 {
     if (old == now) return 1.f;
     if (old == -INFINITY) return 0.f;
-    const float was = reference_add<BF>(old, scale), is = reference_add<BF>(now, scale);
-    const bool far0 = fabsf(was) >= FAR, far1 = fabsf(is) >= FAR;
     float x = is - was;
+    const bool far0 = fabsf(was) >= FAR, far1 = fabsf(is) >= FAR;
     if (far0 || far1)
         x = far0 && far1 ? (old - now) * scale : far1 ? fmaf(-now, scale, -was) + lift(BF) : fmaf(old, scale, is) - lift(BF);
     return ex2(x);
+}
+
+template <bool BF>
+__device__ __forceinline__ float reference_factor(float old, float now, float scale)
+{
+    return reference_factor<BF>(old, reference_add<BF>(old, scale), now, reference_add<BF>(now, scale), scale);
 }
 
 }  // namespace sv

@@ -1,18 +1,21 @@
-"""Attention over scores so large that a reference times the scale keeps no digits behind the point, or passes fp32."""
+"""Every attention over scores so large that a reference times the scale keeps no digits behind the point, or passes fp32."""
 import math
 
 import pytest
 import torch
 
+import plain64_cache as pc
+import speculative_decoding_verification_verify_gb300 as sv
 import test_gpu_attention as ta
 import test_gpu_attention_e4m3 as te
+import test_gpu_chunk as th
 
 pytestmark = pytest.mark.gpu
 
 DEV = torch.device("cuda:0")
 BF, FP = torch.bfloat16, torch.float16
 HALF = {BF: 2.0 ** -8, FP: 2.0 ** -11}
-FORMS = ["nodes", "nodes e4m3"]
+FORMS = ["nodes", "nodes e4m3", "chunk", "chunk e4m3"]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -26,7 +29,9 @@ def _built():
 def call(form, s, scale):
     if form == "nodes":
         return ta.call(s, scale=scale)
-    return te.call(te.pack(s, *s["k_cache"].shape[1:]), scale=scale)
+    if form == "nodes e4m3":
+        return te.call(te.pack(s, *s["k_cache"].shape[1:]), scale=scale)
+    return th.call(th.pack(s, form == "chunk e4m3"), scale=scale)
 
 
 def by_class(form, dtype, c, N, Hq, scale, big, step, order, seed):
@@ -83,7 +88,7 @@ def test_scores_around_2_24(form, c, N, Hq, order, sign):
         compare(got, share, lse, dtype, c + N)
 
 
-@pytest.mark.parametrize("form", ["nodes"])
+@pytest.mark.parametrize("form", ["nodes", "chunk"])
 @pytest.mark.parametrize("c", [700, 40000])
 @pytest.mark.parametrize("order", ["rising", "random", "falling"])
 @pytest.mark.parametrize("sign", [1, -1])
