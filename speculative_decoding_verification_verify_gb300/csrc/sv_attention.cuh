@@ -1129,7 +1129,7 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
 #pragma unroll
                         for (int i = 0; i < IT; ++i) {
                             const float f = jm[x * NQ + c0 + WARPS * i];
-                            if (f == 0.f) continue;
+                            if (f < 0.f) continue;
                             acc[i].x += f * y[i].x;
                             acc[i].y += f * y[i].y;
                             acc[i].z += f * y[i].z;
@@ -1153,8 +1153,9 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
 #pragma unroll 1
                         for (int x = 0; x < parts; ++x) {
                             const float m = jm[x * NQ + t], l = jl[x * NQ + t];
-                            // 0: the part's positions have no weight in this row
-                            const float f = l == 0.f ? 0.f : sv::reference_factor<BF>(m, top, P.scale_log2);
+                            // Below 0: the part's positions have no weight in this row.  (Next to none is 0, and leaves
+                            // what is not finite among their values NaN.)
+                            const float f = l == 0.f ? -1.f : sv::reference_factor<BF>(m, top, P.scale_log2);
                             if (l != 0.f) sum += f * l, rsum += f * jr[x * NQ + t];
                             jm[x * NQ + t] = f;
                         }

@@ -806,10 +806,11 @@ __global__ void __launch_bounds__(JT) finish_kernel(const __grid_constant__ Para
             const float f0 = sv::reference_factor<BF>(top, now, P.scale_log2), f1 = sv::reference_factor<BF>(m, now, P.scale_log2);
             top = now;
             sum = sum * f0 + l * f1;
-            acc.x = (f0 == 0.f ? 0.f : acc.x * f0) + (f1 == 0.f ? 0.f : o.x * f1);
-            acc.y = (f0 == 0.f ? 0.f : acc.y * f0) + (f1 == 0.f ? 0.f : o.y * f1);
-            acc.z = (f0 == 0.f ? 0.f : acc.z * f0) + (f1 == 0.f ? 0.f : o.z * f1);
-            acc.w = (f0 == 0.f ? 0.f : acc.w * f0) + (f1 == 0.f ? 0.f : o.w * f1);
+            // (A factor of 0 leaves what is not finite among values of next to no weight NaN.)
+            acc.x = acc.x * f0 + o.x * f1;
+            acc.y = acc.y * f0 + o.y * f1;
+            acc.z = acc.z * f0 + o.z * f1;
+            acc.w = acc.w * f0 + o.w * f1;
         };
         if (live) {
 #pragma unroll 4

@@ -1,11 +1,10 @@
-"""Every attention over scores so large that a reference times the scale keeps no digits behind the point, or passes fp32."""
+"""Every attention over scores so large that a reference times the scale keeps no digits behind the point, or passes fp32;
+and infinite values among positions of next to no weight."""
 import math
 
 import pytest
 import torch
 
-import plain64_cache as pc
-import speculative_decoding_verification_verify_gb300 as sv
 import test_gpu_attention as ta
 import test_gpu_attention_e4m3 as te
 import test_gpu_chunk as th
@@ -98,3 +97,23 @@ def test_references_beyond_fp32(form, c, order, sign):
     assert ((share == 0) | (share == share.amax(1, keepdim=True))).all()
     compare(got._replace(lse=torch.zeros_like(got.lse)), share, torch.zeros_like(share[:, 0]), BF, c + 8)
     assert (got.lse == sign * math.inf).all()
+
+
+@pytest.mark.parametrize("form", ["nodes", "chunk"])
+@pytest.mark.parametrize("c", [300, 40000])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_infinite_values_of_little_weight(form, c, bad):
+    """A value that is not finite shows in each row that sees it, though its weight is below fp32's numbers; the other
+    elements are the others'."""
+    s = ta.make([c], 4, 2, 1, 64, BF, seed=c)
+    at = s["slot_table"][0, : c + 4].long()
+    s["q"].zero_()
+    s["q"][..., 0] = 1
+    s["k_cache"][at] = 0
+    s["k_cache"][at[c - 30], 0, 0] = 256  # (the others' weights: e^-256)
+    s["v_cache"][at[5], 0, 7] = bad
+    got = call(form, s, 1.0)
+    assert not torch.isfinite(got.out[..., 7].float()).any()
+    want = s["v_cache"][at[c - 30], 0].expand_as(got.out)
+    rest = torch.arange(64, device=DEV) != 7
+    assert torch.equal(got.out[..., rest], want[..., rest])
