@@ -394,10 +394,12 @@ int spec_verify_kv_append_ex(const void *q, const void *k, const void *v, int dt
 /*
  * Positions of the paged cache as contiguous rows of 16 bits (for a caller's own attention, for moving a request to
  * another cache): k_out[b][n] and v_out[b][n] [Hkv][D] = the rows of position first[b] + n, n < num_rows[b] (NULL:
- * all N); the rows past num_rows are 0.  From a cache of 8-bit rows the values are exact (in fp16: where fp16 holds
- * them; what append_ex wrote from fp16 it does).  k_out and v_out are 32-byte aligned.  Arguments as for spec_verify_kv_append_ex; dtype is the outputs' and, where its rows
- * have 16 bits, the cache's.  Device status codes: 5 (num_rows outside [0, N], first below 0, or first + num_rows
- * beyond max_pos): the request's rows are NaN; 6 (a slot outside the pool): that row is NaN.  One launch, no workspace.
+ * all N); the rows past num_rows are 0.  From a cache of 8-bit rows the values are exact, in bf16 but for the digits
+ * below 2^-133, which its subnormals lack (cut off), in fp16 where fp16 holds them (what append_ex wrote from fp16 it
+ * does).  k_out and v_out are 32-byte aligned.  Arguments as for spec_verify_kv_append_ex; dtype is the outputs' and,
+ * where its rows have 16 bits, the cache's.  Device status codes: 5 (num_rows outside [0, N], first below 0, or first +
+ * num_rows beyond max_pos): the request's rows are NaN; 6 (a slot outside the pool): that row is NaN.  One launch, no
+ * workspace.
  */
 int spec_verify_kv_read(const void *k_cache, const void *v_cache, int cache_dtype, int64_t num_slots,
                         int64_t k_slot_stride, int64_t v_slot_stride, const int32_t *slot_table, int max_pos,
@@ -407,7 +409,7 @@ int spec_verify_kv_read(const void *k_cache, const void *v_cache, int cache_dtyp
 /*
  * spec_verify_attention over a cache of 8-bit rows (spec_verify_kv_append_ex).  Arguments, outputs, faults and workspace
  * rules as there, but for the caches' layout: slot strides in bytes, multiples of 16 below 2^31.  The keys and values
- * that enter are what the rows stand for, exactly.
+ * that enter are those that spec_verify_kv_read gives in q's type.
  */
 size_t spec_verify_attention_e4m3_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int max_pos);
 int spec_verify_attention_e4m3(const void *q, int dtype, int64_t q_stride, const void *k_cache,

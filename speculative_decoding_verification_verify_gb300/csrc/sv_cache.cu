@@ -334,8 +334,12 @@ __global__ void __launch_bounds__(READ_NT) read_kernel(const Read P)
         for (int i = 0; i < READ_U; ++i) {
             if (!to[i]) continue;
             if (E4 && scale[i]) {
+                // (In bf16 as the attentions widen, so that its subnormals are the same to all.  In fp16 rows that were
+                // written from bf16 may have powers that it lacks.)
                 const float f = __uint_as_float(scale[i] << 23);
+                const sv::E4m3Scale<true> widen(sv::E4m3Scale<true>::bits(scale[i] & 0xff));
                 auto two = [&](uint32_t bits) {
+                    if (BF) return widen(bits);
                     const float2 z = sv::e4m3_unpack(bits & 0xffffu);
                     return Half2<BF>::pack(z.x * f, z.y * f);
                 };

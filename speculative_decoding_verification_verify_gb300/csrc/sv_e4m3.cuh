@@ -4,8 +4,9 @@
 // up to a multiple of 16 bytes; what a value stands for is e4m3 * 2^e.  e is the smallest exponent with which the
 // head's largest value is within e4m3's 448.  A power of two does for a floating-point format what any other scale
 // would (e4m3's four digits are the same all over its range), and the products are exact in 16 bits: four digits
-// times a power.  So a row that is read back, by whichever kernel, has the same values, and moving a row's bytes
-// (accepted-path compaction) moves its scales.
+// times a power.  (But for bf16's subnormals, below 2^-126, of heads that are smaller than 2^-116 throughout: the digits
+// that they lack are cut off.)  So a row that is read back, by whichever kernel, has the same values, and moving a row's
+// bytes (accepted-path compaction) moves its scales.
 #pragma once
 
 #include "sv_ops.cuh"

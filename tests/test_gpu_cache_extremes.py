@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import plain64_cache as pc
+import speculative_decoding_verification_verify_gb300 as sv
 import test_gpu_cache as tc
 from plain64 import rotate
 
@@ -63,3 +64,25 @@ def test_norms_whose_factors_pass_fp32(e4m3):
             s[x + "_norm"].mul_(2.0 ** up)
         got = tc.check(s, eps=0.0)
         assert torch.isfinite(got.float()).all() and got.float().abs().max() > 2.0 ** (up - 2)
+
+
+def test_the_smallest_values_are_the_same_for_all_who_read_them():
+    """Keys whose finest digits lie below bf16's smallest subnormal: each kernel sees the same 16 bits.  An attention's
+    lse over one position is the scaled product with its key: with a query of one dimension, an element of the key."""
+    D = 64
+    s = tc.setup(1, 1, D, 1, D, D, BF, True, seed=3, norm=False, committed=[0])
+    s["cos_sin"] = tc.make(1, 1, 1, 1, D, D, BF, committed=[40])["cos_sin"][7:8].contiguous()
+    s["k"].mul_(2.0 ** -129)
+    tc.call(s)
+    back = sv.spec_verify_kv_read(s["k_cache"], s["v_cache"], s["slot_table"], s["committed"], 1, kv_heads=1, head_dim=D,
+                                  dtype=BF).k[0, 0, 0].double()
+    row = s["k_cache"][int(s["slot_table"][0, 0])]
+    stored = pc.decode(row, 1, D)[0]
+    assert int(((stored * 2.0 ** 133) % 1 != 0).sum()) > 4
+    assert ((back - stored).abs() < 2.0 ** -133).all()
+    q = torch.eye(D, device=DEV).mul(2.0 ** 100).to(BF).view(1, 1, D, D)
+    for f in (sv.spec_verify_attention_e4m3, sv.spec_verify_attention_chunk):
+        lse = f(q, s["k_cache"], s["v_cache"], s["slot_table"], s["committed"], kv_heads=1, scale=2.0 ** 40, want_lse=True).lse
+        seen = lse[0, 0].double() / 2.0 ** 140
+        # The product is exact; the scale's and the logarithm's base's roundings are a few of 2^-24 of scores from 2^7 on.
+        assert ((seen - back).abs() <= 2.0 ** -21 * back.abs()).all()
