@@ -269,6 +269,8 @@ _workspaces = _Workspaces(torch.zeros)
 # Not the verifiers' workspace: the planner overwrites its buffer, whose counter region the
 # verifiers need to stay zero.
 _plan_workspaces = _Workspaces(torch.empty)
+# Nor are chunks' parts the verifiers' (52 MB a stream): they need no fill, a call writes what it reads.
+_chunk_workspaces = _Workspaces(torch.empty)
 
 
 def workspace_for(nbytes: int, device: torch.device, stream: torch.cuda.Stream) -> torch.Tensor:
@@ -279,9 +281,11 @@ def workspace_for(nbytes: int, device: torch.device, stream: torch.cuda.Stream) 
 def spec_verify_reset_workspaces() -> None:
     """Forget the buffers kept for calls without a workspace: the next call on each stream takes a new,
     zero-filled one.  Needed after device status 7 (a wait inside a kernel ran out), which leaves counters
-    behind on which later calls would join too early.  A graph's calls begin with a fill and need it not;
-    a caller's own workspace is the caller's to zero."""
-    _workspaces.forget()
+    behind on which later calls would join too early; and a way to give their memory back, the planner's and the
+    chunks' too.  A graph's calls begin with a fill and need it not; a caller's own workspace is the caller's to
+    zero."""
+    for kept in (_workspaces, _plan_workspaces, _chunk_workspaces):
+        kept.forget()
 
 
 def _ptr(t: Optional[torch.Tensor]):

@@ -10,10 +10,6 @@ import torch
 from . import binding as b
 
 
-# Not the verifiers' workspace, whose fill with zeros this one does not need: a call writes what it reads.
-_chunk_workspaces = b._Workspaces(torch.empty)
-
-
 class Rows(NamedTuple):
     k: torch.Tensor
     v: torch.Tensor
@@ -184,7 +180,7 @@ def spec_verify_attention_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     raw = b._raw_stream(stream, dev)
     if workspace is None:
         nbytes = spec_verify_attention_chunk_workspace_bytes(B, N, Hq, Hkv, D, max_pos)
-        workspace = _chunk_workspaces.get(nbytes, dev, stream, raw)
+        workspace = b._chunk_workspaces.get(nbytes, dev, stream, raw)
     rc = b._on(dev, lib.spec_verify_attention_chunk)(
         q.data_ptr(), code, b._row_stride("q", q, B, N, Hq, D), k_cache.data_ptr(), v_cache.data_ptr(), rows, S, ks, vs,
         b._index("slot_table", slot_table, (B, max_pos), dev), max_pos, b._index("committed", committed, (B,), dev),
