@@ -423,7 +423,8 @@ int spec_verify_attention_e4m3(const void *q, int dtype, int64_t q_stride, const
  * Attention of a chunk of a prompt over one layer's paged cache, causal: node n of request b sees the positions
  * j <= committed + n, its own included (append first).  A whole prompt is a chunk with committed = 0; requests of
  * different lengths come as one padded batch with num_nodes.  Arguments as for spec_verify_attention, without a tree
- * and with any N (B * N and N * Hq / Hkv below 2^31), and
+ * and with any N (B * N below 2^31; with g = Hq / Hkv, N * g below 2^31 - 256, max_pos below 2^31 - 1024 and
+ * B * Hkv * (N * g + 256) * g * (max_pos + N + 768) below 2^62), and
  *   cache_dtype    dtype: 16-bit rows; SPEC_VERIFY_E4M3: 8-bit rows, slot strides in bytes (spec_verify_kv_append_ex)
  *   workspace      spec_verify_attention_chunk_workspace_bytes(...) bytes, 256-byte aligned; rules as for the verifiers'
  *                  (their counters are not touched)

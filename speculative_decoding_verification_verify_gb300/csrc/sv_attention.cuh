@@ -32,8 +32,8 @@
 // weights reach from 2^15 (of 65504) down to 2^-32 of an ordinary largest one.  131072 positions at
 // 2^-25.2 of one other, together 0.003 of the sum, were lost with a reference of weight 1.
 // An exponent is one fused operation on the score and the reference's rounded product with the scale.  From
-// FAR on that rounding is whole exponents, and the reference is taken from the scores before.  (Everywhere:
-// 101.6 us against 100.7 for the tree of 16 below, 44.7 against 44.4 for the 96 requests.)
+// FAR on that rounding is whole exponents, and the reference is taken from the scores before (sv_reference.cuh).
+// (Everywhere: 101.6 us against 100.7 for the tree of 16 below, 44.7 against 44.4 for the 96 requests.)
 //
 // Measured (GB300, copy rate 6.68 TB/s; 32 query and 8 key heads of 128 unless said): 64 chains of 8 over
 // 509 to 8192 positions 122-125 us for 742 MB, 5.9-6.1 TB/s; one tree of 16 over 131000 positions 100 us
@@ -52,8 +52,10 @@
 // memory but the chain through a tile, some 3400 clocks: copies, widening, scores, softmax and products each wait for
 // the one before, at two tiles in flight, and every look at a barrier or a word of shared memory takes 100 to 200 clocks
 // beside 64 KB of stores and 64 KB of copies and reads a tile; no unit of the SM is half busy.  Measured: the 64 chains
-// 156 us for 377 MB, 2.4 TB/s; the tree of 16 134 us; one token of 64 requests over 8192 positions 360 us (16-bit rows
-// 125, 101 and 320 us: 8-bit rows save memory, not time).
+// 158 us for 377 MB, 2.4 TB/s; the tree of 16 135.5 us; one token of 64 requests over 8192 positions 362 us (16-bit rows
+// 125, 101 and 321 us: 8-bit rows save memory, not time).  A head's CTAs are a whole number, and the rest of the SMs is
+// idle: one token of 8 requests over 8192 positions takes 207 us with 32 heads (128 CTAs), 275 with 40 (120), 413 with
+// 56 (112), 877 with 80 (80) and 910 with 96 (96); over 16-bit rows 169, 206, 281, 396 and 468.
 #pragma once
 
 #include "sv_e4m3.cuh"
@@ -169,12 +171,13 @@ struct Misc {
     Join join[2];
     int joins[2];
     int8_t par[sv::MAX_TREE];
-    // 8-bit rows: of the tiles ahead, the rows' slots (in the order of the copies), the key head (-1: no more), the rows that there are, the segment.
+    // 8-bit rows: of the tiles ahead, the rows' slots (in the order of the copies), the key head (-1: no more), the rows
+    // that there are, the segment.
     struct __align__(16) Slots {
         int slot[TILE];
         int h, left, seg, pad;
     } slots[E4 ? SLOTS : 1];
-    uint64_t slotfull[SLOTS], slotempty[SLOTS];
+    uint64_t slotfull[E4 ? SLOTS : 1], slotempty[E4 ? SLOTS : 1];
 };
 
 __device__ __forceinline__ float warp_max(float x)
@@ -378,6 +381,8 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             // with the one AHEAD tiles on, whose slots are listed, while it is widened.
             constexpr int AHEAD = L::AHEAD;
             using Feed = sv::E4m3Feed<BF, DP, AHEAD>;
+            // (kv is 0 or 1.  Written as 1 for the second warpgroup, the compiler spills more: the 64 chains take 180 us
+            // instead of 158.)
             const int cw = warp & 3, kv = warp < 4 ? 0 : (warp - 4 - 4 * WG) >> 2;
             Feed feed(s0 + L::R0 + kv * L::RING, cw, lane, P.D);
             const unsigned char *const cache = kv ? P.v : P.k;
@@ -438,14 +443,13 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (!E4 && warp < 4) {
-            const int cw = warp;
             // ---- tiles into shared memory -------------------------------------------------
             // A row's CPR chunks go to CPR lanes, 32 / CPR rows to a warp's copy.  A lane keeps the
             // slot of one of its warp's 32 rows; they are read one tile ahead of the copies.
-            [[maybe_unused]] constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
+            constexpr int CPR = DP / 8, RPI = 32 / CPR, ITER = TILE / (4 * RPI);
             const int chunk = lane % CPR, sub = lane / CPR;
-            const int own = cw * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot it keeps
-            const int first = cw * RPI + sub;                                  // its row of the first copy
+            const int own = warp * RPI + lane % RPI + 4 * RPI * (lane / RPI);  // the row whose slot it keeps
+            const int first = warp * RPI + sub;                                // its row of the first copy
             const bool wide = chunk * 8 < P.D;
             Seg g = {};
             int seg = -1, j = 0, slot = -1, u = 0;
@@ -490,42 +494,40 @@ __global__ void __launch_bounds__(threads(NQ, E4), ctas_per_sm(NQ, E4)) attentio
                 }
                 return ok;
             };
-            {
-                const uint32_t to = (chunk >> 3) * TILE * 128 + first * 128 + (((chunk & 7) ^ (first & 7)) << 4);
-                for (int found = seek(true); found == 1 && ok;) {
-                    const int slots = check(j * TILE + own >= g.c + g.nn);
-                    const int64_t at = (int64_t)g.h * P.D + (wide ? chunk * 8 : 0);
-                    const bool whole = __all_sync(0xffffffffu, slots >= 0 && wide);
-                    found = seek(false);
-    #pragma unroll 1
-                    for (int kv = 0; kv < 2 && ok; ++kv, ++u) {
-                        if (!room()) break;
-                        const uint32_t dst = s0 + (u % NU) * L::UNIT + to;
-                        const unsigned char *base = (kv ? P.v : P.k) + 2 * at;
-                        const uint32_t stride = (uint32_t)(kv ? P.v_slot : P.k_slot) * 2;
-                        if (whole) {
-    #pragma unroll
-                            for (int i = 0; i < ITER; ++i) {
-                                const uint32_t s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
-                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 4 * RPI * 128),
-                                             "l"(base + (uint64_t)s * stride)
-                                             : "memory");
-                            }
-                        } else {
-    #pragma unroll 4
-                            for (int i = 0; i < ITER; ++i) {  // zeros where there is nothing to copy
-                                const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
-                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 4 * RPI * 128),
-                                             "l"(base + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride), "r"(s >= 0 && wide ? 16 : 0)
-                                             : "memory");
-                            }
+            const uint32_t to = (chunk >> 3) * TILE * 128 + first * 128 + (((chunk & 7) ^ (first & 7)) << 4);
+            for (int found = seek(true); found == 1 && ok;) {
+                const int slots = check(j * TILE + own >= g.c + g.nn);
+                const int64_t at = (int64_t)g.h * P.D + (wide ? chunk * 8 : 0);
+                const bool whole = __all_sync(0xffffffffu, slots >= 0 && wide);
+                found = seek(false);
+#pragma unroll 1
+                for (int kv = 0; kv < 2 && ok; ++kv, ++u) {
+                    if (!room()) break;
+                    const uint32_t dst = s0 + (u % NU) * L::UNIT + to;
+                    const unsigned char *base = (kv ? P.v : P.k) + 2 * at;
+                    const uint32_t stride = (uint32_t)(kv ? P.v_slot : P.k_slot) * 2;
+                    if (whole) {
+#pragma unroll
+                        for (int i = 0; i < ITER; ++i) {
+                            const uint32_t s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 4 * RPI * 128),
+                                         "l"(base + (uint64_t)s * stride)
+                                         : "memory");
                         }
-                        // The unit's barrier hears of each thread's copies as they land; nobody waits for them here.
-                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&ms.full[u % NU]))
-                                     : "memory");
+                    } else {
+#pragma unroll 4
+                        for (int i = 0; i < ITER; ++i) {  // zeros where there is nothing to copy
+                            const int s = __shfl_sync(0xffffffffu, slots, i * RPI + sub);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 4 * RPI * 128),
+                                         "l"(base + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride), "r"(s >= 0 && wide ? 16 : 0)
+                                         : "memory");
+                        }
                     }
-                    if (found == 2 && ok) found = seek(true);
+                    // The unit's barrier hears of each thread's copies as they land; nobody waits for them here.
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&ms.full[u % NU]))
+                                 : "memory");
                 }
+                if (found == 2 && ok) found = seek(true);
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp == 4) {

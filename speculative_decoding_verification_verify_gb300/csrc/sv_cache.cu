@@ -9,10 +9,12 @@
 // pairs (as in sv_append.cu); the lanes that share a head are neighbours, so that a norm's sum and a head's largest
 // magnitude are a few exchanges, and a row passes through registers once.
 //
-// Measured (GB300, copy rate 6.68 TB/s; 32 query and 8 key heads of 128): append of 8194 rows of fp16 with norms to 8-bit
-// rows 42 us for 185 MB, 4.4 TB/s, its instructions at 70% of the issue slots; with the rows read back 58 us for 237 MB.
-// 384 rows 4.5 us, one row 3 us.  Read of 48 requests' 24 thousand 8-bit rows 27 us for 127 MB, 4.7 TB/s; of 60001 rows of 4
-// heads of 80 28 us for 116 MB, 4.1 TB/s: the chain slot table, slot, row at 48 warps an SM.
+// Measured (GB300, copy rate 6.68 TB/s; 32 query and 8 key heads of 128; in a graph, a call waited for in a row of calls
+// in brackets): append of 8194 rows with norms to 8-bit rows 44 us (48) for 185 MB, 4.2 TB/s, its instructions at 76% of the
+// issue slots; to 16-bit rows 39 us (42) for 201 MB, 5.1 TB/s; 384 rows 4.5 us, one row 3 us.  Read of 48 requests' 24
+// thousand 8-bit rows 27 us (29) for 127 MB, 4.7 TB/s; of 60001 rows of 4 heads of 80 28 us (31) for 117 MB, 4.2 TB/s: the
+// chain slot table, slot, row at 48 warps an SM.  Of 16-bit rows, 48 x 504 in all 33 us (36) for 198 MB, 6.0 TB/s; 60001 of
+// 4 x 80 28 us (31) for 154 MB, 5.5 TB/s.
 #include "sv_e4m3.cuh"
 
 #include <initializer_list>

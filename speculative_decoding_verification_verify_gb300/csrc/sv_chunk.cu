@@ -13,8 +13,10 @@
 //
 // While one half's softmax runs, the other's products do: the tensor cores are fed by the halves in turn.  A thread has
 // a row, so maxima and sums are its own; the softmax's reference moves only when a score passes it by a factor of more
-// than 2^8 in weight (a vote of 32 rows), and the accumulators are scaled then, by the same warps.  Weights are
-// rounded to q's type for the product with v; maxima, sums and accumulators are fp32.
+// than 2^8 in weight (a vote of 32 rows), and the accumulators are scaled then, by the same warps.  Maxima, sums and
+// accumulators are fp32.  Weights are rounded to q's type for the product with v, as the matrix instruction has it; the sum
+// that divides is of the unrounded ones, whose roundings are as often up as down.  (A second sum of the rounded ones, as the
+// nodes' kernel has, would be an unpacking and an addition more for each weight of the part that bounds the kernel.)
 //
 // Each CTA takes an equal run of the batch's work: the blocks of all requests and key heads on one axis of costs
 // (positions that a block sees, plus SEGMENT for its beginning and end), cut into equal pieces; where a cut falls
@@ -25,9 +27,9 @@
 // products, warp 5 lists the run's segments (a segment: the run's tiles of one block), warps 8-11 and 12-15 are the
 // halves' softmax.
 //
-// Measured (GB300, products at 1922 TFLOP/s; 32 query and 8 key heads of 128): 2048 tokens behind 14337 375-390 us, 1.32-1.37
-// PFLOP/s; 4096 behind 28001 over 8-bit rows 1660-1680 us, 1.2 PFLOP/s; 8 prompts of 512 to 4096 (heads of 64, fp16) 347
-// us, 630 TFLOP/s; 3 x 67 tokens behind 901 to 9001 (14 and 2 heads of 80) 26 us.  A half's turn is some 3300
+// Measured (GB300, products at 1922 TFLOP/s; 32 query and 8 key heads of 128): 2048 tokens behind 14337 391-395 us, 1.31-1.32
+// PFLOP/s; 4096 behind 28001 over 8-bit rows 1680 us, 1.2 PFLOP/s; 8 prompts of 512 to 4096 (heads of 64, fp16) 349
+// us, 627 TFLOP/s; 3 x 67 tokens behind 901 to 9001 (14 and 2 heads of 80) 27-28 us.  A half's turn is some 3300
 // clocks a tile: 1700 of softmax (scores and maximum 300, vote 300, weights 900), then the products of its own weights
 // and next scores behind the other half's, 1024 of 2048 clocks of tensor work.  With heads of 64 the products
 // are half of that and the softmax the same; scores issued before the weights' products (there are columns of TMEM
@@ -50,7 +52,9 @@ constexpr int MAX_SMS = 192;
 constexpr int NT = 512;
 constexpr int SEGS = 4;         // segments listed ahead
 constexpr int SEGMENT = 384;    // the cost of a block's beginning and end, in positions
-constexpr int MIN_TILES = 4;    // of a run (2: 16 tokens behind 30000, one key head, 53 us for a call waited for, against 45.5; 6: 3 x 67 tokens 50 against 44)
+// Of a run.  (2: 16 tokens behind 30000, one key head, 53 us for a call waited for, against 45.5; 6: 3 x 67 tokens 50
+// against 44.)
+constexpr int MIN_TILES = 4;
 constexpr float SLACK = 8.f;    // log2 of how much a weight may pass the reference's
 
 // A block in parts: of CTA c0's run the second part, of c0 + 1 .. c1's the first.
@@ -748,7 +752,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Pa
 }
 
 // The second kernel: rows of nodes that are not there, requests whose lengths are wrong, and the blocks in parts.  (The
-// first has two warps with nothing to do, but no registers for them: 8-bit rows 1690 us against 1990 below.)  A slice is 4 rows of a block; 4 groups of threads take every fourth part, a thread 4 dimensions of a row.
+// first has two warps with nothing to do, but no registers for them: 4096 tokens over 8-bit rows took 1990 us against
+// 1690.)  A slice is 4 rows of a block; 4 groups of threads take every fourth part, a thread 4 dimensions of a row.
 constexpr int JT = 512, SLICES = ROWS / 4;
 
 template <bool BF>

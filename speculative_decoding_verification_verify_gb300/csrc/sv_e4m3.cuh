@@ -13,9 +13,9 @@
 
 namespace sv {
 
-// Exponents end at 7, whatever the type: 2^(120 + e), by which the attention kernels bring a value's bits to bf16,
-// is then a number, and values saturate at 448 * 2^7 = 57344, which fp16 holds.  They begin where 2^e is a normal
-// fp32; in fp16 at -15, below which nothing is gained: e4m3's smallest step is then 2^-24, fp16's own.
+// Exponents end at 7, whatever the type: values saturate at 448 * 2^7 = 57344, the largest of them that fp16 holds, and
+// one limit serves both types (bf16's larger values are lost by it).  They begin where 2^e is a normal fp32; in fp16
+// at -15, below which nothing is gained: e4m3's smallest step is then 2^-24, fp16's own.
 constexpr int E4M3_HI = 7;
 __host__ __device__ constexpr int e4m3_lo(bool bf16) { return bf16 ? -126 : -15; }
 
@@ -51,7 +51,8 @@ __device__ __forceinline__ uint32_t e4m3_half2(uint32_t bits)
 __device__ __forceinline__ float2 e4m3_unpack(uint32_t bits) { return Half2<false>::unpack(e4m3_half2(bits)); }
 
 // Values in 16 bits, times their head's power of two: exact, NaN too.  128 values of a thread take 800 clocks of four
-// warps in bf16, 380 in fp16, half of it the conversions at a quarter of the rate.  `bits` of a head are the factor in the type.  (Shifting the bits to where bf16 has them and one product is as many instructions, but knows no NaN.)
+// warps in bf16, 380 in fp16, half of it the conversions at a quarter of the rate.  `bits` of a head are the factor in
+// the type.  (Shifting the bits to where bf16 has them and one product is as many instructions, but knows no NaN.)
 template <bool BF>
 struct E4m3Scale;
 
